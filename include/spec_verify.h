@@ -268,6 +268,104 @@ int spec_filter_top_k_top_p(void* logits, int dtype, int n, int V, const int32_t
 int spec_gamma_select(const float* signals, const float* comp, const float* model, int B,
                       int32_t* gamma_star, float* expected, spec_stream_t stream);
 
+/* The calls below train a drafter against the target: the record of a
+ * teacher's row, the loss of a student's rows against such records, and the
+ * cross entropy of the vocabulary projection.  Rows are [n, ...] row-major and
+ * contiguous; a batch [B, G, V] is n = B G rows.  Losses and log masses are in
+ * nats.  Calls are enqueued on `stream`, allocate nothing, and give the same
+ * bits for the same inputs.  `status` [n] is optional (NULL). */
+
+#define SPEC_MAX_TOPK 256
+#define SPEC_DISTILL_MAX_V (1 << 20)
+
+/* The record of teacher rows: for row r of logits [n, V] at temperature T,
+ *   top_logits [n, K] fp32, top_index [n, K] int32: the K largest logits, the
+ *     largest first, equal values (-0 and +0 among them) by ascending token;
+ *   tail_lse   [n] fp32: ln sum e^{x_v / T} over the tokens not recorded, -inf
+ *     when they have no mass.
+ * A logit of -inf is not recorded: a row with fewer than K others (a filtered
+ * row) ends with entries of logit -inf and index -1.
+ *   K           1 <= K <= min(V, SPEC_MAX_TOPK);
+ *   temperature [n] fp32 or NULL (= 1);
+ *   status      0, SPEC_ST_NONFINITE (a NaN or +inf, or no finite logit) or
+ *     SPEC_ST_BAD_TEMPERATURE; such a row has NaN logits, indices -1 and a NaN
+ *     tail.
+ * No workspace.  Host errors: SPEC_ERR_INVALID_ARG (n < 1, V outside [2, 2^28),
+ * K, dtype, NULL required pointers, misalignment), SPEC_ERR_CUDA,
+ * SPEC_ERR_UNSUPPORTED. */
+int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const float* temperature,
+                     float* top_logits, int32_t* top_index, float* tail_lse, int32_t* status,
+                     spec_stream_t stream);
+
+/* The loss of student rows against teacher records, and its gradient (the DLite
+ * page's distillation losses: forward KL, TV, CE, position weights).  For row r
+ * with the record (x_k, t_k) and tail, over the K tokens and one bucket for all
+ * others, p_k = e^{x_k / T} / Z and p_rest = e^{tail} / Z (Z makes them sum to
+ * 1), q = softmax(logits / T), q_rest the sum of q over the others:
+ *   KL = sum_b p_b ln(p_b / q_b), TV = 1/2 sum_b |p_b - q_b|, CE = -ln q_label,
+ *   loss[r] = row_weight[r] (kl KL + tv TV + ce CE);
+ *   grad_logits = the gradient of the sum of the losses by logits.
+ *   logits      [n, V], SPEC_F32 or SPEC_BF16, V <= SPEC_DISTILL_MAX_V;
+ *   top_logits, top_index [n, K], 1 <= K <= SPEC_MAX_TOPK: entries in any order;
+ *     an entry of index -1 is left out, whatever its logit;
+ *   tail_lse    [n] or NULL; NULL or -inf: the teacher has no mass outside the
+ *     record, p is renormalised over its K logits;
+ *   label       [n] int32 or NULL; -1 or NULL: no CE term;
+ *   row_weight  [n] fp32 or NULL (= 1); of a row of weight 0 (padding) nothing
+ *     is read, its loss, parts and gradient are 0;
+ *   temperature [n] fp32 or NULL (= 1), of both distributions;
+ *   kl, tv, ce  coefficients, finite; a term of coefficient 0 is left out;
+ *   loss        [n] fp32; parts [n, 3] fp32 or NULL: KL, TV, CE (0 without a
+ *     label), without weight and coefficients;
+ *   grad_logits [n, V] of the logits' dtype or NULL (loss alone).  It may be
+ *     `logits` itself, which is then overwritten; any other overlap is refused.
+ *   status      0, SPEC_ST_BAD_TOKEN (a label or index outside [-1, V), or an
+ *     index recorded twice), SPEC_ST_BAD_TEMPERATURE, SPEC_ST_NONFINITE (a NaN
+ *     or +inf in the row or the record, no finite logit, or a record without
+ *     mass): such a row has NaN losses and a gradient of 0.
+ * KL is +inf where some q_b = 0 < p_b, CE where q_label = 0; the gradient stays
+ * finite.  Without the gradient each row is read once.  With it, pass the
+ * upstream gradient of a row's loss as a factor of row_weight.
+ * No workspace.  Host errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_CUDA,
+ * SPEC_ERR_UNSUPPORTED. */
+int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const float* top_logits,
+                      const int32_t* top_index, const float* tail_lse, const int32_t* label,
+                      const float* row_weight, const float* temperature, float kl, float tv, float ce,
+                      float* loss, float* parts, void* grad_logits, int32_t* status, spec_stream_t stream);
+
+/* Softmax cross entropy of a vocabulary projection without its logits in
+ * memory.  With l = hidden weight^T,
+ *   lse[r] = ln sum_v e^{l_rv}, loss[r] = lse[r] - l_{r, label[r]};
+ * and, with g = grad_loss[r], G_rv = g (e^{l_rv - lse[r]} - [v = label[r]]),
+ *   grad_hidden = G weight, grad_weight = G^T hidden.
+ *   hidden [n, H], weight [V, H]: SPEC_BF16 (products of bf16, fp32 sums); H a
+ *     multiple of 8, both 16-byte aligned;
+ *   label  [n] int32; -1: the row takes no part (loss 0, lse 0, gradient 0), and
+ *     what its hidden state holds does not matter;
+ *   lse    [n] fp32: written by the forward call, read by the backward call;
+ *   grad_loss [n] fp32 or NULL (= 1); a row of grad_loss 0 takes no part;
+ *   grad_hidden [n, H], grad_weight [V, H] bf16, written; either may be NULL (a
+ *     frozen projection), not both.  G is rounded to bf16 once, before the two
+ *     products that read it;
+ *   status [n] or NULL (forward): 0, SPEC_ST_BAD_TOKEN (label outside [-1, V):
+ *     loss and lse NaN), SPEC_ST_NONFINITE (a logit of the row is NaN or +inf,
+ *     or none is finite: loss and lse NaN).  The backward call leaves out rows
+ *     with a bad label or an lse that is not finite.
+ *   workspace: spec_linear_ce_workspace_bytes(n, H, V, backward) bytes, 256-byte
+ *     aligned, no initial contents.  Calls that share one must not overlap on
+ *     the device; that holds for captured graphs too.
+ * Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^20], H outside [8, 65536]
+ * or not a multiple of 8, V outside [2, 2^28), dtype, NULL required pointers,
+ * misalignment), SPEC_ERR_WORKSPACE, SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
+size_t spec_linear_ce_workspace_bytes(int n, int H, int V, int backward);
+int spec_linear_ce_forward(const void* hidden, const void* weight, int dtype, int n, int H, int V,
+                           const int32_t* label, float* loss, float* lse, int32_t* status,
+                           void* workspace, size_t workspace_bytes, spec_stream_t stream);
+int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, int n, int H, int V,
+                            const int32_t* label, const float* lse, const float* grad_loss,
+                            void* grad_hidden, void* grad_weight,
+                            void* workspace, size_t workspace_bytes, spec_stream_t stream);
+
 /* Size of the library-owned scratch used by spec_verify_sample_static: 8 MiB.
  * It holds the workspace of spec_workspace_bytes(B, G, V) <= this value, e.g.
  * B <= 268 at G = 8, V = 151936, or B <= 276 at G = 7, V = 151936. */

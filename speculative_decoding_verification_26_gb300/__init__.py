@@ -13,3 +13,7 @@ from ._lib import (  # noqa: F401
     verify_greedy, verify_onehot, verify_sample, workspace, workspace_bytes,
 )
 from ._lib import STATIC_WORKSPACE_BYTES, verify_sample_static  # noqa: F401
+from ._lib import (  # noqa: F401
+    DISTILL_MAX_V, MAX_TOPK, distill_topk, linear_ce_backward, linear_ce_forward, linear_ce_workspace,
+    linear_ce_workspace_bytes, topk_logits,
+)

@@ -68,6 +68,17 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.spec_filter_top_k_top_p.restype = I
         L.spec_gamma_select.restype = I
         L.spec_draft_signals.restype = I
+        F = ctypes.c_float
+        L.spec_topk_logits.argtypes = [P, I, I, I, I, P, P, P, P, P, P]
+        L.spec_topk_logits.restype = I
+        L.spec_distill_topk.argtypes = [P, I, I, I, I, P, P, P, P, P, P, F, F, F, P, P, P, P, P]
+        L.spec_distill_topk.restype = I
+        L.spec_linear_ce_workspace_bytes.argtypes = [I, I, I, I]
+        L.spec_linear_ce_workspace_bytes.restype = SZ
+        L.spec_linear_ce_forward.argtypes = [P, P, I, I, I, I, P, P, P, P, P, SZ, P]
+        L.spec_linear_ce_forward.restype = I
+        L.spec_linear_ce_backward.argtypes = [P, P, I, I, I, I, P, P, P, P, P, P, SZ, P]
+        L.spec_linear_ce_backward.restype = I
         if path is None:
             _lib = L
         return L
@@ -335,6 +346,175 @@ def draft_signals(draft, gamma, temperature, *, row_signals=False, ws=None, out=
     r = {"signals": sig, "status": st}
     if rs is not None:
         r["row_signals"] = rs
+    return r
+
+
+MAX_TOPK = 256
+DISTILL_MAX_V = 1 << 20
+
+
+def _call(dev, name, *args):
+    """Call the C entry point with `dev` current and its current stream last."""
+    torch = _torch()
+    f = getattr(lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        rc = f(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = f(*args, _stream(dev))
+    if rc != OK:
+        raise SpecVerifyError(rc, name)
+
+
+def topk_logits(logits, K, temperature=None, *, out=None):
+    """The record of teacher rows: logits [..., V] (n rows, fp32 or bf16),
+    temperature [n] fp32 or None; returns {"top_logits": [n, K] fp32,
+    "top_index": [n, K] int32, "tail_lse": [n], "status": [n]} (see
+    spec_topk_logits)."""
+    torch = _torch()
+    V = logits.shape[-1]
+    n = logits.numel() // V
+    dev = logits.device
+    _check(logits, "logits", device=dev)
+    _check(temperature, "temperature", torch.float32, (n,), dev)
+    o = out or {}
+    top = _out(o, "top_logits", lambda: torch.empty(n, K, dtype=torch.float32, device=dev))
+    idx = _out(o, "top_index", lambda: torch.empty(n, K, dtype=torch.int32, device=dev))
+    tail = _out(o, "tail_lse", lambda: torch.empty(n, dtype=torch.float32, device=dev))
+    st = _out(o, "status", lambda: torch.empty(n, dtype=torch.int32, device=dev))
+    if o:
+        _check(top, "top_logits", torch.float32, (n, K), dev)
+        _check(idx, "top_index", torch.int32, (n, K), dev)
+        _check(tail, "tail_lse", torch.float32, (n,), dev)
+        _check(st, "status", torch.int32, (n,), dev)
+    _call(dev, "spec_topk_logits", _ptr(logits), _dtype_code(logits), n, V, K, _ptr(temperature), _ptr(top),
+          _ptr(idx), _ptr(tail), _ptr(st))
+    return {"top_logits": top, "top_index": idx, "tail_lse": tail, "status": st}
+
+
+def distill_topk(logits, top_logits, top_index, tail_lse=None, *, label=None, row_weight=None, temperature=None,
+                 kl=1.0, tv=0.0, ce=0.0, grad=False, out=None):
+    """The loss of student rows `logits` [..., V] (n rows, fp32 or bf16) against
+    records (topk_logits), and with `grad` its gradient by the logits; label [n]
+    int32, row_weight [n], temperature [n] fp32, each optional.  Returns
+    {"loss": [n], "parts": [n, 3] (KL, TV, CE), "status": [n]} and "grad" (as
+    `logits`; out={"grad": logits} overwrites them).  See spec_distill_topk."""
+    torch = _torch()
+    V = logits.shape[-1]
+    n = logits.numel() // V
+    dev = logits.device
+    K = top_logits.shape[-1]
+    _check(logits, "logits", device=dev)
+    _check(top_logits, "top_logits", torch.float32, (n, K), dev)
+    _check(top_index, "top_index", torch.int32, (n, K), dev)
+    _check(tail_lse, "tail_lse", torch.float32, (n,), dev)
+    _check(label, "label", torch.int32, (n,), dev)
+    _check(row_weight, "row_weight", torch.float32, (n,), dev)
+    _check(temperature, "temperature", torch.float32, (n,), dev)
+    o = out or {}
+    loss = _out(o, "loss", lambda: torch.empty(n, dtype=torch.float32, device=dev))
+    parts = _out(o, "parts", lambda: torch.empty(n, 3, dtype=torch.float32, device=dev))
+    st = _out(o, "status", lambda: torch.empty(n, dtype=torch.int32, device=dev))
+    g = _out(o, "grad", lambda: torch.empty_like(logits)) if grad else None
+    if o:
+        _check(loss, "loss", torch.float32, (n,), dev)
+        _check(parts, "parts", torch.float32, (n, 3), dev)
+        _check(st, "status", torch.int32, (n,), dev)
+        _check(g, "grad", logits.dtype, logits.shape, dev)
+    _call(dev, "spec_distill_topk", _ptr(logits), _dtype_code(logits), n, V, K, _ptr(top_logits), _ptr(top_index),
+          _ptr(tail_lse), _ptr(label), _ptr(row_weight), _ptr(temperature), kl, tv, ce, _ptr(loss), _ptr(parts),
+          _ptr(g), _ptr(st))
+    r = {"loss": loss, "parts": parts, "status": st}
+    if grad:
+        r["grad"] = g
+    return r
+
+
+def linear_ce_workspace_bytes(n: int, H: int, V: int, backward: bool) -> int:
+    return int(lib().spec_linear_ce_workspace_bytes(int(n), int(H), int(V), int(bool(backward))))
+
+
+_ce_ws_cache: dict = {}
+
+
+def linear_ce_workspace(n, H, V, device, *, backward):
+    """A cached workspace of linear_ce_forward / linear_ce_backward for these
+    sizes (reused by calls on the same stream; calls sharing it must not overlap
+    on the device).  Under stream capture it is new: a graph keeps its own."""
+    torch = _torch()
+    need = linear_ce_workspace_bytes(n, H, V, backward)
+    if need == 0:
+        raise ValueError("sizes outside the library limits")
+    make = lambda: torch.empty(need, dtype=torch.uint8, device=device)   # noqa: E731
+    if torch.cuda.is_current_stream_capturing():
+        return make()
+    key = (str(device), torch.cuda.current_stream(device).cuda_stream)
+    ws = _ce_ws_cache.get(key)
+    if ws is None or ws.numel() < need:
+        _ce_ws_cache.pop(key, None)
+        ws = _ce_ws_cache[key] = make()
+    return ws
+
+
+def _ce_inputs(hidden, weight, label):
+    torch = _torch()
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden is [n, H] and weight [V, H]")
+    n, H = hidden.shape
+    V = weight.shape[0]
+    dev = hidden.device
+    _check(hidden, "hidden", torch.bfloat16, (n, H), dev)
+    _check(weight, "weight", torch.bfloat16, (V, H), dev)
+    _check(label, "label", torch.int32, (n,), dev)
+    return n, H, V, dev
+
+
+def linear_ce_forward(hidden, weight, label, *, ws=None, out=None):
+    """Cross entropy of the projection hidden [n, H] times weight [V, H] (bf16)
+    against label [n] int32 (-1: the row takes no part), without its logits.
+    Returns {"loss": [n], "lse": [n], "status": [n]} (see spec_linear_ce_forward)."""
+    torch = _torch()
+    n, H, V, dev = _ce_inputs(hidden, weight, label)
+    o = out or {}
+    loss = _out(o, "loss", lambda: torch.empty(n, dtype=torch.float32, device=dev))
+    lse = _out(o, "lse", lambda: torch.empty(n, dtype=torch.float32, device=dev))
+    st = _out(o, "status", lambda: torch.empty(n, dtype=torch.int32, device=dev))
+    if o:
+        _check(loss, "loss", torch.float32, (n,), dev)
+        _check(lse, "lse", torch.float32, (n,), dev)
+        _check(st, "status", torch.int32, (n,), dev)
+    ws = ws if ws is not None else linear_ce_workspace(n, H, V, dev, backward=False)
+    _check(ws, "ws", torch.uint8, device=dev)
+    _call(dev, "spec_linear_ce_forward", _ptr(hidden), _ptr(weight), BF16, n, H, V, _ptr(label), _ptr(loss),
+          _ptr(lse), _ptr(st), _ptr(ws), ws.numel())
+    return {"loss": loss, "lse": lse, "status": st}
+
+
+def linear_ce_backward(hidden, weight, label, lse, grad_loss=None, *, need_hidden=True, need_weight=True, ws=None,
+                       out=None):
+    """Gradients of sum(grad_loss * loss) by hidden and weight; lse as
+    linear_ce_forward returned it, grad_loss [n] fp32 or None (= 1).  Returns
+    {"grad_hidden": [n, H] bf16, "grad_weight": [V, H] bf16}, without the one
+    that is not needed (see spec_linear_ce_backward)."""
+    torch = _torch()
+    n, H, V, dev = _ce_inputs(hidden, weight, label)
+    _check(lse, "lse", torch.float32, (n,), dev)
+    _check(grad_loss, "grad_loss", torch.float32, (n,), dev)
+    o = out or {}
+    gh = _out(o, "grad_hidden", lambda: torch.empty_like(hidden)) if need_hidden else None
+    gw = _out(o, "grad_weight", lambda: torch.empty_like(weight)) if need_weight else None
+    if o:
+        _check(gh, "grad_hidden", torch.bfloat16, (n, H), dev)
+        _check(gw, "grad_weight", torch.bfloat16, (V, H), dev)
+    ws = ws if ws is not None else linear_ce_workspace(n, H, V, dev, backward=True)
+    _check(ws, "ws", torch.uint8, device=dev)
+    _call(dev, "spec_linear_ce_backward", _ptr(hidden), _ptr(weight), BF16, n, H, V, _ptr(label), _ptr(lse),
+          _ptr(grad_loss), _ptr(gh), _ptr(gw), _ptr(ws), ws.numel())
+    r = {}
+    if need_hidden:
+        r["grad_hidden"] = gh
+    if need_weight:
+        r["grad_weight"] = gw
     return r
 
 

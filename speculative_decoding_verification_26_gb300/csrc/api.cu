@@ -14,6 +14,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 
@@ -29,6 +30,7 @@ thread_local cudaEvent_t g_prof_begin = nullptr, g_prof_end = nullptr;
 
 struct DevState {
   bool ready = false;
+  int sms = 0;        // multiprocessors
   int ctas = 0;       // resident verify CTAs on the device (SMs x CTAs per SM, at most 2 per SM)
   int status = SPEC_OK;
 };
@@ -48,10 +50,12 @@ int device_state(int* ctas) {
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return SPEC_ERR_CUDA;
+    d.sms = n;
     if (major != 10 || minor != 3) {
       d.status = SPEC_ERR_UNSUPPORTED;   // the library carries sm_103a code only
     } else {
       cudaError_t e = configure_kernels();
+      if (e == cudaSuccess) e = configure_distill();
       int per_sm = 0;
       if (e == cudaSuccess) e = verify_blocks_per_sm(&per_sm);
       if (e != cudaSuccess) return SPEC_ERR_CUDA;
@@ -67,6 +71,17 @@ int device_state(int* ctas) {
   }
   *ctas = d.ctas;
   return d.status;
+}
+
+// Multiprocessors of the current device, after a device_state that succeeded.
+int current_sms() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
+  return g_dev[dev].sms;
+}
+
+bool ce_sizes_ok(int n, int H, int V) {
+  return n >= 1 && n <= (1 << 20) && H >= 8 && H <= 65536 && H % 8 == 0 && V >= 2 && V < (1 << 28);
 }
 
 bool sizes_ok(int B, int G, int V) {
@@ -381,6 +396,123 @@ int spec_gamma_select(const float* signals, const float* comp, const float* mode
     return SPEC_ERR_CUDA;
   ++g_launches;
   return SPEC_OK;
+}
+
+int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const float* temperature, float* top_logits,
+                     int32_t* top_index, float* tail_lse, int32_t* status, spec_stream_t stream) {
+  if (n < 1 || V < 2 || V >= (1 << 28) || K < 1 || K > SPEC_MAX_TOPK || K > V) return SPEC_ERR_INVALID_ARG;
+  if (!logits || !top_logits || !top_index || !tail_lse || (dtype != SPEC_F32 && dtype != SPEC_BF16))
+    return SPEC_ERR_INVALID_ARG;
+  const void* ptrs4[] = {temperature, top_logits, top_index, tail_lse, status};
+  for (const void* p : ptrs4)
+    if (!aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(logits, dtype == SPEC_BF16 ? 2 : 4)) return SPEC_ERR_INVALID_ARG;
+  int ctas = 0;
+  const int ds = device_state(&ctas);
+  if (ds != SPEC_OK) return ds;
+  RecordParams P{};
+  P.logits = static_cast<const unsigned char*>(logits);
+  P.dtype = dtype; P.n = n; P.V = V; P.K = K;
+  P.temperature = temperature;
+  P.top_logits = top_logits; P.top_index = top_index; P.tail_lse = tail_lse; P.status = status;
+  if (launch_record(P, current_sms(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
+  ++g_launches;
+  return SPEC_OK;
+}
+
+int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const float* top_logits,
+                      const int32_t* top_index, const float* tail_lse, const int32_t* label, const float* row_weight,
+                      const float* temperature, float kl, float tv, float ce, float* loss, float* parts,
+                      void* grad_logits, int32_t* status, spec_stream_t stream) {
+  if (n < 1 || V < 2 || V > SPEC_DISTILL_MAX_V || K < 1 || K > SPEC_MAX_TOPK) return SPEC_ERR_INVALID_ARG;
+  if (!logits || !top_logits || !top_index || !loss || (dtype != SPEC_F32 && dtype != SPEC_BF16))
+    return SPEC_ERR_INVALID_ARG;
+  if (!std::isfinite(kl) || !std::isfinite(tv) || !std::isfinite(ce)) return SPEC_ERR_INVALID_ARG;
+  const void* ptrs4[] = {top_logits, top_index, tail_lse, label, row_weight, temperature, loss, parts, status};
+  for (const void* p : ptrs4)
+    if (!aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
+  const size_t es = dtype == SPEC_BF16 ? 2 : 4;
+  if (!aligned(logits, es) || !aligned(grad_logits, es)) return SPEC_ERR_INVALID_ARG;
+  if (grad_logits && grad_logits != logits) {        // in place, or apart
+    const uintptr_t a = reinterpret_cast<uintptr_t>(logits), b = reinterpret_cast<uintptr_t>(grad_logits);
+    if ((a < b ? b - a : a - b) < (size_t)n * V * es) return SPEC_ERR_INVALID_ARG;
+  }
+  int ctas = 0;
+  const int ds = device_state(&ctas);
+  if (ds != SPEC_OK) return ds;
+  DistillParams P{};
+  P.logits = static_cast<const unsigned char*>(logits);
+  P.dtype = dtype; P.n = n; P.V = V; P.K = K;
+  P.top_logits = top_logits; P.top_index = top_index; P.tail_lse = tail_lse;
+  P.label = label; P.row_weight = row_weight; P.temperature = temperature;
+  P.kl = kl; P.tv = tv; P.ce = ce;
+  P.loss = loss; P.parts = parts; P.status = status;
+  P.grad = static_cast<unsigned char*>(grad_logits);
+  if (launch_distill(P, current_sms(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
+  ++g_launches;
+  return SPEC_OK;
+}
+
+size_t spec_linear_ce_workspace_bytes(int n, int H, int V, int backward) {
+  if (!ce_sizes_ok(n, H, V)) return 0;
+  CeParams P{};
+  P.n = n; P.H = H; P.V = V;
+  return ce_layout(P, backward != 0, nullptr);
+}
+
+int spec_linear_ce_forward(const void* hidden, const void* weight, int dtype, int n, int H, int V,
+                           const int32_t* label, float* loss, float* lse, int32_t* status, void* workspace,
+                           size_t workspace_bytes, spec_stream_t stream) {
+  if (!ce_sizes_ok(n, H, V) || dtype != SPEC_BF16 || !hidden || !weight || !label || !loss || !lse)
+    return SPEC_ERR_INVALID_ARG;
+  if (!aligned(hidden, 16) || !aligned(weight, 16)) return SPEC_ERR_INVALID_ARG;
+  const void* ptrs4[] = {label, loss, lse, status};
+  for (const void* p : ptrs4)
+    if (!aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
+  CeParams P{};
+  P.n = n; P.H = H; P.V = V;
+  if (!workspace || workspace_bytes < ce_layout(P, false, workspace)) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return SPEC_ERR_INVALID_ARG;
+  int ctas = 0;
+  const int ds = device_state(&ctas);
+  if (ds != SPEC_OK) return ds;
+  P.hidden = static_cast<const __nv_bfloat16*>(hidden);
+  P.weight = static_cast<const __nv_bfloat16*>(weight);
+  P.label = label; P.loss = loss; P.lse = lse; P.status = status;
+  int launches = 0;
+  const cudaError_t e = launch_ce_forward(P, current_sms(), reinterpret_cast<cudaStream_t>(stream), &launches);
+  g_launches += launches;
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, int n, int H, int V,
+                            const int32_t* label, const float* lse, const float* grad_loss, void* grad_hidden,
+                            void* grad_weight, void* workspace, size_t workspace_bytes, spec_stream_t stream) {
+  if (!ce_sizes_ok(n, H, V) || dtype != SPEC_BF16 || !hidden || !weight || !label || !lse)
+    return SPEC_ERR_INVALID_ARG;
+  if (!grad_hidden && !grad_weight) return SPEC_ERR_INVALID_ARG;
+  const void* ptrs16[] = {hidden, weight, grad_hidden, grad_weight};
+  for (const void* p : ptrs16)
+    if (!aligned(p, 16)) return SPEC_ERR_INVALID_ARG;
+  const void* ptrs4[] = {label, lse, grad_loss};
+  for (const void* p : ptrs4)
+    if (!aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
+  CeParams P{};
+  P.n = n; P.H = H; P.V = V;
+  if (!workspace || workspace_bytes < ce_layout(P, true, workspace)) return SPEC_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return SPEC_ERR_INVALID_ARG;
+  int ctas = 0;
+  const int ds = device_state(&ctas);
+  if (ds != SPEC_OK) return ds;
+  P.hidden = static_cast<const __nv_bfloat16*>(hidden);
+  P.weight = static_cast<const __nv_bfloat16*>(weight);
+  P.label = label; P.lse_in = lse; P.grad_loss = grad_loss;
+  P.grad_hidden = static_cast<__nv_bfloat16*>(grad_hidden);
+  P.grad_weight = static_cast<__nv_bfloat16*>(grad_weight);
+  int launches = 0;
+  const cudaError_t e = launch_ce_backward(P, current_sms(), reinterpret_cast<cudaStream_t>(stream), &launches);
+  g_launches += launches;
+  return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 int spec_draft_signals(const void* draft_logits, int dtype, int B, int G, int V, const int32_t* gamma,

@@ -3,6 +3,7 @@
 // copy, scoped atomics) and the per-row softmax statistics.
 #pragma once
 
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -518,6 +519,71 @@ struct FiltParams {
   int32_t* status;               // [n] or null
 };
 cudaError_t launch_filter(const FiltParams& P, int grid, cudaStream_t s);
+
+// Parameters of the teacher-record kernel (record.cu).
+struct RecordParams {
+  const unsigned char* logits;   // [n, V]
+  int dtype, n, V, K;
+  const float* temperature;      // [n] or null (= 1)
+  float* top_logits;             // [n, K]
+  int32_t* top_index;            // [n, K]
+  float* tail_lse;               // [n]
+  int32_t* status;               // [n] or null
+};
+cudaError_t launch_record(const RecordParams& P, int nsm, cudaStream_t s);
+
+// Parameters of the distillation kernel (distill.cu).
+constexpr int kDistillMaxV = SPEC_DISTILL_MAX_V;
+struct DistillParams {
+  const unsigned char* logits;   // [n, V]
+  int dtype, n, V, K;
+  const float* top_logits;       // [n, K]
+  const int32_t* top_index;      // [n, K]
+  const float* tail_lse;         // [n] or null (no rest)
+  const int32_t* label;          // [n] or null (no CE term)
+  const float* row_weight;       // [n] or null (= 1)
+  const float* temperature;      // [n] or null (= 1)
+  float kl, tv, ce;
+  float* loss;                   // [n]
+  float* parts;                  // [n, 3] or null
+  unsigned char* grad;           // [n, V] or null
+  int32_t* status;               // [n] or null
+};
+cudaError_t launch_distill(const DistillParams& P, int nsm, cudaStream_t s);
+cudaError_t configure_distill();   // dynamic shared-memory limit, current device
+
+// Parameters of the linear cross entropy (linear_ce.cu).  Row tiles are
+// kCeRowTile high, vocabulary tiles kCeVocabTile wide.
+constexpr int kCeRowTile = 256, kCeVocabTile = 256;
+struct CeParams {
+  const __nv_bfloat16* hidden;   // [n, H]
+  const __nv_bfloat16* weight;   // [V, H]
+  int n, H, V;
+  const int32_t* label;          // [n]
+  const float* lse_in;           // [n], backward
+  const float* grad_loss;        // [n] or null (= 1), backward
+  float* loss;                   // [n], forward
+  float* lse;                    // [n], forward
+  int32_t* status;               // [n] or null, forward
+  __nv_bfloat16* grad_hidden;    // [n, H] or null, backward
+  __nv_bfloat16* grad_weight;    // [V, H] or null, backward
+  // workspace views; compact rows are the rows that take part, in order
+  int n_pad;                     // n in whole row tiles
+  int piece;                     // vocabulary rows of a piece of the backward pass
+  int* count;                    // compact rows
+  int* row_of;                   // [n_pad] the row of a compact row
+  int* lab;                      // [n_pad] its label, -1 past the last
+  int* pos_of;                   // [n] the compact row of a row, -1: none
+  __nv_bfloat16* rows;           // [n_pad, H] compact hidden states, zeros past the last
+  float* label_logit;            // [n_pad]
+  float2* part;                  // [vocabulary tiles, n_pad] maximum and sum
+  float *lse_c, *g_c;            // [n_pad]
+  __nv_bfloat16* soft;           // [n_pad, piece] the gradient by the logits
+  float* acc;                    // [n_pad, H] sums of grad_hidden
+};
+size_t ce_layout(CeParams& P, bool backward, void* base);   // fills the views, returns the bytes
+cudaError_t launch_ce_forward(const CeParams& P, int nsm, cudaStream_t s, int* launches);
+cudaError_t launch_ce_backward(const CeParams& P, int nsm, cudaStream_t s, int* launches);
 
 // The SpecKV gamma selector (gamma.cu): model of SPEC_GAMMA_MODEL_FLOATS values.
 constexpr int kGammaModelFloats = SPEC_GAMMA_MODEL_FLOATS;

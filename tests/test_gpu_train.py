@@ -1,0 +1,586 @@
+"""The drafter-training calls on the GPU against 64-bit plain implementations.
+
+Tolerances.  A weight 2^{(x - m) c} carries about 1e-6 for exponents that
+matter (an fma's half step at |a| <= 32, c to 2^-24, ex2.approx), and a thread
+adds at most a few hundred of them one after another: a sum of V terms is off
+by at most 2e-5 relative, its logarithm by 2e-5 absolute (TOL).  Losses are sums
+of p (ln p - ln q) with two such logarithms; gradients are held, element by
+element, to 1e-4 of the sum of their terms' magnitudes, and half a step of the
+output type.  The projection's logits are fp32 sums of H exact products:
+(8 + sqrt H) 2^-23 of the sum of magnitudes; G is rounded to bf16 once, so
+its products are off by 2^-8 of the sum of their terms' magnitudes.
+"""
+import math
+
+import pytest
+import torch
+
+import train_plain as TP
+
+pytestmark = pytest.mark.gpu
+
+TOL = 2e-5
+INF, NAN = math.inf, math.nan
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float32: 2.0 ** -24}
+
+
+@pytest.fixture(scope="module")
+def sv():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_verification_26_gb300 as m
+    m.lib()
+    return m
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rows(n, V, dtype, seed, scale=3.0):
+    g = gen(seed)
+    bias = -1.1 * torch.log1p(torch.randperm(V, generator=g).float())
+    return (torch.randn(n, V, generator=g) * scale + bias).to(dtype)
+
+
+def cuda(*ts):
+    return [None if t is None else t.cuda() for t in ts]
+
+
+def offset(t, elems):
+    """The same tensor on the GPU, `elems` elements past an aligned start."""
+    buf = torch.zeros(t.numel() + elems, dtype=t.dtype, device="cuda")
+    v = buf[elems:].view(t.shape)
+    v.copy_(t)
+    return v
+
+
+# ---------------------------------------------------------------------- records
+
+def check_record(sv, x, K, T, dev_x=None):
+    r = sv.topk_logits(x.cuda() if dev_x is None else dev_x, K, None if T is None else T.cuda())
+    T = torch.ones(x.shape[0]) if T is None else T
+    top, idx, tail = TP.record(x, K, T)
+    assert r["status"].cpu().eq(0).all()
+    assert torch.equal(r["top_index"].cpu().long(), idx.long())
+    assert torch.equal(r["top_logits"].cpu().double(), top)
+    got = r["tail_lse"].cpu().double()
+    fin = torch.isfinite(tail)
+    assert torch.equal(torch.isfinite(got), fin) and torch.equal(got[~fin], tail[~fin])
+    assert ((got - tail)[fin].abs() <= TOL + 3e-7 * tail[fin].abs()).all(), (got - tail)[fin].abs().max()
+    return r
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V,K", [(1, 2, 1), (1, 2, 2), (3, 7, 7), (5, 100, 100), (2, 256, 256), (4, 1001, 256),
+                                   (9, 4093, 33), (3, 8191, 256), (2, 65537, 1), (2, 151936, 64), (40, 20000, 5),
+                                   (160, 5000, 16), (320, 5003, 8), (700, 1000, 3)])
+def test_record(sv, n, V, K, dtype):
+    T = torch.rand(n, generator=gen(V)) * 1.5 + 0.3
+    check_record(sv, rows(n, V, dtype, n + V + K), K, T)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_record_ties_and_filtered_rows(sv, dtype):
+    V, K = 30011, 48
+    x = rows(9, V, dtype, 5)
+    x[0] = 1.5                                        # all equal
+    x[1] = torch.round(x[1].float()).to(dtype)        # few values
+    x[2, :20000] = 40.0                               # a tie past any candidate list
+    x[3] = torch.where(x[3] < x[3].float().topk(10).values[-1], torch.tensor(-INF, dtype=dtype), x[3])
+    x[4] = -INF
+    x[4, V - 1] = -2.0                                # one token
+    x[5, ::2] = 0.0
+    x[5, 1::2] = -0.0                                 # equal zeros
+    x[6] = -INF
+    x[6, 1000:1000 + K] = 3.0                         # exactly K equal logits, nothing else
+    x[7, V - 3:] = 50.0
+    x[8] = torch.arange(V, dtype=torch.float32).to(dtype) * 0.001
+    x[5] = torch.clamp(x[5].float(), max=0.0).to(dtype)
+    check_record(sv, x, K, torch.linspace(0.5, 2.0, 9))
+
+
+@pytest.mark.parametrize("shift", [1, 3, 5])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_record_of_rows_off_alignment(sv, dtype, shift):
+    x = rows(3, 10007, dtype, 8)
+    check_record(sv, x, 20, None, dev_x=offset(x, shift))
+
+
+def test_record_row_errors(sv):
+    x = rows(6, 3001, torch.float32, 2)
+    x[0, 3000] = NAN
+    x[1, 0] = INF
+    x[2] = -INF
+    T = torch.tensor([1.0, 1.0, 1.0, 0.0, NAN, 1.0])
+    r = sv.topk_logits(x.cuda(), 9, T.cuda())
+    assert r["status"].cpu().tolist() == [1, 1, 1, 64, 64, 0]
+    assert (r["top_index"][:5] == -1).all() and r["top_logits"][:5].isnan().all() and r["tail_lse"][:5].isnan().all()
+    ok = TP.record(x[5:], 9, T[5:])
+    assert torch.equal(r["top_index"][5:].cpu().long(), ok[1])
+
+
+def test_record_tail_does_not_cancel(sv):
+    """Nearly all of the mass in the record: the tail keeps its precision."""
+    x = torch.full((2, 5000), -30.0) + torch.rand(2, 5000, generator=gen(1))
+    x[:, :4] = 20.0
+    check_record(sv, x, 4, None)
+
+
+# ------------------------------------------------------------------ distillation
+
+def make_distill(n, V, K, dtype, seed, tail=True):
+    g = gen(seed)
+    T = torch.rand(n, generator=g) * 0.8 + 0.5
+    x = rows(n, V, dtype, seed + 1)
+    z = (x.float() + 1.5 * torch.randn(n, V, generator=g)).to(dtype)
+    top, idx, tl = TP.record(x, K, T)
+    label = torch.randint(0, V, (n,), generator=g)
+    if n > 1:
+        label[1] = idx[1, 0]
+        label[n - 1] = -1
+    w = torch.rand(n, generator=g) + 0.2
+    return dict(z=z, top=top.float(), idx=idx.to(torch.int32), tail=tl.float() if tail else None,
+                label=label.to(torch.int32), w=w, T=T)
+
+
+def check_distill(sv, d, kl, tv, ce, grad=True, z_dev=None, out=None, ref=None):
+    z = d["z"]
+    loss, parts, g64, size = ref or TP.distill(z, d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"], kl, tv, ce)
+    top, idx, tail, label, w, T = cuda(d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"])
+    r = sv.distill_topk(z.cuda() if z_dev is None else z_dev, top, idx, tail, label=label, row_weight=w,
+                        temperature=T, kl=kl, tv=tv, ce=ce, grad=grad, out=out)
+    assert r["status"].cpu().eq(0).all(), r["status"]
+    gl, gp = r["loss"].cpu().double(), r["parts"].cpu().double()
+    tol_parts = 3 * TOL + 2e-6 * torch.where(torch.isfinite(parts), parts.abs(), 0.0)
+    for a, b, t in ((gp, parts, tol_parts),
+                    (gl, loss, d["w"].double().abs() * (abs(kl) + abs(tv) + abs(ce)) * 3 * TOL + 4e-6 * torch.where(
+                        torch.isfinite(loss), loss.abs(), 0.0))):
+        fin = torch.isfinite(b)
+        assert torch.equal(torch.isfinite(a), fin) and torch.equal(a[~fin], b[~fin])
+        assert ((a - b).abs() <= t)[fin].all(), (a - b)[fin].abs().max()
+    if grad:
+        e = (r["grad"].cpu().double() - g64).abs()
+        lim = 1e-4 * size + HALF[z.dtype] * g64.abs() + 1e-37
+        assert (e <= lim).all(), (e - lim).max()
+    return r
+
+
+@pytest.mark.parametrize("kl,tv,ce", [(1.0, 0.0, 0.0), (0.0, 1.0, 0.0), (0.0, 0.0, 1.0), (0.7, 1.0, 0.1)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V,K,tail", [(1, 2, 1, True), (2, 9, 9, True), (5, 100, 7, False), (3, 1001, 256, True),
+                                        (4, 8191, 64, True), (3, 8191, 64, False), (2, 40001, 1, True)])
+def test_distill(sv, n, V, K, tail, dtype, kl, tv, ce):
+    check_distill(sv, make_distill(n, V, K, dtype, n + V + K, tail), kl, tv, ce)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V,K", [(1, 151936, 64), (20, 50021, 16), (48, 20011, 16), (100, 7000, 16), (400, 3001, 5)])
+def test_distill_batches(sv, n, V, K, dtype):
+    """Few rows and many: every split of a row over CTAs."""
+    d = make_distill(n, V, K, dtype, 7)
+    d["w"][::7] = 0
+    check_distill(sv, d, 0.7, 1.0, 0.1)
+
+
+def test_distill_loss_alone_is_the_same(sv):
+    d = make_distill(4, 5003, 20, torch.bfloat16, 3)
+    a = check_distill(sv, d, 1.0, 1.0, 0.5)
+    b = check_distill(sv, d, 1.0, 1.0, 0.5, grad=False)
+    assert torch.equal(a["loss"], b["loss"]) and torch.equal(a["parts"], b["parts"]) and "grad" not in b
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_distill_in_place_and_off_alignment(sv, dtype):
+    d = make_distill(3, 10007, 20, dtype, 4)
+    a = check_distill(sv, d, 1.0, 1.0, 0.5)
+    z = d["z"].cuda()
+    b = check_distill(sv, d, 1.0, 1.0, 0.5, z_dev=z, out={"grad": z})
+    assert b["grad"].data_ptr() == z.data_ptr() and torch.equal(a["grad"], b["grad"])
+    for zs, gs in ((1, 1), (3, 0), (0, 5)):
+        c = check_distill(sv, d, 1.0, 1.0, 0.5, z_dev=offset(d["z"], zs), out={"grad": offset(d["z"], gs)})
+        # another split into vectors and single elements: other orders of the sums
+        assert torch.allclose(a["loss"], c["loss"], rtol=1e-5, atol=1e-5)
+
+
+def test_distill_masked_rows_and_entries(sv):
+    """Weight 0: NaN rows, bad tokens and bad temperatures do not matter.  Index
+    -1: the entry's logit does not matter.  -inf logits of the student."""
+    d = make_distill(6, 3001, 12, torch.float32, 9)
+    d["w"][2] = 0
+    d["z"][2] = NAN
+    d["idx"][2] = 99999
+    d["T"][2] = 1.0
+    d["idx"][3, 5:] = -1
+    d["top"][3, 5:] = NAN
+    d["z"][4, ::3] = -INF
+    keep = d["idx"][4].long()
+    d["z"][4, keep] = 1.0
+    d["label"][4] = 1
+    d["z"][4, 1] = 0.5
+    zero = d["idx"][2].clone()
+    ref = dict(d)
+    ref["idx"] = d["idx"].clone()
+    ref["idx"][2] = 0
+    r64 = TP.distill(ref["z"], d["top"], ref["idx"], d["tail"], d["label"], d["w"], d["T"], 1.0, 1.0, 0.5)
+    r = check_distill(sv, d, 1.0, 1.0, 0.5, ref=r64)
+    assert (r["grad"][2] == 0).all() and r["loss"][2] == 0 and zero[0] == 99999
+
+
+def test_distill_infinite_losses(sv):
+    """q = 0 under teacher mass: the loss is +inf, the gradient finite."""
+    d = make_distill(3, 501, 6, torch.float32, 10)
+    d["z"][0, int(d["idx"][0, 2])] = -INF             # KL = inf
+    d["label"][1] = int(d["idx"][1, 0])
+    d["z"][1, int(d["idx"][1, 0])] = -INF             # CE = inf and KL = inf
+    d["z"][2] = -INF
+    d["z"][2, d["idx"][2].long()] = 2.0               # q_rest = 0 < p_rest
+    d["label"][2] = -1
+    top, idx, tail, label, w, T = cuda(d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"])
+    r = sv.distill_topk(d["z"].cuda(), top, idx, tail, label=label, row_weight=w, temperature=T, kl=1.0, tv=1.0,
+                        ce=0.5, grad=True)
+    assert torch.isinf(r["loss"]).all() and r["status"].eq(0).all() and torch.isfinite(r["grad"]).all()
+    # the terms that are infinite are left out at coefficient 0
+    r = sv.distill_topk(d["z"].cuda(), top, idx, tail, label=label, row_weight=w, temperature=T, kl=0.0, tv=1.0,
+                        ce=0.0)
+    assert torch.isfinite(r["loss"]).all()
+
+
+def test_distill_row_errors(sv):
+    d = make_distill(9, 701, 5, torch.float32, 11)
+    d["z"][0, 700] = NAN
+    d["z"][1] = -INF
+    d["label"][2] = 701
+    d["idx"][3, 4] = 701
+    d["idx"][4, 1] = d["idx"][4, 0]                   # recorded twice
+    d["T"][5] = -1
+    d["idx"][6] = -1
+    d["tail"][6] = -INF                               # no mass
+    d["tail"][7] = NAN
+    top, idx, tail, label, w, T = cuda(d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"])
+    r = sv.distill_topk(d["z"].cuda(), top, idx, tail, label=label, row_weight=w, temperature=T, ce=1.0, tv=1.0,
+                        grad=True)
+    assert r["status"].cpu().tolist() == [1, 1, 2, 2, 2, 64, 1, 1, 0]
+    assert r["loss"][:8].isnan().all() and r["parts"][:8].isnan().all() and (r["grad"][:8] == 0).all()
+    sub = {k: (v[8:] if v is not None else None) for k, v in d.items()}
+    a = check_distill(sv, sub, 1.0, 1.0, 1.0)
+    assert torch.equal(a["loss"], r["loss"][8:]) and torch.equal(a["grad"], r["grad"][8:])
+
+
+def test_distill_gradient_against_differences(sv):
+    """The returned gradient against central differences of the returned losses:
+    fp32 losses to ~1e-6 over steps of 0.02 leave 1e-4, the third order 1e-4."""
+    d = make_distill(3, 40, 6, torch.float32, 12)
+    top, idx, tail, label, w, T = cuda(d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"])
+    f = lambda z, grad=False: sv.distill_topk(z, top, idx, tail, label=label, row_weight=w, temperature=T,   # noqa
+                                              kl=1.0, tv=0.0, ce=0.5, grad=grad)
+    z = d["z"].cuda()
+    g = f(z, True)["grad"]
+    for v in range(40):
+        e = torch.zeros_like(z)
+        e[:, v] = 0.02
+        diff = (f(z + e)["loss"] - f(z - e)["loss"]) / 0.04
+        assert torch.allclose(diff, g[:, v], atol=5e-4), (v, diff, g[:, v])
+
+
+# ----------------------------------------------------------- linear cross entropy
+
+def make_ce(n, H, V, seed):
+    g = gen(seed)
+    w = (torch.randn(V, H, generator=g) * (2.0 / math.sqrt(H))).to(torch.bfloat16)
+    label = torch.randint(0, V, (n,), generator=g)
+    h = torch.randn(n, H, generator=g) + torch.rand(n, 1, generator=g) * 4 * w[label].float()
+    return h.to(torch.bfloat16), w, label.to(torch.int32)
+
+
+def ce_tol(h, w):
+    H = h.shape[1]
+    h = torch.nan_to_num(h.double())
+    size = (h.abs() @ w.double().abs().t()).max(1).values
+    return (8 + math.sqrt(H)) * 2.0 ** -23 * size + 2 * TOL
+
+
+def check_ce_forward(sv, h, w, label, **kw):
+    r = sv.linear_ce_forward(*cuda(h, w, label), **kw)
+    safe = h.clone()
+    safe[label < 0] = 0
+    loss, lse = TP.ce_forward(safe, w, label)
+    tol = ce_tol(safe, w)
+    assert r["status"].cpu().eq(0).all()
+    for k, b in (("loss", loss), ("lse", lse)):
+        e = (r[k].cpu().double() - b).abs()
+        assert (e <= 2 * tol + 2e-7 * b.abs()).all(), (k, (e - tol).max())
+    return r
+
+
+def check_ce_grads(r, want):
+    for k, b, lim in (("grad_hidden", want[0], want[2]), ("grad_weight", want[1], want[3])):
+        if k in r:
+            e = (r[k].cpu().double() - b).abs()
+            assert (e <= lim).all(), (k, (e / lim).max())
+
+
+def check_ce_backward(sv, h, w, label, g, **kw):
+    hd, wd, ld = cuda(h, w, label)
+    f = sv.linear_ce_forward(hd, wd, ld)
+    r = sv.linear_ce_backward(hd, wd, ld, f["lse"], None if g is None else g.cuda(), **kw)
+    gr = torch.ones(h.shape[0]) if g is None else g
+    safe = h.clone()
+    safe[(label < 0) | (gr == 0)] = 0
+    delta = 4 * float(ce_tol(safe, w).max())             # the logits' and lse's
+    check_ce_grads(r, TP.ce_backward(safe, w, label, gr, delta))
+    return r
+
+
+CE_SIZES = [(1, 8, 2), (2, 8, 300), (1, 64, 1000), (7, 72, 257), (64, 128, 513), (130, 200, 1023), (257, 64, 2000),
+            (300, 264, 5000), (513, 512, 3001), (40, 1024, 777)]
+
+
+@pytest.mark.parametrize("n,H,V", CE_SIZES)
+def test_ce_forward(sv, n, H, V):
+    check_ce_forward(sv, *make_ce(n, H, V, n + H + V))
+
+
+@pytest.mark.parametrize("n,H,V", CE_SIZES)
+def test_ce_backward(sv, n, H, V):
+    h, w, label = make_ce(n, H, V, n + H + V)
+    check_ce_backward(sv, h, w, label, torch.rand(n, generator=gen(1)) / n)
+
+
+def test_ce_large_vocabulary_in_several_pieces(sv):
+    """A small batch whose G does not fit one piece (checked on a few rows)."""
+    n, H, V = 1024, 64, 151936
+    assert sv.linear_ce_workspace_bytes(n, H, V, True) < 2 * n * V + (64 << 20)
+    h, w, label = make_ce(n, H, V, 4)
+    g = torch.rand(n, generator=gen(2)) / n
+    hd, wd, ld, gd = cuda(h, w, label, g)
+    f = sv.linear_ce_forward(hd, wd, ld)
+    r = sv.linear_ce_backward(hd, wd, ld, f["lse"], gd)
+    W = wd.double()
+    l = hd.double() @ W.t()
+    lse = torch.logsumexp(l, 1)
+    assert ((f["lse"].double() - lse).abs() <= 1e-4).all()
+    p = torch.exp(l - lse[:, None]) * gd.double()[:, None]
+    G = p.clone()
+    G[torch.arange(n, device="cuda"), ld.long()] -= gd.double()
+    off = 2.0 ** -8 * G.abs() + 2e-4 * p                 # see train_plain.ce_backward
+    for got, want, lim in ((r["grad_hidden"], G @ W, off @ W.abs()),
+                           (r["grad_weight"], G.t() @ hd.double(), off.t() @ hd.double().abs())):
+        e = (got.double() - want).abs()
+        assert (e <= lim + 2.0 ** -8 * want.abs() + 1e-37).all(), (e / lim).max()
+
+
+@pytest.mark.parametrize("n,H,V", [(300, 64, 700), (5, 16, 40)])
+def test_ce_masked_rows(sv, n, H, V):
+    """Rows without a label and of weight 0 hold NaN and infinities."""
+    h, w, label = make_ce(n, H, V, 6)
+    g = torch.rand(n, generator=gen(3)) + 0.1
+    label[::3] = -1
+    h[::3] = NAN
+    check_ce_forward(sv, h, w, label)
+    g[1::3] = 0
+    h2 = h.clone()
+    h2[1::3] = INF
+    f = sv.linear_ce_forward(*cuda(h2, w, label))
+    assert f["status"][1].item() == 1 and f["lse"][1].isnan() and f["loss"][0] == 0
+    lse = sv.linear_ce_forward(*cuda(torch.nan_to_num(h, nan=0.0), w, label))["lse"]
+    r = sv.linear_ce_backward(*cuda(h2, w, label), lse, g.cuda())
+    safe = h2.clone()
+    safe[::3] = 0
+    safe[1::3] = 0
+    check_ce_grads(r, TP.ce_backward(safe, w, label, g, 4 * float(ce_tol(safe, w).max())))
+    assert (r["grad_hidden"][::3] == 0).all() and (r["grad_hidden"][1::3] == 0).all()
+
+
+def test_ce_no_row_takes_part(sv):
+    h, w, label = make_ce(3, 32, 100, 1)
+    label[:] = -1
+    f = sv.linear_ce_forward(*cuda(h, w, label))
+    assert (f["loss"] == 0).all() and (f["lse"] == 0).all() and (f["status"] == 0).all()
+    out = {"grad_hidden": torch.full((3, 32), 7.0, dtype=torch.bfloat16, device="cuda"),
+           "grad_weight": torch.full((100, 32), 7.0, dtype=torch.bfloat16, device="cuda")}
+    sv.linear_ce_backward(*cuda(h, w, label), f["lse"], out=out)
+    assert (out["grad_hidden"] == 0).all() and (out["grad_weight"] == 0).all()
+
+
+def test_ce_row_errors(sv):
+    h, w, label = make_ce(6, 32, 100, 2)
+    label[1], label[2] = 100, -2
+    h[3, 5] = NAN
+    f = sv.linear_ce_forward(*cuda(h, w, label))
+    assert f["status"].cpu().tolist() == [0, 2, 2, 1, 0, 0]
+    assert f["loss"][1:4].isnan().all() and f["lse"][1:4].isnan().all()
+    r = sv.linear_ce_backward(*cuda(h, w, label), f["lse"])
+    keep = torch.tensor([0, 4, 5])
+    want = TP.ce_backward(h[keep], w, label[keep], torch.ones(3), 4 * float(ce_tol(h[keep], w).max()))
+    check_ce_grads({"grad_weight": r["grad_weight"], "grad_hidden": r["grad_hidden"][keep.cuda()]}, want)
+    assert (r["grad_hidden"][1:4] == 0).all()
+
+
+def test_ce_one_gradient_alone(sv):
+    h, w, label = make_ce(70, 72, 900, 3)
+    g = torch.rand(70, generator=gen(5))
+    both = check_ce_backward(sv, h, w, label, g)
+    a = check_ce_backward(sv, h, w, label, g, need_weight=False)
+    b = check_ce_backward(sv, h, w, label, g, need_hidden=False)
+    assert list(a) == ["grad_hidden"] and list(b) == ["grad_weight"]
+    assert torch.equal(a["grad_hidden"], both["grad_hidden"]) and torch.equal(b["grad_weight"], both["grad_weight"])
+    check_ce_backward(sv, h, w, label, None)
+
+
+def test_ce_shared_labels(sv):
+    """Every row has the same label: its weight row gathers all of them."""
+    h, w, label = make_ce(200, 64, 300, 8)
+    label[:] = 17
+    check_ce_forward(sv, h, w, label)
+    check_ce_backward(sv, h, w, label, torch.rand(200, generator=gen(6)))
+
+
+def test_ce_stale_workspace(sv):
+    """Nothing of the workspace's old contents reaches the results."""
+    h, w, label = make_ce(300, 72, 3001, 12)
+    label[::5] = -1
+    g = torch.rand(300, generator=gen(7))
+    ws = torch.full((sv.linear_ce_workspace_bytes(300, 72, 3001, True),), 0xFF, dtype=torch.uint8, device="cuda")
+    check_ce_forward(sv, h, w, label, ws=ws)
+    ws.fill_(0xFF)
+    check_ce_backward(sv, h, w, label, g, ws=ws)
+
+
+# ------------------------------------------------------------- calls around them
+
+def all_calls(sv, x, z, T, label, w, h, wt, cl, gl, ws):
+    """The four calls as a training step makes them."""
+    r = sv.topk_logits(x, 16, T)
+    d = sv.distill_topk(z, r["top_logits"], r["top_index"], r["tail_lse"], label=label, row_weight=w, temperature=T,
+                        kl=1.0, tv=1.0, ce=0.1, grad=True)
+    f = sv.linear_ce_forward(h, wt, cl, ws=ws[0])
+    b = sv.linear_ce_backward(h, wt, cl, f["lse"], gl, ws=ws[1])
+    return [r["top_logits"], r["top_index"], r["tail_lse"], d["loss"], d["parts"], d["grad"], f["loss"], f["lse"],
+            b["grad_hidden"], b["grad_weight"]]
+
+
+def step_inputs(seed, n=37, V=9001, H=136):
+    g = gen(seed)
+    x, z = rows(n, V, torch.bfloat16, seed), rows(n, V, torch.bfloat16, seed + 50)
+    label = torch.randint(0, V, (n,), generator=g).to(torch.int32)
+    label[3] = -1
+    h, wt, cl = make_ce(n, H, V, seed)
+    cl[5] = -1
+    return cuda(x, z, torch.rand(n, generator=g) + 0.4, label, torch.rand(n, generator=g), h, wt, cl,
+                torch.rand(n, generator=g))
+
+
+def step_ws(sv, n=37, V=9001, H=136):
+    return [torch.empty(sv.linear_ce_workspace_bytes(n, H, V, b), dtype=torch.uint8, device="cuda") for b in (0, 1)]
+
+
+def test_repeated_captured_and_on_two_streams(sv):
+    """The same bits from a second call, from a replayed graph on new inputs, and
+    from two streams at once with a workspace each."""
+    A, B = step_inputs(1), step_inputs(2)
+    want_a = [t.clone() for t in all_calls(sv, *A, step_ws(sv))]
+    want_b = [t.clone() for t in all_calls(sv, *B, step_ws(sv))]
+    for p, q in zip(want_a, all_calls(sv, *A, step_ws(sv))):
+        assert torch.equal(p, q)
+    torch.cuda.synchronize()
+    # two streams, interleaved
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    ws1, ws2 = step_ws(sv), step_ws(sv)
+    s1.wait_stream(torch.cuda.current_stream())
+    s2.wait_stream(torch.cuda.current_stream())
+    got = []
+    for _ in range(4):
+        with torch.cuda.stream(s1):
+            got.append((want_a, all_calls(sv, *A, ws1)))
+        with torch.cuda.stream(s2):
+            got.append((want_b, all_calls(sv, *B, ws2)))
+    torch.cuda.synchronize()
+    for want, g in got:
+        for p, q in zip(want, g):
+            assert torch.equal(p, q)
+    # a graph, replayed on other inputs
+    ins = [t.clone() for t in A]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = all_calls(sv, *ins, ws1)
+    for src, want in ((A, want_a), (B, want_b), (A, want_a)):
+        for d, t in zip(ins, src):
+            d.copy_(t)
+        graph.replay()
+        torch.cuda.synchronize()
+        for p, q in zip(want, outs):
+            assert torch.equal(p, q)
+
+
+def test_captured_call_has_its_own_workspace(sv):
+    h, w, label = cuda(*make_ce(50, 64, 700, 5))
+    eager = sv.linear_ce_forward(h, w, label)["loss"].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = sv.linear_ce_forward(h, w, label)
+    other = sv.linear_ce_forward(h * 2, w, label)["loss"].clone()   # the eager workspace in between
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out["loss"], eager) and not torch.equal(other, eager)
+
+
+def test_rows_behind_the_last_stay(sv):
+    """Outputs are views into larger buffers: what lies behind them stays."""
+    d = make_distill(3, 1003, 6, torch.bfloat16, 21)
+    buf = torch.full((5, 1003), 3.0, dtype=torch.bfloat16, device="cuda")
+    check_distill(sv, d, 1.0, 1.0, 0.1, out={"grad": buf[1:4]})
+    assert (buf[0] == 3).all() and (buf[4] == 3).all()
+    h, w, label = make_ce(3, 64, 303, 3)
+    gh = torch.full((5, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    gw = torch.full((305, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    check_ce_backward(sv, h, w, label, torch.ones(3), out={"grad_hidden": gh[1:4], "grad_weight": gw[1:304]})
+    assert (gh[0] == 3).all() and (gh[4] == 3).all() and (gw[0] == 3).all() and (gw[304] == 3).all()
+
+
+def test_verified_chains_are_distilled(sv):
+    """As used together: chains are verified, their target rows filtered and
+    recorded, and the draft rows trained on the records; the loss's parts agree
+    with the divergence statistics of the same rows, and CE on the committed
+    tokens through the projection agrees with CE on its logits."""
+    import numpy as np
+
+    import parity as PT
+    from speculative_decoding_verification_26_gb300 import workloads as W
+    import oracle as O
+    wl = PT.make_workload(O.load(), "c3", 0)
+    wl_t, wl_d = PT.logits_dev(wl, "target", "cuda"), PT.logits_dev(wl, "draft", "cuda")
+    B, G, V = wl_d.shape
+    toks, gam, T, u = (torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in
+                       (wl.draft_tokens, wl.gamma, wl.temperature, wl.uniforms))
+    ver = sv.verify_sample(wl_t, wl_d, toks, gam, T, u)
+    rows_t = wl_t[:, :G].reshape(B * G, V).contiguous()
+    T_rows = T.repeat_interleave(G)
+    rec = sv.topk_logits(rows_t, 256, T_rows)
+    committed = ver["tokens"][:, :G].reshape(-1).contiguous()       # -1 past the drawn token
+    d = sv.distill_topk(wl_d, rec["top_logits"], rec["top_index"], rec["tail_lse"], label=committed,
+                        temperature=T_rows, kl=1.0, tv=1.0, ce=0.1, grad=True)
+    assert (d["status"] == 0).all()
+    st = sv.divergence_stats(wl_t, wl_d, gam, T)["stats"].view(-1, 5)
+    # a bucket for the rest can only lower KL and TV (data processing)
+    assert (d["parts"][:, 0] <= st[:, 2] * math.log(2) + 1e-4).all()
+    assert (d["parts"][:, 1] <= st[:, 1] / 2 + 1e-4).all() and (d["parts"][:, 1] > 0).all()
+    # with the whole row filtered to the record, the record is the row: KL, TV and 1 - A agree
+    sv.filter_top_k_top_p(rows_t, torch.full((B * G,), 50, dtype=torch.int32, device="cuda"))
+    rec = sv.topk_logits(rows_t, 256, T_rows)
+    assert torch.isinf(rec["tail_lse"]).any()
+    tf = torch.cat([rows_t.view(B, G, V), wl_t[:, G:]], 1).contiguous()
+    d = sv.distill_topk(wl_d, rec["top_logits"], rec["top_index"], rec["tail_lse"], temperature=T_rows, tv=1.0)
+    st = sv.divergence_stats(tf, wl_d, gam, T)["stats"].view(-1, 5)
+    whole = torch.isinf(rec["tail_lse"])
+    assert torch.allclose(d["parts"][whole, 0], st[whole, 2] * math.log(2), rtol=2e-5, atol=2e-5)
+    assert torch.allclose(d["parts"][whole, 1], 1 - st[whole, 0], rtol=2e-5, atol=2e-5)
+    assert torch.allclose(d["parts"][whole, 1], st[whole, 1] / 2, rtol=2e-5, atol=2e-5)
+    # the projection: its losses are those of its logits, row by row
+    h, w, _ = cuda(*make_ce(B * G, 64, V, 3))
+    f = sv.linear_ce_forward(h, w, committed)
+    logits = (h.double() @ w.double().t()).float()
+    idx0 = torch.full((B * G, 1), -1, dtype=torch.int32, device="cuda")
+    c = sv.distill_topk(logits, torch.zeros(B * G, 1, device="cuda"), idx0, torch.zeros(B * G, device="cuda"),
+                        label=committed, kl=0.0, ce=1.0)
+    assert torch.allclose(f["loss"], c["loss"], atol=1e-4)
