@@ -355,7 +355,8 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
  *     aligned, no initial contents.  Calls that share one must not overlap on
  *     the device; that holds for captured graphs too.
  * Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^20], H outside [8, 65536]
- * or not a multiple of 8, V outside [2, 2^28), dtype, NULL required pointers,
+ * or not a multiple of 8, V outside [2, 2^28), ceil(n / 256) ceil(V / 256) of
+ * 2^30 or more, dtype, NULL required pointers,
  * misalignment), SPEC_ERR_WORKSPACE, SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
 size_t spec_linear_ce_workspace_bytes(int n, int H, int V, int backward);
 int spec_linear_ce_forward(const void* hidden, const void* weight, int dtype, int n, int H, int V,

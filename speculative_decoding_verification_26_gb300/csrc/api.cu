@@ -56,6 +56,7 @@ int device_state(int* ctas) {
     } else {
       cudaError_t e = configure_kernels();
       if (e == cudaSuccess) e = configure_distill();
+      if (e == cudaSuccess) e = configure_linear_ce();
       int per_sm = 0;
       if (e == cudaSuccess) e = verify_blocks_per_sm(&per_sm);
       if (e != cudaSuccess) return SPEC_ERR_CUDA;
@@ -81,7 +82,9 @@ int current_sms() {
 }
 
 bool ce_sizes_ok(int n, int H, int V) {
-  return n >= 1 && n <= (1 << 20) && H >= 8 && H <= 65536 && H % 8 == 0 && V >= 2 && V < (1 << 28);
+  // tiles of 256 x 256 logits are counted in 32 bits
+  return n >= 1 && n <= (1 << 20) && H >= 8 && H <= 65536 && H % 8 == 0 && V >= 2 && V < (1 << 28) &&
+         ((n + 255ll) / 256) * ((V + 255ll) / 256) < (1ll << 30);
 }
 
 bool sizes_ok(int B, int G, int V) {

@@ -552,9 +552,7 @@ struct DistillParams {
 cudaError_t launch_distill(const DistillParams& P, int nsm, cudaStream_t s);
 cudaError_t configure_distill();   // dynamic shared-memory limit, current device
 
-// Parameters of the linear cross entropy (linear_ce.cu).  Row tiles are
-// kCeRowTile high, vocabulary tiles kCeVocabTile wide.
-constexpr int kCeRowTile = 256, kCeVocabTile = 256;
+// Parameters of the linear cross entropy (linear_ce.cu).
 struct CeParams {
   const __nv_bfloat16* hidden;   // [n, H]
   const __nv_bfloat16* weight;   // [V, H]
@@ -570,7 +568,8 @@ struct CeParams {
   // workspace views; compact rows are the rows that take part, in order
   int n_pad;                     // n in whole row tiles
   int piece;                     // vocabulary rows of a piece of the backward pass
-  int* count;                    // compact rows
+  int splits, split_steps;       // of grad_hidden's sum over a piece: parts, and stages of k in each
+  int* count;                    // compact rows; [1]: a wait ran out
   int* row_of;                   // [n_pad] the row of a compact row
   int* lab;                      // [n_pad] its label, -1 past the last
   int* pos_of;                   // [n] the compact row of a row, -1: none
@@ -579,9 +578,10 @@ struct CeParams {
   float2* part;                  // [vocabulary tiles, n_pad] maximum and sum
   float *lse_c, *g_c;            // [n_pad]
   __nv_bfloat16* soft;           // [n_pad, piece] the gradient by the logits
-  float* acc;                    // [n_pad, H] sums of grad_hidden
+  float* acc;                    // [splits, n_pad, H] sums of grad_hidden
 };
 size_t ce_layout(CeParams& P, bool backward, void* base);   // fills the views, returns the bytes
+cudaError_t configure_linear_ce();   // shared-memory limits, the tensor-map encoder
 cudaError_t launch_ce_forward(const CeParams& P, int nsm, cudaStream_t s, int* launches);
 cudaError_t launch_ce_backward(const CeParams& P, int nsm, cudaStream_t s, int* launches);
 

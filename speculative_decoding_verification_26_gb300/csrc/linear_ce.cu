@@ -16,8 +16,10 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <cstring>
 
 #include "rows.cuh"
+#include "tc_gemm.cuh"
 
 namespace sv {
 namespace {
@@ -77,7 +79,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
       P.lse[r] = z;
       if (P.status) P.status[r] = y == -1 ? SPEC_ST_OK : SPEC_ST_BAD_TOKEN;
     }
-    if (blockIdx.x == 0 && lane == 0) *P.count = all;
+    if (blockIdx.x == 0 && lane == 0) { P.count[0] = all; P.count[1] = 0; }
   }
   __syncthreads();
   const int nv = P.H / 8;
@@ -99,183 +101,333 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
   }
 }
 
-// 64 x 64 tile of sum_k A(i, k) B(j, k), 256 threads, 4 x 4 sums each.
-struct Operand {
-  const __nv_bfloat16* p;
-  long long outer, inner;                    // strides of i (or j) and of k
-  int limit;                                 // i (or j) below it
+// ---------------------------------------------------------------------------
+// The three products, as work of tc_run (see tc_gemm.cuh).
+
+struct CeMaps {
+  // k inner: boxes of 64 k x 128 rows; k outer: 64 columns x 64 k
+  CUtensorMap rows, weight, soft, rows_t, weight_t, soft_t;
 };
-constexpr int kTile = 64, kStep = 16, kCeThreads = 256;
 
-__device__ __forceinline__ void tile_product(const Operand& A, const Operand& B, int i0, int j0, int K,
-                                             float (&acc)[4][4]) {
-  __shared__ float sa[kStep][kTile + 1], sb[kStep][kTile + 1];
-  const int tid = threadIdx.x, ti = tid >> 4, tj = tid & 15;
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) acc[a][b] = 0.f;
-  for (int k0 = 0; k0 < K; k0 += kStep) {
-    for (int t = tid; t < kTile * kStep; t += kCeThreads) {
-      // neighbours along the operand's unit stride
-      const int ia = A.inner == 1 ? t / kStep : t % kTile, ka = A.inner == 1 ? t % kStep : t / kTile;
-      const int jb = B.inner == 1 ? t / kStep : t % kTile, kb = B.inner == 1 ? t % kStep : t / kTile;
-      sa[ka][ia] = i0 + ia < A.limit && k0 + ka < K
-                       ? __bfloat162float(A.p[(i0 + ia) * A.outer + (k0 + ka) * A.inner]) : 0.f;
-      sb[kb][jb] = j0 + jb < B.limit && k0 + kb < K
-                       ? __bfloat162float(B.p[(j0 + jb) * B.outer + (k0 + kb) * B.inner]) : 0.f;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kStep; ++k) {
-      float x[4], y[4];
-#pragma unroll
-      for (int a = 0; a < 4; ++a) { x[a] = sa[k][ti * 4 + a]; y[a] = sb[k][tj * 4 + a]; }
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int b = 0; b < 4; ++b) acc[a][b] = fmaf(x[a], y[b], acc[a][b]);
-    }
-    __syncthreads();
+// Tiles of logits: rows x vocabulary.  Groups of kGroup row tiles (4096 rows),
+// within a group the vocabulary outer and the rows inner: the pairs at work read
+// few vocabulary tiles and one group's rows, both from L2, and the weights come
+// from HBM once a group.
+constexpr int kGroup = 16;
+struct LogitTiles {
+  int row_tiles, vocab_tiles;
+  __device__ __forceinline__ void at(int t, int& mb, int& vt) const {
+    const int per = kGroup * vocab_tiles, g = t / per, first = g * kGroup;
+    const int size = row_tiles - first < kGroup ? row_tiles - first : kGroup;
+    const int u = t - g * per;
+    vt = u / size;
+    mb = first + u - vt * size;
   }
-}
+};
 
-// one vocabulary tile's maximum and sum of each row, and the label's logit
-__global__ void __launch_bounds__(kCeThreads) ce_forward(const __grid_constant__ CeParams P) {
-  const int i0 = blockIdx.y * kTile, v0 = blockIdx.x * kTile, count = *P.count;
-  if (i0 >= count) return;
-  float acc[4][4];
-  tile_product({P.rows, P.H, 1, P.n_pad}, {P.weight, P.H, 1, P.V}, i0, v0, P.H, acc);
-  const int ti = threadIdx.x >> 4, tj = threadIdx.x & 15;
+constexpr float kLn2 = 0.693147180559945f;
+
+// forward: a tile's maximum and sum of each row, and the label's logit
+struct ForwardWork {
+  const CeParams& P;
+  const CeMaps& M;
+  LogitTiles lt;
+  __device__ __forceinline__ int count() const { return lt.row_tiles * lt.vocab_tiles; }
+  __device__ __forceinline__ TcTile tile(int t) const {
+    int mb, vt;
+    lt.at(t, mb, vt);
+    return {{&M.rows, true, mb * kTcTile, 0}, {&M.weight, true, vt * kTcTile, 0}, (P.H + kTcK - 1) / kTcK};
+  }
+  __device__ __forceinline__ void epilogue(int t, int row, uint32_t tmem, bool) const {
+    int mb, vt;
+    lt.at(t, mb, vt);
+    const int i = mb * kTcTile + row, v0 = vt * kTcTile, at = P.lab[i] - v0;   // the label's column
+    float m = -INFINITY, s = 0.f;
+    for (int c0 = 0; c0 < kTcTile; c0 += 32) {
+      float x[32];
+      tc_load32(x, tmem + c0);
+      if (at >= c0 && at < c0 + 32) {
+        float z = 0.f;
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const int i = i0 + ti * 4 + a, y = P.lab[i];
-    float m = -INFINITY;
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int v = v0 + tj * 4 + b;
-      if (v < P.V) {
-        m = acc[a][b] != acc[a][b] ? INFINITY : fmaxf(m, acc[a][b]);   // a NaN makes the row's sum NaN below
-        if (v == y) P.label_logit[i] = acc[a][b];
+        for (int c = 0; c < 32; ++c) z = c0 + c == at ? x[c] : z;
+        P.label_logit[i] = z;
       }
+      const int left = P.V - v0 - c0;
+      if (left < 32) {
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+          if (c >= left) x[c] = -INFINITY;
+      }
+      float top = x[0];
+#pragma unroll
+      for (int c = 1; c < 32; ++c) top = fmaxf(top, x[c]);
+      top = fmaxf(m, top);
+      if (top > m) {
+        s *= ex2((m - top) * kLog2eHi);
+        m = top;
+      }
+      const float ref = -m * kLog2eHi;
+      float a = 0.f, b = 0.f;
+#pragma unroll
+      for (int c = 0; c < 32; c += 2) {
+        a += ex2(fmaf(x[c], kLog2eHi, ref));
+        b += ex2(fmaf(x[c + 1], kLog2eHi, ref));
+      }
+      s += a + b;
     }
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    float s = 0.f;
-#pragma unroll
-    for (int b = 0; b < 4; ++b)
-      if (v0 + tj * 4 + b < P.V) s += ex2((acc[a][b] - m) * kLog2eHi);
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    if (tj == 0) P.part[(size_t)blockIdx.x * P.n_pad + i] = make_float2(m, s);
+    P.part[(size_t)vt * P.n_pad + i] = make_float2(m, s);
   }
+};
+
+__device__ __forceinline__ uint4 pack8(const float* v) {
+  uint32_t u[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+    memcpy(&u[k], &b, 4);
+  }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
-__global__ void __launch_bounds__(256) merge_rows(const __grid_constant__ CeParams P) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= *P.count) return;
-  const int tiles = (P.V + kTile - 1) / kTile;
+// backward: G of a piece as bf16, its one rounding before the two products that
+// read it; the logits and the softmax are fp32
+struct SoftWork {
+  const CeParams& P;
+  const CeMaps& M;
+  LogitTiles lt;
+  int v_begin;
+  __device__ __forceinline__ int count() const { return lt.row_tiles * lt.vocab_tiles; }
+  __device__ __forceinline__ TcTile tile(int t) const {
+    int mb, vt;
+    lt.at(t, mb, vt);
+    return {{&M.rows, true, mb * kTcTile, 0}, {&M.weight, true, v_begin + vt * kTcTile, 0}, (P.H + kTcK - 1) / kTcK};
+  }
+  __device__ __forceinline__ void epilogue(int t, int row, uint32_t tmem, bool) const {
+    int mb, vt;
+    lt.at(t, mb, vt);
+    const int i = mb * kTcTile + row, v0 = v_begin + vt * kTcTile, at = P.lab[i] - v0;
+    const float g = P.g_c[i], ref = -P.lse_c[i] * kLog2eHi;
+    __nv_bfloat16* out = P.soft + (size_t)i * P.piece + vt * kTcTile;
+    for (int c0 = 0; c0 < kTcTile; c0 += 32) {
+      float x[32];
+      tc_load32(x, tmem + c0);
+      const int left = P.V - v0 - c0;
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        x[c] = ex2(fmaf(x[c], kLog2eHi, ref)) - (c0 + c == at ? 1.f : 0.f);
+        x[c] = c < left && g != 0.f ? x[c] * g : 0.f;   // also past the last row that counts
+      }
+#pragma unroll
+      for (int c = 0; c < 32; c += 8) *reinterpret_cast<uint4*>(out + c0 + c) = pack8(x + c);
+    }
+  }
+};
+
+// backward: a piece's part of dh (k: the piece's vocabulary, in `splits` parts
+// of `per` stages) and its rows of dW (k: the rows that count)
+struct GradWork {
+  const CeParams& P;
+  const CeMaps& M;
+  int v_begin, len, row_tiles, col_tiles, steps_x, steps_w, hidden_tiles, weight_tiles;
+  __device__ __forceinline__ int count() const { return hidden_tiles + weight_tiles; }
+  __device__ __forceinline__ void hidden_at(int t, int& mb, int& nb, int& sp) const {
+    nb = t % col_tiles;
+    mb = t / col_tiles % row_tiles;
+    sp = t / (col_tiles * row_tiles);
+  }
+  __device__ __forceinline__ TcTile tile(int t) const {
+    if (t < hidden_tiles) {
+      int mb, nb, sp;
+      hidden_at(t, mb, nb, sp);
+      const int first = sp * P.split_steps, left = steps_x - first;
+      return {{&M.soft, true, mb * kTcTile, first * kTcK},
+              {&M.weight_t, false, nb * kTcTile, v_begin + first * kTcK},
+              left < 0 ? 0 : left < P.split_steps ? left : P.split_steps};
+    }
+    t -= hidden_tiles;
+    const int vb = t / col_tiles, nb = t % col_tiles;
+    return {{&M.soft_t, false, vb * kTcTile, 0}, {&M.rows_t, false, nb * kTcTile, 0}, steps_w};
+  }
+  __device__ __forceinline__ void epilogue(int t, int row, uint32_t tmem, bool any) const {
+    if (t < hidden_tiles) {
+      int mb, nb, sp;
+      hidden_at(t, mb, nb, sp);
+      const int i = mb * kTcTile + row;
+      float* out = P.acc + ((size_t)sp * P.n_pad + i) * P.H + nb * kTcTile;
+      for (int c0 = 0; c0 < kTcTile && nb * kTcTile + c0 < P.H; c0 += 32) {
+        float x[32];
+        if (any) {
+          tc_load32(x, tmem + c0);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) x[c] = 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 32; c += 4) {
+          if (nb * kTcTile + c0 + c >= P.H) break;         // H is a multiple of 8
+          float4* at = reinterpret_cast<float4*>(out + c0 + c);
+          float4 v = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+          if (v_begin != 0) {
+            const float4 o = *at;
+            v.x += o.x; v.y += o.y; v.z += o.z; v.w += o.w;
+          }
+          *at = v;
+        }
+      }
+      return;
+    }
+    t -= hidden_tiles;
+    const int vb = t / col_tiles, nb = t % col_tiles, v = v_begin + vb * kTcTile + row;
+    __nv_bfloat16* out = P.grad_weight + (size_t)v * P.H + nb * kTcTile;
+    for (int c0 = 0; c0 < kTcTile && nb * kTcTile + c0 < P.H; c0 += 32) {
+      float x[32];
+      if (any) {
+        tc_load32(x, tmem + c0);
+      } else {
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c] = 0.f;
+      }
+      if (v >= P.V) continue;
+#pragma unroll
+      for (int c = 0; c < 32; c += 8)
+        if (nb * kTcTile + c0 + c < P.H) *reinterpret_cast<uint4*>(out + c0 + c) = pack8(x + c);
+    }
+  }
+};
+
+__global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
+    ce_forward(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M) {
+  const LogitTiles lt{(*P.count + kTcTile - 1) / kTcTile, (P.V + kTcTile - 1) / kTcTile};
+  tc_run(ForwardWork{P, M, lt}, P.count + 1);
+}
+
+__device__ __forceinline__ int piece_len(const CeParams& P, int v_begin) {
+  return P.V - v_begin < P.piece ? P.V - v_begin : P.piece;
+}
+__global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
+    ce_softmax(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
+  const LogitTiles lt{(*P.count + kTcTile - 1) / kTcTile, (piece_len(P, v_begin) + kTcTile - 1) / kTcTile};
+  tc_run(SoftWork{P, M, lt, v_begin}, P.count + 1);
+}
+__global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
+    ce_grads(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
+  const int len = piece_len(P, v_begin), count = *P.count;
+  const int rt = (count + kTcTile - 1) / kTcTile, ct = (P.H + kTcTile - 1) / kTcTile;
+  const int ht = P.grad_hidden ? rt * ct * P.splits : 0;
+  const int wt = P.grad_weight ? (len + kTcTile - 1) / kTcTile * ct : 0;
+  tc_run(GradWork{P, M, v_begin, len, rt, ct, (len + kTcK - 1) / kTcK, (count + kTcK - 1) / kTcK, ht, wt},
+         P.count + 1);
+}
+
+// lse and loss of the rows that count: the tiles' maxima and sums, each warp a
+// share of the tiles of 32 rows
+constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
+__global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constant__ CeParams P) {
+  __shared__ float2 s_part[kMergeWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  if (blockIdx.x * 32 >= *P.count) return;
+  const int tiles = (P.V + kTcTile - 1) / kTcTile;
   float m = -INFINITY, s = 0.f;
-  for (int t = 0; t < tiles; ++t) m = fmaxf(m, P.part[(size_t)t * P.n_pad + i].x);
-  for (int t = 0; t < tiles; ++t) {
-    const float2 p = P.part[(size_t)t * P.n_pad + i];
-    s += p.y * ex2((p.x - m) * kLog2eHi);
-  }
-  const float lse = m + 0.693147180559945f * log2f(s);
-  const bool ok = isfinite(m) && isfinite(lse);
-  const int r = P.row_of[i];
-  P.lse[r] = ok ? lse : __int_as_float(0x7fc00000);
-  P.loss[r] = ok ? lse - P.label_logit[i] : __int_as_float(0x7fc00000);
-  if (P.status) P.status[r] = ok ? SPEC_ST_OK : SPEC_ST_NONFINITE;
+  auto add = [&](float2 p) {                 // a NaN sum stays
+    const float top = fmaxf(m, p.x);
+    if (top == -INFINITY) return;
+    s = s * ex2((m - top) * kLog2eHi) + p.y * ex2((p.x - top) * kLog2eHi);
+    m = top;
+  };
+#pragma unroll 4
+  for (int t = warp; t < tiles; t += kMergeWarps) add(P.part[(size_t)t * P.n_pad + i]);
+  s_part[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp != 0 || i >= *P.count) return;
+  for (int w = 1; w < kMergeWarps; ++w) add(s_part[w][lane]);
+  const float lse = m + kLn2 * log2f(s), nan = __int_as_float(0x7fc00000);
+  const int failed = P.count[1], r = P.row_of[i];
+  const bool ok = isfinite(m) && isfinite(lse) && !failed;
+  P.lse[r] = ok ? lse : nan;
+  P.loss[r] = ok ? lse - P.label_logit[i] : nan;
+  if (P.status) P.status[r] = failed ? SPEC_ST_TIMEOUT : ok ? SPEC_ST_OK : SPEC_ST_NONFINITE;
 }
 
-// G of vocabulary rows [v_begin, v_begin + piece) as bf16: the one rounding of G
-// before the products that read it; the logits and the softmax are fp32
-__global__ void __launch_bounds__(kCeThreads) ce_softmax(const __grid_constant__ CeParams P, int v_begin) {
-  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
-  if (i0 >= P.n_pad) return;
-  float acc[4][4];
-  tile_product({P.rows, P.H, 1, P.n_pad}, {P.weight + (size_t)v_begin * P.H, P.H, 1, P.V - v_begin}, i0, j0, P.H, acc);
-  const int ti = threadIdx.x >> 4, tj = threadIdx.x & 15;
-#pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    const int i = i0 + ti * 4 + a, y = P.lab[i];
-    const float g = P.g_c[i], lse = P.lse_c[i];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int j = j0 + tj * 4 + b, v = v_begin + j;
-      const float p = v < P.V && g != 0.f ? g * (ex2((acc[a][b] - lse) * kLog2eHi) - (v == y ? 1.f : 0.f)) : 0.f;
-      P.soft[(size_t)i * P.piece + j] = __float2bfloat16_rn(p);
-    }
-  }
-}
-
-__global__ void __launch_bounds__(kCeThreads) ce_grad_weight(const __grid_constant__ CeParams P, int v_begin) {
-  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
-  const int len = P.V - v_begin < P.piece ? P.V - v_begin : P.piece;
-  if (i0 >= len) return;
-  float acc[4][4];
-  tile_product({P.soft, 1, P.piece, len}, {P.rows, 1, P.H, P.H}, i0, j0, *P.count, acc);
-  const int ti = threadIdx.x >> 4, tj = threadIdx.x & 15;
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int i = i0 + ti * 4 + a, j = j0 + tj * 4 + b;
-      if (i < len && j < P.H) P.grad_weight[(size_t)(v_begin + i) * P.H + j] = __float2bfloat16_rn(acc[a][b]);
-    }
-}
-
-__global__ void __launch_bounds__(kCeThreads) ce_grad_hidden(const __grid_constant__ CeParams P, int v_begin) {
-  const int i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
-  const int len = P.V - v_begin < P.piece ? P.V - v_begin : P.piece;
-  if (i0 >= *P.count) return;
-  float acc[4][4];
-  tile_product({P.soft, P.piece, 1, P.n_pad}, {P.weight + (size_t)v_begin * P.H, 1, P.H, P.H}, i0, j0, len, acc);
-  const int ti = threadIdx.x >> 4, tj = threadIdx.x & 15;
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const int i = i0 + ti * 4 + a, j = j0 + tj * 4 + b;
-      if (j < P.H) {
-        float* at = P.acc + (size_t)i * P.H + j;
-        *at = v_begin == 0 ? acc[a][b] : *at + acc[a][b];
+// Every row of dh: the sum of its parts, or zeros where the row took no part.
+// After a wait that ran out (no healthy call) both gradients are NaN.
+__global__ void __launch_bounds__(256) finish_grads(const __grid_constant__ CeParams P) {
+  const long long me = blockIdx.x * 256ll + threadIdx.x, all = gridDim.x * 256ll;
+  const bool failed = P.count[1] != 0;
+  const uint4 nans = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
+  const int nv = P.H / 8;
+  if (failed && P.grad_weight)
+    for (long long t = me; t < (long long)P.V * nv; t += all) reinterpret_cast<uint4*>(P.grad_weight)[t] = nans;
+  if (!P.grad_hidden) return;
+  for (long long t = me; t < (long long)P.n * nv; t += all) {
+    const int r = (int)(t / nv), j = (int)(t % nv) * 8, pos = P.pos_of[r];
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (pos >= 0)
+      for (int sp = 0; sp < P.splits; ++sp) {
+        const float4* a = reinterpret_cast<const float4*>(P.acc + ((size_t)sp * P.n_pad + pos) * P.H + j);
+        const float4 u = a[0], v = a[1];
+        x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
+        x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
       }
-    }
+    reinterpret_cast<uint4*>(P.grad_hidden)[t] = failed ? nans : pack8(x);
+  }
 }
 
-// every row of dh: its sum, or zeros where the row took no part
-__global__ void __launch_bounds__(256) scatter_rows(const __grid_constant__ CeParams P) {
-  const long long total = (long long)P.n * P.H;
-  for (long long t = blockIdx.x * 256ll + threadIdx.x; t < total; t += gridDim.x * 256ll) {
-    const int r = (int)(t / P.H), pos = P.pos_of[r];
-    P.grad_hidden[t] = __float2bfloat16_rn(pos < 0 ? 0.f : P.acc[(size_t)pos * P.H + t % P.H]);
-  }
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled g_encode = nullptr;              // set once by configure_linear_ce
+
+// bf16 matrix of `height` rows of `width`, boxes of 64 columns x `box` rows
+bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t height, uint32_t box) {
+  const cuuint64_t dims[2] = {width, height}, strides[1] = {width * 2};
+  const cuuint32_t boxes[2] = {(cuuint32_t)kTcK, box}, ones[2] = {1, 1};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, boxes, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
 
+cudaError_t configure_linear_ce() {
+  cudaDriverEntryPointQueryResult found;
+  void* f = nullptr;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return e;
+  if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+  g_encode = reinterpret_cast<EncodeTiled>(f);
+  const int smem = (int)kTcSmem;
+  e = cudaFuncSetAttribute(ce_forward, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_softmax, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_grads, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e;
+}
+
 cudaError_t launch_ce_forward(const CeParams& P, int nsm, cudaStream_t s, int* launches) {
+  CeMaps M;
+  memset(&M, 0, sizeof M);
+  if (!encode(&M.rows, P.rows, P.H, P.n_pad, kTcHalf) || !encode(&M.weight, P.weight, P.H, P.V, kTcHalf))
+    return cudaErrorInvalidValue;
   gather_rows<false><<<P.n_pad / kGatherRows, kGatherThreads, 0, s>>>(P);
-  ce_forward<<<dim3((P.V + kTile - 1) / kTile, P.n_pad / kTile), kCeThreads, 0, s>>>(P);
-  merge_rows<<<(P.n_pad + 255) / 256, 256, 0, s>>>(P);
+  ce_forward<<<nsm / 2 * 2, kTcThreads, kTcSmem, s>>>(P, M);
+  merge_rows<<<P.n_pad / 32, kMergeThreads, 0, s>>>(P);
   *launches = 3;
   return cudaGetLastError();
 }
 
 cudaError_t launch_ce_backward(const CeParams& P, int nsm, cudaStream_t s, int* launches) {
+  CeMaps M;
+  memset(&M, 0, sizeof M);
+  if (!encode(&M.rows, P.rows, P.H, P.n_pad, kTcHalf) || !encode(&M.weight, P.weight, P.H, P.V, kTcHalf) ||
+      !encode(&M.soft, P.soft, P.piece, P.n_pad, kTcHalf) || !encode(&M.rows_t, P.rows, P.H, P.n_pad, kTcK) ||
+      !encode(&M.weight_t, P.weight, P.H, P.V, kTcK) || !encode(&M.soft_t, P.soft, P.piece, P.n_pad, kTcK))
+    return cudaErrorInvalidValue;
   gather_rows<true><<<P.n_pad / kGatherRows, kGatherThreads, 0, s>>>(P);
-  int n = 1;
-  const int hb = (P.H + kTile - 1) / kTile;
-  for (int v = 0; v < P.V; v += P.piece) {
-    ce_softmax<<<dim3(P.piece / kTile, P.n_pad / kTile), kCeThreads, 0, s>>>(P, v);
-    ++n;
-    if (P.grad_weight) { ce_grad_weight<<<dim3(hb, P.piece / kTile), kCeThreads, 0, s>>>(P, v); ++n; }
-    if (P.grad_hidden) { ce_grad_hidden<<<dim3(hb, P.n_pad / kTile), kCeThreads, 0, s>>>(P, v); ++n; }
-    if (v > P.V - P.piece) break;            // the last piece (v + piece may pass 2^31 - 1)
+  int n = 2;
+  for (long long v = 0; v < P.V; v += P.piece, n += 2) {
+    ce_softmax<<<nsm / 2 * 2, kTcThreads, kTcSmem, s>>>(P, M, (int)v);
+    ce_grads<<<nsm / 2 * 2, kTcThreads, kTcSmem, s>>>(P, M, (int)v);
   }
-  if (P.grad_hidden) { scatter_rows<<<4 * nsm, 256, 0, s>>>(P); ++n; }
+  finish_grads<<<4 * nsm, 256, 0, s>>>(P);
   *launches = n;
   return cudaGetLastError();
 }
@@ -288,26 +440,37 @@ size_t ce_layout(CeParams& P, bool backward, void* base) {
     at = (at + bytes + 255) / 256 * 256;
     return p;
   };
-  P.n_pad = (P.n + kCeRowTile - 1) / kCeRowTile * kCeRowTile;
+  P.n_pad = (P.n + kTcTile - 1) / kTcTile * kTcTile;
   P.count = reinterpret_cast<int*>(place(256));
   P.row_of = reinterpret_cast<int*>(place(4ull * P.n_pad));
   P.lab = reinterpret_cast<int*>(place(4ull * P.n_pad));
   P.rows = reinterpret_cast<__nv_bfloat16*>(place(2ull * P.n_pad * P.H));
   if (!backward) {
     P.label_logit = reinterpret_cast<float*>(place(4ull * P.n_pad));
-    P.part = reinterpret_cast<float2*>(place(8ull * P.n_pad * ((P.V + kTile - 1) / kTile)));
+    P.part = reinterpret_cast<float2*>(place(8ull * P.n_pad * ((P.V + kTcTile - 1) / kTcTile)));
     return at;
   }
   // G of a piece takes at most about 256 MB, and a piece is a whole number of tiles
-  const long long all = (P.V + kCeVocabTile - 1ll) / kCeVocabTile * kCeVocabTile;
-  long long piece = (128ll << 20) / P.n_pad / kCeVocabTile * kCeVocabTile;
-  if (piece < kCeVocabTile) piece = kCeVocabTile;
+  const long long all = (P.V + kTcTile - 1ll) / kTcTile * kTcTile;
+  long long piece = (128ll << 20) / P.n_pad / kTcTile * kTcTile;
+  if (piece < kTcTile) piece = kTcTile;
   P.piece = (int)(piece < all ? piece : all);
+  // dh = G W sums over the whole piece, dW = G^T h over the rows: where few rows
+  // make the former the longer chain, its k is split so that no tile has more than
+  // about half of a pair's share of all stages (76 pairs)
+  const long long rt = P.n_pad / kTcTile, ct = (P.H + kTcTile - 1) / kTcTile;
+  const long long steps_x = P.piece / kTcK, steps_w = (P.n + kTcK - 1) / kTcK;
+  const long long share = (rt * ct * steps_x + P.piece / kTcTile * ct * steps_w) / 76;
+  long long most = share / 2 < 8 ? 8 : share / 2;
+  if (most < (steps_x + 63) / 64) most = (steps_x + 63) / 64;
+  if (most > steps_x) most = steps_x;
+  P.split_steps = (int)most;
+  P.splits = (int)((steps_x + most - 1) / most);
   P.pos_of = reinterpret_cast<int*>(place(4ull * P.n));
   P.lse_c = reinterpret_cast<float*>(place(4ull * P.n_pad));
   P.g_c = reinterpret_cast<float*>(place(4ull * P.n_pad));
   P.soft = reinterpret_cast<__nv_bfloat16*>(place(2ull * P.n_pad * P.piece));
-  P.acc = reinterpret_cast<float*>(place(4ull * P.n_pad * P.H));
+  P.acc = reinterpret_cast<float*>(place(4ull * P.splits * P.n_pad * P.H));
   return at;
 }
 

@@ -1,0 +1,275 @@
+// tc_gemm.cuh -- matrix products on the tensor cores of sm_103a: operands staged
+// in shared memory by TMA, tcgen05.mma over a pair of CTAs, sums in TMEM.
+//
+// A pair of CTAs (a cluster of two) computes a 256 x 256 tile of sum_k A(i, k)
+// B(j, k): each CTA stages 128 rows of A and 128 of B, the leader issues the
+// products for both (cta_group::2), and each CTA holds the sums of its own 128
+// rows: 256 of its 512 TMEM columns, so that the epilogue of one tile overlaps
+// the products of the next.  A 128 x 256 tile by one CTA would stage 48 KB for the same
+// products that the pair does with 32 KB per CTA: 96 bytes a clock per SM
+// from L2 against 64.
+// Warps: 0-3 epilogue (TMEM lanes 32 w .. 32 w + 31), 4 producer, 5 products.
+// Operands of bf16, sums of fp32.
+#pragma once
+
+#include <cuda.h>
+
+#include "common.cuh"
+
+namespace sv {
+
+constexpr int kTcTile = 256;                 // tile rows and columns of a pair
+constexpr int kTcHalf = 128;                 // of one CTA
+constexpr int kTcK = 64;                     // k per stage: 128 bytes of bf16, one swizzle row
+constexpr int kTcStages = 6;
+constexpr int kTcOperand = kTcHalf * kTcK * 2;           // 16 KB
+constexpr int kTcStage = 2 * kTcOperand;
+constexpr int kTcThreads = 192;
+constexpr int kTcProducer = 4, kTcIssuer = 5;            // warps
+constexpr uint32_t kTcColumns = 512;
+// A wait gives up after about 2 s; no healthy call comes near.  After one the
+// CTA waits kTcDrain cycles (~1 ms) for the copies and products still in flight.
+constexpr long long kTcWaitCycles = 4000000000ll, kTcDrain = 2000000ll;
+
+struct TcShared {
+  uint64_t full[kTcStages], empty[kTcStages], done[2], drained[2];
+  uint32_t tmem;
+  int failed;
+};
+constexpr size_t kTcSmem = kTcStages * (size_t)kTcStage + 1024 + sizeof(TcShared);
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// the same shared address in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// Waits for a phase, at most kTcWaitCycles; also gives up when another role of
+// this CTA has.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+  uint32_t ok;
+  long long t0 = 0;
+  for (int spin = 0;; ++spin) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if ((spin & 63) == 63) {
+      const long long t = clock64();
+      if (t0 == 0) t0 = t;
+      if (*failed || t - t0 > kTcWaitCycles) {
+        *failed = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// One box of a 2-D tensor map into this CTA's shared memory, counted on a
+// barrier of either CTA of the pair.  x is a multiple of 8 elements (16 bytes).
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+      "l"(map), "r"(bar), "r"(x), "r"(y)
+      : "memory");
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle, 64 bf16 wide rows.
+//   k inner:  rows of 64 k; 8 rows a swizzle atom (1 KB apart); 16 k are 32 bytes.
+//   k outer:  64 k rows of 64 i (8 KB); 8 k an atom (1 KB apart), the next 64 i
+//             8 KB on; 16 k are 2 KB.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, bool k_inner) {
+  const uint64_t lead = k_inner ? 1 : 8192 >> 4;
+  return (uint64_t)((addr & 0x3FFFF) >> 4) | lead << 16 | (uint64_t)(1024 >> 4) << 32 | 1ull << 46 | 2ull << 61;
+}
+// kind::f16 instruction: fp32 sums, bf16 operands, M = N = 256
+__device__ __forceinline__ uint32_t tc_idesc(bool a_k_inner, bool b_k_inner) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (a_k_inner ? 0u : 1u << 15) | (b_k_inner ? 0u : 1u << 16) |
+         (kTcTile >> 3) << 17 | (kTcTile >> 4) << 24;
+}
+__device__ __forceinline__ void tc_mma(uint32_t tmem, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+      : "memory");
+}
+// the barrier at this offset in both CTAs, once the products issued so far are done
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 32 columns of this warp's 32 lanes: v[c] is column col + c of the thread's row
+__device__ __forceinline__ void tc_load32(float (&v)[32], uint32_t addr) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
+}
+
+// One operand of a tile: rows i0 .. i0 + 255 (the CTA's half from i0 + 128 rank)
+// over k0 .. of a matrix whose map has k inner (box 64 x 128) or i inner (box 64 x 64).
+struct TcOperand {
+  const CUtensorMap* map;
+  bool k_inner;
+  int i0, k0;
+};
+__device__ __forceinline__ void tc_stage(uint32_t dst, const TcOperand& o, uint32_t rank, int k, uint32_t bar) {
+  const int i = o.i0 + (int)rank * kTcHalf;
+  if (o.k_inner) {
+    tma_box(dst, o.map, o.k0 + k, i, bar);
+  } else {
+    tma_box(dst, o.map, i, o.k0 + k, bar);
+    tma_box(dst + kTcOperand / 2, o.map, i + 64, o.k0 + k, bar);
+  }
+}
+
+// The persistent kernel.  Work::count() tiles; Work::tile(t) gives its operands
+// and the number of stages of k (0: no product); Work::epilogue(t, row, tmem,
+// any) is called by the 128 epilogue threads with the thread's tile row and the
+// TMEM address of its first column.  Pair c does the tiles c, c + pairs, ...
+struct TcTile {
+  TcOperand a, b;
+  int steps;
+};
+template <class Work>
+__device__ __forceinline__ void tc_run(const Work& work, int* error) {
+  extern __shared__ unsigned char tc_smem[];
+  const uint32_t base = (smem_u32(tc_smem) + 1023) & ~1023u;
+  TcShared& S = *reinterpret_cast<TcShared*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = work.count();
+  volatile int* failed = &S.failed;
+
+  if (threadIdx.x == 0) {
+    S.failed = 0;
+    for (int i = 0; i < kTcStages; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&S.done[i], 1); mbar_init(&S.drained[i], 8); }
+    fence_mbar_init();
+  }
+  __syncthreads();
+  cluster_sync();                            // both CTAs' barriers are ready
+  if (warp == kTcIssuer) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)),
+                 "r"(kTcColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                            // both halves of the tensor memory are allocated
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+
+  if (warp == kTcProducer) {
+    if (lane == 0) {
+      int it = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const TcTile tile = work.tile(t);
+        for (int k = 0; k < tile.steps; ++k, ++it) {
+          const int st = it % kTcStages;
+          if (!(ok = tc_wait(&S.empty[st], ((it / kTcStages) & 1) ^ 1, failed))) break;
+          const uint32_t bar = map_rank(smem_u32(&S.full[st]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&S.full[st], 2 * kTcStage);   // both CTAs' halves
+          const uint32_t at = base + st * kTcStage;
+          tc_stage(at, tile.a, rank, k * kTcK, bar);
+          tc_stage(at + kTcOperand, tile.b, rank, k * kTcK, bar);
+        }
+      }
+    }
+  } else if (warp == kTcIssuer) {
+    if (rank == 0 && lane == 0) {
+      int it = 0, n = 0;
+      bool ok = true;
+      for (int t = pair; t < tiles && ok; t += pairs) {
+        const TcTile tile = work.tile(t);
+        if (tile.steps == 0) continue;
+        const int buf = n & 1;
+        if (!(ok = tc_wait(&S.drained[buf], ((n >> 1) & 1) ^ 1, failed))) break;
+        tc_fence_after();
+        const uint32_t idesc = tc_idesc(tile.a.k_inner, tile.b.k_inner), d = tmem + buf * kTcTile;
+        const uint32_t sa = tile.a.k_inner ? 32 >> 4 : 2048 >> 4, sb = tile.b.k_inner ? 32 >> 4 : 2048 >> 4;
+        for (int k = 0; k < tile.steps; ++k, ++it) {
+          const int st = it % kTcStages;
+          if (!(ok = tc_wait(&S.full[st], (it / kTcStages) & 1, failed))) break;
+          tc_fence_after();
+          const uint64_t da = tc_desc(base + st * kTcStage, tile.a.k_inner);
+          const uint64_t db = tc_desc(base + st * kTcStage + kTcOperand, tile.b.k_inner);
+#pragma unroll
+          for (int q = 0; q < kTcK / 16; ++q)
+            tc_mma(d, da + (uint64_t)(q * sa), db + (uint64_t)(q * sb), idesc, k > 0 || q > 0);
+          tc_commit(&S.empty[st]);
+        }
+        if (ok) tc_commit(&S.done[buf]);
+        ++n;
+      }
+    }
+  } else {
+    int n = 0;
+    for (int t = pair; t < tiles; t += pairs) {
+      const int row = (int)rank * kTcHalf + warp * 32 + lane;
+      const int steps = work.tile(t).steps;
+      const int buf = n & 1;
+      if (steps > 0) {
+        const bool ok = tc_wait(&S.done[buf], (n >> 1) & 1, failed);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        tc_fence_after();
+      }
+      work.epilogue(t, row, tmem + buf * kTcTile + ((uint32_t)(warp * 32) << 16), steps > 0);
+      if (steps > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.drained[buf]), 0));
+        ++n;
+      }
+    }
+  }
+  __syncwarp();
+  if (__any_sync(0xffffffffu, *failed)) {    // copies or products may still be in flight
+    const long long t0 = clock64();
+    while (clock64() - t0 < kTcDrain) {}
+    if (lane == 0) *error = 1;
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();                            // neither CTA leaves while the other signals it
+  tc_fence_after();
+  if (warp == kTcIssuer)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcColumns) : "memory");
+}
+
+}  // namespace sv
