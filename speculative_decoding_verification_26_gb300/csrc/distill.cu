@@ -14,7 +14,7 @@
 //   w/T [ q_v (kl + ce + tv (s_r/2 - S) - kl p_r / q_r) - ce [v = y] ]  else.
 // For a token outside the record it is e^{z_v / T} times one factor of the row.
 //
-// One CTA per row.  The recorded tokens are marked in a bit map, and the sum of
+// A cluster of CS CTAs per row (one where rows fill the GPU).  The recorded tokens are marked in a bit map, and the sum of
 // the others leaves them out: q_r as 1 - sum q_k would cancel.  The gradient
 // pass reads the row again (from L2) and writes factor times weight everywhere;
 // then the K tokens and the label get their own values.
@@ -37,36 +37,29 @@ __device__ __forceinline__ void store_logit(unsigned char* row, int e, float v) 
   if constexpr (DT == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(row)[e] = __float2bfloat16_rn(v);
   else reinterpret_cast<float*>(row)[e] = v;
 }
-template <int DT, int PER>
-__device__ __forceinline__ uint4 pack_row(const float (&g)[PER]) {
-  uint32_t u[4];
-  if constexpr (DT == SPEC_BF16) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(g[2 * k], g[2 * k + 1]);
-      memcpy(&u[k], &b, 4);
-    }
-  } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) u[k] = __float_as_uint(g[k]);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
-}
 
-template <int DT>
+template <int DT, int CS>
 __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_constant__ DistillParams P) {
   constexpr int PER = RowType<DT>::PER, ES = RowType<DT>::ES;
   extern __shared__ uint32_t s_bits[];       // one bit per token of the row (offset PER: see below)
   __shared__ float s_f[kDisWarps];
   __shared__ float s_g[kDisWarps];
+  __shared__ float s_part[2][2];             // this CTA's maximum and sum, for the cluster (by turns)
+  const int rank = CS == 1 ? 0 : (int)cluster_rank();
+  int turn = 0;
   const int V = P.V, K = P.K, tid = threadIdx.x;
   const int words = (V + PER + 31) / 32 + 1;
   const float nan = __int_as_float(0x7fc00000);
   for (int i = tid; i < words; i += kDisThreads) s_bits[i] = 0;
-  for (int r = blockIdx.x; r < P.n; r += gridDim.x) {
+  for (int r = blockIdx.x / CS; r < P.n; r += gridDim.x / CS) {
     const unsigned char* row = P.logits + (size_t)r * V * ES;
     unsigned char* grow = P.grad ? P.grad + (size_t)r * V * ES : nullptr;
     const RowSpan sp = row_span<DT>(row, V);
+    const RowShare sh = row_share<CS>(sp, rank);
+    auto my_element = [&](int e) {           // whether this CTA writes token e's gradient
+      const int j = e < sp.head ? -1 : (e - sp.head) / PER;
+      return j < 0 || j >= sp.nvec ? sh.ends : j >= sh.lo && j < sh.hi;
+    };
     // vectors of the gradient row start where those of the logit row do, or it is written element by element
     const bool gvec = ((reinterpret_cast<uintptr_t>(grow) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
     const float w = P.row_weight ? P.row_weight[r] : 1.f;
@@ -77,16 +70,16 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
       if (!grow) return;
       if (gvec) {
         uint4* gv = reinterpret_cast<uint4*>(grow + (size_t)sp.head * ES);
-        for (int j = tid; j < sp.nvec; j += kDisThreads) gv[j] = make_uint4(0, 0, 0, 0);
-        const int ends = sp.head + (V - sp.tail0);
+        for (int j = sh.lo + tid; j < sh.hi; j += kDisThreads) gv[j] = make_uint4(0, 0, 0, 0);
+        const int ends = sh.ends ? sp.head + (V - sp.tail0) : 0;
         if (tid < ends) store_logit<DT>(grow, tid < sp.head ? tid : sp.tail0 + (tid - sp.head), 0.f);
       } else {
-        for (int e = tid; e < V; e += kDisThreads) store_logit<DT>(grow, e, 0.f);
+        for (int e = rank * kDisThreads + tid; e < V; e += CS * kDisThreads) store_logit<DT>(grow, e, 0.f);
       }
     };
     if (w == 0.f) {                          // a padded row: nothing of it is read
       zero_grad();
-      if (tid == 0) {
+      if (rank == 0 && tid == 0) {
         P.loss[r] = 0.f;
         if (P.parts) { P.parts[3 * (size_t)r] = 0.f; P.parts[3 * (size_t)r + 1] = 0.f; P.parts[3 * (size_t)r + 2] = 0.f; }
         if (P.status) P.status[r] = SPEC_ST_OK;
@@ -145,35 +138,71 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
     // the student's rest: running maximum and sum of the tokens not recorded
     float m = -INFINITY, s = 0.f;
     const unsigned char* bytes = reinterpret_cast<const unsigned char*>(s_bits);
-    auto add = [&](float x) {
-      if (x > m) {
-        s *= m == -INFINITY ? 0.f : ex2((m - x) * c);
-        m = x;
-      }
-      if (m != -INFINITY) s += ex2((x - m) * c);
-      else if (x != x) s = x;
+    const float2 C2 = make_float2(c, c);
+    auto raise = [&](float x) {
+      s *= m == -INFINITY ? 0.f : ex2(ref_of(m, c) - ref_of(x, c));
+      m = x;
     };
-    for_row<DT, kDisThreads, 4>(row, sp, V,
-        [&](int j, float (&x)[PER]) {
+    for_row<DT, kDisThreads, 8>(row, sp, sh, V,
+        [&](int j, const uint4& w) {
           const uint32_t mark = PER == 8 ? bytes[j + 1] : (bytes[(j + 1) >> 1] >> (((j + 1) & 1) * 4)) & 15u;
-          if (mark) {
+          if (mark == 0) {
+            const float top = vec_max<DT>(w);
+            if (top > m) raise(top);
+            const float nr = m == -INFINITY ? 0.f : -ref_of(m, c);       // all -inf so far: weights of 0
+            const float2 R2 = make_float2(nr, nr);
+            float2 t = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < PER; ++k)
-              if (mark >> k & 1) x[k] = -INFINITY;
+            for (int k = 0; k < PER / 2; ++k) {
+              const float2 a = __ffma2_rn(vec_pair<DT>(w, k), C2, R2);
+              t = __fadd2_rn(t, make_float2(ex2(a.x), ex2(a.y)));
+            }
+            s += t.x + t.y;
+          } else {
+#pragma unroll
+            for (int k = 0; k < PER; ++k) {
+              const float2 p = vec_pair<DT>(w, k / 2);
+              const float x = k & 1 ? p.y : p.x;
+              if (mark >> k & 1) continue;
+              if (x > m) raise(x);
+              s += ex2(fmaf(x, c, m == -INFINITY ? 0.f : -ref_of(m, c)));
+            }
           }
-#pragma unroll
-          for (int k = 0; k < PER; ++k) add(x[k]);
         },
         [&](int e, float x) {
           const int bit = e - sp.head + PER;
-          if (!(s_bits[bit >> 5] >> (bit & 31) & 1)) add(x);
+          if (s_bits[bit >> 5] >> (bit & 31) & 1) return;
+          if (x > m) raise(x);
+          s += ex2(fmaf(x, c, m == -INFINITY ? 0.f : -ref_of(m, c)));
         });
     __syncthreads();                         // s_f and s_g are read, and the map
     if (mine) atomicAnd(&s_bits[(idx - sp.head + PER) >> 5], ~(1u << ((idx - sp.head + PER) & 31)));
-    const float mall = fmaxf(cta_max<kDisWarps>(fmaxf(m, zk), s_f), -INFINITY);
-    const float ref = ref_of(mall, c);
+    float mall = cta_max<kDisWarps>(fmaxf(m, zk), s_f);
+    if constexpr (CS > 1) {                  // every CTA holds all zk: the maximum of both is the row's
+      if (tid == 0) s_part[turn][0] = mall;
+    }
     // one exponent rule for every weight from here on: 2^{x c - ref}
-    const float rest = cta_sum<kDisWarps>(m == -INFINITY ? s : s * ex2(fmaf(m, c, -ref)), s_g);
+    auto moved = [&](float sum, float from, float to) {
+      return from == -INFINITY ? sum : sum * ex2(ref_of(from, c) - ref_of(to, c));
+    };
+    float rest = cta_sum<kDisWarps>(moved(s, m, mall), s_g);
+    if constexpr (CS > 1) {
+      if (tid == 0) s_part[turn][1] = rest;
+      cluster_sync();
+      float pm[CS], ps[CS];
+#pragma unroll
+      for (int q = 0; q < CS; ++q) {
+        const uint32_t from = map_rank(smem_u32(s_part[turn]), q);
+        pm[q] = __uint_as_float(ld_cluster(from));
+        ps[q] = __uint_as_float(ld_cluster(from + 4));
+        mall = fmaxf(mall, pm[q]);
+      }
+      rest = 0.f;
+#pragma unroll
+      for (int q = 0; q < CS; ++q) rest += moved(ps[q], pm[q], mall);
+      turn ^= 1;
+    }
+    const float ref = ref_of(mall, c);
     const float fk = mine ? ex2(fmaf(zk, c, -ref)) : 0.f;
     __syncthreads();
     const float S = cta_sum<kDisWarps>(fk, s_f) + rest;
@@ -182,7 +211,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
     if (__syncthreads_or(st & SPEC_ST_BAD_TOKEN)) st |= SPEC_ST_BAD_TOKEN;
     if (st != 0) {                           // the same in every thread
       zero_grad();
-      if (tid == 0) {
+      if (rank == 0 && tid == 0) {
         P.loss[r] = nan;
         if (P.parts) { P.parts[3 * (size_t)r] = nan; P.parts[3 * (size_t)r + 1] = nan; P.parts[3 * (size_t)r + 2] = nan; }
         if (P.status) P.status[r] = st;
@@ -203,7 +232,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
     const float kl = kls + (pr > 0.f ? pr * ((lt - top - l2Z) - (log2f(rest) - l2S)) * kLn2 : 0.f);
     const float tv = 0.5f * (tvs + fabsf(pr - qr));
     const float ce = y >= 0 ? (l2S - fmaf(zy, c, -ref)) * kLn2 : 0.f;
-    if (tid == 0) {
+    if (rank == 0 && tid == 0) {
       float l = 0.f;
       if (P.kl != 0.f) l += P.kl * kl;
       if (P.tv != 0.f) l += P.tv * tv;
@@ -224,39 +253,83 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
     const float gy = ex2(fmaf(zy, c, -ref)) * rest_f - wT * lce;     // the label's, where it is not recorded
     if (gvec) {
       uint4* gv = reinterpret_cast<uint4*>(grow + (size_t)sp.head * ES);
-      for_row<DT, kDisThreads, 4>(row, sp, V,
-          [&](int j, float (&x)[PER]) {
+      const float2 R2 = make_float2(-ref, -ref), F2 = make_float2(rest_f, rest_f);
+      for_row<DT, kDisThreads, 4>(row, sp, sh, V,
+          [&](int j, const uint4& w) {
+            uint32_t u[4];
 #pragma unroll
-            for (int k = 0; k < PER; ++k) x[k] = ex2(fmaf(x[k], c, -ref)) * rest_f;
-            gv[j] = pack_row<DT, PER>(x);
+            for (int k = 0; k < PER / 2; ++k) {
+              const float2 a = __ffma2_rn(vec_pair<DT>(w, k), C2, R2);
+              const float2 g = __fmul2_rn(make_float2(ex2(a.x), ex2(a.y)), F2);
+              if constexpr (DT == SPEC_BF16) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(g.x, g.y);
+                memcpy(&u[k], &b, 4);
+              } else {
+                u[2 * k] = __float_as_uint(g.x);
+                u[2 * k + 1] = __float_as_uint(g.y);
+              }
+            }
+            __stcs(gv + j, make_uint4(u[0], u[1], u[2], u[3]));
           },
           [&](int e, float x) { store_logit<DT>(grow, e, ex2(fmaf(x, c, -ref)) * rest_f); });
     } else {
-      for (int e = tid; e < V; e += kDisThreads)
+      for (int e = rank * kDisThreads + tid; e < V; e += CS * kDisThreads)
         store_logit<DT>(grow, e, ex2(fmaf(row_logit<DT>(row, e), c, -ref)) * rest_f);
+      if constexpr (CS > 1) cluster_sync();  // the tokens below may be another CTA's
     }
     const int recorded = __syncthreads_or(mine && idx == y);   // the pass's stores come before these
-    if (mine) store_logit<DT>(grow, idx, gk);
-    if (tid == 0 && y >= 0 && !recorded) store_logit<DT>(grow, y, gy);
+    if (mine && my_element(idx)) store_logit<DT>(grow, idx, gk);
+    if (tid == 0 && y >= 0 && !recorded && my_element(y)) store_logit<DT>(grow, y, gy);
     __syncthreads();
   }
+  if constexpr (CS > 1) cluster_sync();      // no CTA leaves while its partial sums are read
+}
+
+template <int DT, int CS>
+cudaError_t launch_as(const DistillParams& P, int nsm, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  const int most = 2 * nsm / CS;             // clusters resident at once, two CTAs per SM
+  cfg.gridDim = dim3((P.n < most ? P.n : most) * CS);
+  cfg.blockDim = dim3(kDisThreads);
+  cfg.dynamicSmemBytes = ((size_t)(P.V + 8 + 31) / 32 + 1) * 4;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {CS, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, distill_kernel<DT, CS>, P);
+}
+
+template <int DT>
+cudaError_t launch_of(const DistillParams& P, int nsm, cudaStream_t s) {
+  const int cs = row_cluster(P.n, P.V, RowType<DT>::ES, nsm);
+  if (cs == 8) return launch_as<DT, 8>(P, nsm, s);
+  if (cs == 4) return launch_as<DT, 4>(P, nsm, s);
+  if (cs == 2) return launch_as<DT, 2>(P, nsm, s);
+  return launch_as<DT, 1>(P, nsm, s);
+}
+
+template <int DT>
+cudaError_t configure_as() {
+  const int most = ((kDistillMaxV + 8 + 31) / 32 + 1) * 4;
+  const auto attr = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(distill_kernel<DT, 1>, attr, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(distill_kernel<DT, 2>, attr, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(distill_kernel<DT, 4>, attr, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(distill_kernel<DT, 8>, attr, most);
+  return e;
 }
 
 }  // namespace
 
 cudaError_t launch_distill(const DistillParams& P, int nsm, cudaStream_t s) {
-  const int grid = P.n < 2 * nsm ? P.n : 2 * nsm;
-  const size_t smem = ((size_t)(P.V + 8 + 31) / 32 + 1) * 4;
-  if (P.dtype == SPEC_BF16) distill_kernel<SPEC_BF16><<<grid, kDisThreads, smem, s>>>(P);
-  else distill_kernel<SPEC_F32><<<grid, kDisThreads, smem, s>>>(P);
-  return cudaGetLastError();
+  return P.dtype == SPEC_BF16 ? launch_of<SPEC_BF16>(P, nsm, s) : launch_of<SPEC_F32>(P, nsm, s);
 }
 
 cudaError_t configure_distill() {
-  const int most = ((kDistillMaxV + 8 + 31) / 32 + 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(distill_kernel<SPEC_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  if (e != cudaSuccess) return e;
-  return cudaFuncSetAttribute(distill_kernel<SPEC_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+  const cudaError_t e = configure_as<SPEC_BF16>();
+  return e == cudaSuccess ? configure_as<SPEC_F32>() : e;
 }
 
 }  // namespace sv

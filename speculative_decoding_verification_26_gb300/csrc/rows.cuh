@@ -12,19 +12,10 @@ struct RowType;
 template <>
 struct RowType<SPEC_BF16> {
   static constexpr int ES = 2, PER = 8;
-  __device__ __forceinline__ static void unpack(uint4 w, float (&x)[8]) {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) { x[2 * k] = bf16_lo(u[k]); x[2 * k + 1] = bf16_hi(u[k]); }
-  }
 };
 template <>
 struct RowType<SPEC_F32> {
   static constexpr int ES = 4, PER = 4;
-  __device__ __forceinline__ static void unpack(uint4 w, float (&x)[4]) {
-    x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y);
-    x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
-  }
 };
 
 // One logit by a plain load (a row that the same kernel also writes).
@@ -70,35 +61,109 @@ __device__ __forceinline__ RowSpan row_span(const unsigned char* row, int V) {
   return s;
 }
 
-// Calls fv(j, x) for each vector j of this thread (x its PER logits) and
-// fe(e, x) for each single element e.  U vectors are loaded before any is
-// used, so that a thread has that many 16-byte loads in flight.
+// A 16-byte vector as pairs of logits.
+template <int DT>
+__device__ __forceinline__ float2 vec_pair(const uint4& w, int k) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  if constexpr (DT == SPEC_BF16) return make_float2(bf16_lo(u[k]), bf16_hi(u[k]));
+  else return make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1]));
+}
+__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {      // a number before a NaN
+  uint32_t d;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ uint32_t max_nan_bf2(uint32_t a, uint32_t b) {  // a NaN before a number
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+// The largest logit of a vector, NaNs left out.
+template <int DT>
+__device__ __forceinline__ float vec_max(const uint4& w) {
+  if constexpr (DT == SPEC_BF16) {
+    const uint32_t m = max_bf2(max_bf2(w.x, w.y), max_bf2(w.z, w.w));
+    return fmaxf(bf16_lo(m), bf16_hi(m));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
+}
+
+// A CTA's share of a row that a cluster of CS CTAs reads: vectors [lo, hi), and
+// both ends' single elements by the first.
+struct RowShare {
+  int lo, hi;
+  bool ends;
+};
+template <int CS>
+__device__ __forceinline__ RowShare row_share(const RowSpan& sp, int rank) {
+  if constexpr (CS == 1) return {0, sp.nvec, true};
+  const int per = (sp.nvec + CS - 1) / CS, lo = rank * per;
+  return {lo < sp.nvec ? lo : sp.nvec, lo + per < sp.nvec ? lo + per : sp.nvec, rank == 0};
+}
+
+// CTAs per row: the largest cluster that keeps every CTA resident at once, two per
+// SM, and leaves each at least 16 KB of the row (two vectors a thread).
+inline int row_cluster(int n, int V, int es, int nsm) {
+  for (int cs = 8; cs > 1; cs /= 2)
+    if ((long long)n * cs <= 2 * nsm && (long long)V * es >= cs * 16384ll) return cs;
+  return 1;
+}
+
+// Calls fv(j, w) for each vector j of this thread (w its 16 bytes) and fe(e, x)
+// for each single element e.  U vectors are loaded before any is used, so that
+// a thread has that many 16-byte loads in flight.
 template <int DT, int THREADS, int U, class FV, class FE>
-__device__ __forceinline__ void for_row(const unsigned char* row, const RowSpan& sp, int V, FV&& fv, FE&& fe) {
-  constexpr int ES = RowType<DT>::ES, PER = RowType<DT>::PER;
-  const uint4* vec = reinterpret_cast<const uint4*>(row + (size_t)sp.head * ES);
-  for (int j0 = threadIdx.x; j0 < sp.nvec; j0 += THREADS * U) {
+__device__ __forceinline__ void for_row(const unsigned char* row, const RowSpan& sp, const RowShare& sh, int V, FV&& fv,
+                                        FE&& fe) {
+  const uint4* vec = reinterpret_cast<const uint4*>(row + (size_t)sp.head * RowType<DT>::ES);
+  int j0 = sh.lo + (int)threadIdx.x;
+  for (; j0 + (U - 1) * THREADS < sh.hi; j0 += THREADS * U) {
     uint4 w[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * THREADS;
-      if (j < sp.nvec) w[u] = vec[j];
-    }
+    for (int u = 0; u < U; ++u) w[u] = vec[j0 + u * THREADS];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int j = j0 + u * THREADS;
-      if (j < sp.nvec) {
-        float x[PER];
-        RowType<DT>::unpack(w[u], x);
-        fv(j, x);
-      }
-    }
+    for (int u = 0; u < U; ++u) fv(j0 + u * THREADS, w[u]);
   }
+  for (; j0 < sh.hi; j0 += THREADS) {
+    const uint4 w = vec[j0];
+    fv(j0, w);
+  }
+  if (!sh.ends) return;
   const int ends = sp.head + (V - sp.tail0);
   if ((int)threadIdx.x < ends) {
     const int e = (int)threadIdx.x < sp.head ? (int)threadIdx.x : sp.tail0 + ((int)threadIdx.x - sp.head);
     fe(e, row_logit<DT>(row, e));
   }
+}
+
+// ---------------------------------------------------------------------------
+// clusters
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of the cluster; writes before it, to shared memory too, are seen after it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// the same shared address in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
 }
 
 // Sum over the CTA, the same bits in every thread; `scratch` holds WARPS values
