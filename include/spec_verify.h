@@ -290,9 +290,9 @@ int spec_gamma_select(const float* signals, const float* comp, const float* mode
  *   status      0, SPEC_ST_NONFINITE (a NaN or +inf, or no finite logit) or
  *     SPEC_ST_BAD_TEMPERATURE; such a row has NaN logits, indices -1 and a NaN
  *     tail.
- * No workspace.  Host errors: SPEC_ERR_INVALID_ARG (n < 1, V outside [2, 2^28),
- * K, dtype, NULL required pointers, misalignment), SPEC_ERR_CUDA,
- * SPEC_ERR_UNSUPPORTED. */
+ * No workspace.  Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^30], V
+ * outside [2, 2^28), K, dtype, NULL required pointers, misalignment),
+ * SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
 int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const float* temperature,
                      float* top_logits, int32_t* top_index, float* tail_lse, int32_t* status,
                      spec_stream_t stream);
@@ -322,12 +322,14 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
  *   status      0, SPEC_ST_BAD_TOKEN (a label or index outside [-1, V), or an
  *     index recorded twice), SPEC_ST_BAD_TEMPERATURE, SPEC_ST_NONFINITE (a NaN
  *     or +inf in the row or the record, no finite logit, or a record without
- *     mass): such a row has NaN losses and a gradient of 0.
+ *     mass), SPEC_ST_TIMEOUT (an internal wait hit its time limit): such a row
+ *     has NaN losses and a gradient of 0.
  * KL is +inf where some q_b = 0 < p_b, CE where q_label = 0; the gradient stays
  * finite.  Without the gradient each row is read once.  With it, pass the
  * upstream gradient of a row's loss as a factor of row_weight.
- * No workspace.  Host errors: SPEC_ERR_INVALID_ARG, SPEC_ERR_CUDA,
- * SPEC_ERR_UNSUPPORTED. */
+ * No workspace.  Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^30], V, K,
+ * dtype, coefficients, NULL required pointers, misalignment, overlap),
+ * SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
 int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const float* top_logits,
                       const int32_t* top_index, const float* tail_lse, const int32_t* label,
                       const float* row_weight, const float* temperature, float kl, float tv, float ce,
@@ -349,7 +351,9 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
  *     products that read it;
  *   status [n] or NULL (forward): 0, SPEC_ST_BAD_TOKEN (label outside [-1, V):
  *     loss and lse NaN), SPEC_ST_NONFINITE (a logit of the row is NaN or +inf,
- *     or none is finite: loss and lse NaN).  The backward call leaves out rows
+ *     or none is finite: loss and lse NaN), SPEC_ST_TIMEOUT (an internal wait hit
+ *     its time limit; the backward call then fills its outputs with NaN).  The
+ *     backward call leaves out rows
  *     with a bad label or an lse that is not finite.
  *   workspace: spec_linear_ce_workspace_bytes(n, H, V, backward) bytes, 256-byte
  *     aligned, no initial contents.  Calls that share one must not overlap on

@@ -34,7 +34,6 @@ struct DevState {
   int ctas = 0;       // resident verify CTAs on the device (SMs x CTAs per SM, at most 2 per SM)
   int status = SPEC_OK;
 };
-constexpr int kMaxDevices = 64;
 DevState g_dev[kMaxDevices];
 std::mutex g_mu;
 
@@ -55,7 +54,8 @@ int device_state(int* ctas) {
       d.status = SPEC_ERR_UNSUPPORTED;   // the library carries sm_103a code only
     } else {
       cudaError_t e = configure_kernels();
-      if (e == cudaSuccess) e = configure_distill();
+      if (e == cudaSuccess) e = configure_record(dev);
+      if (e == cudaSuccess) e = configure_distill(dev);
       if (e == cudaSuccess) e = configure_linear_ce();
       int per_sm = 0;
       if (e == cudaSuccess) e = verify_blocks_per_sm(&per_sm);
@@ -74,10 +74,11 @@ int device_state(int* ctas) {
   return d.status;
 }
 
-// Multiprocessors of the current device, after a device_state that succeeded.
-int current_sms() {
+// The current device and its multiprocessors, after a device_state that succeeded.
+int current_sms(int* device) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 1;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
+  *device = dev;
   return g_dev[dev].sms;
 }
 
@@ -403,7 +404,7 @@ int spec_gamma_select(const float* signals, const float* comp, const float* mode
 
 int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const float* temperature, float* top_logits,
                      int32_t* top_index, float* tail_lse, int32_t* status, spec_stream_t stream) {
-  if (n < 1 || V < 2 || V >= (1 << 28) || K < 1 || K > SPEC_MAX_TOPK || K > V) return SPEC_ERR_INVALID_ARG;
+  if (n < 1 || n > (1 << 30) || V < 2 || V >= (1 << 28) || K < 1 || K > SPEC_MAX_TOPK || K > V) return SPEC_ERR_INVALID_ARG;
   if (!logits || !top_logits || !top_index || !tail_lse || (dtype != SPEC_F32 && dtype != SPEC_BF16))
     return SPEC_ERR_INVALID_ARG;
   const void* ptrs4[] = {temperature, top_logits, top_index, tail_lse, status};
@@ -418,7 +419,9 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
   P.dtype = dtype; P.n = n; P.V = V; P.K = K;
   P.temperature = temperature;
   P.top_logits = top_logits; P.top_index = top_index; P.tail_lse = tail_lse; P.status = status;
-  if (launch_record(P, current_sms(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
+  int dev = 0;
+  const int sms = current_sms(&dev);
+  if (launch_record(P, dev, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
   ++g_launches;
   return SPEC_OK;
 }
@@ -427,7 +430,7 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
                       const int32_t* top_index, const float* tail_lse, const int32_t* label, const float* row_weight,
                       const float* temperature, float kl, float tv, float ce, float* loss, float* parts,
                       void* grad_logits, int32_t* status, spec_stream_t stream) {
-  if (n < 1 || V < 2 || V > SPEC_DISTILL_MAX_V || K < 1 || K > SPEC_MAX_TOPK) return SPEC_ERR_INVALID_ARG;
+  if (n < 1 || n > (1 << 30) || V < 2 || V > SPEC_DISTILL_MAX_V || K < 1 || K > SPEC_MAX_TOPK) return SPEC_ERR_INVALID_ARG;
   if (!logits || !top_logits || !top_index || !loss || (dtype != SPEC_F32 && dtype != SPEC_BF16))
     return SPEC_ERR_INVALID_ARG;
   if (!std::isfinite(kl) || !std::isfinite(tv) || !std::isfinite(ce)) return SPEC_ERR_INVALID_ARG;
@@ -451,7 +454,9 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
   P.kl = kl; P.tv = tv; P.ce = ce;
   P.loss = loss; P.parts = parts; P.status = status;
   P.grad = static_cast<unsigned char*>(grad_logits);
-  if (launch_distill(P, current_sms(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
+  int dev = 0;
+  const int sms = current_sms(&dev);
+  if (launch_distill(P, dev, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
   ++g_launches;
   return SPEC_OK;
 }
@@ -482,8 +487,8 @@ int spec_linear_ce_forward(const void* hidden, const void* weight, int dtype, in
   P.hidden = static_cast<const __nv_bfloat16*>(hidden);
   P.weight = static_cast<const __nv_bfloat16*>(weight);
   P.label = label; P.loss = loss; P.lse = lse; P.status = status;
-  int launches = 0;
-  const cudaError_t e = launch_ce_forward(P, current_sms(), reinterpret_cast<cudaStream_t>(stream), &launches);
+  int launches = 0, dev = 0;
+  const cudaError_t e = launch_ce_forward(P, current_sms(&dev), reinterpret_cast<cudaStream_t>(stream), &launches);
   g_launches += launches;
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
@@ -512,8 +517,8 @@ int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, i
   P.label = label; P.lse_in = lse; P.grad_loss = grad_loss;
   P.grad_hidden = static_cast<__nv_bfloat16*>(grad_hidden);
   P.grad_weight = static_cast<__nv_bfloat16*>(grad_weight);
-  int launches = 0;
-  const cudaError_t e = launch_ce_backward(P, current_sms(), reinterpret_cast<cudaStream_t>(stream), &launches);
+  int launches = 0, dev = 0;
+  const cudaError_t e = launch_ce_backward(P, current_sms(&dev), reinterpret_cast<cudaStream_t>(stream), &launches);
   g_launches += launches;
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -520,6 +520,8 @@ struct FiltParams {
 };
 cudaError_t launch_filter(const FiltParams& P, int grid, cudaStream_t s);
 
+constexpr int kMaxDevices = 64;
+
 // Parameters of the teacher-record kernel (record.cu).
 struct RecordParams {
   const unsigned char* logits;   // [n, V]
@@ -530,7 +532,8 @@ struct RecordParams {
   float* tail_lse;               // [n]
   int32_t* status;               // [n] or null
 };
-cudaError_t launch_record(const RecordParams& P, int nsm, cudaStream_t s);
+cudaError_t launch_record(const RecordParams& P, int dev, int nsm, cudaStream_t s);
+cudaError_t configure_record(int dev);    // resident clusters of the current device `dev`
 
 // Parameters of the distillation kernel (distill.cu).
 constexpr int kDistillMaxV = SPEC_DISTILL_MAX_V;
@@ -549,8 +552,8 @@ struct DistillParams {
   unsigned char* grad;           // [n, V] or null
   int32_t* status;               // [n] or null
 };
-cudaError_t launch_distill(const DistillParams& P, int nsm, cudaStream_t s);
-cudaError_t configure_distill();   // dynamic shared-memory limit, current device
+cudaError_t launch_distill(const DistillParams& P, int dev, int nsm, cudaStream_t s);
+cudaError_t configure_distill(int dev);   // dynamic shared-memory limit and resident clusters, current device `dev`
 
 // Parameters of the linear cross entropy (linear_ce.cu).
 struct CeParams {

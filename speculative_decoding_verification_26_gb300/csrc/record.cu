@@ -319,10 +319,12 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
   }
 }
 
+int g_clusters[kMaxDevices][2][4];           // resident at once, by device, dtype and log2 CS
+
 template <int DT, int CS>
-cudaError_t launch_as(const RecordParams& P, int nsm, cudaStream_t s) {
+cudaError_t launch_as(const RecordParams& P, int dev, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  const int most = 2 * nsm / CS;             // clusters resident at once, two CTAs per SM
+  const int most = g_clusters[dev][DT == SPEC_BF16][log2_of(CS)];
   cfg.gridDim = dim3((P.n < most ? P.n : most) * CS);
   cfg.blockDim = dim3(kRecThreads);
   cfg.stream = s;
@@ -335,18 +337,33 @@ cudaError_t launch_as(const RecordParams& P, int nsm, cudaStream_t s) {
 }
 
 template <int DT>
-cudaError_t launch_of(const RecordParams& P, int nsm, cudaStream_t s) {
+cudaError_t launch_of(const RecordParams& P, int dev, int nsm, cudaStream_t s) {
   const int cs = row_cluster(P.n, P.V, RowType<DT>::ES, nsm);
-  if (cs == 8) return launch_as<DT, 8>(P, nsm, s);
-  if (cs == 4) return launch_as<DT, 4>(P, nsm, s);
-  if (cs == 2) return launch_as<DT, 2>(P, nsm, s);
-  return launch_as<DT, 1>(P, nsm, s);
+  if (cs == 8) return launch_as<DT, 8>(P, dev, s);
+  if (cs == 4) return launch_as<DT, 4>(P, dev, s);
+  if (cs == 2) return launch_as<DT, 2>(P, dev, s);
+  return launch_as<DT, 1>(P, dev, s);
+}
+
+template <int DT>
+cudaError_t configure_as(int dev) {
+  int* g = g_clusters[dev][DT == SPEC_BF16];
+  cudaError_t e = resident_clusters(record_kernel<DT, 1>, 1, kRecThreads, 0, &g[0]);
+  if (e == cudaSuccess) e = resident_clusters(record_kernel<DT, 2>, 2, kRecThreads, 0, &g[1]);
+  if (e == cudaSuccess) e = resident_clusters(record_kernel<DT, 4>, 4, kRecThreads, 0, &g[2]);
+  if (e == cudaSuccess) e = resident_clusters(record_kernel<DT, 8>, 8, kRecThreads, 0, &g[3]);
+  return e;
 }
 
 }  // namespace
 
-cudaError_t launch_record(const RecordParams& P, int nsm, cudaStream_t s) {
-  return P.dtype == SPEC_BF16 ? launch_of<SPEC_BF16>(P, nsm, s) : launch_of<SPEC_F32>(P, nsm, s);
+cudaError_t launch_record(const RecordParams& P, int dev, int nsm, cudaStream_t s) {
+  return P.dtype == SPEC_BF16 ? launch_of<SPEC_BF16>(P, dev, nsm, s) : launch_of<SPEC_F32>(P, dev, nsm, s);
+}
+
+cudaError_t configure_record(int dev) {
+  const cudaError_t e = configure_as<SPEC_BF16>(dev);
+  return e == cudaSuccess ? configure_as<SPEC_F32>(dev) : e;
 }
 
 }  // namespace sv

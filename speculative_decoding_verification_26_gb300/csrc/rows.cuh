@@ -94,6 +94,24 @@ __device__ __forceinline__ float vec_max(const uint4& w) {
   }
 }
 
+// The largest logit of several vectors, NaNs left out.
+template <int DT, int N>
+__device__ __forceinline__ float vecs_max(const uint4 (&w)[N]) {
+  if constexpr (DT == SPEC_BF16) {
+    uint32_t m[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) m[u] = max_bf2(max_bf2(w[u].x, w[u].y), max_bf2(w[u].z, w[u].w));
+#pragma unroll
+    for (int u = 1; u < N; ++u) m[0] = max_bf2(m[0], m[u]);
+    return fmaxf(bf16_lo(m[0]), bf16_hi(m[0]));
+  } else {
+    float m = vec_max<DT>(w[0]);
+#pragma unroll
+    for (int u = 1; u < N; ++u) m = fmaxf(m, vec_max<DT>(w[u]));
+    return m;
+  }
+}
+
 // A CTA's share of a row that a cluster of CS CTAs reads: vectors [lo, hi), and
 // both ends' single elements by the first.
 struct RowShare {
@@ -113,6 +131,27 @@ inline int row_cluster(int n, int V, int es, int nsm) {
   for (int cs = 8; cs > 1; cs /= 2)
     if ((long long)n * cs <= 2 * nsm && (long long)V * es >= cs * 16384ll) return cs;
   return 1;
+}
+
+inline int log2_of(int cs) { return cs == 8 ? 3 : cs == 4 ? 2 : cs == 2 ? 1 : 0; }
+
+// Clusters of `cs` CTAs of a kernel that the current device holds at once: fewer
+// than its SMs allow, where the SMs of a GPC do not divide by cs.  A persistent
+// grid of more would leave whole clusters for a second wave.
+template <class K>
+inline cudaError_t resident_clusters(K kernel, int cs, int threads, size_t smem, int* out) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1024 * cs);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)cs, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaOccupancyMaxActiveClusters(out, kernel, &cfg);
+  if (e == cudaSuccess && *out < 1) *out = 1;
+  return e;
 }
 
 // Calls fv(j, w) for each vector j of this thread (w its 16 bytes) and fe(e, x)
@@ -164,6 +203,51 @@ __device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+
+// 16 bytes to the same shared address of CTA `rank` of the cluster, counted there
+// on a barrier: no fence on this side, the barrier's phase orders them for the reader.
+__device__ __forceinline__ void send16(const void* at, const uint64_t* bar, uint32_t rank, uint32_t a, uint32_t b,
+                                       uint32_t c, uint32_t d) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(
+                   map_rank(smem_u32(at), rank)),
+               "r"(map_rank(smem_u32(bar), rank)), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// A wait for a phase of a barrier gives up after about 2 s, which no healthy
+// call comes near, or once another role of the CTA has (*failed).  The thread
+// sleeps in hardware in between (a polling warp takes issue slots from the
+// others).  A CTA with a failed wait lets kDrainCycles (~1 ms) pass before it
+// ends, for the copies still in flight.
+constexpr long long kDrainCycles = 2000000ll;
+constexpr uint32_t kSleepNs = 100000;
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+  uint32_t ok;
+  long long t0 = 0;
+  for (;;) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepNs)
+        : "memory");
+    if (ok) return true;
+    const long long t = clock64();
+    if (t0 == 0) t0 = t;
+    if (*failed || t - t0 > kWaitLimitCycles) {
+      *failed = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void drain_after_failure() {
+  const long long t0 = clock64();
+  while (clock64() - t0 < kDrainCycles) {}
 }
 
 // Sum over the CTA, the same bits in every thread; `scratch` holds WARPS values

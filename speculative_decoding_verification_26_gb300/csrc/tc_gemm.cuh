@@ -27,9 +27,6 @@ constexpr int kTcStage = 2 * kTcOperand;
 constexpr int kTcThreads = 192;
 constexpr int kTcProducer = 4, kTcIssuer = 5;            // warps
 constexpr uint32_t kTcColumns = 512;
-// A wait gives up after about 2 s; no healthy call comes near.  After one the
-// CTA waits kTcDrain cycles (~1 ms) for the copies and products still in flight.
-constexpr long long kTcWaitCycles = 4000000000ll, kTcDrain = 2000000ll;
 
 struct TcShared {
   uint64_t full[kTcStages], empty[kTcStages], done[2], drained[2];
@@ -37,33 +34,6 @@ struct TcShared {
   int failed;
 };
 constexpr size_t kTcSmem = kTcStages * (size_t)kTcStage + 1024 + sizeof(TcShared);
-
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
-// Waits for a phase, at most kTcWaitCycles; also gives up when another role of
-// this CTA has.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
-  uint32_t ok;
-  long long t0 = 0;
-  for (int spin = 0;; ++spin) {
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if ((spin & 63) == 63) {
-      const long long t = clock64();
-      if (t0 == 0) t0 = t;
-      if (*failed || t - t0 > kTcWaitCycles) {
-        *failed = 1;
-        return false;
-      }
-    }
-  }
-}
 
 // One box of a 2-D tensor map into this CTA's shared memory, counted on a
 // barrier of either CTA of the pair.  x is a multiple of 8 elements (16 bytes).
@@ -187,7 +157,7 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
         const TcTile tile = work.tile(t);
         for (int k = 0; k < tile.steps; ++k, ++it) {
           const int st = it % kTcStages;
-          if (!(ok = tc_wait(&S.empty[st], ((it / kTcStages) & 1) ^ 1, failed))) break;
+          if (!(ok = bounded_wait(&S.empty[st], ((it / kTcStages) & 1) ^ 1, failed))) break;
           const uint32_t bar = map_rank(smem_u32(&S.full[st]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&S.full[st], 2 * kTcStage);   // both CTAs' halves
           const uint32_t at = base + st * kTcStage;
@@ -204,13 +174,13 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
         const TcTile tile = work.tile(t);
         if (tile.steps == 0) continue;
         const int buf = n & 1;
-        if (!(ok = tc_wait(&S.drained[buf], ((n >> 1) & 1) ^ 1, failed))) break;
+        if (!(ok = bounded_wait(&S.drained[buf], ((n >> 1) & 1) ^ 1, failed))) break;
         tc_fence_after();
         const uint32_t idesc = tc_idesc(tile.a.k_inner, tile.b.k_inner), d = tmem + buf * kTcTile;
         const uint32_t sa = tile.a.k_inner ? 32 >> 4 : 2048 >> 4, sb = tile.b.k_inner ? 32 >> 4 : 2048 >> 4;
         for (int k = 0; k < tile.steps; ++k, ++it) {
           const int st = it % kTcStages;
-          if (!(ok = tc_wait(&S.full[st], (it / kTcStages) & 1, failed))) break;
+          if (!(ok = bounded_wait(&S.full[st], (it / kTcStages) & 1, failed))) break;
           tc_fence_after();
           const uint64_t da = tc_desc(base + st * kTcStage, tile.a.k_inner);
           const uint64_t db = tc_desc(base + st * kTcStage + kTcOperand, tile.b.k_inner);
@@ -230,7 +200,7 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
       const int steps = work.tile(t).steps;
       const int buf = n & 1;
       if (steps > 0) {
-        const bool ok = tc_wait(&S.done[buf], (n >> 1) & 1, failed);
+        const bool ok = bounded_wait(&S.done[buf], (n >> 1) & 1, failed);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
       }
@@ -245,8 +215,7 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
   }
   __syncwarp();
   if (__any_sync(0xffffffffu, *failed)) {    // copies or products may still be in flight
-    const long long t0 = clock64();
-    while (clock64() - t0 < kTcDrain) {}
+    drain_after_failure();
     if (lane == 0) *error = 1;
   }
   __syncwarp();

@@ -31,7 +31,7 @@ RECORD = dict(logits=FAKE, dtype=1, n=4, V=1024, K=8, temperature=None, top=FAKE
 
 
 @pytest.mark.parametrize("change", [
-    {"logits": None}, {"logits": ODD}, {"dtype": 2}, {"n": 0}, {"V": 1}, {"V": 1 << 28}, {"K": 0}, {"K": 257},
+    {"logits": None}, {"logits": ODD}, {"dtype": 2}, {"n": 0}, {"n": (1 << 30) + 1}, {"V": 1}, {"V": 1 << 28}, {"K": 0}, {"K": 257},
     {"V": 7}, {"top": None}, {"idx": None}, {"tail": None}, {"tail": ODD}, {"temperature": ODD}, {"status": ODD}])
 def test_record_refusals(L, change):
     assert L.spec_topk_logits(*bad(RECORD, **change)) == 1
@@ -42,7 +42,7 @@ DISTILL = dict(logits=FAKE, dtype=1, n=4, V=1024, K=8, top=FAKE, idx=FAKE, tail=
 
 
 @pytest.mark.parametrize("change", [
-    {"logits": None}, {"logits": ODD}, {"dtype": 2}, {"n": 0}, {"V": 1}, {"V": (1 << 20) + 1}, {"K": 0}, {"K": 257},
+    {"logits": None}, {"logits": ODD}, {"dtype": 2}, {"n": 0}, {"n": (1 << 30) + 1}, {"V": 1}, {"V": (1 << 20) + 1}, {"K": 0}, {"K": 257},
     {"top": None}, {"idx": None}, {"loss": None}, {"label": ODD}, {"parts": ODD}, {"grad": ODD},
     {"kl": float("nan")}, {"tv": float("inf")}, {"ce": float("nan")},
     {"grad": P(0x7f0000000000 + 2 * 1024)}, {"grad": P(0x7f0000000000 - 2)}])
@@ -55,6 +55,7 @@ FWD = dict(hidden=FAKE, weight=FAKE, dtype=1, n=4, H=64, V=1000, label=FAKE, los
 BWD = dict(hidden=FAKE, weight=FAKE, dtype=1, n=4, H=64, V=1000, label=FAKE, lse=FAKE, g=None, gh=FAKE, gw=FAKE,
            ws=FAKE, size=1 << 30, stream=None)
 EITHER = [({"hidden": None}, 1), ({"weight": None}, 1), ({"dtype": 0}, 1), ({"n": 0}, 1), ({"n": (1 << 20) + 1}, 1),
+          ({"n": 1 << 20, "V": (1 << 28) - 1}, 1),
           ({"H": 0}, 1), ({"H": 65544}, 1), ({"H": 60}, 1), ({"V": 1}, 1), ({"V": 1 << 28}, 1), ({"label": None}, 1),
           ({"lse": None}, 1), ({"hidden": P(0x7f0000000008)}, 1), ({"weight": P(0x7f0000000008)}, 1),
           ({"ws": None}, 2), ({"size": 1024}, 2), ({"ws": P(0x7f0000000010)}, 1)]
