@@ -282,7 +282,7 @@ int spec_gamma_select(const float* signals, const float* comp, const float* mode
  *   top_logits [n, K] fp32, top_index [n, K] int32: the K largest logits, the
  *     largest first, equal values (-0 and +0 among them) by ascending token;
  *   tail_lse   [n] fp32: ln sum e^{x_v / T} over the tokens not recorded, -inf
- *     when they have no mass.
+ *     when they have no mass (weights below 2^-126 of the row's largest are 0).
  * A logit of -inf is not recorded: a row with fewer than K others (a filtered
  * row) ends with entries of logit -inf and index -1.
  *   K           1 <= K <= min(V, SPEC_MAX_TOPK);

@@ -490,9 +490,10 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
           unsigned char* mine = s_ring + (size_t)at.stage * kDisStage + 16 * tid;
           const uint4* vec = reinterpret_cast<const uint4*>(mine);
           const int left = sh.hi - j - tid;
-          // the marked logits become -inf in this thread's own vectors, so that the sums
+          // The marked logits become -inf in this thread's own vectors, so that the sums
           // below are straight code; the next copy into the stage comes after these
-          // stores by the proxy fence
+          // stores by the proxy fence.  (Masking the loaded registers costs more:
+          // 91 us against 82 for 2048 x 128256.)
           uint32_t mark = map[word];
           if (mark != 0) {
             do {

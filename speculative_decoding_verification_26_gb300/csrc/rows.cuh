@@ -112,6 +112,52 @@ __device__ __forceinline__ float vecs_max(const uint4 (&w)[N]) {
   }
 }
 
+template <int DT>
+__device__ __forceinline__ uint4 minus_infinity() {
+  const uint32_t v = DT == SPEC_BF16 ? 0xFF80FF80u : 0xFF800000u;
+  return make_uint4(v, v, v, v);
+}
+// Marks (bit u PER + k) of the logits of vectors that are at least `least` (of a
+// bf16 row: a bf16 value).
+template <int DT, int N>
+__device__ __forceinline__ uint32_t mark_from(const uint4 (&w)[N], float least) {
+  uint32_t mark = 0;
+  const __nv_bfloat162 bar = __float2bfloat162_rn(least);
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    const uint32_t word[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == SPEC_BF16) {
+        __nv_bfloat162 x;
+        memcpy(&x, &word[i], 4);
+        const uint32_t ge = __hge2_mask(x, bar);             // 0xFFFF per half
+        mark |= ((ge & 1u) | (ge >> 31 << 1)) << (8 * u + 2 * i);
+      } else {
+        if (__uint_as_float(word[i]) >= least) mark |= 1u << (4 * u + i);
+      }
+    }
+  }
+  return mark;
+}
+// Vectors whose marked logits (bit u PER + k) become -inf.
+template <int DT, int N>
+__device__ __forceinline__ void drop_marked(uint4 (&w)[N], uint32_t mark) {
+#pragma unroll
+  for (int u = 0; u < N; ++u) {
+    uint32_t* word[4] = {&w[u].x, &w[u].y, &w[u].z, &w[u].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (DT == SPEC_BF16) {
+        const uint32_t two = mark >> (8 * u + 2 * i) & 3u, cover = (two & 1u) * 0xFFFFu | (two >> 1) * 0xFFFF0000u;
+        *word[i] = (*word[i] & ~cover) | (0xFF80FF80u & cover);
+      } else {
+        if (mark >> (4 * u + i) & 1u) *word[i] = 0xFF800000u;
+      }
+    }
+  }
+}
+
 // A CTA's share of a row that a cluster of CS CTAs reads: vectors [lo, hi), and
 // both ends' single elements by the first.
 struct RowShare {
@@ -216,6 +262,13 @@ __device__ __forceinline__ void send16(const void* at, const uint64_t* bar, uint
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.b32 [%0], {%2, %3, %4, %5}, [%1];" ::"r"(
                    map_rank(smem_u32(at), rank)),
                "r"(map_rank(smem_u32(bar), rank)), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+// 8 bytes to a shared address of the cluster, counted on a barrier of the same CTA.
+__device__ __forceinline__ void send8(uint32_t addr, uint32_t bar, unsigned long long v) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b64 [%0], %2, [%1];" ::"r"(addr), "r"(bar),
+               "l"(v)
                : "memory");
 }
 

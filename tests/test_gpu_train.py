@@ -65,6 +65,9 @@ def check_record(sv, x, K, T, dev_x=None):
     assert torch.equal(r["top_index"].cpu().long(), idx.long())
     assert torch.equal(r["top_logits"].cpu().double(), top)
     got = r["tail_lse"].cpu().double()
+    # a weight beside the row's largest logit below 2^-126 is 0 in fp32 (e^-87.3 = 2^-126): a
+    # rest whose whole mass is below that has none, and its tail is -inf
+    tail = torch.where(tail - top[:, 0] / T.double() < -87.3, -INF, tail)
     fin = torch.isfinite(tail)
     assert torch.equal(torch.isfinite(got), fin) and torch.equal(got[~fin], tail[~fin])
     assert ((got - tail)[fin].abs() <= TOL + 3e-7 * tail[fin].abs()).all(), (got - tail)[fin].abs().max()
@@ -98,6 +101,30 @@ def test_record_ties_and_filtered_rows(sv, dtype):
     x[8] = torch.arange(V, dtype=torch.float32).to(dtype) * 0.001
     x[5] = torch.clamp(x[5].float(), max=0.0).to(dtype)
     check_record(sv, x, K, torch.linspace(0.5, 2.0, 9))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V", [(3, 4000), (2, 70001), (350, 9000)])
+def test_record_masks_of_finite_values(sv, n, V, dtype):
+    """Rows masked with the type's lowest value, with zeros, or by clamping; large
+    values in one period of positions; sorted rows."""
+    K = 40
+    x = rows(n, V, dtype, 31)
+    low = torch.finfo(dtype).min
+    g = gen(4)
+    x[0] = torch.where(torch.rand(V, generator=g) < 20.0 / V, x[0], torch.tensor(low, dtype=dtype))
+    x[1] = torch.where(torch.rand(V, generator=g) < 0.001, x[1].abs(), torch.tensor(0.0, dtype=dtype))
+    if n > 2:
+        x[2] = low
+        x[2, V - 1] = 1.0
+    if n > 8:
+        x[3] = x[3].clamp(max=-2.0)
+        x[4] = x[4].sort().values
+        x[5] = x[5].sort(descending=True).values
+        x[6] = (torch.arange(V) % 2048 < 8).to(dtype) * 9 + x[6] * 0.01
+        x[7] = (torch.arange(V) % 1000 < 300).to(dtype) * 9 + x[7] * 0.1
+        x[8] = -(torch.arange(V) % 3).to(dtype)
+    check_record(sv, x, K, torch.rand(n, generator=g) + 0.5)
 
 
 @pytest.mark.parametrize("shift", [1, 3, 5])
