@@ -24,10 +24,13 @@
 namespace sv {
 namespace {
 
-constexpr int kGatherThreads = 256, kGatherRows = 32;
+constexpr int kGatherThreads = 256;
+// Rows of a CTA: one per warp; 64 past 32768 rows, where each CTA's pass over all
+// labels would cost more than the copies.
+constexpr int kGatherFew = 8, kGatherMany = 64;
 
 // The rows that count, in order: row_of, their labels, and their hidden states.
-template <bool BWD>
+template <bool BWD, int kGatherRows>
 __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_constant__ CeParams P) {
   __shared__ int s_before[kGatherThreads / 32], s_all[kGatherThreads / 32];
   __shared__ int s_row[kGatherRows];
@@ -57,27 +60,30 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
   all = 0;
   for (int w = 0; w < kGatherThreads / 32; ++w) { before += s_before[w]; all += s_all[w]; }
   if (warp == 0) {
-    const int r = r0 + lane;
-    const bool v = r < P.n && counts(r);
-    const unsigned vote = __ballot_sync(0xffffffffu, v);
-    const int at = before + __popc(vote & ((1u << lane) - 1));
-    s_row[lane] = v ? at : -1;
-    if (v) {
-      const int y = P.label[r];
-      P.row_of[at] = r;
-      P.lab[at] = y;
-      if (BWD) {
-        P.lse_c[at] = P.lse_in[r];
-        P.g_c[at] = P.grad_loss ? P.grad_loss[r] : 1.f;
+    for (int i0 = 0, base = before; i0 < kGatherRows; i0 += 32) {
+      const int i = i0 + lane, r = r0 + i;
+      const bool v = i < kGatherRows && r < P.n && counts(r);
+      const unsigned vote = __ballot_sync(0xffffffffu, v);
+      const int at = base + __popc(vote & ((1u << lane) - 1));
+      base += __popc(vote);
+      if (i < kGatherRows) s_row[i] = v ? at : -1;
+      if (v) {
+        P.row_of[at] = r;
+        P.lab[at] = P.label[r];
+        if (BWD) {
+          P.lse_c[at] = P.lse_in[r];
+          P.g_c[at] = P.grad_loss ? P.grad_loss[r] : 1.f;
+        }
       }
-    }
-    if (BWD && r < P.n) P.pos_of[r] = v ? at : -1;
-    if (!BWD && r < P.n && !v) {
-      const int y = P.label[r];
-      const float z = y == -1 ? 0.f : __int_as_float(0x7fc00000);
-      P.loss[r] = z;
-      P.lse[r] = z;
-      if (P.status) P.status[r] = y == -1 ? SPEC_ST_OK : SPEC_ST_BAD_TOKEN;
+      if (i >= kGatherRows || r >= P.n) continue;
+      if (BWD) P.pos_of[r] = v ? at : -1;
+      if (!BWD && !v) {
+        const int y = P.label[r];
+        const float z = y == -1 ? 0.f : __int_as_float(0x7fc00000);
+        P.loss[r] = z;
+        P.lse[r] = z;
+        if (P.status) P.status[r] = y == -1 ? SPEC_ST_OK : SPEC_ST_BAD_TOKEN;
+      }
     }
     if (blockIdx.x == 0 && lane == 0) { P.count[0] = all; P.count[1] = 0; }
   }
@@ -87,12 +93,17 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
     if (s_row[i] >= 0) {
       const uint4* src = reinterpret_cast<const uint4*>(P.hidden + (size_t)(r0 + i) * P.H);
       uint4* dst = reinterpret_cast<uint4*>(P.rows + (size_t)s_row[i] * P.H);
+#pragma unroll 8
       for (int k = lane; k < nv; k += 32) dst[k] = src[k];
     }
-    const int at = r0 + i;                   // places past the last row that counts
+    // places past the last row that counts: dW sums over whole stages of rows, and a
+    // stage's last rows are zero; what lies behind them only reaches rows of its own
+    const int at = r0 + i;
     if (at >= all) {
-      uint4* dst = reinterpret_cast<uint4*>(P.rows + (size_t)at * P.H);
-      for (int k = lane; k < nv; k += 32) dst[k] = make_uint4(0, 0, 0, 0);
+      if (BWD && at < (all + kTcK - 1) / kTcK * kTcK) {
+        uint4* dst = reinterpret_cast<uint4*>(P.rows + (size_t)at * P.H);
+        for (int k = lane; k < nv; k += 32) dst[k] = make_uint4(0, 0, 0, 0);
+      }
       if (lane == 0) {
         P.lab[at] = -1;
         if (BWD) { P.lse_c[at] = 0.f; P.g_c[at] = 0.f; }
@@ -107,6 +118,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
 struct CeMaps {
   // k inner: boxes of 64 k x 128 rows; k outer: 64 columns x 64 k
   CUtensorMap rows, weight, soft, rows_t, weight_t, soft_t;
+  CUtensorMap soft_out, grad_weight;         // stores: boxes of 64 columns x 32 rows
 };
 
 // Tiles of logits: rows x vocabulary.  Groups of kGroup row tiles (4096 rows),
@@ -115,7 +127,11 @@ struct CeMaps {
 // from HBM once a group.
 constexpr int kGroup = 16;
 struct LogitTiles {
-  int row_tiles, vocab_tiles;
+  int row_tiles, vocab_tiles, rows;          // rows that count
+  __device__ __forceinline__ int index(int l, int pair, int pairs) const {
+    const int t = pair + l * pairs;
+    return t < row_tiles * vocab_tiles ? t : -1;
+  }
   __device__ __forceinline__ void at(int t, int& mb, int& vt) const {
     const int per = kGroup * vocab_tiles, g = t / per, first = g * kGroup;
     const int size = row_tiles - first < kGroup ? row_tiles - first : kGroup;
@@ -132,20 +148,22 @@ struct ForwardWork {
   const CeParams& P;
   const CeMaps& M;
   LogitTiles lt;
-  __device__ __forceinline__ int count() const { return lt.row_tiles * lt.vocab_tiles; }
+  __device__ __forceinline__ int index(int l, int pair, int pairs) const { return lt.index(l, pair, pairs); }
   __device__ __forceinline__ TcTile tile(int t) const {
     int mb, vt;
     lt.at(t, mb, vt);
     return {{&M.rows, true, mb * kTcTile, 0}, {&M.weight, true, vt * kTcTile, 0}, (P.H + kTcK - 1) / kTcK};
   }
-  __device__ __forceinline__ void epilogue(int t, int row, uint32_t tmem, bool) const {
+  __device__ __forceinline__ void epilogue(int t, TcHalfRow& e) const {
     int mb, vt;
     lt.at(t, mb, vt);
-    const int i = mb * kTcTile + row, v0 = vt * kTcTile, at = P.lab[i] - v0;   // the label's column
+    const int i = mb * kTcTile + e.row, v0 = vt * kTcTile + e.col;
+    if (i - (int)(threadIdx.x & 31) >= lt.rows) return;      // none of the warp's rows counts
+    const int at = P.lab[i] - v0;            // the label's column
     float m = -INFINITY, s = 0.f;
-    for (int c0 = 0; c0 < kTcTile; c0 += 32) {
+    for (int c0 = 0; c0 < kTcHalf; c0 += 32) {
       float x[32];
-      tc_load32(x, tmem + c0);
+      tc_load32(x, e.tmem + c0);
       if (at >= c0 && at < c0 + 32) {
         float z = 0.f;
 #pragma unroll
@@ -166,7 +184,7 @@ struct ForwardWork {
         s *= ex2((m - top) * kLog2eHi);
         m = top;
       }
-      const float ref = -m * kLog2eHi;
+      const float ref = m == -INFINITY ? 0.f : -m * kLog2eHi;          // a half past the vocabulary: weights of 0
       float a = 0.f, b = 0.f;
 #pragma unroll
       for (int c = 0; c < 32; c += 2) {
@@ -175,7 +193,11 @@ struct ForwardWork {
       }
       s += a + b;
     }
-    P.part[(size_t)vt * P.n_pad + i] = make_float2(m, s);
+    const float2 other = e.join(make_float2(m, s));
+    if (e.col != 0) return;
+    const float top = fmaxf(m, other.x);     // a NaN sum stays
+    s = s * ex2((m - top) * kLog2eHi) + (other.x == -INFINITY ? other.y : other.y * ex2((other.x - top) * kLog2eHi));
+    P.part[(size_t)vt * P.n_pad + i] = make_float2(top, s);
   }
 };
 
@@ -196,40 +218,71 @@ struct SoftWork {
   const CeMaps& M;
   LogitTiles lt;
   int v_begin;
-  __device__ __forceinline__ int count() const { return lt.row_tiles * lt.vocab_tiles; }
+  __device__ __forceinline__ int index(int l, int pair, int pairs) const { return lt.index(l, pair, pairs); }
   __device__ __forceinline__ TcTile tile(int t) const {
     int mb, vt;
     lt.at(t, mb, vt);
     return {{&M.rows, true, mb * kTcTile, 0}, {&M.weight, true, v_begin + vt * kTcTile, 0}, (P.H + kTcK - 1) / kTcK};
   }
-  __device__ __forceinline__ void epilogue(int t, int row, uint32_t tmem, bool) const {
+  __device__ __forceinline__ void epilogue(int t, TcHalfRow& e) const {
     int mb, vt;
     lt.at(t, mb, vt);
-    const int i = mb * kTcTile + row, v0 = v_begin + vt * kTcTile, at = P.lab[i] - v0;
+    const int i = mb * kTcTile + e.row, first = i - (int)(threadIdx.x & 31), v0 = v_begin + vt * kTcTile + e.col;
+    // a stage's last rows are zero (G sums over rows in whole stages); later ones are not read
+    if (first >= (lt.rows + kTcK - 1) / kTcK * kTcK) return;
+    const int at = P.lab[i] - v0;
     const float g = P.g_c[i], ref = -P.lse_c[i] * kLog2eHi;
-    __nv_bfloat16* out = P.soft + (size_t)i * P.piece + vt * kTcTile;
-    for (int c0 = 0; c0 < kTcTile; c0 += 32) {
-      float x[32];
-      tc_load32(x, tmem + c0);
-      const int left = P.V - v0 - c0;
+    for (int c0 = 0; c0 < kTcHalf; c0 += 64) {
+      uint4 out[8];
 #pragma unroll
-      for (int c = 0; c < 32; ++c) {
-        x[c] = ex2(fmaf(x[c], kLog2eHi, ref)) - (c0 + c == at ? 1.f : 0.f);
-        x[c] = c < left && g != 0.f ? x[c] * g : 0.f;   // also past the last row that counts
+      for (int h = 0; h < 2; ++h) {
+        float x[32];
+        tc_load32(x, e.tmem + c0 + 32 * h);
+        const int left = P.V - v0 - c0 - 32 * h, mark = at - c0 - 32 * h;
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          x[c] = ex2(fmaf(x[c], kLog2eHi, ref)) - (c == mark ? 1.f : 0.f);
+          x[c] = c < left && g != 0.f ? x[c] * g : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) out[4 * h + c] = pack8(x + 8 * c);
       }
-#pragma unroll
-      for (int c = 0; c < 32; c += 8) *reinterpret_cast<uint4*>(out + c0 + c) = pack8(x + c);
+      e.store.put(&M.soft_out, vt * kTcTile + e.col + c0, first, out);
     }
   }
 };
+
+// Stages of k that a tile of dW takes at least: the time to write it.
+constexpr int kStoreSteps = 6;
 
 // backward: a piece's part of dh (k: the piece's vocabulary, in `splits` parts
 // of `per` stages) and its rows of dW (k: the rows that count)
 struct GradWork {
   const CeParams& P;
   const CeMaps& M;
-  int v_begin, len, row_tiles, col_tiles, steps_x, steps_w, hidden_tiles, weight_tiles;
-  __device__ __forceinline__ int count() const { return hidden_tiles + weight_tiles; }
+  int v_begin, rows, row_tiles, col_tiles, steps_x, steps_w, hidden_tiles, weight_tiles;
+  // The long tiles of dh first, round robin.  Pairs that have one less of them take
+  // `lead` tiles of dW in its place before the others join: a pair's tiles of dh are
+  // few (120 for 4096 rows), and one more is a third of its work.
+  __device__ __forceinline__ int index(int l, int pair, int pairs) const {
+    const int more = hidden_tiles % pairs, own = hidden_tiles / pairs + (pair < more);
+    if (l < own) return pair + l * pairs;
+    l -= own;
+    const int light = pairs - more;
+    int lead = 0;
+    if (more != 0 && steps_w > 0) {
+      const int w = steps_w > kStoreSteps ? steps_w : kStoreSteps;
+      lead = (P.split_steps + w / 2) / w;
+      if (lead > weight_tiles / light) lead = weight_tiles / light;
+    }
+    int t;
+    if (pair >= more) {
+      t = l < lead ? l * light + (pair - more) : lead * light + (l - lead) * pairs + pair;
+    } else {
+      t = lead * light + l * pairs + pair;
+    }
+    return t < weight_tiles ? hidden_tiles + t : -1;
+  }
   __device__ __forceinline__ void hidden_at(int t, int& mb, int& nb, int& sp) const {
     nb = t % col_tiles;
     mb = t / col_tiles % row_tiles;
@@ -248,23 +301,26 @@ struct GradWork {
     const int vb = t / col_tiles, nb = t % col_tiles;
     return {{&M.soft_t, false, vb * kTcTile, 0}, {&M.rows_t, false, nb * kTcTile, 0}, steps_w};
   }
-  __device__ __forceinline__ void epilogue(int t, int row, uint32_t tmem, bool any) const {
+  __device__ __forceinline__ void epilogue(int t, TcHalfRow& e) const {
+    const int lane = threadIdx.x & 31;
     if (t < hidden_tiles) {
       int mb, nb, sp;
       hidden_at(t, mb, nb, sp);
-      const int i = mb * kTcTile + row;
-      float* out = P.acc + ((size_t)sp * P.n_pad + i) * P.H + nb * kTcTile;
-      for (int c0 = 0; c0 < kTcTile && nb * kTcTile + c0 < P.H; c0 += 32) {
+      const int i = mb * kTcTile + e.row, j0 = nb * kTcTile + e.col;
+      if (i - lane >= rows) return;          // none of the warp's rows counts
+      float* out = P.acc + ((size_t)sp * P.n_pad + i) * P.H + j0;
+      for (int c0 = 0; c0 < kTcHalf && j0 + c0 < P.H; c0 += 32) {
         float x[32];
-        if (any) {
-          tc_load32(x, tmem + c0);
+        if (e.any) {
+          tc_load32(x, e.tmem + c0);
         } else {
 #pragma unroll
           for (int c = 0; c < 32; ++c) x[c] = 0.f;
         }
+        if (i >= rows) continue;
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
-          if (nb * kTcTile + c0 + c >= P.H) break;         // H is a multiple of 8
+          if (j0 + c0 + c >= P.H) break;     // H is a multiple of 8
           float4* at = reinterpret_cast<float4*>(out + c0 + c);
           float4 v = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
           if (v_begin != 0) {
@@ -277,27 +333,31 @@ struct GradWork {
       return;
     }
     t -= hidden_tiles;
-    const int vb = t / col_tiles, nb = t % col_tiles, v = v_begin + vb * kTcTile + row;
-    __nv_bfloat16* out = P.grad_weight + (size_t)v * P.H + nb * kTcTile;
-    for (int c0 = 0; c0 < kTcTile && nb * kTcTile + c0 < P.H; c0 += 32) {
-      float x[32];
-      if (any) {
-        tc_load32(x, tmem + c0);
-      } else {
+    const int vb = t / col_tiles, nb = t % col_tiles, first = v_begin + vb * kTcTile + e.row - lane;
+    const int j0 = nb * kTcTile + e.col;
+    if (first >= P.V) return;
+    for (int c0 = 0; c0 < kTcHalf && j0 + c0 < P.H; c0 += 64) {
+      uint4 out[8];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) x[c] = 0.f;
+      for (int h = 0; h < 2; ++h) {
+        if (e.any) {
+          float x[32];
+          tc_load32(x, e.tmem + c0 + 32 * h);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) out[4 * h + c] = pack8(x + 8 * c);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) out[4 * h + c] = make_uint4(0, 0, 0, 0);
+        }
       }
-      if (v >= P.V) continue;
-#pragma unroll
-      for (int c = 0; c < 32; c += 8)
-        if (nb * kTcTile + c0 + c < P.H) *reinterpret_cast<uint4*>(out + c0 + c) = pack8(x + c);
+      e.store.put(&M.grad_weight, j0 + c0, first, out);
     }
   }
 };
 
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     ce_forward(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M) {
-  const LogitTiles lt{(*P.count + kTcTile - 1) / kTcTile, (P.V + kTcTile - 1) / kTcTile};
+  const LogitTiles lt{(*P.count + kTcTile - 1) / kTcTile, (P.V + kTcTile - 1) / kTcTile, *P.count};
   tc_run(ForwardWork{P, M, lt}, P.count + 1);
 }
 
@@ -306,7 +366,8 @@ __device__ __forceinline__ int piece_len(const CeParams& P, int v_begin) {
 }
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     ce_softmax(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
-  const LogitTiles lt{(*P.count + kTcTile - 1) / kTcTile, (piece_len(P, v_begin) + kTcTile - 1) / kTcTile};
+  const LogitTiles lt{(*P.count + kTcTile - 1) / kTcTile, (piece_len(P, v_begin) + kTcTile - 1) / kTcTile,
+                      *P.count};
   tc_run(SoftWork{P, M, lt, v_begin}, P.count + 1);
 }
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
@@ -315,13 +376,13 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
   const int rt = (count + kTcTile - 1) / kTcTile, ct = (P.H + kTcTile - 1) / kTcTile;
   const int ht = P.grad_hidden ? rt * ct * P.splits : 0;
   const int wt = P.grad_weight ? (len + kTcTile - 1) / kTcTile * ct : 0;
-  tc_run(GradWork{P, M, v_begin, len, rt, ct, (len + kTcK - 1) / kTcK, (count + kTcK - 1) / kTcK, ht, wt},
+  tc_run(GradWork{P, M, v_begin, count, rt, ct, (len + kTcK - 1) / kTcK, (count + kTcK - 1) / kTcK, ht, wt},
          P.count + 1);
 }
 
 // lse and loss of the rows that count: the tiles' maxima and sums, each warp a
 // share of the tiles of 32 rows
-constexpr int kMergeThreads = 512, kMergeWarps = kMergeThreads / 32;
+constexpr int kMergeThreads = 1024, kMergeWarps = kMergeThreads / 32;
 __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constant__ CeParams P) {
   __shared__ float2 s_part[kMergeWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
@@ -334,8 +395,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constan
     s = s * ex2((m - top) * kLog2eHi) + p.y * ex2((p.x - top) * kLog2eHi);
     m = top;
   };
-#pragma unroll 4
-  for (int t = warp; t < tiles; t += kMergeWarps) add(P.part[(size_t)t * P.n_pad + i]);
+  for (int t0 = warp; t0 < tiles; t0 += 8 * kMergeWarps) {
+    float2 p[8];                             // eight loads in flight
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int t = t0 + u * kMergeWarps;
+      p[u] = t < tiles ? P.part[(size_t)t * P.n_pad + i] : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u) add(p[u]);
+  }
   s_part[warp][lane] = make_float2(m, s);
   __syncthreads();
   if (warp != 0 || i >= *P.count) return;
@@ -358,17 +427,24 @@ __global__ void __launch_bounds__(256) finish_grads(const __grid_constant__ CePa
   if (failed && P.grad_weight)
     for (long long t = me; t < (long long)P.V * nv; t += all) reinterpret_cast<uint4*>(P.grad_weight)[t] = nans;
   if (!P.grad_hidden) return;
-  for (long long t = me; t < (long long)P.n * nv; t += all) {
-    const int r = (int)(t / nv), j = (int)(t % nv) * 8, pos = P.pos_of[r];
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (pos >= 0)
+  const int nq = P.H / 4;
+  for (long long t = me; t < (long long)P.n * nq; t += all) {
+    const int r = (int)(t / nq), j = (int)(t % nq) * 4, pos = P.pos_of[r];
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (pos >= 0) {
+      const float* a = P.acc + (size_t)pos * P.H + j;
+      const size_t stride = (size_t)P.n_pad * P.H;
+#pragma unroll 8
       for (int sp = 0; sp < P.splits; ++sp) {
-        const float4* a = reinterpret_cast<const float4*>(P.acc + ((size_t)sp * P.n_pad + pos) * P.H + j);
-        const float4 u = a[0], v = a[1];
-        x[0] += u.x; x[1] += u.y; x[2] += u.z; x[3] += u.w;
-        x[4] += v.x; x[5] += v.y; x[6] += v.z; x[7] += v.w;
+        const float4 u = *reinterpret_cast<const float4*>(a + sp * stride);
+        s.x += u.x; s.y += u.y; s.z += u.z; s.w += u.w;
       }
-    reinterpret_cast<uint4*>(P.grad_hidden)[t] = failed ? nans : pack8(x);
+    }
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(s.x, s.y), hi = __floats2bfloat162_rn(s.z, s.w);
+    uint2 o;
+    memcpy(&o.x, &lo, 4);
+    memcpy(&o.y, &hi, 4);
+    reinterpret_cast<uint2*>(P.grad_hidden)[t] = failed ? make_uint2(nans.x, nans.x) : o;
   }
 }
 
@@ -384,6 +460,12 @@ bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t height, ui
   return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, boxes, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool BWD>
+void launch_gather(const CeParams& P, cudaStream_t s) {
+  if (P.n <= 32768) gather_rows<BWD, kGatherFew><<<P.n_pad / kGatherFew, kGatherThreads, 0, s>>>(P);
+  else gather_rows<BWD, kGatherMany><<<P.n_pad / kGatherMany, kGatherThreads, 0, s>>>(P);
 }
 
 }  // namespace
@@ -407,7 +489,7 @@ cudaError_t launch_ce_forward(const CeParams& P, int nsm, cudaStream_t s, int* l
   memset(&M, 0, sizeof M);
   if (!encode(&M.rows, P.rows, P.H, P.n_pad, kTcHalf) || !encode(&M.weight, P.weight, P.H, P.V, kTcHalf))
     return cudaErrorInvalidValue;
-  gather_rows<false><<<P.n_pad / kGatherRows, kGatherThreads, 0, s>>>(P);
+  launch_gather<false>(P, s);
   ce_forward<<<nsm / 2 * 2, kTcThreads, kTcSmem, s>>>(P, M);
   merge_rows<<<P.n_pad / 32, kMergeThreads, 0, s>>>(P);
   *launches = 3;
@@ -419,9 +501,11 @@ cudaError_t launch_ce_backward(const CeParams& P, int nsm, cudaStream_t s, int* 
   memset(&M, 0, sizeof M);
   if (!encode(&M.rows, P.rows, P.H, P.n_pad, kTcHalf) || !encode(&M.weight, P.weight, P.H, P.V, kTcHalf) ||
       !encode(&M.soft, P.soft, P.piece, P.n_pad, kTcHalf) || !encode(&M.rows_t, P.rows, P.H, P.n_pad, kTcK) ||
-      !encode(&M.weight_t, P.weight, P.H, P.V, kTcK) || !encode(&M.soft_t, P.soft, P.piece, P.n_pad, kTcK))
+      !encode(&M.weight_t, P.weight, P.H, P.V, kTcK) || !encode(&M.soft_t, P.soft, P.piece, P.n_pad, kTcK) ||
+      !encode(&M.soft_out, P.soft, P.piece, P.n_pad, 32) ||
+      (P.grad_weight && !encode(&M.grad_weight, P.grad_weight, P.H, P.V, 32)))
     return cudaErrorInvalidValue;
-  gather_rows<true><<<P.n_pad / kGatherRows, kGatherThreads, 0, s>>>(P);
+  launch_gather<true>(P, s);
   int n = 2;
   for (long long v = 0; v < P.V; v += P.piece, n += 2) {
     ce_softmax<<<nsm / 2 * 2, kTcThreads, kTcSmem, s>>>(P, M, (int)v);
@@ -459,7 +543,8 @@ size_t ce_layout(CeParams& P, bool backward, void* base) {
   // make the former the longer chain, its k is split so that no tile has more than
   // about half of a pair's share of all stages (76 pairs)
   const long long rt = P.n_pad / kTcTile, ct = (P.H + kTcTile - 1) / kTcTile;
-  const long long steps_x = P.piece / kTcK, steps_w = (P.n + kTcK - 1) / kTcK;
+  const long long steps_x = P.piece / kTcK, rows_w = (P.n + kTcK - 1) / kTcK;
+  const long long steps_w = rows_w > kStoreSteps ? rows_w : kStoreSteps;
   const long long share = (rt * ct * steps_x + P.piece / kTcTile * ct * steps_w) / 76;
   long long most = share / 2 < 8 ? 8 : share / 2;
   if (most < (steps_x + 63) / 64) most = (steps_x + 63) / 64;

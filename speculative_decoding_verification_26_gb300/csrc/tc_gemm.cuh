@@ -8,7 +8,9 @@
 // the products of the next.  A 128 x 256 tile by one CTA would stage 48 KB for the same
 // products that the pair does with 32 KB per CTA: 96 bytes a clock per SM
 // from L2 against 64.
-// Warps: 0-3 epilogue (TMEM lanes 32 w .. 32 w + 31), 4 producer, 5 products.
+// Warps: 0-7 epilogue (TMEM lanes 32 (w % 4) on, columns 128 (w / 4) on), 8 producer,
+// 9 products.  With four epilogue warps a tile's epilogue takes longer than the products
+// of a tile of k up to about 1024.
 // Operands of bf16, sums of fp32.
 #pragma once
 
@@ -24,8 +26,9 @@ constexpr int kTcK = 64;                     // k per stage: 128 bytes of bf16, 
 constexpr int kTcStages = 6;
 constexpr int kTcOperand = kTcHalf * kTcK * 2;           // 16 KB
 constexpr int kTcStage = 2 * kTcOperand;
-constexpr int kTcThreads = 192;
-constexpr int kTcProducer = 4, kTcIssuer = 5;            // warps
+constexpr int kTcEpilogue = 8;                           // warps
+constexpr int kTcThreads = kTcEpilogue * 32 + 64;
+constexpr int kTcProducer = kTcEpilogue, kTcIssuer = kTcEpilogue + 1;
 constexpr uint32_t kTcColumns = 512;
 
 struct TcShared {
@@ -33,7 +36,10 @@ struct TcShared {
   uint32_t tmem;
   int failed;
 };
-constexpr size_t kTcSmem = kTcStages * (size_t)kTcStage + 1024 + sizeof(TcShared);
+constexpr int kTcBox = 32 * 128;                        // 32 rows of 64 bf16 on their way to memory
+constexpr int kTcStaging = kTcEpilogue * kTcBox;
+constexpr size_t kTcSmem = kTcStages * (size_t)kTcStage + kTcStaging + 1024 + sizeof(TcShared);
+static_assert(kTcSmem <= 232448, "shared memory of a CTA");
 
 // One box of a 2-D tensor map into this CTA's shared memory, counted on a
 // barrier of either CTA of the pair.  x is a multiple of 8 elements (16 bytes).
@@ -94,6 +100,37 @@ __device__ __forceinline__ void tc_load32(float (&v)[32], uint32_t addr) {
   for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
 }
 
+// An epilogue warp's stores: 32 rows of 64 bf16 at a time, thread = row, through
+// shared memory (swizzled: no bank conflicts, and whole lines to L2; 16-byte stores
+// by rows halve the write rate).  The map has boxes of 64 columns x 32 rows; what
+// lies outside the matrix is left out.  x is a multiple of 8.
+struct TcStore {
+  uint32_t box;
+  __device__ __forceinline__ void put(const CUtensorMap* map, int x, int y, const uint4 (&v)[8]) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t row = box + lane * 128;
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");       // the last one has left
+    __syncwarp();
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + (uint32_t)((c ^ (lane & 7)) << 4)), "r"(v[c].x),
+                   "r"(v[c].y), "r"(v[c].z), "r"(v[c].w)
+                   : "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) {
+      asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x),
+                   "r"(y), "r"(box)
+                   : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  }
+  __device__ __forceinline__ void finish() const {
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+};
+
 // One operand of a tile: rows i0 .. i0 + 255 (the CTA's half from i0 + 128 rank)
 // over k0 .. of a matrix whose map has k inner (box 64 x 128) or i inner (box 64 x 64).
 struct TcOperand {
@@ -111,28 +148,48 @@ __device__ __forceinline__ void tc_stage(uint32_t dst, const TcOperand& o, uint3
   }
 }
 
-// The persistent kernel.  Work::count() tiles; Work::tile(t) gives its operands
-// and the number of stages of k (0: no product); Work::epilogue(t, row, tmem,
-// any) is called by the 128 epilogue threads with the thread's tile row and the
-// TMEM address of its first column.  Pair c does the tiles c, c + pairs, ...
+// The persistent kernel.  Work::index(l, pair, pairs) is a pair's l-th tile, -1 after
+// its last; Work::tile(t) gives a tile's operands and the number of stages of k
+// (0: no product); Work::epilogue(t, e) is called by the epilogue threads.
 struct TcTile {
   TcOperand a, b;
   int steps;
+};
+// An epilogue thread's half row of a tile: the tile row, its first column of 128, the
+// TMEM address of that, and whether there is a product (else the sums are 0).
+struct TcHalfRow {
+  int row, col;
+  uint32_t tmem;
+  bool any;
+  float2* halves;                            // of this tile, by row % 128 (in the staging: either is used)
+  int turn;
+  TcStore store;
+  // The second half's value to the thread of the first half, which gets it.
+  __device__ __forceinline__ float2 join(float2 v) const {
+    const int quarter = (threadIdx.x >> 5) & 3, id = 1 + 2 * quarter + turn, at = row & (kTcHalf - 1);
+    if (col != 0) {
+      halves[at] = v;
+      asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+      return v;
+    }
+    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+    return halves[at];
+  }
 };
 template <class Work>
 __device__ __forceinline__ void tc_run(const Work& work, int* error) {
   extern __shared__ unsigned char tc_smem[];
   const uint32_t base = (smem_u32(tc_smem) + 1023) & ~1023u;
-  TcShared& S = *reinterpret_cast<TcShared*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage);
+  TcShared& S = *reinterpret_cast<TcShared*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage + kTcStaging);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
-  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1, tiles = work.count();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   volatile int* failed = &S.failed;
 
   if (threadIdx.x == 0) {
     S.failed = 0;
     for (int i = 0; i < kTcStages; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&S.done[i], 1); mbar_init(&S.drained[i], 8); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&S.done[i], 1); mbar_init(&S.drained[i], 2 * kTcEpilogue); }
     fence_mbar_init();
   }
   __syncthreads();
@@ -153,7 +210,7 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
     if (lane == 0) {
       int it = 0;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
+      for (int l = 0, t; ok && (t = work.index(l, pair, pairs)) >= 0; ++l) {
         const TcTile tile = work.tile(t);
         for (int k = 0; k < tile.steps; ++k, ++it) {
           const int st = it % kTcStages;
@@ -170,7 +227,7 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
     if (rank == 0 && lane == 0) {
       int it = 0, n = 0;
       bool ok = true;
-      for (int t = pair; t < tiles && ok; t += pairs) {
+      for (int l = 0, t; ok && (t = work.index(l, pair, pairs)) >= 0; ++l) {
         const TcTile tile = work.tile(t);
         if (tile.steps == 0) continue;
         const int buf = n & 1;
@@ -195,8 +252,11 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
     }
   } else {
     int n = 0;
-    for (int t = pair; t < tiles; t += pairs) {
-      const int row = (int)rank * kTcHalf + warp * 32 + lane;
+    TcHalfRow e;
+    e.row = (int)rank * kTcHalf + (warp & 3) * 32 + lane;
+    e.col = (warp >> 2) * kTcHalf;
+    e.store.box = base + kTcStages * kTcStage + (uint32_t)warp * kTcBox;
+    for (int l = 0, t; (t = work.index(l, pair, pairs)) >= 0; ++l) {
       const int steps = work.tile(t).steps;
       const int buf = n & 1;
       if (steps > 0) {
@@ -204,7 +264,11 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
       }
-      work.epilogue(t, row, tmem + buf * kTcTile + ((uint32_t)(warp * 32) << 16), steps > 0);
+      e.tmem = tmem + buf * kTcTile + e.col + ((uint32_t)((warp & 3) * 32) << 16);
+      e.any = steps > 0;
+      e.halves = reinterpret_cast<float2*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage) + buf * kTcHalf;
+      e.turn = buf;
+      work.epilogue(t, e);
       if (steps > 0) {
         tc_fence_before();
         __syncwarp();
@@ -212,6 +276,7 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
         ++n;
       }
     }
+    e.store.finish();
   }
   __syncwarp();
   if (__any_sync(0xffffffffu, *failed)) {    // copies or products may still be in flight
