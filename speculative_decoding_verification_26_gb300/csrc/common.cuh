@@ -576,7 +576,8 @@ struct CeParams {
   int* row_of;                   // [n_pad] the row of a compact row
   int* lab;                      // [n_pad] its label, -1 past the last
   int* pos_of;                   // [n] the compact row of a row, -1: none
-  __nv_bfloat16* rows;           // [n_pad, H] compact hidden states, zeros past the last
+  int row_stride;                // of `rows`: H in whole 128-byte lines
+  __nv_bfloat16* rows;           // [n_pad, row_stride] compact hidden states
   float* label_logit;            // [n_pad]
   float2* part;                  // [vocabulary tiles, n_pad] maximum and sum
   float *lse_c, *g_c;            // [n_pad]

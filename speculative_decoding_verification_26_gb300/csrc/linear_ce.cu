@@ -32,6 +32,7 @@ constexpr int kGatherFew = 8, kGatherMany = 64;
 // The rows that count, in order: row_of, their labels, and their hidden states.
 template <bool BWD, int kGatherRows>
 __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_constant__ CeParams P) {
+  griddep_launch();                          // the next kernel's set-up needs nothing of this one
   __shared__ int s_before[kGatherThreads / 32], s_all[kGatherThreads / 32];
   __shared__ int s_row[kGatherRows];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -92,7 +93,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
   for (int i = warp; i < kGatherRows; i += kGatherThreads / 32) {
     if (s_row[i] >= 0) {
       const uint4* src = reinterpret_cast<const uint4*>(P.hidden + (size_t)(r0 + i) * P.H);
-      uint4* dst = reinterpret_cast<uint4*>(P.rows + (size_t)s_row[i] * P.H);
+      uint4* dst = reinterpret_cast<uint4*>(P.rows + (size_t)s_row[i] * P.row_stride);
 #pragma unroll 8
       for (int k = lane; k < nv; k += 32) dst[k] = src[k];
     }
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
     const int at = r0 + i;
     if (at >= all) {
       if (BWD && at < (all + kTcK - 1) / kTcK * kTcK) {
-        uint4* dst = reinterpret_cast<uint4*>(P.rows + (size_t)at * P.H);
+        uint4* dst = reinterpret_cast<uint4*>(P.rows + (size_t)at * P.row_stride);
         for (int k = lane; k < nv; k += 32) dst[k] = make_uint4(0, 0, 0, 0);
       }
       if (lane == 0) {
@@ -355,29 +356,34 @@ struct GradWork {
   }
 };
 
-__global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
-    ce_forward(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M) {
-  const LogitTiles lt{(*P.count + kTcTile - 1) / kTcTile, (P.V + kTcTile - 1) / kTcTile, *P.count};
-  tc_run(ForwardWork{P, M, lt}, P.count + 1);
-}
-
 __device__ __forceinline__ int piece_len(const CeParams& P, int v_begin) {
   return P.V - v_begin < P.piece ? P.V - v_begin : P.piece;
 }
+// Each kernel's work is made after tc_run's set-up, which waits for the kernel before.
+__global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
+    ce_forward(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M) {
+  tc_run([&] {
+    const int count = *P.count;
+    return ForwardWork{P, M, {(count + kTcTile - 1) / kTcTile, (P.V + kTcTile - 1) / kTcTile, count}};
+  }, P.count + 1);
+}
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     ce_softmax(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
-  const LogitTiles lt{(*P.count + kTcTile - 1) / kTcTile, (piece_len(P, v_begin) + kTcTile - 1) / kTcTile,
-                      *P.count};
-  tc_run(SoftWork{P, M, lt, v_begin}, P.count + 1);
+  tc_run([&] {
+    const int count = *P.count;
+    return SoftWork{P, M, {(count + kTcTile - 1) / kTcTile, (piece_len(P, v_begin) + kTcTile - 1) / kTcTile, count},
+                    v_begin};
+  }, P.count + 1);
 }
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     ce_grads(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
-  const int len = piece_len(P, v_begin), count = *P.count;
-  const int rt = (count + kTcTile - 1) / kTcTile, ct = (P.H + kTcTile - 1) / kTcTile;
-  const int ht = P.grad_hidden ? rt * ct * P.splits : 0;
-  const int wt = P.grad_weight ? (len + kTcTile - 1) / kTcTile * ct : 0;
-  tc_run(GradWork{P, M, v_begin, count, rt, ct, (len + kTcK - 1) / kTcK, (count + kTcK - 1) / kTcK, ht, wt},
-         P.count + 1);
+  tc_run([&] {
+    const int len = piece_len(P, v_begin), count = *P.count;
+    const int rt = (count + kTcTile - 1) / kTcTile, ct = (P.H + kTcTile - 1) / kTcTile;
+    const int ht = P.grad_hidden ? rt * ct * P.splits : 0;
+    const int wt = P.grad_weight ? (len + kTcTile - 1) / kTcTile * ct : 0;
+    return GradWork{P, M, v_begin, count, rt, ct, (len + kTcK - 1) / kTcK, (count + kTcK - 1) / kTcK, ht, wt};
+  }, P.count + 1);
 }
 
 // lse and loss of the rows that count: the tiles' maxima and sums, each warp a
@@ -386,6 +392,8 @@ constexpr int kMergeThreads = 1024, kMergeWarps = kMergeThreads / 32;
 __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constant__ CeParams P) {
   __shared__ float2 s_part[kMergeWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = blockIdx.x * 32 + lane;
+  griddep_launch();
+  griddep_wait();
   if (blockIdx.x * 32 >= *P.count) return;
   const int tiles = (P.V + kTcTile - 1) / kTcTile;
   float m = -INFINITY, s = 0.f;
@@ -395,15 +403,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constan
     s = s * ex2((m - top) * kLog2eHi) + p.y * ex2((p.x - top) * kLog2eHi);
     m = top;
   };
-  for (int t0 = warp; t0 < tiles; t0 += 8 * kMergeWarps) {
-    float2 p[8];                             // eight loads in flight
+  constexpr int U = 20;                      // loads in flight: a vocabulary of 163840 in one go
+  for (int t0 = warp; t0 < tiles; t0 += U * kMergeWarps) {
+    float2 p[U];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int t = t0 + u * kMergeWarps;
       p[u] = t < tiles ? P.part[(size_t)t * P.n_pad + i] : make_float2(-INFINITY, 0.f);
     }
 #pragma unroll
-    for (int u = 0; u < 8; ++u) add(p[u]);
+    for (int u = 0; u < U; ++u) add(p[u]);
   }
   s_part[warp][lane] = make_float2(m, s);
   __syncthreads();
@@ -420,6 +429,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constan
 // Every row of dh: the sum of its parts, or zeros where the row took no part.
 // After a wait that ran out (no healthy call) both gradients are NaN.
 __global__ void __launch_bounds__(256) finish_grads(const __grid_constant__ CeParams P) {
+  griddep_wait();
   const long long me = blockIdx.x * 256ll + threadIdx.x, all = gridDim.x * 256ll;
   const bool failed = P.count[1] != 0;
   const uint4 nans = make_uint4(0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u);
@@ -453,9 +463,9 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 EncodeTiled g_encode = nullptr;              // set once by configure_linear_ce
 
-// bf16 matrix of `height` rows of `width`, boxes of 64 columns x `box` rows
-bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t height, uint32_t box) {
-  const cuuint64_t dims[2] = {width, height}, strides[1] = {width * 2};
+// bf16 matrix of `height` rows of `width`, `stride` apart, boxes of 64 columns x `box` rows
+bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t stride, uint64_t height, uint32_t box) {
+  const cuuint64_t dims[2] = {width, height}, strides[1] = {stride * 2};
   const cuuint32_t boxes[2] = {(cuuint32_t)kTcK, box}, ones[2] = {1, 1};
   return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, boxes, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -484,36 +494,58 @@ cudaError_t configure_linear_ce() {
   return e;
 }
 
+// A kernel after another of the call: its set-up may overlap the end of that one.
+template <class K, class... A>
+cudaError_t launch_after(K kernel, int grid, int threads, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_ce_forward(const CeParams& P, int nsm, cudaStream_t s, int* launches) {
   CeMaps M;
   memset(&M, 0, sizeof M);
-  if (!encode(&M.rows, P.rows, P.H, P.n_pad, kTcHalf) || !encode(&M.weight, P.weight, P.H, P.V, kTcHalf))
+  if (!encode(&M.rows, P.rows, P.H, P.row_stride, P.n_pad, kTcHalf) ||
+      !encode(&M.weight, P.weight, P.H, P.H, P.V, kTcHalf))
     return cudaErrorInvalidValue;
   launch_gather<false>(P, s);
-  ce_forward<<<nsm / 2 * 2, kTcThreads, kTcSmem, s>>>(P, M);
-  merge_rows<<<P.n_pad / 32, kMergeThreads, 0, s>>>(P);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_after(ce_forward, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M);
+  if (e == cudaSuccess) e = launch_after(merge_rows, P.n_pad / 32, kMergeThreads, 0, s, P);
   *launches = 3;
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_ce_backward(const CeParams& P, int nsm, cudaStream_t s, int* launches) {
   CeMaps M;
   memset(&M, 0, sizeof M);
-  if (!encode(&M.rows, P.rows, P.H, P.n_pad, kTcHalf) || !encode(&M.weight, P.weight, P.H, P.V, kTcHalf) ||
-      !encode(&M.soft, P.soft, P.piece, P.n_pad, kTcHalf) || !encode(&M.rows_t, P.rows, P.H, P.n_pad, kTcK) ||
-      !encode(&M.weight_t, P.weight, P.H, P.V, kTcK) || !encode(&M.soft_t, P.soft, P.piece, P.n_pad, kTcK) ||
-      !encode(&M.soft_out, P.soft, P.piece, P.n_pad, 32) ||
-      (P.grad_weight && !encode(&M.grad_weight, P.grad_weight, P.H, P.V, 32)))
+  if (!encode(&M.rows, P.rows, P.H, P.row_stride, P.n_pad, kTcHalf) ||
+      !encode(&M.weight, P.weight, P.H, P.H, P.V, kTcHalf) ||
+      !encode(&M.soft, P.soft, P.piece, P.piece, P.n_pad, kTcHalf) ||
+      !encode(&M.rows_t, P.rows, P.H, P.row_stride, P.n_pad, kTcK) ||
+      !encode(&M.weight_t, P.weight, P.H, P.H, P.V, kTcK) ||
+      !encode(&M.soft_t, P.soft, P.piece, P.piece, P.n_pad, kTcK) ||
+      !encode(&M.soft_out, P.soft, P.piece, P.piece, P.n_pad, 32) ||
+      (P.grad_weight && !encode(&M.grad_weight, P.grad_weight, P.H, P.H, P.V, 32)))
     return cudaErrorInvalidValue;
   launch_gather<true>(P, s);
+  cudaError_t e = cudaGetLastError();
   int n = 2;
-  for (long long v = 0; v < P.V; v += P.piece, n += 2) {
-    ce_softmax<<<nsm / 2 * 2, kTcThreads, kTcSmem, s>>>(P, M, (int)v);
-    ce_grads<<<nsm / 2 * 2, kTcThreads, kTcSmem, s>>>(P, M, (int)v);
+  for (long long v = 0; v < P.V && e == cudaSuccess; v += P.piece, n += 2) {
+    e = launch_after(ce_softmax, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M, (int)v);
+    if (e == cudaSuccess) e = launch_after(ce_grads, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M, (int)v);
   }
-  finish_grads<<<4 * nsm, 256, 0, s>>>(P);
+  if (e == cudaSuccess) e = launch_after(finish_grads, 4 * nsm, 256, 0, s, P);
   *launches = n;
-  return cudaGetLastError();
+  return e;
 }
 
 size_t ce_layout(CeParams& P, bool backward, void* base) {
@@ -528,7 +560,10 @@ size_t ce_layout(CeParams& P, bool backward, void* base) {
   P.count = reinterpret_cast<int*>(place(256));
   P.row_of = reinterpret_cast<int*>(place(4ull * P.n_pad));
   P.lab = reinterpret_cast<int*>(place(4ull * P.n_pad));
-  P.rows = reinterpret_cast<__nv_bfloat16*>(place(2ull * P.n_pad * P.H));
+  // rows start on 128-byte lines: a box row of 64 columns that straddles two takes
+  // twice the L2 requests
+  P.row_stride = (P.H + kTcK - 1) / kTcK * kTcK;
+  P.rows = reinterpret_cast<__nv_bfloat16*>(place(2ull * P.n_pad * P.row_stride));
   if (!backward) {
     P.label_logit = reinterpret_cast<float*>(place(4ull * P.n_pad));
     P.part = reinterpret_cast<float2*>(place(8ull * P.n_pad * ((P.V + kTcTile - 1) / kTcTile)));

@@ -176,8 +176,9 @@ struct TcHalfRow {
     return halves[at];
   }
 };
-template <class Work>
-__device__ __forceinline__ void tc_run(const Work& work, int* error) {
+// `make` gives the work, once the kernel before has ended.
+template <class Make>
+__device__ __forceinline__ void tc_run(Make&& make, int* error) {
   extern __shared__ unsigned char tc_smem[];
   const uint32_t base = (smem_u32(tc_smem) + 1023) & ~1023u;
   TcShared& S = *reinterpret_cast<TcShared*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage + kTcStaging);
@@ -205,6 +206,9 @@ __device__ __forceinline__ void tc_run(const Work& work, int* error) {
   cluster_sync();                            // both halves of the tensor memory are allocated
   tc_fence_after();
   const uint32_t tmem = S.tmem;
+  griddep_launch();
+  griddep_wait();
+  const auto work = make();
 
   if (warp == kTcProducer) {
     if (lane == 0) {
