@@ -353,17 +353,45 @@ MAX_TOPK = 256
 DISTILL_MAX_V = 1 << 20
 
 
+# The calls below take a few microseconds on the device for few rows, so their host
+# side is kept short: entry points looked up once, addresses as plain integers, and
+# the raw handle of the current stream (torch.cuda.current_stream builds an object
+# for 2 us).
+_entry: dict = {}
+
+
 def _call(dev, name, *args):
     """Call the C entry point with `dev` current and its current stream last."""
     torch = _torch()
-    f = getattr(lib(), name)
-    if torch.cuda.current_device() == dev.index:
-        rc = f(*args, _stream(dev))
+    f = _entry.get(name)
+    if f is None:
+        f = _entry[name] = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == dev.index:
+        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     else:
         with torch.cuda.device(dev):
-            rc = f(*args, _stream(dev))
+            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
     if rc != OK:
         raise SpecVerifyError(rc, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _want(t, name, dtype, shape, device):
+    """_check, with the common case first."""
+    if t is not None and not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+        _check(t, name, dtype, shape, device)
+
+
+def _result(o, key, shape, dtype, dev):
+    """out[key], checked, or a new tensor."""
+    t = o.get(key) if o else None
+    if t is None:
+        return _torch().empty(shape, dtype=dtype, device=dev)
+    _check(t, key, dtype, shape, dev)
+    return t
 
 
 def topk_logits(logits, K, temperature=None, *, out=None):
@@ -375,20 +403,15 @@ def topk_logits(logits, K, temperature=None, *, out=None):
     V = logits.shape[-1]
     n = logits.numel() // V
     dev = logits.device
-    _check(logits, "logits", device=dev)
-    _check(temperature, "temperature", torch.float32, (n,), dev)
-    o = out or {}
-    top = _out(o, "top_logits", lambda: torch.empty(n, K, dtype=torch.float32, device=dev))
-    idx = _out(o, "top_index", lambda: torch.empty(n, K, dtype=torch.int32, device=dev))
-    tail = _out(o, "tail_lse", lambda: torch.empty(n, dtype=torch.float32, device=dev))
-    st = _out(o, "status", lambda: torch.empty(n, dtype=torch.int32, device=dev))
-    if o:
-        _check(top, "top_logits", torch.float32, (n, K), dev)
-        _check(idx, "top_index", torch.int32, (n, K), dev)
-        _check(tail, "tail_lse", torch.float32, (n,), dev)
-        _check(st, "status", torch.int32, (n,), dev)
-    _call(dev, "spec_topk_logits", _ptr(logits), _dtype_code(logits), n, V, K, _ptr(temperature), _ptr(top),
-          _ptr(idx), _ptr(tail), _ptr(st))
+    f32 = torch.float32
+    _check(logits, "logits")
+    _want(temperature, "temperature", f32, (n,), dev)
+    top = _result(out, "top_logits", (n, K), f32, dev)
+    idx = _result(out, "top_index", (n, K), torch.int32, dev)
+    tail = _result(out, "tail_lse", (n,), f32, dev)
+    st = _result(out, "status", (n,), torch.int32, dev)
+    _call(dev, "spec_topk_logits", logits.data_ptr(), _dtype_code(logits), n, V, K, _addr(temperature),
+          top.data_ptr(), idx.data_ptr(), tail.data_ptr(), st.data_ptr())
     return {"top_logits": top, "top_index": idx, "tail_lse": tail, "status": st}
 
 
@@ -403,27 +426,22 @@ def distill_topk(logits, top_logits, top_index, tail_lse=None, *, label=None, ro
     V = logits.shape[-1]
     n = logits.numel() // V
     dev = logits.device
+    f32, i32 = torch.float32, torch.int32
     K = top_logits.shape[-1]
-    _check(logits, "logits", device=dev)
-    _check(top_logits, "top_logits", torch.float32, (n, K), dev)
-    _check(top_index, "top_index", torch.int32, (n, K), dev)
-    _check(tail_lse, "tail_lse", torch.float32, (n,), dev)
-    _check(label, "label", torch.int32, (n,), dev)
-    _check(row_weight, "row_weight", torch.float32, (n,), dev)
-    _check(temperature, "temperature", torch.float32, (n,), dev)
-    o = out or {}
-    loss = _out(o, "loss", lambda: torch.empty(n, dtype=torch.float32, device=dev))
-    parts = _out(o, "parts", lambda: torch.empty(n, 3, dtype=torch.float32, device=dev))
-    st = _out(o, "status", lambda: torch.empty(n, dtype=torch.int32, device=dev))
-    g = _out(o, "grad", lambda: torch.empty_like(logits)) if grad else None
-    if o:
-        _check(loss, "loss", torch.float32, (n,), dev)
-        _check(parts, "parts", torch.float32, (n, 3), dev)
-        _check(st, "status", torch.int32, (n,), dev)
-        _check(g, "grad", logits.dtype, logits.shape, dev)
-    _call(dev, "spec_distill_topk", _ptr(logits), _dtype_code(logits), n, V, K, _ptr(top_logits), _ptr(top_index),
-          _ptr(tail_lse), _ptr(label), _ptr(row_weight), _ptr(temperature), kl, tv, ce, _ptr(loss), _ptr(parts),
-          _ptr(g), _ptr(st))
+    _check(logits, "logits")
+    _want(top_logits, "top_logits", f32, (n, K), dev)
+    _want(top_index, "top_index", i32, (n, K), dev)
+    _want(tail_lse, "tail_lse", f32, (n,), dev)
+    _want(label, "label", i32, (n,), dev)
+    _want(row_weight, "row_weight", f32, (n,), dev)
+    _want(temperature, "temperature", f32, (n,), dev)
+    loss = _result(out, "loss", (n,), f32, dev)
+    parts = _result(out, "parts", (n, 3), f32, dev)
+    st = _result(out, "status", (n,), i32, dev)
+    g = _result(out, "grad", logits.shape, logits.dtype, dev) if grad else None
+    _call(dev, "spec_distill_topk", logits.data_ptr(), _dtype_code(logits), n, V, K, top_logits.data_ptr(),
+          top_index.data_ptr(), _addr(tail_lse), _addr(label), _addr(row_weight), _addr(temperature), kl, tv, ce,
+          loss.data_ptr(), parts.data_ptr(), _addr(g), st.data_ptr())
     r = {"loss": loss, "parts": parts, "status": st}
     if grad:
         r["grad"] = g
@@ -442,13 +460,14 @@ def linear_ce_workspace(n, H, V, device, *, backward):
     sizes (reused by calls on the same stream; calls sharing it must not overlap
     on the device).  Under stream capture it is new: a graph keeps its own."""
     torch = _torch()
+    device = torch.device(device)
     need = linear_ce_workspace_bytes(n, H, V, backward)
     if need == 0:
         raise ValueError("sizes outside the library limits")
     make = lambda: torch.empty(need, dtype=torch.uint8, device=device)   # noqa: E731
     if torch.cuda.is_current_stream_capturing():
         return make()
-    key = (str(device), torch.cuda.current_stream(device).cuda_stream)
+    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
     ws = _ce_ws_cache.get(key)
     if ws is None or ws.numel() < need:
         _ce_ws_cache.pop(key, None)
@@ -464,8 +483,8 @@ def _ce_inputs(hidden, weight, label):
     V = weight.shape[0]
     dev = hidden.device
     _check(hidden, "hidden", torch.bfloat16, (n, H), dev)
-    _check(weight, "weight", torch.bfloat16, (V, H), dev)
-    _check(label, "label", torch.int32, (n,), dev)
+    _want(weight, "weight", torch.bfloat16, (V, H), dev)
+    _want(label, "label", torch.int32, (n,), dev)
     return n, H, V, dev
 
 
@@ -475,18 +494,15 @@ def linear_ce_forward(hidden, weight, label, *, ws=None, out=None):
     Returns {"loss": [n], "lse": [n], "status": [n]} (see spec_linear_ce_forward)."""
     torch = _torch()
     n, H, V, dev = _ce_inputs(hidden, weight, label)
-    o = out or {}
-    loss = _out(o, "loss", lambda: torch.empty(n, dtype=torch.float32, device=dev))
-    lse = _out(o, "lse", lambda: torch.empty(n, dtype=torch.float32, device=dev))
-    st = _out(o, "status", lambda: torch.empty(n, dtype=torch.int32, device=dev))
-    if o:
-        _check(loss, "loss", torch.float32, (n,), dev)
-        _check(lse, "lse", torch.float32, (n,), dev)
-        _check(st, "status", torch.int32, (n,), dev)
-    ws = ws if ws is not None else linear_ce_workspace(n, H, V, dev, backward=False)
-    _check(ws, "ws", torch.uint8, device=dev)
-    _call(dev, "spec_linear_ce_forward", _ptr(hidden), _ptr(weight), BF16, n, H, V, _ptr(label), _ptr(loss),
-          _ptr(lse), _ptr(st), _ptr(ws), ws.numel())
+    loss = _result(out, "loss", (n,), torch.float32, dev)
+    lse = _result(out, "lse", (n,), torch.float32, dev)
+    st = _result(out, "status", (n,), torch.int32, dev)
+    if ws is None:
+        ws = linear_ce_workspace(n, H, V, dev, backward=False)
+    else:
+        _check(ws, "ws", torch.uint8, device=dev)
+    _call(dev, "spec_linear_ce_forward", hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
+          loss.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel())
     return {"loss": loss, "lse": lse, "status": st}
 
 
@@ -498,18 +514,16 @@ def linear_ce_backward(hidden, weight, label, lse, grad_loss=None, *, need_hidde
     that is not needed (see spec_linear_ce_backward)."""
     torch = _torch()
     n, H, V, dev = _ce_inputs(hidden, weight, label)
-    _check(lse, "lse", torch.float32, (n,), dev)
-    _check(grad_loss, "grad_loss", torch.float32, (n,), dev)
-    o = out or {}
-    gh = _out(o, "grad_hidden", lambda: torch.empty_like(hidden)) if need_hidden else None
-    gw = _out(o, "grad_weight", lambda: torch.empty_like(weight)) if need_weight else None
-    if o:
-        _check(gh, "grad_hidden", torch.bfloat16, (n, H), dev)
-        _check(gw, "grad_weight", torch.bfloat16, (V, H), dev)
-    ws = ws if ws is not None else linear_ce_workspace(n, H, V, dev, backward=True)
-    _check(ws, "ws", torch.uint8, device=dev)
-    _call(dev, "spec_linear_ce_backward", _ptr(hidden), _ptr(weight), BF16, n, H, V, _ptr(label), _ptr(lse),
-          _ptr(grad_loss), _ptr(gh), _ptr(gw), _ptr(ws), ws.numel())
+    _want(lse, "lse", torch.float32, (n,), dev)
+    _want(grad_loss, "grad_loss", torch.float32, (n,), dev)
+    gh = _result(out, "grad_hidden", (n, H), torch.bfloat16, dev) if need_hidden else None
+    gw = _result(out, "grad_weight", (V, H), torch.bfloat16, dev) if need_weight else None
+    if ws is None:
+        ws = linear_ce_workspace(n, H, V, dev, backward=True)
+    else:
+        _check(ws, "ws", torch.uint8, device=dev)
+    _call(dev, "spec_linear_ce_backward", hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
+          lse.data_ptr(), _addr(grad_loss), _addr(gh), _addr(gw), ws.data_ptr(), ws.numel())
     r = {}
     if need_hidden:
         r["grad_hidden"] = gh
