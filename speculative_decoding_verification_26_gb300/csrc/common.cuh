@@ -581,6 +581,7 @@ struct CeParams {
   float* label_logit;            // [n_pad]
   float2* part;                  // [vocabulary tiles, n_pad] maximum and sum
   float *lse_c, *g_c;            // [n_pad]
+  float* label_g;                // [n_pad] the gradient by the label's logit
   __nv_bfloat16* soft;           // [n_pad, piece] the gradient by the logits
   float* acc;                    // [splits, n_pad, H] sums of grad_hidden
 };

@@ -94,8 +94,30 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
     if (s_row[i] >= 0) {
       const uint4* src = reinterpret_cast<const uint4*>(P.hidden + (size_t)(r0 + i) * P.H);
       uint4* dst = reinterpret_cast<uint4*>(P.rows + (size_t)s_row[i] * P.row_stride);
-#pragma unroll 8
-      for (int k = lane; k < nv; k += 32) dst[k] = src[k];
+      // the label's logit on the way: products of bf16 are exact in fp32, and the sums are
+      // rounded to nearest (the tensor cores' are not, see ForwardWork)
+      const uint4* wl = reinterpret_cast<const uint4*>(P.weight + (size_t)P.label[r0 + i] * P.H);
+      float a = 0.f, b = 0.f;
+#pragma unroll 4
+      for (int k = lane; k < nv; k += 32) {
+        const uint4 x = src[k], w = wl[k];
+        dst[k] = x;
+        a = fmaf(bf16_lo(x.x), bf16_lo(w.x), a);
+        b = fmaf(bf16_hi(x.x), bf16_hi(w.x), b);
+        a = fmaf(bf16_lo(x.y), bf16_lo(w.y), a);
+        b = fmaf(bf16_hi(x.y), bf16_hi(w.y), b);
+        a = fmaf(bf16_lo(x.z), bf16_lo(w.z), a);
+        b = fmaf(bf16_hi(x.z), bf16_hi(w.z), b);
+        a = fmaf(bf16_lo(x.w), bf16_lo(w.w), a);
+        b = fmaf(bf16_hi(x.w), bf16_hi(w.w), b);
+      }
+      a += b;
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
+      if (lane == 0) {
+        if (BWD) P.label_g[s_row[i]] = P.g_c[s_row[i]] * expm1f(a - P.lse_in[r0 + i]);
+        else P.label_logit[s_row[i]] = a;
+      }
     }
     // places past the last row that counts: dW sums over whole stages of rows, and a
     // stage's last rows are zero; what lies behind them only reaches rows of its own
@@ -107,7 +129,7 @@ __global__ void __launch_bounds__(kGatherThreads) gather_rows(const __grid_const
       }
       if (lane == 0) {
         P.lab[at] = -1;
-        if (BWD) { P.lse_c[at] = 0.f; P.g_c[at] = 0.f; }
+        if (BWD) { P.lse_c[at] = 0.f; P.g_c[at] = 0.f; P.label_g[at] = 0.f; }
       }
     }
   }
@@ -144,7 +166,10 @@ struct LogitTiles {
 
 constexpr float kLn2 = 0.693147180559945f;
 
-// forward: a tile's maximum and sum of each row, and the label's logit
+// Forward: a tile's maximum and sum of each row, without the label.  The tensor cores
+// cut their sums off (about 1e-5 of a logit of 16 over H = 2048), and where the label
+// has nearly all of the mass its loss is as small as that: the label's logit is summed
+// apart (gather_rows), and the loss is ln(1 + the others' weights beside the label's).
 struct ForwardWork {
   const CeParams& P;
   const CeMaps& M;
@@ -166,10 +191,9 @@ struct ForwardWork {
       float x[32];
       tc_load32(x, e.tmem + c0);
       if (at >= c0 && at < c0 + 32) {
-        float z = 0.f;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) z = c0 + c == at ? x[c] : z;
-        P.label_logit[i] = z;
+        for (int c = 0; c < 32; ++c)
+          if (c0 + c == at) x[c] = -INFINITY;
       }
       const int left = P.V - v0 - c0;
       if (left < 32) {
@@ -232,7 +256,7 @@ struct SoftWork {
     // a stage's last rows are zero (G sums over rows in whole stages); later ones are not read
     if (first >= (lt.rows + kTcK - 1) / kTcK * kTcK) return;
     const int at = P.lab[i] - v0;
-    const float g = P.g_c[i], ref = -P.lse_c[i] * kLog2eHi;
+    const float g = P.g_c[i], gy = P.label_g[i], ref = -P.lse_c[i] * kLog2eHi;
     for (int c0 = 0; c0 < kTcHalf; c0 += 64) {
       uint4 out[8];
 #pragma unroll
@@ -242,8 +266,8 @@ struct SoftWork {
         const int left = P.V - v0 - c0 - 32 * h, mark = at - c0 - 32 * h;
 #pragma unroll
         for (int c = 0; c < 32; ++c) {
-          x[c] = ex2(fmaf(x[c], kLog2eHi, ref)) - (c == mark ? 1.f : 0.f);
-          x[c] = c < left && g != 0.f ? x[c] * g : 0.f;
+          x[c] = c < left && g != 0.f ? g * ex2(fmaf(x[c], kLog2eHi, ref)) : 0.f;
+          if (c == mark) x[c] = gy;
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) out[4 * h + c] = pack8(x + 8 * c);
@@ -418,11 +442,16 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constan
   __syncthreads();
   if (warp != 0 || i >= *P.count) return;
   for (int w = 1; w < kMergeWarps; ++w) add(s_part[w][lane]);
-  const float lse = m + kLn2 * log2f(s), nan = __int_as_float(0x7fc00000);
+  // with the label: lse - z = ln(1 + others / e^z), where z is the larger without lse's rounding
+  const float z = P.label_logit[i], top = fmaxf(m, z), nan = __int_as_float(0x7fc00000);
+  const float others = m == -INFINITY ? s : s * ex2((m - top) * kLog2eHi);
+  const float own = ex2((z - top) * kLog2eHi);
+  const float loss = z >= m ? log1pf(others) : (top - z) + kLn2 * log2f(others + own);
+  const float lse = top + kLn2 * log2f(others + own);
   const int failed = P.count[1], r = P.row_of[i];
-  const bool ok = isfinite(m) && isfinite(lse) && !failed;
+  const bool ok = isfinite(top) && isfinite(lse) && !failed;
   P.lse[r] = ok ? lse : nan;
-  P.loss[r] = ok ? lse - P.label_logit[i] : nan;
+  P.loss[r] = ok ? loss : nan;
   if (P.status) P.status[r] = failed ? SPEC_ST_TIMEOUT : ok ? SPEC_ST_OK : SPEC_ST_NONFINITE;
 }
 
@@ -589,6 +618,7 @@ size_t ce_layout(CeParams& P, bool backward, void* base) {
   P.pos_of = reinterpret_cast<int*>(place(4ull * P.n));
   P.lse_c = reinterpret_cast<float*>(place(4ull * P.n_pad));
   P.g_c = reinterpret_cast<float*>(place(4ull * P.n_pad));
+  P.label_g = reinterpret_cast<float*>(place(4ull * P.n_pad));
   P.soft = reinterpret_cast<__nv_bfloat16*>(place(2ull * P.n_pad * P.piece));
   P.acc = reinterpret_cast<float*>(place(4ull * P.splits * P.n_pad * P.H));
   return at;
