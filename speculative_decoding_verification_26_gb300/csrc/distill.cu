@@ -57,7 +57,7 @@ struct DisShared {
   uint64_t marked[2], summed[2], factors[2], fixed[2], written[2], message[2];
   float part_m[2][kDisWarps], part_s[2][kDisWarps];
   uint4 msg[2][8];                           // maximum, sum, status of each CTA of the cluster
-  float c[2], ref[2], factor[2];
+  float c[2], top[2], factor[2];
   int skip[2], zero[2];
   uint32_t ends[2];                          // marks of the single elements: head from bit 0, tail from bit 8
   int fix_idx[SPEC_MAX_TOPK + 1];            // the recorded tokens and the label: token, or -1, and gradient
@@ -83,9 +83,10 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
-// a sum of weights moved from the reference of one maximum to another's
+// Weights are 2^{(x - m) c}, m a maximum: m c apart would overflow for rows masked with
+// the type's lowest value.  A sum of weights moved from one maximum to another:
 __device__ __forceinline__ float moved(float sum, float from, float to, float c) {
-  return from == -INFINITY ? sum : sum * ex2(ref_of(from, c) - ref_of(to, c));
+  return from == -INFINITY ? sum : sum * ex2((from - to) * c);
 }
 
 // A token's mark, o elements into the share: a unit of kDisPer * PER bits per stage
@@ -288,7 +289,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
       // the tail does not).
       xmax = warp_max(xmax);
       R.zmax = warp_max(zmax);
-      const float x0 = xmax == -INFINITY ? 0.f : xmax, x0c = __fmul_rn(x0, sc.c);
+      const float x0 = xmax == -INFINITY ? 0.f : xmax, x0c = fmaxf(__fmul_rn(x0, sc.c), -3.4028235e38f);
       const float lt = tail == -INFINITY ? -INFINITY
                                            : (fmaf(tail, kLog2eHi, -x0c) - fmaf(x0, sc.c, -x0c)) +
                                                  (tail * kLog2eLo - x0 * sc.lo);
@@ -372,9 +373,8 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
           for (int q = 0; q < CS; ++q) rest += moved(__uint_as_float(msg[q].y), __uint_as_float(msg[q].x), mall, c);
         }
         ++live;
-        // one exponent rule for every weight from here on: 2^{x c - ref}; the record's own
-        // weights move there by `up`
-        const float zy = raw_value<DT>(R.zy), ref = ref_of(mall, c), lift = R.zmax == -INFINITY ? 0.f : fmaf(R.zmax, c, -ref), up = ex2(lift);
+        // every weight is beside mall from here on; the record's own move there by `up`
+        const float zy = raw_value<DT>(R.zy), lift = R.zmax == -INFINITY ? 0.f : (R.zmax - mall) * c, up = ex2(lift);
         const float sum = fmaf(R.F, up, rest);
         if (!isfinite(mall) || !isfinite(sum)) st |= SPEC_ST_NONFINITE;
         const float rS = 1.f / sum, l2S = log2f(sum), qr = rest * rS;
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         // rest = 0: no token of the rest has weight, its factor does not matter
         const float factor = ((base + P.tv * sr) * rS - (rest > 0.f ? P.kl * R.pr / rest : 0.f)) * wT;
         if (P.grad && lane == 0) {
-          S.ref[b] = ref;
+          S.top[b] = mall;
           S.factor[b] = factor;
           S.zero[b] = st != 0;
           mbar_arrive(&S.factors[b]);
@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         if (R.pr > 0.f) kl += R.pr * (R.lpr - (log2f(rest) - l2S));
         kl *= kLn2;
         tv = 0.5f * (tv + fabsf(R.pr - qr));
-        ce = R.y >= 0 ? (l2S - fmaf(zy, c, -ref)) * kLn2 : 0.f;
+        ce = R.y >= 0 ? (l2S - (zy - mall) * c) * kLn2 : 0.f;
         if (P.kl != 0.f) loss += P.kl * kl;
         if (P.tv != 0.f) loss += P.tv * tv;
         if (P.ce != 0.f) loss += P.ce * ce;
@@ -422,7 +422,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
           }
           if (lane == 0) {                   // the label, where it is not recorded
             S.fix_idx[K] = R.recorded ? -1 : R.y;
-            S.fix_g[K] = ex2(fmaf(zy, c, -ref)) * factor - wT * lce;
+            S.fix_g[K] = ex2((zy - mall) * c) * factor - wT * lce;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.fixed[b]);
@@ -477,13 +477,13 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         if (tid < ends) end_x = row_logit<DT>(row, end_e);
         // pass 1: running maximum and sum of the tokens not recorded
         float m = -INFINITY, s = 0.f;
-        float nr = 0.f;                      // -R(m); 0 while all are -inf: weights of 0
+        float nm = 0.f;                      // -m; 0 while all are -inf: weights of 0
         const auto* map = reinterpret_cast<const typename MarkUnit<kDisPer * PER>::type*>(maps + b * map_words);
         const float2 C2 = make_float2(c, c);
         auto raise = [&](float x) {
           s = moved(s, m, x, c);
           m = x;
-          nr = -ref_of(x, c);
+          nm = -x;
         };
         for (int j = sh.lo, word = tid; j < sh.hi; j += kDisStageVecs, word += kDisConsumers) {
           bounded_wait(&S.full[at.stage], at.phase, failed);
@@ -509,13 +509,13 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
             for (int u = 0; u < kDisPer; ++u) w[u] = vec[u * kDisConsumers];
             const float top = vecs_max<DT>(w);
             if (top > m) raise(top);
-            const float2 R2 = make_float2(nr, nr);
+            const float2 M2 = make_float2(nm, nm);
             float2 t[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int u = 0; u < kDisPer; ++u)
 #pragma unroll
               for (int k = 0; k < PER / 2; ++k) {
-                const float2 a = __ffma2_rn(vec_pair<DT>(w[u], k), C2, R2);
+                const float2 a = __fmul2_rn(__fadd2_rn(vec_pair<DT>(w[u], k), M2), C2);
                 t[k & 1] = __fadd2_rn(t[k & 1], make_float2(ex2(a.x), ex2(a.y)));
               }
             t[0] = __fadd2_rn(t[0], t[1]);
@@ -526,11 +526,11 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
               const uint4 w = vec[u * kDisConsumers];
               const float top = vec_max<DT>(w);
               if (top > m) raise(top);
-              const float2 R2 = make_float2(nr, nr);
+              const float2 M2 = make_float2(nm, nm);
               float2 t = make_float2(0.f, 0.f);
 #pragma unroll
               for (int k = 0; k < PER / 2; ++k) {
-                const float2 a = __ffma2_rn(vec_pair<DT>(w, k), C2, R2);
+                const float2 a = __fmul2_rn(__fadd2_rn(vec_pair<DT>(w, k), M2), C2);
                 t = __fadd2_rn(t, make_float2(ex2(a.x), ex2(a.y)));
               }
               s += t.x + t.y;
@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         }
         if (tid < ends && !(S.ends[b] >> (tid < sp.head ? tid : 8 + tid - sp.head) & 1)) {
           if (end_x > m) raise(end_x);
-          s += ex2(fmaf(end_x, c, nr));
+          s += ex2((end_x + nm) * c);
         }
         const float top = warp_max(m);
         s = warp_sum(moved(s, m, top, c));
@@ -556,18 +556,18 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
 
       // pass 2: every token's gradient as if outside the record
       bounded_wait(&S.factors[b], turn, failed);
-      const float ref = S.ref[b], factor = S.factor[b];
+      const float top = S.top[b], factor = S.factor[b];
       const bool zero = S.zero[b] != 0;
       // vectors of the gradient row start where those of the logit row do, or it is written element by element
       const bool gvec = ((reinterpret_cast<uintptr_t>(grow) ^ reinterpret_cast<uintptr_t>(row)) & 15u) == 0;
-      const float2 C2 = make_float2(c, c), R2 = make_float2(-ref, -ref), F2 = make_float2(factor, factor);
+      const float2 C2 = make_float2(c, c), M2 = make_float2(-top, -top), F2 = make_float2(factor, factor);
       uint4* gv = reinterpret_cast<uint4*>(grow + (size_t)sp.head * ES);
       RingAt from = keep ? row_at : at;
       auto gradient = [&](const uint4& w) {
         uint32_t o[4];
 #pragma unroll
         for (int k = 0; k < PER / 2; ++k) {
-          const float2 a = __ffma2_rn(vec_pair<DT>(w, k), C2, R2);
+          const float2 a = __fmul2_rn(__fadd2_rn(vec_pair<DT>(w, k), M2), C2);
           const float2 g = __fmul2_rn(make_float2(ex2(a.x), ex2(a.y)), F2);
           if constexpr (DT == SPEC_BF16) {
             const __nv_bfloat162 h = __floats2bfloat162_rn(g.x, g.y);
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
           from.next(stages);
         }
       }
-      if (tid < ends) store_logit<DT>(grow, end_e, zero ? 0.f : ex2(fmaf(end_x, c, -ref)) * factor);
+      if (tid < ends) store_logit<DT>(grow, end_e, zero ? 0.f : ex2((end_x - top) * c) * factor);
       // over them, once every consumer's stores are out, one warp stores the recorded
       // tokens' and the label's (warps take turns; the others go on)
       __syncwarp();

@@ -171,7 +171,7 @@ def make_distill(n, V, K, dtype, seed, tail=True):
                 label=label.to(torch.int32), w=w, T=T)
 
 
-def check_distill(sv, d, kl, tv, ce, grad=True, z_dev=None, out=None, ref=None):
+def check_distill(sv, d, kl, tv, ce, grad=True, z_dev=None, out=None, ref=None, kl_finite=True):
     z = d["z"]
     loss, parts, g64, size = ref or TP.distill(z, d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"], kl, tv, ce)
     top, idx, tail, label, w, T = cuda(d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"])
@@ -179,6 +179,8 @@ def check_distill(sv, d, kl, tv, ce, grad=True, z_dev=None, out=None, ref=None):
                         temperature=T, kl=kl, tv=tv, ce=ce, grad=grad, out=out)
     assert r["status"].cpu().eq(0).all(), r["status"]
     gl, gp = r["loss"].cpu().double(), r["parts"].cpu().double()
+    if not kl_finite:                                 # of the order of 1e38: fp32 has no such logarithms
+        parts, gp = parts[:, 1:], gp[:, 1:]
     tol_parts = 3 * TOL + 2e-6 * torch.where(torch.isfinite(parts), parts.abs(), 0.0)
     for a, b, t in ((gp, parts, tol_parts),
                     (gl, loss, d["w"].double().abs() * (abs(kl) + abs(tv) + abs(ce)) * 3 * TOL + 4e-6 * torch.where(
@@ -252,6 +254,29 @@ def test_distill_masked_rows_and_entries(sv):
     r64 = TP.distill(ref["z"], d["top"], ref["idx"], d["tail"], d["label"], d["w"], d["T"], 1.0, 1.0, 0.5)
     r = check_distill(sv, d, 1.0, 1.0, 0.5, ref=r64)
     assert (r["grad"][2] == 0).all() and r["loss"][2] == 0 and zero[0] == 99999
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_distill_masks_of_the_lowest_value(sv, dtype):
+    """Student rows masked with the type's lowest value: runs of it before the first
+    other logit, at recorded tokens, at every token but one, and everywhere."""
+    low = torch.finfo(dtype).min
+    d = make_distill(5, 20011, 12, dtype, 33)
+    g = gen(5)
+    d["z"][0, :15000] = low
+    d["z"][0, d["idx"][0].long()] = 1.5
+    d["z"][1] = torch.where(torch.rand(20011, generator=g) < 0.5, d["z"][1], torch.tensor(low, dtype=dtype))
+    d["z"][1, d["idx"][1].long()] = 2.0
+    d["z"][1, int(d["label"][1])] = 0.5
+    d["z"][2] = low
+    d["z"][2, d["idx"][2].long()[:1]] = 0.25
+    d["z"][3] = low                                   # a uniform student
+    d["T"][3] = 1.0
+    d["label"][:] = d["idx"][:, 0]
+    # KL with q = e^{-1e38}: far past fp32, left out of rows 2 and so of all
+    check_distill(sv, d, 0.0, 1.0, 1.0, kl_finite=False)
+    sub = {k: (v[3:] if v is not None else None) for k, v in d.items()}
+    check_distill(sv, sub, 1.0, 1.0, 0.5)
 
 
 def test_distill_infinite_losses(sv):
