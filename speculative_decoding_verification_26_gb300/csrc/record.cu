@@ -52,7 +52,9 @@ constexpr int kRecStage = 16 * kRecStageVecs;
 constexpr int kRecStages = 3;
 constexpr int kMaxGroups = 10;                             // of a thread and row
 constexpr int kMaxima = 4 * kRecConsumers;
-constexpr int kAbove = 768, kTies = 256, kList = kAbove + kTies;
+constexpr int kAbove = 512, kTies = 128, kList = kAbove + kTies;
+static_assert(kMaxGroups * kRecConsumers * 2 <= (kList + 2) * 8, "a list holds the numbers of all groups");
+static_assert(kMaxGroups * kRecConsumers <= 32 * kFinThreads, "a finisher's marks");
 constexpr float kLn2 = 0.693147180559945f;
 
 // order of a float as an unsigned integer, -0 and +0 alike
@@ -424,7 +426,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
       }
       fin_sync();
       if (t == 0) mbar_arrive(&S.freed[b]);
-      // the marked groups, logit by logit
+      // The marked groups, logit by logit.
       unsigned long long* list = S.list[0];
       int above = 0, ties = 0;
       auto take = [&](int e, float x) {      // counted, and listed while there is room
@@ -437,46 +439,64 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
         const int slot = atomicAdd(counter, 1);
         if (slot < room) list[(tie ? kAbove : 0) + slot] = candidate(x, e);
       };
+      // their numbers in order (in the leader's list, which fills up after the counts are
+      // exchanged), so that every thread has its vectors, four at a time, in a fixed order
+      uint16_t* numbers = reinterpret_cast<uint16_t*>(S.list[1]);
+      int before = __popc(marked);
+#pragma unroll
+      for (int off = 1; off < 32; off *= 2) {
+        const int v = __shfl_up_sync(0xffffffffu, before, off);
+        if (lane >= off) before += v;
+      }
+      if (lane == 31) S.part_ties[fw] = before;
+      fin_sync();
+      int nm = 0;
+      before -= __popc(marked);
+      for (int w = 0; w < kFinWarps; ++w) {
+        if (w < fw) before += S.part_ties[w];
+        nm += S.part_ties[w];
+      }
+      for (; marked != 0; marked &= marked - 1) numbers[before++] = (uint16_t)(t + (__ffs((int)marked) - 1) * kFinThreads);
+      fin_sync();
       const uint4* vec = reinterpret_cast<const uint4*>(row + (size_t)sp.head * ES);
-      while (__any_sync(0xffffffffu, marked != 0)) {
-        if (marked != 0) {
-          const int bit = __ffs((int)marked) - 1, g = t + bit * kFinThreads;
-          marked &= marked - 1;
-          const int j0 = sh.lo + g / kRecConsumers * group * kRecStageVecs + g % kRecConsumers;
+      const int per = kRecPer * group;       // vectors of a group: kRecConsumers apart
+      auto place_of = [&](unsigned v) {      // of the v-th vector of the marked groups: its place in the row, or past it
+        const unsigned q = v / (unsigned)per;
+        if ((int)q >= nm) return sh.hi;
+        const int g = numbers[q];
+        return sh.lo + g / kRecConsumers * group * kRecStageVecs + g % kRecConsumers + (int)(v - q * per) * kRecConsumers;
+      };
 #pragma unroll 1
-          for (int q = 0; q < group; ++q) {
-            uint4 w[kRecPer];
+      for (int v0 = t; v0 < nm * per; v0 += 4 * kFinThreads) {               // below 2^23: V < 2^28
+        uint4 w[4];
+        int at[4];
 #pragma unroll
-            for (int u = 0; u < kRecPer; ++u) {
-              const int j = j0 + (q * kRecPer + u) * kRecConsumers;
-              w[u] = j < sh.hi ? vec[j] : minus_infinity<DT>();
-            }
+        for (int u = 0; u < 4; ++u) {
+          at[u] = place_of((unsigned)(v0 + u * kFinThreads));
+          w[u] = at[u] < sh.hi ? vec[at[u]] : minus_infinity<DT>();
+        }
+#pragma unroll 1
+        for (int u = 0; u < 4 && v0 + u * kFinThreads < nm * per; ++u) {
+          const uint4 old = u == 0 ? w[0] : u == 1 ? w[1] : u == 2 ? w[2] : w[3];
+          const int j = u == 0 ? at[0] : u == 1 ? at[1] : u == 2 ? at[2] : at[3];
+          uint4 one[1] = {old};
+          uint32_t mark = 0;
+          if (vec_max<DT>(old) >= least) {
+            mark = mark_from<DT>(one, least);
+            drop_marked<DT>(one, mark);
+          }
 #pragma unroll
-            for (int u = 0; u < kRecPer; ++u) {
-              uint32_t mark = 0;
-              if (vec_max<DT>(w[u]) >= least) {
-                uint4 one[1] = {w[u]};
-                mark = mark_from<DT>(one, least);
-                drop_marked<DT>(one, mark);
-                const uint4 old = w[u];
-                w[u] = one[0];
-                while (mark != 0) {
-                  const int k = __ffs((int)mark) - 1;
-                  mark &= mark - 1;
-                  const uint32_t word = k < PER / 2 ? (k < PER / 4 ? old.x : old.y) : (k < PER * 3 / 4 ? old.z : old.w);
-                  take(sp.head + (j0 + (q * kRecPer + u) * kRecConsumers) * PER + k,
-                       DT == SPEC_BF16 ? (k & 1 ? bf16_hi(word) : bf16_lo(word)) : __uint_as_float(word));
-                }
-              }
-#pragma unroll
-              for (int k = 0; k < PER / 2; ++k) {
-                const float2 x = vec_pair<DT>(w[u], k);
-                sum += ex2((x.x - top) * c) + ex2((x.y - top) * c);
-              }
-            }
+          for (int k = 0; k < PER / 2; ++k) {
+            const float2 x = vec_pair<DT>(one[0], k);
+            sum += ex2((x.x - top) * c) + ex2((x.y - top) * c);
+          }
+          for (; mark != 0; mark &= mark - 1) {
+            const int k = __ffs((int)mark) - 1;
+            const uint32_t word = k < PER / 2 ? (k < PER / 4 ? old.x : old.y) : (k < PER * 3 / 4 ? old.z : old.w);
+            take(sp.head + j * PER + k,
+                 DT == SPEC_BF16 ? (k & 1 ? bf16_hi(word) : bf16_lo(word)) : __uint_as_float(word));
           }
         }
-        __syncwarp();
       }
       const int ends = sh.ends ? sp.head + (V - sp.tail0) : 0;               // single elements
       if (t < ends) {
@@ -689,9 +709,14 @@ cudaError_t launch_as(const RecordParams& P, int dev, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, record_kernel<DT, CS>, P, group);
 }
 
+// Two CTAs share a row of 256 KB or more even where the rows fill the GPU: the work
+// after the stream is shared, and the last round of rows is shorter (512 x 151936
+// bf16: 43.6 us, 46.4 with one; 600 x 128256 fp32: 119 and 146; but 2048 x 32000
+// bf16, rows of 64 KB: 89 us, 53 with one).
 template <int DT>
 cudaError_t launch_of(const RecordParams& P, int dev, int nsm, cudaStream_t s) {
-  const int cs = row_cluster(P.n, P.V, RowType<DT>::ES, nsm);
+  int cs = row_cluster(P.n, P.V, RowType<DT>::ES, nsm);
+  if (cs == 1 && (long long)P.V * RowType<DT>::ES >= 256 * 1024) cs = 2;
   if (cs == 8) return launch_as<DT, 8>(P, dev, s);
   if (cs == 4) return launch_as<DT, 4>(P, dev, s);
   if (cs == 2) return launch_as<DT, 2>(P, dev, s);
