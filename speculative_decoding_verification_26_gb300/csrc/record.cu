@@ -605,12 +605,14 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
   } else {                                   // consumers
     RecRing at;
     int i = 0;
+    float T = first < P.n && P.temperature ? P.temperature[first] : 1.f;      // a row ahead: a load takes 2 us here
     for (int r = first; r < P.n; r += step, ++i) {
       const int b = i & 1;
       const unsigned char* row = P.logits + (size_t)r * V * ES;
       const RowSpan sp = row_span<DT>(row, V);
       const RowShare sh = row_share<CS>(sp, rank);
-      const float given = P.temperature ? P.temperature[r] : 1.f;
+      const float given = T;
+      if (P.temperature && r + step < P.n) T = P.temperature[r + step];
       const int ends = sh.ends ? sp.head + (V - sp.tail0) : 0;
       const float end_x = tid < ends ? row_logit<DT>(row, tid < sp.head ? tid : sp.tail0 + (tid - sp.head)) : -INFINITY;
       const float c = scale_split(temperature_ok(given) ? given : 1.f).c;

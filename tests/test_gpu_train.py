@@ -127,6 +127,13 @@ def test_record_masks_of_finite_values(sv, n, V, dtype):
     check_record(sv, x, K, torch.rand(n, generator=g) + 0.5)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V", [(2, 2500003), (20, 600000)])
+def test_record_of_long_rows(sv, n, V, dtype):
+    """Several stages to a group, and records of the largest size."""
+    check_record(sv, rows(n, V, dtype, 41), 256, torch.rand(n, generator=gen(6)) + 0.5)
+
+
 @pytest.mark.parametrize("shift", [1, 3, 5])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_record_of_rows_off_alignment(sv, dtype, shift):
@@ -210,6 +217,24 @@ def test_distill_batches(sv, n, V, K, dtype):
     d = make_distill(n, V, K, dtype, 7)
     d["w"][::7] = 0
     check_distill(sv, d, 0.7, 1.0, 0.1)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V", [(2, 1 << 20), (3, (1 << 20) - 3), (6, 400001)])
+def test_distill_long_rows(sv, n, V, dtype):
+    """Up to the largest vocabulary: shares that do not stay in shared memory."""
+    check_distill(sv, make_distill(n, V, 200, dtype, 8), 0.7, 1.0, 0.1)
+    check_distill(sv, make_distill(n, V, 40, dtype, 8), 1.0, 0.0, 0.1, grad=False)
+
+
+def test_distill_more_entries_than_tokens(sv):
+    """K past V: the record ends with entries that are left out."""
+    d = make_distill(3, 7, 7, torch.float32, 14)
+    for k, v in (("idx", -1), ("top", NAN)):
+        t = torch.full((3, 100), v, dtype=d[k].dtype)
+        t[:, 50:57] = d[k]
+        d[k] = t
+    check_distill(sv, d, 1.0, 1.0, 1.0)
 
 
 def test_distill_loss_alone_is_the_same(sv):
