@@ -52,8 +52,8 @@ constexpr int kRecStage = 16 * kRecStageVecs;
 constexpr int kRecStages = 3;
 constexpr int kMaxGroups = 10;                             // of a thread and row
 constexpr int kMaxima = 4 * kRecConsumers;
-constexpr int kAbove = 512, kTies = 128, kList = kAbove + kTies;
-static_assert(kMaxGroups * kRecConsumers * 2 <= (kList + 2) * 8, "a list holds the numbers of all groups");
+constexpr int kAbove = 768, kTies = 256, kList = kAbove + kTies;             // a power of two: lists are sorted in place
+static_assert(kMaxGroups * kRecConsumers * 2 <= kList * 8, "a list holds the numbers of all groups");
 static_assert(kMaxGroups * kRecConsumers <= 32 * kFinThreads, "a finisher's marks");
 constexpr float kLn2 = 0.693147180559945f;
 
@@ -113,11 +113,12 @@ __device__ __forceinline__ float warp_sum(float v) {
 
 // A bound of a share's want-th largest logit from N of its maxima per lane: a key
 // that `want` or more of them reach, at most an eighth more where there is one.
-// Keys of bf16 logits are told apart by their upper halves.  A bound of
-// kKeyNegInf + 1 takes every finite logit (-inf is never recorded).
+// Keys are told apart by their upper 16 bits for bf16 logits and 20 for fp32 (the
+// bound is the least key of those).  A bound of kKeyNegInf + 1 takes every finite
+// logit (-inf is never recorded).
 template <int DT, int N>
 __device__ __forceinline__ uint32_t bound_of(const uint32_t (&key)[N], int want) {
-  constexpr int shift = DT == SPEC_BF16 ? 16 : 0;
+  constexpr int shift = DT == SPEC_BF16 ? 16 : 12;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
 #pragma unroll
   for (int j = 0; j < N; ++j) { lo = min(lo, key[j]); hi = max(hi, key[j]); }
@@ -153,7 +154,8 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t (&key)[N], int want)
     else { hi = p1 - 1; n = 1 << 30; }
     if (n <= want + want / 8) break;
   }
-  return shift == 0 ? lo : lo << 16 | (lo & 0x8000u ? 0u : 0xFFFFu);
+  if constexpr (DT == SPEC_F32) return lo << shift;
+  else return lo << 16 | (lo & 0x8000u ? 0u : 0xFFFFu);      // of a bf16 value
 }
 // Both bounds of a share (for K, and for its part of K) and its maximum, NaN first.
 template <int DT, int N>
@@ -263,44 +265,59 @@ __device__ __forceinline__ void rank_row(const RecordParams& P, RecShared& S, in
   const float c = scale_split(info.T).c;
   auto weight = [&](float x) { return ex2((x - info.m) * c); };
   const int n = above + (listed_ties ? ties : 0);
-  if (t == 0) list[n] = 0;                   // the keys are read by twos
-  fin_sync();
-  constexpr int kEach = kList / kFinThreads;
-  int place[kEach];
-  unsigned long long mine[kEach];
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    if (q * kFinThreads >= n) break;
-    const int i = t + q * kFinThreads;
-    mine[q] = i < n ? list[i] : 0;
-    int before = 0;
+  auto record = [&](int place, unsigned long long key) {
+    const float x = key_value((uint32_t)(key >> 32));
+    const int e = (int)~(uint32_t)key;
+    top[place] = x == 0.f ? row_logit<DT>(row, e) : x;       // the key has lost a zero's sign
+    ti[place] = e;
+  };
+  float extra = 0.f;                         // weights past K, in the order of their places
+  if (n <= kFinThreads) {
+    // a candidate's place: the number of candidates before it
+    if (t == 0) list[n] = 0;                 // the keys are read by twos
+    fin_sync();
+    const unsigned long long mine = t < n ? list[t] : 0;
+    int place = 0;
     const ulonglong2* pair = reinterpret_cast<const ulonglong2*>(list);
 #pragma unroll 4
     for (int j = 0; j < (n + 1) / 2; ++j) {
       const ulonglong2 p = pair[j];
-      before += (p.x > mine[q]) + (p.y > mine[q]);
+      place += (p.x > mine) + (p.y > mine);
     }
-    place[q] = before;
-  }
-  fin_sync();                                // the list is read: it takes the weights past K, by place
-  float* left = reinterpret_cast<float*>(list);
-#pragma unroll
-  for (int q = 0; q < kEach; ++q) {
-    if (q * kFinThreads >= n) break;
-    if (t + q * kFinThreads >= n) continue;
-    const float x = key_value((uint32_t)(mine[q] >> 32));
-    const int e = (int)~(uint32_t)mine[q];
-    if (place[q] < K) {
-      top[place[q]] = x == 0.f ? row_logit<DT>(row, e) : x;  // the key has lost a zero's sign
-      ti[place[q]] = e;
-    } else {
-      left[place[q] - K] = weight(x);
+    fin_sync();                              // the list is read: it takes the weights past K, by place
+    float* left = reinterpret_cast<float*>(list);
+    if (t < n) {
+      if (place < K) record(place, mine);
+      else left[place - K] = weight(key_value((uint32_t)(mine >> 32)));
     }
-  }
-  float extra = 0.f;
-  if (n > K) {
+    if (n > K) {
+      fin_sync();
+      if (t < n - K) extra = left[t];
+    }
+  } else {
+    // more candidates than finishers are sorted (305: 6000 clocks; counting took 17000)
+    int size = 2 * kFinThreads;
+    while (size < n) size *= 2;
+    for (int i = n + t; i < size; i += kFinThreads) list[i] = 0;
     fin_sync();
-    for (int i = t; i < n - K; i += kFinThreads) extra += left[i];
+#pragma unroll 1
+    for (int width = 2; width <= size; width *= 2)
+#pragma unroll 1
+      for (int gap = width / 2; gap > 0; gap /= 2) {
+        for (int p = t; p < size / 2; p += kFinThreads) {
+          const int i = 2 * p - (p & (gap - 1)), j = i + gap;
+          const unsigned long long a = list[i], b = list[j];
+          if ((a < b) == ((i & width) == 0)) { list[i] = b; list[j] = a; }
+        }
+        fin_sync();
+      }
+    for (int i = t; i < n; i += kFinThreads) {
+      const unsigned long long key = list[i];
+      if (i < K) record(i, key);
+      else extra += weight(key_value((uint32_t)(key >> 32)));
+    }
+  }
+  if (n > K) {
     extra = warp_sum(extra);
     if (lane == 0) S.part[warp] = extra;
     fin_sync();
