@@ -287,9 +287,9 @@ int spec_gamma_select(const float* signals, const float* comp, const float* mode
  * row) ends with entries of logit -inf and index -1.
  *   K           1 <= K <= min(V, SPEC_MAX_TOPK);
  *   temperature [n] fp32 or NULL (= 1);
- *   status      0, SPEC_ST_NONFINITE (a NaN or +inf, or no finite logit) or
- *     SPEC_ST_BAD_TEMPERATURE; such a row has NaN logits, indices -1 and a NaN
- *     tail.
+ *   status      0, SPEC_ST_NONFINITE (a NaN or +inf, or no finite logit),
+ *     SPEC_ST_BAD_TEMPERATURE or SPEC_ST_TIMEOUT (an internal wait hit its time
+ *     limit); such a row has NaN logits, indices -1 and a NaN tail.
  * No workspace.  Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^30], V
  * outside [2, 2^28), K, dtype, NULL required pointers, misalignment),
  * SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
@@ -347,21 +347,21 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
  *   lse    [n] fp32: written by the forward call, read by the backward call;
  *   grad_loss [n] fp32 or NULL (= 1); a row of grad_loss 0 takes no part;
  *   grad_hidden [n, H], grad_weight [V, H] bf16, written; either may be NULL (a
- *     frozen projection), not both.  G is rounded to bf16 once, before the two
- *     products that read it;
+ *     frozen projection), not both.  grad_hidden may be `hidden` itself; any other
+ *     overlap of the gradients with weight, hidden or one another is refused.  G is
+ *     rounded to bf16 once, before the two products that read it;
  *   status [n] or NULL (forward): 0, SPEC_ST_BAD_TOKEN (label outside [-1, V):
  *     loss and lse NaN), SPEC_ST_NONFINITE (a logit of the row is NaN or +inf,
  *     or none is finite: loss and lse NaN), SPEC_ST_TIMEOUT (an internal wait hit
  *     its time limit; the backward call then fills its outputs with NaN).  The
- *     backward call leaves out rows
- *     with a bad label or an lse that is not finite.
+ *     backward call leaves out rows with a bad label or an lse that is not finite.
  *   workspace: spec_linear_ce_workspace_bytes(n, H, V, backward) bytes, 256-byte
  *     aligned, no initial contents.  Calls that share one must not overlap on
  *     the device; that holds for captured graphs too.
  * Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^20], H outside [8, 65536]
  * or not a multiple of 8, V outside [2, 2^28), ceil(n / 256) ceil(V / 256) of
- * 2^30 or more, dtype, NULL required pointers,
- * misalignment), SPEC_ERR_WORKSPACE, SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
+ * 2^30 or more, dtype, NULL required pointers, misalignment, overlap),
+ * SPEC_ERR_WORKSPACE, SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
 size_t spec_linear_ce_workspace_bytes(int n, int H, int V, int backward);
 int spec_linear_ce_forward(const void* hidden, const void* weight, int dtype, int n, int H, int V,
                            const int32_t* label, float* loss, float* lse, int32_t* status,

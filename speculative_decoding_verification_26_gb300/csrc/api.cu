@@ -82,6 +82,11 @@ int current_sms(int* device) {
   return g_dev[dev].sms;
 }
 
+bool overlap(const void* a, size_t an, const void* b, size_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + bn && y < x + an;
+}
+
 bool ce_sizes_ok(int n, int H, int V) {
   // tiles of 256 x 256 logits are counted in 32 bits
   return n >= 1 && n <= (1 << 20) && H >= 8 && H <= 65536 && H % 8 == 0 && V >= 2 && V < (1 << 28) &&
@@ -440,8 +445,7 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
   const size_t es = dtype == SPEC_BF16 ? 2 : 4;
   if (!aligned(logits, es) || !aligned(grad_logits, es)) return SPEC_ERR_INVALID_ARG;
   if (grad_logits && grad_logits != logits) {        // in place, or apart
-    const uintptr_t a = reinterpret_cast<uintptr_t>(logits), b = reinterpret_cast<uintptr_t>(grad_logits);
-    if ((a < b ? b - a : a - b) < (size_t)n * V * es) return SPEC_ERR_INVALID_ARG;
+    if (overlap(logits, (size_t)n * V * es, grad_logits, (size_t)n * V * es)) return SPEC_ERR_INVALID_ARG;
   }
   int ctas = 0;
   const int ds = device_state(&ctas);
@@ -505,6 +509,12 @@ int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, i
   const void* ptrs4[] = {label, lse, grad_loss};
   for (const void* p : ptrs4)
     if (!aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
+  // rows of grad_weight are written while others of weight are still to be read
+  const size_t nh = 2 * (size_t)n * H, vh = 2 * (size_t)V * H;
+  if (overlap(grad_weight, vh, weight, vh) || overlap(grad_weight, vh, hidden, nh) ||
+      overlap(grad_hidden, nh, weight, vh) || overlap(grad_hidden, nh, grad_weight, vh) ||
+      (grad_hidden != hidden && overlap(grad_hidden, nh, hidden, nh)))
+    return SPEC_ERR_INVALID_ARG;
   CeParams P{};
   P.n = n; P.H = H; P.V = V;
   if (!workspace || workspace_bytes < ce_layout(P, true, workspace)) return SPEC_ERR_WORKSPACE;

@@ -124,6 +124,8 @@ def test_record_masks_of_finite_values(sv, n, V, dtype):
         x[6] = (torch.arange(V) % 2048 < 8).to(dtype) * 9 + x[6] * 0.01
         x[7] = (torch.arange(V) % 1000 < 300).to(dtype) * 9 + x[7] * 0.1
         x[8] = -(torch.arange(V) % 3).to(dtype)
+        x[9] = torch.where(torch.rand(V, generator=g) < 20.0 / V, x[9], torch.tensor(-1e9, dtype=dtype))
+        x[10] = torch.where(torch.rand(V, generator=g) < 20.0 / V, x[10], torch.tensor(-1e-9, dtype=dtype))
     check_record(sv, x, K, torch.rand(n, generator=g) + 0.5)
 
 
@@ -503,6 +505,19 @@ def test_ce_one_gradient_alone(sv):
     assert list(a) == ["grad_hidden"] and list(b) == ["grad_weight"]
     assert torch.equal(a["grad_hidden"], both["grad_hidden"]) and torch.equal(b["grad_weight"], both["grad_weight"])
     check_ce_backward(sv, h, w, label, None)
+
+
+def test_ce_gradient_over_its_hidden_states(sv):
+    h, w, label = make_ce(40, 64, 500, 15)
+    g = torch.rand(40, generator=gen(8))
+    a = check_ce_backward(sv, h, w, label, g)
+    hd, wd, ld, gd = cuda(h, w, label, g)
+    lse = sv.linear_ce_forward(hd, wd, ld)["lse"]
+    b = sv.linear_ce_backward(hd, wd, ld, lse, gd, out={"grad_hidden": hd})
+    assert b["grad_hidden"].data_ptr() == hd.data_ptr()
+    assert torch.equal(a["grad_hidden"], hd) and torch.equal(a["grad_weight"], b["grad_weight"])
+    with pytest.raises(sv.SpecVerifyError):
+        sv.linear_ce_backward(h.cuda(), wd, ld, lse, gd, out={"grad_weight": wd})
 
 
 def test_ce_shared_labels(sv):
