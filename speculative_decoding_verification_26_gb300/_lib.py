@@ -353,26 +353,43 @@ MAX_TOPK = 256
 DISTILL_MAX_V = 1 << 20
 
 
-# The calls below take a few microseconds on the device for few rows, so their host
-# side is kept short: entry points looked up once, addresses as plain integers, and
-# the raw handle of the current stream (torch.cuda.current_stream builds an object
-# for 2 us).
-_entry: dict = {}
+class _Hot:
+    """What the calls below need of torch and the library, looked up once.  They
+    take a few microseconds on the device for few rows, so their host side is kept
+    short: addresses as plain integers, checks with the common case first, and the
+    raw handle of the current stream (torch.cuda.current_stream builds an object)."""
+
+    def __init__(self):
+        import torch
+        L = lib()
+        self.torch, self.empty = torch, torch.empty
+        self.f32, self.i32, self.bf16 = torch.float32, torch.int32, torch.bfloat16
+        self.code = {torch.float32: F32, torch.bfloat16: BF16}
+        self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+        self.topk, self.distill = L.spec_topk_logits, L.spec_distill_topk
+        self.ce_forward, self.ce_backward = L.spec_linear_ce_forward, L.spec_linear_ce_backward
 
 
-def _call(dev, name, *args):
-    """Call the C entry point with `dev` current and its current stream last."""
-    torch = _torch()
-    f = _entry.get(name)
-    if f is None:
-        f = _entry[name] = getattr(lib(), name)
-    if torch._C._cuda_getDevice() == dev.index:
-        rc = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+_hot_state = None
+
+
+def _hot():
+    global _hot_state
+    if _hot_state is None:
+        _hot_state = _Hot()
+    return _hot_state
+
+
+def _call(h, dev, f, *args):
+    """Call the C entry point f with `dev` current and its current stream last."""
+    i = dev.index
+    if h.device() == i:
+        rc = f(*args, h.stream(i))
     else:
-        with torch.cuda.device(dev):
-            rc = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+        with h.torch.cuda.device(dev):
+            rc = f(*args, h.stream(i))
     if rc != OK:
-        raise SpecVerifyError(rc, name)
+        raise SpecVerifyError(rc, f.__name__)
 
 
 def _addr(t):
@@ -380,16 +397,16 @@ def _addr(t):
 
 
 def _want(t, name, dtype, shape, device):
-    """_check, with the common case first."""
-    if t is not None and not (t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous()):
+    """_check of a tensor or None, with the common case first."""
+    if t is not None and not (t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous()):
         _check(t, name, dtype, shape, device)
 
 
-def _result(o, key, shape, dtype, dev):
+def _result(out, key, shape, dtype, dev):
     """out[key], checked, or a new tensor."""
-    t = o.get(key) if o else None
+    t = out.get(key)
     if t is None:
-        return _torch().empty(shape, dtype=dtype, device=dev)
+        return _hot().empty(shape, dtype=dtype, device=dev)
     _check(t, key, dtype, shape, dev)
     return t
 
@@ -399,19 +416,24 @@ def topk_logits(logits, K, temperature=None, *, out=None):
     temperature [n] fp32 or None; returns {"top_logits": [n, K] fp32,
     "top_index": [n, K] int32, "tail_lse": [n], "status": [n]} (see
     spec_topk_logits)."""
-    torch = _torch()
+    h = _hot()
+    f32, i32 = h.f32, h.i32
+    _check(logits, "logits")
     V = logits.shape[-1]
     n = logits.numel() // V
     dev = logits.device
-    f32 = torch.float32
-    _check(logits, "logits")
-    _want(temperature, "temperature", f32, (n,), dev)
-    top = _result(out, "top_logits", (n, K), f32, dev)
-    idx = _result(out, "top_index", (n, K), torch.int32, dev)
-    tail = _result(out, "tail_lse", (n,), f32, dev)
-    st = _result(out, "status", (n,), torch.int32, dev)
-    _call(dev, "spec_topk_logits", logits.data_ptr(), _dtype_code(logits), n, V, K, _addr(temperature),
-          top.data_ptr(), idx.data_ptr(), tail.data_ptr(), st.data_ptr())
+    if temperature is not None:
+        _want(temperature, "temperature", f32, (n,), dev)
+    if out is None:
+        empty = h.empty
+        top, idx = empty((n, K), dtype=f32, device=dev), empty((n, K), dtype=i32, device=dev)
+        tail, st = empty((n,), dtype=f32, device=dev), empty((n,), dtype=i32, device=dev)
+    else:
+        top, idx = _result(out, "top_logits", (n, K), f32, dev), _result(out, "top_index", (n, K), i32, dev)
+        tail, st = _result(out, "tail_lse", (n,), f32, dev), _result(out, "status", (n,), i32, dev)
+    code = h.code.get(logits.dtype)
+    _call(h, dev, h.topk, logits.data_ptr(), _dtype_code(logits) if code is None else code, n, V, K,
+          _addr(temperature), top.data_ptr(), idx.data_ptr(), tail.data_ptr(), st.data_ptr())
     return {"top_logits": top, "top_index": idx, "tail_lse": tail, "status": st}
 
 
@@ -422,26 +444,33 @@ def distill_topk(logits, top_logits, top_index, tail_lse=None, *, label=None, ro
     int32, row_weight [n], temperature [n] fp32, each optional.  Returns
     {"loss": [n], "parts": [n, 3] (KL, TV, CE), "status": [n]} and "grad" (as
     `logits`; out={"grad": logits} overwrites them).  See spec_distill_topk."""
-    torch = _torch()
+    h = _hot()
+    f32, i32 = h.f32, h.i32
+    _check(logits, "logits")
     V = logits.shape[-1]
     n = logits.numel() // V
     dev = logits.device
-    f32, i32 = torch.float32, torch.int32
     K = top_logits.shape[-1]
-    _check(logits, "logits")
+    rows = (n,)
     _want(top_logits, "top_logits", f32, (n, K), dev)
     _want(top_index, "top_index", i32, (n, K), dev)
-    _want(tail_lse, "tail_lse", f32, (n,), dev)
-    _want(label, "label", i32, (n,), dev)
-    _want(row_weight, "row_weight", f32, (n,), dev)
-    _want(temperature, "temperature", f32, (n,), dev)
-    loss = _result(out, "loss", (n,), f32, dev)
-    parts = _result(out, "parts", (n, 3), f32, dev)
-    st = _result(out, "status", (n,), i32, dev)
-    g = _result(out, "grad", logits.shape, logits.dtype, dev) if grad else None
-    _call(dev, "spec_distill_topk", logits.data_ptr(), _dtype_code(logits), n, V, K, top_logits.data_ptr(),
-          top_index.data_ptr(), _addr(tail_lse), _addr(label), _addr(row_weight), _addr(temperature), kl, tv, ce,
-          loss.data_ptr(), parts.data_ptr(), _addr(g), st.data_ptr())
+    _want(tail_lse, "tail_lse", f32, rows, dev)
+    _want(label, "label", i32, rows, dev)
+    _want(row_weight, "row_weight", f32, rows, dev)
+    _want(temperature, "temperature", f32, rows, dev)
+    if out is None:
+        empty = h.empty
+        loss, parts = empty(rows, dtype=f32, device=dev), empty((n, 3), dtype=f32, device=dev)
+        st = empty(rows, dtype=i32, device=dev)
+        g = empty(logits.shape, dtype=logits.dtype, device=dev) if grad else None
+    else:
+        loss, parts = _result(out, "loss", rows, f32, dev), _result(out, "parts", (n, 3), f32, dev)
+        st = _result(out, "status", rows, i32, dev)
+        g = _result(out, "grad", logits.shape, logits.dtype, dev) if grad else None
+    code = h.code.get(logits.dtype)
+    _call(h, dev, h.distill, logits.data_ptr(), _dtype_code(logits) if code is None else code, n, V, K,
+          top_logits.data_ptr(), top_index.data_ptr(), _addr(tail_lse), _addr(label), _addr(row_weight),
+          _addr(temperature), kl, tv, ce, loss.data_ptr(), parts.data_ptr(), _addr(g), st.data_ptr())
     r = {"loss": loss, "parts": parts, "status": st}
     if grad:
         r["grad"] = g
@@ -459,32 +488,31 @@ def linear_ce_workspace(n, H, V, device, *, backward):
     """A cached workspace of linear_ce_forward / linear_ce_backward for these
     sizes (reused by calls on the same stream; calls sharing it must not overlap
     on the device).  Under stream capture it is new: a graph keeps its own."""
-    torch = _torch()
-    device = torch.device(device)
+    h = _hot()
+    device = h.torch.device(device)
     need = linear_ce_workspace_bytes(n, H, V, backward)
     if need == 0:
         raise ValueError("sizes outside the library limits")
-    make = lambda: torch.empty(need, dtype=torch.uint8, device=device)   # noqa: E731
-    if torch.cuda.is_current_stream_capturing():
-        return make()
-    key = (device.index, torch._C._cuda_getCurrentRawStream(device.index))
+    if h.torch.cuda.is_current_stream_capturing():
+        return h.empty(need, dtype=h.torch.uint8, device=device)
+    i = h.device() if device.index is None else device.index
+    key = (i, h.stream(i))
     ws = _ce_ws_cache.get(key)
     if ws is None or ws.numel() < need:
         _ce_ws_cache.pop(key, None)
-        ws = _ce_ws_cache[key] = make()
+        ws = _ce_ws_cache[key] = h.empty(need, dtype=h.torch.uint8, device=device)
     return ws
 
 
-def _ce_inputs(hidden, weight, label):
-    torch = _torch()
+def _ce_inputs(h, hidden, weight, label):
     if hidden.dim() != 2 or weight.dim() != 2:
         raise ValueError("hidden is [n, H] and weight [V, H]")
     n, H = hidden.shape
     V = weight.shape[0]
     dev = hidden.device
-    _check(hidden, "hidden", torch.bfloat16, (n, H), dev)
-    _want(weight, "weight", torch.bfloat16, (V, H), dev)
-    _want(label, "label", torch.int32, (n,), dev)
+    _check(hidden, "hidden", h.bf16)
+    _want(weight, "weight", h.bf16, (V, H), dev)
+    _want(label, "label", h.i32, (n,), dev)
     return n, H, V, dev
 
 
@@ -492,16 +520,16 @@ def linear_ce_forward(hidden, weight, label, *, ws=None, out=None):
     """Cross entropy of the projection hidden [n, H] times weight [V, H] (bf16)
     against label [n] int32 (-1: the row takes no part), without its logits.
     Returns {"loss": [n], "lse": [n], "status": [n]} (see spec_linear_ce_forward)."""
-    torch = _torch()
-    n, H, V, dev = _ce_inputs(hidden, weight, label)
-    loss = _result(out, "loss", (n,), torch.float32, dev)
-    lse = _result(out, "lse", (n,), torch.float32, dev)
-    st = _result(out, "status", (n,), torch.int32, dev)
+    h = _hot()
+    n, H, V, dev = _ce_inputs(h, hidden, weight, label)
+    o = out or {}
+    loss, lse = _result(o, "loss", (n,), h.f32, dev), _result(o, "lse", (n,), h.f32, dev)
+    st = _result(o, "status", (n,), h.i32, dev)
     if ws is None:
         ws = linear_ce_workspace(n, H, V, dev, backward=False)
     else:
-        _check(ws, "ws", torch.uint8, device=dev)
-    _call(dev, "spec_linear_ce_forward", hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
+        _check(ws, "ws", h.torch.uint8, device=dev)
+    _call(h, dev, h.ce_forward, hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
           loss.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel())
     return {"loss": loss, "lse": lse, "status": st}
 
@@ -512,17 +540,18 @@ def linear_ce_backward(hidden, weight, label, lse, grad_loss=None, *, need_hidde
     linear_ce_forward returned it, grad_loss [n] fp32 or None (= 1).  Returns
     {"grad_hidden": [n, H] bf16, "grad_weight": [V, H] bf16}, without the one
     that is not needed (see spec_linear_ce_backward)."""
-    torch = _torch()
-    n, H, V, dev = _ce_inputs(hidden, weight, label)
-    _want(lse, "lse", torch.float32, (n,), dev)
-    _want(grad_loss, "grad_loss", torch.float32, (n,), dev)
-    gh = _result(out, "grad_hidden", (n, H), torch.bfloat16, dev) if need_hidden else None
-    gw = _result(out, "grad_weight", (V, H), torch.bfloat16, dev) if need_weight else None
+    h = _hot()
+    n, H, V, dev = _ce_inputs(h, hidden, weight, label)
+    _want(lse, "lse", h.f32, (n,), dev)
+    _want(grad_loss, "grad_loss", h.f32, (n,), dev)
+    o = out or {}
+    gh = _result(o, "grad_hidden", (n, H), h.bf16, dev) if need_hidden else None
+    gw = _result(o, "grad_weight", (V, H), h.bf16, dev) if need_weight else None
     if ws is None:
         ws = linear_ce_workspace(n, H, V, dev, backward=True)
     else:
-        _check(ws, "ws", torch.uint8, device=dev)
-    _call(dev, "spec_linear_ce_backward", hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
+        _check(ws, "ws", h.torch.uint8, device=dev)
+    _call(h, dev, h.ce_backward, hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
           lse.data_ptr(), _addr(grad_loss), _addr(gh), _addr(gw), ws.data_ptr(), ws.numel())
     r = {}
     if need_hidden:

@@ -629,7 +629,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         if (!zero)
           for (int k = lane; k <= K; k += 32) {
             const int e = S.fix_idx[k], o = e - sp.head;
-            if (e >= 0 && (o < 0 || e >= sp.tail0 ? sh.ends : o >= sh.lo * PER && o < sh.hi * PER))
+            if (e >= 0 && e < V && (o < 0 || e >= sp.tail0 ? sh.ends : o >= sh.lo * PER && o < sh.hi * PER))
               store_logit<DT>(grow, e, S.fix_g[k]);
           }
       }

@@ -65,6 +65,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;   // order_key(-inf)
+// order_key of the type's lowest value: a bound that takes every finite logit
+template <int DT>
+constexpr uint32_t kKeyLowest = DT == SPEC_BF16 ? 0x0080FFFFu : 0x00800000u;
 // a candidate: larger comes first
 __device__ __forceinline__ unsigned long long candidate(float x, int e) {
   return (unsigned long long)order_key(x) << 32 | (uint32_t)~e;
@@ -93,6 +96,7 @@ struct RecShared {
     float below;
     uint32_t bound;
   } counted;                                 // by recount
+  int stop;                                  // the finishers' decision after a failed wait
   int failed;
 };
 
@@ -111,11 +115,11 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-// A bound of a share's want-th largest logit from N of its maxima per lane: a key
-// that `want` or more of them reach, at most an eighth more where there is one.
-// Keys are told apart by their upper 16 bits for bf16 logits and 20 for fp32 (the
-// bound is the least key of those).  A bound of kKeyNegInf + 1 takes every finite
-// logit (-inf is never recorded).
+// A bound of a share's want-th largest logit from N of its maxima per lane: one of
+// them that `want` or more reach, at most an eighth more where there is one.  Keys are
+// told apart by their upper 16 bits for bf16 logits and 20 for fp32; the bound is the
+// least of those found, whole: a value that many logits share (a mask) is met exactly.
+// -inf is never recorded: a bound is at least kKeyLowest.
 template <int DT, int N>
 __device__ __forceinline__ uint32_t bound_of(const uint32_t (&key)[N], int want) {
   constexpr int shift = DT == SPEC_BF16 ? 16 : 12;
@@ -130,7 +134,7 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t (&key)[N], int want)
     int n = 0;
 #pragma unroll
     for (int j = 0; j < N; ++j) n += (key[j] >> shift) >= lo;
-    if ((int)__reduce_add_sync(0xffffffffu, (unsigned)n) < want) hi = lo;
+    if ((int)__reduce_add_sync(0xffffffffu, (unsigned)n) < want) return kKeyLowest<DT>;
   }
   while (lo < hi) {                          // lo is reached by `want` or more, hi + 1 by fewer
     // four keys between at a time; two counts to a word (at most 1024 each)
@@ -154,8 +158,11 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t (&key)[N], int want)
     else { hi = p1 - 1; n = 1 << 30; }
     if (n <= want + want / 8) break;
   }
-  if constexpr (DT == SPEC_F32) return lo << shift;
-  else return lo << 16 | (lo & 0x8000u ? 0u : 0xFFFFu);      // of a bf16 value
+  uint32_t exact = 0xFFFFFFFFu;
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+    if (key[j] >> shift >= lo) exact = min(exact, key[j]);
+  return __reduce_min_sync(0xffffffffu, exact);
 }
 // Both bounds of a share (for K, and for its part of K) and its maximum, NaN first.
 template <int DT, int N>
@@ -170,7 +177,7 @@ __device__ __forceinline__ float bounds_of(const float* maxima, int K, int part,
   }
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
-  whole = share = kKeyNegInf + 1;
+  whole = share = kKeyLowest<DT>;
   if (isfinite(m)) {
     if (K <= 32 * N) whole = bound_of<DT>(key, K);
     share = part == K ? whole : bound_of<DT>(key, part);
@@ -406,13 +413,17 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
     }
   } else if (warp > kRecWarps) {             // finishers
     const int t = tid - kRecConsumers - 32, fw = t >> 5;
-    int i = 0, live = 0;                     // rows, and rows not refused (the same in every CTA of the cluster)
-    for (int r = first; r < P.n; r += step, ++i) {
+    int i = 0, live = 0, r = first;          // rows, and rows not refused (the same in every CTA of the cluster)
+    for (; r < P.n; r += step, ++i) {
       const int b = i & 1;
       const uint32_t turn = (i >> 1) & 1;
       bounded_wait(&S.bounded[b], turn, failed);
-      if (t == 0) S.above = S.ties = 0;
+      if (t == 0) {
+        S.above = S.ties = 0;
+        S.stop = *failed;
+      }
       fin_sync();
+      if (S.stop) break;                     // the same for all: nothing of this row is known
       const RecRow info = S.row[b];
       const unsigned char* row = P.logits + (size_t)r * V * ES;
       const RowSpan sp = row_span<DT>(row, V);
@@ -484,7 +495,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
         return sh.lo + g / kRecConsumers * group * kRecStageVecs + g % kRecConsumers + (int)(v - q * per) * kRecConsumers;
       };
 #pragma unroll 1
-      for (int v0 = t; v0 < nm * per; v0 += 4 * kFinThreads) {               // below 2^23: V < 2^28
+      for (int v0 = t; v0 < nm * per; v0 += 4 * kFinThreads) {               // below 2^26: V < 2^28
         uint4 w[4];
         int at[4];
 #pragma unroll
@@ -551,6 +562,9 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
         fin_sync();
         if (t < CS) send16(&S.counts[lb][rank], &S.counts_in[lb], t, (uint32_t)above, (uint32_t)ties, __float_as_uint(sum), 0u);
         bounded_wait(&S.counts_in[lb], lturn, failed);
+        if (t == 0) S.stop = *failed;
+        fin_sync();
+        if (S.stop) break;
         int total = 0, all_ties = 0, at = 0, tie_at = 0;
         float below = 0.f;
 #pragma unroll
@@ -574,11 +588,22 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
           for (int k = t; k < ties; k += kFinThreads) send8(to + 8 * (total + tie_at + k), done, list[kAbove + k]);
         if (rank == leader) {
           bounded_wait(bar, (lead >> 1) & 1, failed);
+          if (t == 0) S.stop = *failed;
+          fin_sync();
+          if (S.stop) break;
           rank_row<DT>(P, S, r, info, total, all_ties, below, S.list[1]);
         }
         ++live;
       }
       fin_sync();                            // the lists are free
+    }
+    for (; r < P.n; r += step) {             // after a failed wait: the rows that are left (of any CTA: the same words)
+      const float nan = __int_as_float(0x7fc00000);
+      for (int k = t; k < K; k += kFinThreads) { P.top_logits[(size_t)r * K + k] = nan; P.top_index[(size_t)r * K + k] = -1; }
+      if (t == 0) {
+        P.tail_lse[r] = nan;
+        if (P.status) P.status[r] = SPEC_ST_TIMEOUT;
+      }
     }
   } else if (warp == kRecWarps) {            // picker
     int i = 0;
@@ -609,7 +634,6 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
         }
         bound = max(bound, least);
       }
-      if (bound == order_key(0.f) - 1) ++bound;              // no logit has that key, and its value compares as 0's
       int st = 0;
       if (!temperature_ok(given)) st |= SPEC_ST_BAD_TEMPERATURE;
       if (!isfinite(m)) st |= SPEC_ST_NONFINITE;             // NaN, +inf, or nothing finite
