@@ -6,10 +6,10 @@
 //
 // Rows without a label (and in the backward pass rows of weight 0) take no part:
 // gather_rows copies the rows that count to the front of a compact matrix, so
-// that a masked row costs nothing and a NaN in it reaches nothing, and fills it
-// up with zero rows to a whole tile.
-// Forward: one maximum and sum per row and vocabulary tile, merged by
-// merge_rows.  Backward, for each piece of the vocabulary: G of the piece (the
+// that a masked row costs nothing and a NaN in it reaches nothing; for the
+// backward pass, zero rows fill its last stage of 64.
+// Forward: the label's logit apart (gather_rows), one maximum and sum of the
+// others per row and vocabulary tile, merged by merge_rows.  Backward, for each piece of the vocabulary: G of the piece (the
 // logits again, softmax in the epilogue), dW of the piece, and the piece's part
 // of dh, summed in fp32.
 #include <cuda_bf16.h>
@@ -221,7 +221,9 @@ struct ForwardWork {
     const float2 other = e.join(make_float2(m, s));
     if (e.col != 0) return;
     const float top = fmaxf(m, other.x);     // a NaN sum stays
-    s = s * ex2((m - top) * kLog2eHi) + (other.x == -INFINITY ? other.y : other.y * ex2((other.x - top) * kLog2eHi));
+    // a half without a finite logit has a sum of 0 (or NaN)
+    s = (m == -INFINITY ? s : s * ex2((m - top) * kLog2eHi)) +
+        (other.x == -INFINITY ? other.y : other.y * ex2((other.x - top) * kLog2eHi));
     P.part[(size_t)vt * P.n_pad + i] = make_float2(top, s);
   }
 };
@@ -423,8 +425,8 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constan
   float m = -INFINITY, s = 0.f;
   auto add = [&](float2 p) {                 // a NaN sum stays
     const float top = fmaxf(m, p.x);
-    if (top == -INFINITY) return;
-    s = s * ex2((m - top) * kLog2eHi) + p.y * ex2((p.x - top) * kLog2eHi);
+    if (top == -INFINITY) s += p.y;          // 0, or NaN
+    else s = s * ex2((m - top) * kLog2eHi) + p.y * ex2((p.x - top) * kLog2eHi);
     m = top;
   };
   constexpr int U = 20;                      // loads in flight: a vocabulary of 163840 in one go

@@ -520,6 +520,36 @@ def test_ce_gradient_over_its_hidden_states(sv):
         sv.linear_ce_backward(h.cuda(), wd, ld, lse, gd, out={"grad_weight": wd})
 
 
+@pytest.mark.parametrize("V", [257, 513, 8449])
+def test_ce_label_alone_in_the_last_tile(sv, V):
+    """The last tile of the vocabulary holds one entry, the label."""
+    h, w, label = make_ce(5, 64, V, 21)
+    label[:4] = V - 1
+    check_ce_forward(sv, h, w, label)
+    check_ce_backward(sv, h, w, label, torch.rand(5, generator=gen(9)))
+
+
+@pytest.mark.parametrize("V,lo,hi", [(1000, 0, 300), (9000, 0, 8700), (9000, 300, 9000), (9000, 0, 256),
+                                     (9000, 8448, 8704)])
+def test_ce_vocabulary_masked_by_minus_infinity(sv, V, lo, hi):
+    """Logits of -inf over whole tiles weigh nothing; of NaN they are an error."""
+    h, w, label = make_ce(4, 64, V, 22)
+    h[:, 0] = 1
+    keep = torch.cat([torch.arange(lo), torch.arange(hi, V)])
+    at = label.long() % len(keep)
+    wd = w.clone()
+    wd[lo:hi, 0] = -INF
+    f = sv.linear_ce_forward(*cuda(h, wd, keep[at].to(torch.int32)))
+    cut = sv.linear_ce_forward(*cuda(h, w[keep], at.to(torch.int32)))
+    assert (f["status"] == 0).all()
+    lim = ce_tol(h, w[keep]).cuda()
+    for k in ("loss", "lse"):                            # both within check_ce_forward's bound of the formula
+        assert ((f[k] - cut[k]).abs() <= 4 * lim + 4e-7 * cut[k].abs()).all()
+    wd[lo:hi, 0] = NAN
+    f = sv.linear_ce_forward(*cuda(h, wd, keep[at].to(torch.int32)))
+    assert (f["status"] == 1).all() and f["loss"].isnan().all() and f["lse"].isnan().all()
+
+
 def test_ce_shared_labels(sv):
     """Every row has the same label: its weight row gathers all of them."""
     h, w, label = make_ce(200, 64, 300, 8)
