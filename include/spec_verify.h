@@ -322,8 +322,9 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
  *   status      0, SPEC_ST_BAD_TOKEN (a label or index outside [-1, V), or an
  *     index recorded twice), SPEC_ST_BAD_TEMPERATURE, SPEC_ST_NONFINITE (a NaN
  *     or +inf in the row or the record, no finite logit, or a record without
- *     mass), SPEC_ST_TIMEOUT (an internal wait hit its time limit): such a row
- *     has NaN losses and a gradient of 0.
+ *     mass): such a row has NaN losses and a gradient of 0.  SPEC_ST_TIMEOUT (an
+ *     internal wait hit its time limit): NaN losses, and the gradient of the row
+ *     may not have been written.
  * KL is +inf where some q_b = 0 < p_b, CE where q_label = 0; the gradient stays
  * finite.  Without the gradient each row is read once.  With it, pass the
  * upstream gradient of a row's loss as a factor of row_weight.

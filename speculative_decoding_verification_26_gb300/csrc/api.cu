@@ -424,6 +424,7 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
   P.dtype = dtype; P.n = n; P.V = V; P.K = K;
   P.temperature = temperature;
   P.top_logits = top_logits; P.top_index = top_index; P.tail_lse = tail_lse; P.status = status;
+  P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   int dev = 0;
   const int sms = current_sms(&dev);
   if (launch_record(P, dev, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
@@ -458,6 +459,7 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
   P.kl = kl; P.tv = tv; P.ce = ce;
   P.loss = loss; P.parts = parts; P.status = status;
   P.grad = static_cast<unsigned char*>(grad_logits);
+  P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   int dev = 0;
   const int sms = current_sms(&dev);
   if (launch_distill(P, dev, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
@@ -491,6 +493,7 @@ int spec_linear_ce_forward(const void* hidden, const void* weight, int dtype, in
   P.hidden = static_cast<const __nv_bfloat16*>(hidden);
   P.weight = static_cast<const __nv_bfloat16*>(weight);
   P.label = label; P.loss = loss; P.lse = lse; P.status = status;
+  P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   int launches = 0, dev = 0;
   const cudaError_t e = launch_ce_forward(P, current_sms(&dev), reinterpret_cast<cudaStream_t>(stream), &launches);
   g_launches += launches;
@@ -527,6 +530,7 @@ int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, i
   P.label = label; P.lse_in = lse; P.grad_loss = grad_loss;
   P.grad_hidden = static_cast<__nv_bfloat16*>(grad_hidden);
   P.grad_weight = static_cast<__nv_bfloat16*>(grad_weight);
+  P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
   int launches = 0, dev = 0;
   const cudaError_t e = launch_ce_backward(P, current_sms(&dev), reinterpret_cast<cudaStream_t>(stream), &launches);
   g_launches += launches;

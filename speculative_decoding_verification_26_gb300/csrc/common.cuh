@@ -531,6 +531,7 @@ struct RecordParams {
   int32_t* top_index;            // [n, K]
   float* tail_lse;               // [n]
   int32_t* status;               // [n] or null
+  long long wait_limit;          // as Params::wait_limit
 };
 cudaError_t launch_record(const RecordParams& P, int dev, int nsm, cudaStream_t s);
 cudaError_t configure_record(int dev);    // resident clusters of the current device `dev`
@@ -551,6 +552,7 @@ struct DistillParams {
   float* parts;                  // [n, 3] or null
   unsigned char* grad;           // [n, V] or null
   int32_t* status;               // [n] or null
+  long long wait_limit;          // as Params::wait_limit
 };
 cudaError_t launch_distill(const DistillParams& P, int dev, int nsm, cudaStream_t s);
 cudaError_t configure_distill(int dev);   // dynamic shared-memory limit and resident clusters, current device `dev`
@@ -568,6 +570,7 @@ struct CeParams {
   int32_t* status;               // [n] or null, forward
   __nv_bfloat16* grad_hidden;    // [n, H] or null, backward
   __nv_bfloat16* grad_weight;    // [V, H] or null, backward
+  long long wait_limit;          // as Params::wait_limit
   // workspace views; compact rows are the rows that take part, in order
   int n_pad;                     // n in whole row tiles
   int piece;                     // vocabulary rows of a piece of the backward pass

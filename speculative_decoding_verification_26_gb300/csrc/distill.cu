@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
   const int V = P.V, K = P.K, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = CS == 1 ? 0 : (int)cluster_rank();
   const int first = blockIdx.x / CS, step = gridDim.x / CS;
-  volatile int* failed = &S.failed;
+  const Waits waits{&S.failed, P.wait_limit};
 
   for (int i = tid; i < 2 * map_words; i += kDisThreads) maps[i] = 0;
   if (tid == 0) {
@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         for (int pass = 0; pass < passes; ++pass)
           for (int j = sh.lo; j < sh.hi; j += kDisStageVecs) {
             const uint32_t bytes = 16u * (uint32_t)(sh.hi - j < kDisStageVecs ? sh.hi - j : kDisStageVecs);
-            if (!bounded_wait(&S.empty[at.stage], at.phase ^ 1, failed)) { r = P.n; pass = passes; break; }
+            // after a failed wait, stages are given up unread
+            if (!bounded_wait(&S.empty[at.stage], at.phase ^ 1, waits) || *waits.failed) { r = P.n; pass = passes; break; }
             mbar_arrive_expect_tx(&S.full[at.stage], bytes);
             bulk_load(s_ring + (size_t)at.stage * kDisStage, body + 16ll * j, bytes, &S.full[at.stage]);
             at.next(stages);
@@ -286,6 +287,10 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         zmax = fmaxf(zmax, z[j]);
       }
       if (tail != tail || tail == INFINITY) R.st |= SPEC_ST_NONFINITE;
+      // The label's logit is waited for here, with the others: once this CTA has sent its
+      // sums, another may write its gradient over it.
+      const float zy = raw_value<DT>(R.zy);
+      if (zy != zy || zy == INFINITY) R.st |= SPEC_ST_NONFINITE;
       // The teacher's buckets in base 2, relative to its largest logit x0: a_k =
       // (x_k - x0) c, and tail log2(e) - x0 (c + lo) with the products' roundings
       // put back (x0 c alone is off by 2^-24 |x0 c|, which the K logits share and
@@ -333,13 +338,14 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
     }
     int i = 0, live = 0;
     for (int r = first; r < P.n; r += step, ++i) {
+      if (any_failed(waits)) break;
       const int b = i & 1;
       const bool more = r + step < P.n;
       R = N;
       // the next row's marks and loads go out while the consumers are in pass 1
       if (more) mark(N, W, r + step, b ^ 1);
       if (r + step < P.n - step) fetch(W, r + 2 * step);
-      bounded_wait(&S.summed[b], (i >> 1) & 1, failed);
+      bounded_wait(&S.summed[b], (i >> 1) & 1, waits);
       __syncwarp();
       const unsigned char* row = P.logits + (size_t)r * V * ES;
       unsigned char* grow = P.grad ? P.grad + (size_t)r * V * ES : nullptr;
@@ -354,15 +360,14 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         float s = lane < kDisWarps ? S.part_s[b][lane] : 0.f;
         float mall = fmaxf(R.zmax, warp_max(m));
         float rest = warp_sum(moved(s, m, mall, c));
-        st = R.st | (*failed ? SPEC_ST_TIMEOUT : 0);
-        st = __shfl_sync(0xffffffffu, st, 0);
+        st = R.st;
         if constexpr (CS > 1) {
           const int mb = live & 1;
           if (lane == 0) mbar_arrive_expect_tx(&S.message[mb], 16 * CS);
           __syncwarp();
           if (lane < CS)                     // this CTA's sums to each CTA of the cluster
             send16(&S.msg[mb][rank], &S.message[mb], lane, __float_as_uint(mall), __float_as_uint(rest), (uint32_t)st, 0u);
-          bounded_wait(&S.message[mb], (live >> 1) & 1, failed);
+          bounded_wait(&S.message[mb], (live >> 1) & 1, waits);
           __syncwarp();
           uint4 msg[CS];
 #pragma unroll
@@ -463,6 +468,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
     RingAt at;
     int i = 0;
     for (int r = first; r < P.n; r += step, ++i) {
+      if (any_failed(waits)) break;
       const int b = i & 1;
       const uint32_t turn = (i >> 1) & 1;
       const unsigned char* row = P.logits + (size_t)r * V * ES;
@@ -471,7 +477,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
       const RowShare sh = row_share<CS>(sp, rank);
       const int ends = sh.ends ? sp.head + (V - sp.tail0) : 0;
       const int end_e = tid < sp.head ? tid : sp.tail0 + (tid - sp.head);
-      bounded_wait(&S.marked[b], turn, failed);
+      bounded_wait(&S.marked[b], turn, waits);
       const int skip = S.skip[b];
       const float c = S.c[b];
       const RingAt row_at = at;
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
           nm = -x;
         };
         for (int j = sh.lo, word = tid; j < sh.hi; j += kDisStageVecs, word += kDisConsumers) {
-          bounded_wait(&S.full[at.stage], at.phase, failed);
+          bounded_wait(&S.full[at.stage], at.phase, waits);
           unsigned char* mine = s_ring + (size_t)at.stage * kDisStage + 16 * tid;
           const uint4* vec = reinterpret_cast<const uint4*>(mine);
           const int left = sh.hi - j - tid;
@@ -558,7 +564,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
       if (!P.grad) continue;
 
       // pass 2: every token's gradient as if outside the record
-      bounded_wait(&S.factors[b], turn, failed);
+      bounded_wait(&S.factors[b], turn, waits);
       const float top = S.top[b], factor = S.factor[b];
       const bool zero = S.zero[b] != 0;
       // vectors of the gradient row start where those of the logit row do, or it is written element by element
@@ -583,7 +589,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         return make_uint4(o[0], o[1], o[2], o[3]);
       };
       for (int j = sh.lo; j < sh.hi; j += kDisStageVecs) {
-        if (!skip && !keep) bounded_wait(&S.full[from.stage], from.phase, failed);
+        if (!skip && !keep) bounded_wait(&S.full[from.stage], from.phase, waits);
         const uint4* vec = reinterpret_cast<const uint4*>(s_ring + (size_t)from.stage * kDisStage) + tid;
         const int left = sh.hi - j - tid;
         if (left > (kDisPer - 1) * kDisConsumers && gvec && !zero) {
@@ -624,8 +630,8 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) mbar_arrive(&S.written[b]);
       if (warp == i % kDisWarps) {
-        bounded_wait(&S.written[b], turn, failed);
-        bounded_wait(&S.fixed[b], turn, failed);
+        bounded_wait(&S.written[b], turn, waits);
+        bounded_wait(&S.fixed[b], turn, waits);
         if (!zero)
           for (int k = lane; k <= K; k += 32) {
             const int e = S.fix_idx[k], o = e - sp.head;
@@ -637,9 +643,18 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
     }
   }
   __syncwarp();
-  if (__any_sync(0xffffffffu, *failed)) drain_after_failure();
-  __syncwarp();
+  if (any_failed(waits)) drain_after_failure();
+  __syncthreads();
   if constexpr (CS > 1) cluster_sync();      // no CTA leaves while another sends to it
+  if (S.failed == 0 || warp != kDisWarps) return;
+  // which of its rows the failed wait reached is not told apart
+  for (long long r = first + (long long)lane * step; r < P.n; r += 32ll * step) {
+    const float nan = __int_as_float(0x7fc00000);
+    P.loss[r] = nan;
+    if (P.parts)
+      for (int k = 0; k < 3; ++k) P.parts[3 * r + k] = nan;
+    if (P.status) P.status[r] = SPEC_ST_TIMEOUT;
+  }
 }
 
 struct DisShape {

@@ -391,7 +391,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
   tc_run([&] {
     const int count = *P.count;
     return ForwardWork{P, M, {(count + kTcTile - 1) / kTcTile, (P.V + kTcTile - 1) / kTcTile, count}};
-  }, P.count + 1);
+  }, P.wait_limit, P.count + 1);
 }
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     ce_softmax(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
@@ -399,7 +399,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     const int count = *P.count;
     return SoftWork{P, M, {(count + kTcTile - 1) / kTcTile, (piece_len(P, v_begin) + kTcTile - 1) / kTcTile, count},
                     v_begin};
-  }, P.count + 1);
+  }, P.wait_limit, P.count + 1);
 }
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     ce_grads(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
@@ -409,7 +409,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     const int ht = P.grad_hidden ? rt * ct * P.splits : 0;
     const int wt = P.grad_weight ? (len + kTcTile - 1) / kTcTile * ct : 0;
     return GradWork{P, M, v_begin, count, rt, ct, (len + kTcK - 1) / kTcK, (count + kTcK - 1) / kTcK, ht, wt};
-  }, P.count + 1);
+  }, P.wait_limit, P.count + 1);
 }
 
 // lse and loss of the rows that count: the tiles' maxima and sums, each warp a

@@ -96,7 +96,7 @@ struct RecShared {
     float below;
     uint32_t bound;
   } counted;                                 // by recount
-  int stop;                                  // the finishers' decision after a failed wait
+  int stop[3];                               // the finishers' decision after each wait
   int failed;
 };
 
@@ -239,7 +239,8 @@ __device__ __noinline__ void recount(const RecordParams& P, RecShared& S, int r,
     const uint32_t k = order_key(x);
     const bool above = e < V && k > lo;
     const unsigned vote = __ballot_sync(0xffffffffu, above);
-    if (above) list[at + __popc(vote & ((1u << lane) - 1))] = candidate(x, e);
+    const int to = at + __popc(vote & ((1u << lane) - 1));
+    if (above && to < kAbove) list[to] = candidate(x, e);
     at += __popc(vote);
     if (e < V && k < lo) s += ex2((x - m) * c);
   }
@@ -356,10 +357,9 @@ __device__ __forceinline__ void rank_row(const RecordParams& P, RecShared& S, in
   }
   if (t == 0) {
     // the weights are beside the row's maximum
-    const float tail = below + extra, nan = __int_as_float(0x7fc00000);
-    const bool failed = *(volatile int*)&S.failed != 0;
-    P.tail_lse[r] = failed ? nan : tail > 0.f ? __fdiv_rn(info.m, info.T) + kLn2 * log2f(tail) : -INFINITY;
-    if (P.status) P.status[r] = failed ? SPEC_ST_TIMEOUT : SPEC_ST_OK;
+    const float tail = below + extra;
+    P.tail_lse[r] = tail > 0.f ? __fdiv_rn(info.m, info.T) + kLn2 * log2f(tail) : -INFINITY;
+    if (P.status) P.status[r] = SPEC_ST_OK;
   }
 }
 
@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
   const int V = P.V, K = P.K, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = CS == 1 ? 0 : (int)cluster_rank();
   const int first = blockIdx.x / CS, step = gridDim.x / CS;
-  volatile int* failed = &S.failed;
+  const Waits waits{&S.failed, P.wait_limit};
 
   if (tid == 0) {
     S.failed = 0;
@@ -392,6 +392,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
 
   const int part = (K + CS - 1) / CS;        // a share's part of the record
   const bool few = part <= 64;               // one maximum per thread is enough
+  int left = P.n;                            // a finisher's first row after a failed wait
 
   if (warp == kRecWarps + 1 + kFinWarps) {   // producer
     if (lane == 0) {
@@ -404,7 +405,8 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
         const unsigned char* body = row + (size_t)sp.head * ES;
         for (int j = sh.lo; j < sh.hi; j += kRecStageVecs) {
           const uint32_t bytes = 16u * (uint32_t)(sh.hi - j < kRecStageVecs ? sh.hi - j : kRecStageVecs);
-          if (!(ok = bounded_wait(&S.empty[at.stage], at.phase ^ 1, failed))) break;
+          ok = bounded_wait(&S.empty[at.stage], at.phase ^ 1, waits) && !*waits.failed;      // after it, stages are given up unread
+          if (!ok) break;
           mbar_arrive_expect_tx(&S.full[at.stage], bytes);
           bulk_load(s_ring + (size_t)at.stage * kRecStage, body + 16ll * j, bytes, &S.full[at.stage]);
           at.next(kRecStages);
@@ -417,13 +419,13 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
     for (; r < P.n; r += step, ++i) {
       const int b = i & 1;
       const uint32_t turn = (i >> 1) & 1;
-      bounded_wait(&S.bounded[b], turn, failed);
+      bounded_wait(&S.bounded[b], turn, waits);
       if (t == 0) {
         S.above = S.ties = 0;
-        S.stop = *failed;
+        S.stop[0] = *waits.failed;
       }
       fin_sync();
-      if (S.stop) break;                     // the same for all: nothing of this row is known
+      if (S.stop[0]) break;                     // the same for all: nothing of this row is known
       const RecRow info = S.row[b];
       const unsigned char* row = P.logits + (size_t)r * V * ES;
       const RowSpan sp = row_span<DT>(row, V);
@@ -561,10 +563,10 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
         if (t == 0) mbar_arrive_expect_tx(&S.counts_in[lb], 16 * CS);
         fin_sync();
         if (t < CS) send16(&S.counts[lb][rank], &S.counts_in[lb], t, (uint32_t)above, (uint32_t)ties, __float_as_uint(sum), 0u);
-        bounded_wait(&S.counts_in[lb], lturn, failed);
-        if (t == 0) S.stop = *failed;
+        bounded_wait(&S.counts_in[lb], lturn, waits);
+        if (t == 0) S.stop[1] = *waits.failed;
         fin_sync();
-        if (S.stop) break;
+        if (S.stop[1]) break;
         int total = 0, all_ties = 0, at = 0, tie_at = 0;
         float below = 0.f;
 #pragma unroll
@@ -587,33 +589,27 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
         if (send_ties)
           for (int k = t; k < ties; k += kFinThreads) send8(to + 8 * (total + tie_at + k), done, list[kAbove + k]);
         if (rank == leader) {
-          bounded_wait(bar, (lead >> 1) & 1, failed);
-          if (t == 0) S.stop = *failed;
+          bounded_wait(bar, (lead >> 1) & 1, waits);
+          if (t == 0) S.stop[2] = *waits.failed;
           fin_sync();
-          if (S.stop) break;
+          if (S.stop[2]) break;
           rank_row<DT>(P, S, r, info, total, all_ties, below, S.list[1]);
         }
         ++live;
       }
       fin_sync();                            // the lists are free
     }
-    for (; r < P.n; r += step) {             // after a failed wait: the rows that are left (of any CTA: the same words)
-      const float nan = __int_as_float(0x7fc00000);
-      for (int k = t; k < K; k += kFinThreads) { P.top_logits[(size_t)r * K + k] = nan; P.top_index[(size_t)r * K + k] = -1; }
-      if (t == 0) {
-        P.tail_lse[r] = nan;
-        if (P.status) P.status[r] = SPEC_ST_TIMEOUT;
-      }
-    }
+    left = r;
   } else if (warp == kRecWarps) {            // picker
     int i = 0;
     float T = first < P.n && P.temperature ? P.temperature[first] : 1.f;
     for (int r = first; r < P.n; r += step, ++i) {
+      if (any_failed(waits)) break;
       const int b = i & 1;
       const uint32_t turn = (i >> 1) & 1;
       const float given = T;
       if (P.temperature && r + step < P.n) T = P.temperature[r + step];
-      bounded_wait(&S.summed[b], turn, failed);
+      bounded_wait(&S.summed[b], turn, waits);
       __syncwarp();
       uint32_t bound, share;
       float m = few ? bounds_of<DT, kRecConsumers / 32>(S.maxima, K, part, bound, share)
@@ -622,7 +618,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
         if (lane == 0) mbar_arrive_expect_tx(&S.bounds_in[b], 16 * CS);
         __syncwarp();
         if (lane < CS) send16(&S.bounds[b][rank], &S.bounds_in[b], lane, __float_as_uint(m), bound, share, 0u);
-        bounded_wait(&S.bounds_in[b], turn, failed);
+        bounded_wait(&S.bounds_in[b], turn, waits);
         __syncwarp();
         uint32_t least = 0xFFFFFFFFu;
 #pragma unroll
@@ -648,6 +644,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
     int i = 0;
     float T = first < P.n && P.temperature ? P.temperature[first] : 1.f;      // a row ahead: a load takes 2 us here
     for (int r = first; r < P.n; r += step, ++i) {
+      if (any_failed(waits)) break;
       const int b = i & 1;
       const unsigned char* row = P.logits + (size_t)r * V * ES;
       const RowSpan sp = row_span<DT>(row, V);
@@ -658,12 +655,12 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
       const float end_x = tid < ends ? row_logit<DT>(row, tid < sp.head ? tid : sp.tail0 + (tid - sp.head)) : -INFINITY;
       const float c = scale_split(temperature_ok(given) ? given : 1.f).c;
       const float2 C2 = make_float2(c, c);
-      if (i >= 2) bounded_wait(&S.freed[b], ((i - 2) >> 1) & 1, failed);     // the groups of the row before last
+      if (i >= 2) bounded_wait(&S.freed[b], ((i - 2) >> 1) & 1, waits);     // the groups of the row before last
       float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
       float m = -INFINITY, s = 0.f, bad = 0.f;
       int left_of_group = group, g = 0;
       for (int j = sh.lo; j < sh.hi; j += kRecStageVecs) {
-        bounded_wait(&S.full[at.stage], at.phase, failed);
+        bounded_wait(&S.full[at.stage], at.phase, waits);
         const uint4* vec = reinterpret_cast<const uint4*>(s_ring + (size_t)at.stage * kRecStage) + tid;
         const int left = sh.hi - j - tid;
         uint4 w[kRecPer];
@@ -709,7 +706,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
       }
       if (bad != bad) mx[0] = bad;
       mx[0] = max_nan(mx[0], end_x);
-      if (i >= 1) bounded_wait(&S.bounded[b ^ 1], ((i - 1) >> 1) & 1, failed);             // the last row's maxima are read
+      if (i >= 1) bounded_wait(&S.bounded[b ^ 1], ((i - 1) >> 1) & 1, waits);             // the last row's maxima are read
       if (few) {
         S.maxima[tid] = max_nan(max_nan(mx[0], mx[1]), max_nan(mx[2], mx[3]));
       } else {
@@ -721,9 +718,20 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
     }
   }
   __syncwarp();
-  if (__any_sync(0xffffffffu, *failed)) drain_after_failure();
+  const bool failed = any_failed(waits);
+  if (failed) drain_after_failure();
   __syncwarp();
   if constexpr (CS > 1) cluster_sync();      // no CTA leaves while another sends to it
+  if (!failed) return;
+  for (int r = left; r < P.n; r += step) {   // over what another CTA of the cluster wrote
+    const float nan = __int_as_float(0x7fc00000);
+    const int t = tid - kRecConsumers - 32;
+    for (int k = t; k < K; k += kFinThreads) { P.top_logits[(size_t)r * K + k] = nan; P.top_index[(size_t)r * K + k] = -1; }
+    if (t == 0) {
+      P.tail_lse[r] = nan;
+      if (P.status) P.status[r] = SPEC_ST_TIMEOUT;
+    }
+  }
 }
 
 // Dynamic shared memory: two CTAs per SM (228 KB, 1 KB of it reserved for each).

@@ -1,5 +1,5 @@
 // rows.cuh -- one logit row read by a CTA: the split into a scalar head, a body
-// of 16-byte vectors and a scalar tail, and sums over the CTA in a fixed order.
+// of 16-byte vectors and a scalar tail; clusters and bounded waits.
 #pragma once
 
 #include "common.cuh"
@@ -29,9 +29,9 @@ __device__ __forceinline__ float row_logit(const unsigned char* row, int e) {
 
 // log2(e) / T = c + lo: c the fp32 quotient, lo what it leaves (an fma gives the
 // exact remainder of the division), together good to about 2^-46.  Weights
-// 2^{x c - fl(m c)} take c alone: that scales an exponent by 1 + 2^-24 at most
-// and the common offset cancels in ratios; lo enters where a sum's logarithm is
-// put back into units of the logits.
+// 2^{(x - m) c} take c alone, which scales an exponent by 1 + 2^-24 at most (and
+// x - m first: m c of a row of the type's lowest value would overflow); lo enters
+// where a logarithm is put back into units of the logits.
 struct Scale {
   float c, lo;
 };
@@ -68,14 +68,9 @@ __device__ __forceinline__ float2 vec_pair(const uint4& w, int k) {
   if constexpr (DT == SPEC_BF16) return make_float2(bf16_lo(u[k]), bf16_hi(u[k]));
   else return make_float2(__uint_as_float(u[2 * k]), __uint_as_float(u[2 * k + 1]));
 }
-__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {      // a number before a NaN
+__device__ __forceinline__ uint32_t max_bf2(uint32_t a, uint32_t b) {  // a number before a NaN
   uint32_t d;
   asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t max_nan_bf2(uint32_t a, uint32_t b) {  // a NaN before a number
-  uint32_t d;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -200,33 +195,6 @@ inline cudaError_t resident_clusters(K kernel, int cs, int threads, size_t smem,
   return e;
 }
 
-// Calls fv(j, w) for each vector j of this thread (w its 16 bytes) and fe(e, x)
-// for each single element e.  U vectors are loaded before any is used, so that
-// a thread has that many 16-byte loads in flight.
-template <int DT, int THREADS, int U, class FV, class FE>
-__device__ __forceinline__ void for_row(const unsigned char* row, const RowSpan& sp, const RowShare& sh, int V, FV&& fv,
-                                        FE&& fe) {
-  const uint4* vec = reinterpret_cast<const uint4*>(row + (size_t)sp.head * RowType<DT>::ES);
-  int j0 = sh.lo + (int)threadIdx.x;
-  for (; j0 + (U - 1) * THREADS < sh.hi; j0 += THREADS * U) {
-    uint4 w[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) w[u] = vec[j0 + u * THREADS];
-#pragma unroll
-    for (int u = 0; u < U; ++u) fv(j0 + u * THREADS, w[u]);
-  }
-  for (; j0 < sh.hi; j0 += THREADS) {
-    const uint4 w = vec[j0];
-    fv(j0, w);
-  }
-  if (!sh.ends) return;
-  const int ends = sp.head + (V - sp.tail0);
-  if ((int)threadIdx.x < ends) {
-    const int e = (int)threadIdx.x < sp.head ? (int)threadIdx.x : sp.tail0 + ((int)threadIdx.x - sp.head);
-    fe(e, row_logit<DT>(row, e));
-  }
-}
-
 // ---------------------------------------------------------------------------
 // clusters
 
@@ -245,12 +213,6 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
@@ -272,14 +234,18 @@ __device__ __forceinline__ void send8(uint32_t addr, uint32_t bar, unsigned long
                : "memory");
 }
 
-// A wait for a phase of a barrier gives up after about 2 s, which no healthy
-// call comes near, or once another role of the CTA has (*failed).  The thread
-// sleeps in hardware in between (a polling warp takes issue slots from the
-// others).  A CTA with a failed wait lets kDrainCycles (~1 ms) pass before it
-// ends, for the copies still in flight.
+// A wait for a phase of a barrier gives up after `limit` cycles (by default about 2 s,
+// which no healthy call comes near), or once another role of the CTA has (*failed).
+// The thread sleeps in hardware in between (a polling warp takes issue slots from the
+// others).  A CTA with a failed wait lets kDrainCycles (~1 ms) pass before it ends, for
+// the copies still in flight.
+struct Waits {
+  volatile int* failed;
+  long long limit;
+};
 constexpr long long kDrainCycles = 2000000ll;
 constexpr uint32_t kSleepNs = 100000;
-__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, volatile int* failed) {
+__device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, const Waits& waits) {
   uint32_t ok;
   long long t0 = 0;
   for (;;) {
@@ -287,45 +253,22 @@ __device__ __forceinline__ bool bounded_wait(uint64_t* bar, uint32_t parity, vol
         "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n"
         " selp.u32 %0, 1, 0, p;\n}\n"
         : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(kSleepNs)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(waits.limit < kSleepNs ? (uint32_t)waits.limit : kSleepNs)
         : "memory");
     if (ok) return true;
     const long long t = clock64();
     if (t0 == 0) t0 = t;
-    if (*failed || t - t0 > kWaitLimitCycles) {
-      *failed = 1;
+    if (*waits.failed || t - t0 > waits.limit) {
+      *waits.failed = 1;
       return false;
     }
   }
 }
+// whether a wait of this CTA ran out, the same for the warp
+__device__ __forceinline__ bool any_failed(const Waits& waits) { return __any_sync(0xffffffffu, *waits.failed); }
 __device__ __forceinline__ void drain_after_failure() {
   const long long t0 = clock64();
   while (clock64() - t0 < kDrainCycles) {}
-}
-
-// Sum over the CTA, the same bits in every thread; `scratch` holds WARPS values
-// and may be used again after the next __syncthreads.
-template <int WARPS, class T>
-__device__ __forceinline__ T cta_sum(T v, T* scratch) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  T t = scratch[0];
-#pragma unroll
-  for (int w = 1; w < WARPS; ++w) t += scratch[w];
-  return t;
-}
-template <int WARPS>
-__device__ __forceinline__ float cta_max(float v, float* scratch) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-  if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-  __syncthreads();
-  float t = scratch[0];
-#pragma unroll
-  for (int w = 1; w < WARPS; ++w) t = fmaxf(t, scratch[w]);
-  return t;
 }
 
 }  // namespace sv

@@ -5,9 +5,9 @@
 // B(j, k): each CTA stages 128 rows of A and 128 of B, the leader issues the
 // products for both (cta_group::2), and each CTA holds the sums of its own 128
 // rows: 256 of its 512 TMEM columns, so that the epilogue of one tile overlaps
-// the products of the next.  A 128 x 256 tile by one CTA would stage 48 KB for the same
-// products that the pair does with 32 KB per CTA: 96 bytes a clock per SM
-// from L2 against 64.
+// the products of the next.  A 128 x 256 tile by one CTA would stage 48 KB for the
+// products that a CTA of the pair does with 32 KB: 96 bytes a clock per SM from L2
+// against 64.
 // Warps: 0-7 epilogue (TMEM lanes 32 (w % 4) on, columns 128 (w / 4) on), 8 producer,
 // 9 products.  With four epilogue warps a tile's epilogue takes longer than the products
 // of a tile of k up to about 1024.
@@ -33,6 +33,7 @@ constexpr uint32_t kTcColumns = 512;
 
 struct TcShared {
   uint64_t full[kTcStages], empty[kTcStages], done[2], drained[2];
+  uint64_t half[2][kTcEpilogue / 2];
   uint32_t tmem;
   int failed;
 };
@@ -162,35 +163,40 @@ struct TcHalfRow {
   uint32_t tmem;
   bool any;
   float2* halves;                            // of this tile, by row % 128 (in the staging: either is used)
-  int turn;
+  uint64_t* ready;                           // and the barrier that counts this quarter's 32 of them
+  uint32_t turn, joined;                     // tile mod 2; joins so far mod 2, a bit for each turn
+  Waits waits;
   TcStore store;
-  // The second half's value to the thread of the first half, which gets it.
-  __device__ __forceinline__ float2 join(float2 v) const {
-    const int quarter = (threadIdx.x >> 5) & 3, id = 1 + 2 * quarter + turn, at = row & (kTcHalf - 1);
+  // The second half's value to the thread of the first half, which gets it (after a
+  // wait that ran out, any value); at most once a tile, by both halves of a quarter.
+  __device__ __forceinline__ float2 join(float2 v) {
+    const int at = row & (kTcHalf - 1);
     if (col != 0) {
       halves[at] = v;
-      asm volatile("bar.arrive %0, 64;" ::"r"(id) : "memory");
+      mbar_arrive(ready);
       return v;
     }
-    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+    bounded_wait(ready, joined >> turn & 1, waits);
+    joined ^= 1u << turn;
     return halves[at];
   }
 };
 // `make` gives the work, once the kernel before has ended.
 template <class Make>
-__device__ __forceinline__ void tc_run(Make&& make, int* error) {
+__device__ __forceinline__ void tc_run(Make&& make, long long wait_limit, int* error) {
   extern __shared__ unsigned char tc_smem[];
   const uint32_t base = (smem_u32(tc_smem) + 1023) & ~1023u;
   TcShared& S = *reinterpret_cast<TcShared*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage + kTcStaging);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  volatile int* failed = &S.failed;
+  const Waits waits{&S.failed, wait_limit};
 
   if (threadIdx.x == 0) {
     S.failed = 0;
     for (int i = 0; i < kTcStages; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&S.done[i], 1); mbar_init(&S.drained[i], 2 * kTcEpilogue); }
+    for (int i = 0; i < kTcEpilogue; ++i) mbar_init(&S.half[i & 1][i >> 1], 32);
     fence_mbar_init();
   }
   __syncthreads();
@@ -218,7 +224,7 @@ __device__ __forceinline__ void tc_run(Make&& make, int* error) {
         const TcTile tile = work.tile(t);
         for (int k = 0; k < tile.steps; ++k, ++it) {
           const int st = it % kTcStages;
-          if (!(ok = bounded_wait(&S.empty[st], ((it / kTcStages) & 1) ^ 1, failed))) break;
+          if (!(ok = bounded_wait(&S.empty[st], ((it / kTcStages) & 1) ^ 1, waits))) break;
           const uint32_t bar = map_rank(smem_u32(&S.full[st]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&S.full[st], 2 * kTcStage);   // both CTAs' halves
           const uint32_t at = base + st * kTcStage;
@@ -235,13 +241,13 @@ __device__ __forceinline__ void tc_run(Make&& make, int* error) {
         const TcTile tile = work.tile(t);
         if (tile.steps == 0) continue;
         const int buf = n & 1;
-        if (!(ok = bounded_wait(&S.drained[buf], ((n >> 1) & 1) ^ 1, failed))) break;
+        if (!(ok = bounded_wait(&S.drained[buf], ((n >> 1) & 1) ^ 1, waits))) break;
         tc_fence_after();
         const uint32_t idesc = tc_idesc(tile.a.k_inner, tile.b.k_inner), d = tmem + buf * kTcTile;
         const uint32_t sa = tile.a.k_inner ? 32 >> 4 : 2048 >> 4, sb = tile.b.k_inner ? 32 >> 4 : 2048 >> 4;
         for (int k = 0; k < tile.steps; ++k, ++it) {
           const int st = it % kTcStages;
-          if (!(ok = bounded_wait(&S.full[st], (it / kTcStages) & 1, failed))) break;
+          if (!(ok = bounded_wait(&S.full[st], (it / kTcStages) & 1, waits))) break;
           tc_fence_after();
           const uint64_t da = tc_desc(base + st * kTcStage, tile.a.k_inner);
           const uint64_t db = tc_desc(base + st * kTcStage + kTcOperand, tile.b.k_inner);
@@ -259,19 +265,22 @@ __device__ __forceinline__ void tc_run(Make&& make, int* error) {
     TcHalfRow e;
     e.row = (int)rank * kTcHalf + (warp & 3) * 32 + lane;
     e.col = (warp >> 2) * kTcHalf;
+    e.joined = 0;
+    e.waits = waits;
     e.store.box = base + kTcStages * kTcStage + (uint32_t)warp * kTcBox;
     for (int l = 0, t; (t = work.index(l, pair, pairs)) >= 0; ++l) {
       const int steps = work.tile(t).steps;
       const int buf = n & 1;
       if (steps > 0) {
-        const bool ok = bounded_wait(&S.done[buf], (n >> 1) & 1, failed);
+        const bool ok = bounded_wait(&S.done[buf], (n >> 1) & 1, waits);
         if (!__all_sync(0xffffffffu, ok)) break;
         tc_fence_after();
       }
       e.tmem = tmem + buf * kTcTile + e.col + ((uint32_t)((warp & 3) * 32) << 16);
       e.any = steps > 0;
       e.halves = reinterpret_cast<float2*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage) + buf * kTcHalf;
-      e.turn = buf;
+      e.ready = &S.half[buf][warp & 3];
+      e.turn = (uint32_t)buf;
       work.epilogue(t, e);
       if (steps > 0) {
         tc_fence_before();
@@ -283,7 +292,7 @@ __device__ __forceinline__ void tc_run(Make&& make, int* error) {
     e.store.finish();
   }
   __syncwarp();
-  if (__any_sync(0xffffffffu, *failed)) {    // copies or products may still be in flight
+  if (any_failed(waits)) {    // copies or products may still be in flight
     drain_after_failure();
     if (lane == 0) *error = 1;
   }

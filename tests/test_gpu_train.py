@@ -597,6 +597,57 @@ def step_ws(sv, n=37, V=9001, H=136):
     return [torch.empty(sv.linear_ce_workspace_bytes(n, H, V, b), dtype=torch.uint8, device="cuda") for b in (0, 1)]
 
 
+def test_waits_that_run_out(sv):
+    """With the wait limit at one cycle every row is either right or void with
+    SPEC_ST_TIMEOUT, and the calls return; with the default limit on the same
+    workspaces every row is right again."""
+    ins = step_inputs(3)
+    ws = step_ws(sv)
+    want = [t.clone() for t in all_calls(sv, *ins, ws)]
+    x, z, T, label, w, h, wt, cl, gl = ins
+    # the projection's weights are larger than what a stage or two holds: waits are real
+    big = cuda(*make_ce(700, 512, 9001, 4))
+    more = [rows(n, V, torch.bfloat16, 8).cuda() for n, V in ((600, 40000), (8, 151936))]      # a CTA, and clusters, a row
+    rec = [sv.topk_logits(m, 16) for m in more]
+
+    def losses():
+        return [sv.distill_topk(m.flip(0), r["top_logits"], r["top_index"], r["tail_lse"], kl=1.0, tv=1.0, grad=True)
+                for m, r in zip(more, rec)]
+    loss = losses()
+    f = sv.linear_ce_forward(*big)
+    b = sv.linear_ce_backward(*big, f["lse"])
+    torch.cuda.synchronize()
+    sv.set_wait_limit(1)
+    try:
+        few = sv.topk_logits(x, 16, T)
+        rec1 = [sv.topk_logits(m, 16) for m in more]
+        loss1 = losses()
+        f1 = sv.linear_ce_forward(*big)
+        b1 = sv.linear_ce_backward(*big, f["lse"])
+        torch.cuda.synchronize()
+    finally:
+        sv.set_wait_limit(0)
+    late = 0
+    record_keys, loss_keys = ("top_logits", "top_index", "tail_lse"), ("loss", "parts", "grad")
+    for r, full, keys in ([(few, dict(zip(record_keys, want)), record_keys), (f1, f, ("loss", "lse"))] +
+                          [(a, c, record_keys) for a, c in zip(rec1, rec)] + [(a, c, loss_keys) for a, c in zip(loss1, loss)]):
+        st = r["status"]
+        to = st == sv._lib.ST_TIMEOUT
+        late += int(to.sum())
+        assert ((st == 0) | to).all()
+        for k in keys:
+            assert torch.equal(r[k][~to], full[k][~to]), k
+            if k == "top_index":
+                assert (r[k][to] == -1).all()
+            elif k != "grad":
+                assert r[k][to].isnan().all(), k
+    for k in b:
+        assert torch.equal(b1[k], b[k]) or b1[k].isnan().all(), k
+    assert late > 0, "a one-cycle wait limit timed nothing out"
+    for p, q in zip(want, all_calls(sv, *ins, ws)):
+        assert torch.equal(p, q)
+
+
 def test_repeated_captured_and_on_two_streams(sv):
     """The same bits from a second call, from a replayed graph on new inputs, and
     from two streams at once with a workspace each."""
