@@ -52,7 +52,7 @@ constexpr int kRecStage = 16 * kRecStageVecs;
 constexpr int kRecStages = 3;
 constexpr int kMaxGroups = 10;                             // of a thread and row
 constexpr int kMaxima = 4 * kRecConsumers;
-constexpr int kAbove = 768, kTies = 256, kList = kAbove + kTies;             // a power of two: lists are sorted in place
+constexpr int kAbove = 768, kTies = 256, kList = kAbove + kTies;
 static_assert(kMaxGroups * kRecConsumers * 2 <= kList * 8, "a list holds the numbers of all groups");
 static_assert(kMaxGroups * kRecConsumers <= 32 * kFinThreads, "a finisher's marks");
 constexpr float kLn2 = 0.693147180559945f;
@@ -250,11 +250,38 @@ __device__ __noinline__ void recount(const RecordParams& P, RecShared& S, int r,
   __syncwarp();
 }
 
+// A run of keys in order, largest first, by one warp: a key's place is the number of
+// keys before it.  E of them a lane at a time.
+template <int E>
+__device__ __forceinline__ void order_run(const unsigned long long* from, int len, unsigned long long* to) {
+  const int lane = threadIdx.x & 31;
+  const ulonglong2* pair = reinterpret_cast<const ulonglong2*>(from);
+  for (int k0 = lane; k0 - lane < len; k0 += 32 * E) {
+    unsigned long long mine[E];
+    int place[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) {
+      mine[j] = k0 + 32 * j < len ? from[k0 + 32 * j] : ~0ull;
+      place[j] = 0;
+    }
+#pragma unroll 2
+    for (int p = 0; p < (len + 1) / 2; ++p) {
+      const ulonglong2 two = pair[p];
+#pragma unroll
+      for (int j = 0; j < E; ++j) place[j] += (two.x > mine[j]) + (two.y > mine[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < E; ++j)
+      if (k0 + 32 * j < len) to[place[j]] = mine[j];
+  }
+}
+
 // The record from the candidates: `above` of them above the bound, `ties` equal to
 // it and listed behind the others where there are at most kTies.
 template <int DT>
 __device__ __forceinline__ void rank_row(const RecordParams& P, RecShared& S, int r, const RecRow& info, int above,
-                                         int ties, float below, unsigned long long* list) {
+                                         int ties, float below, unsigned long long* list,
+                                         unsigned long long* spare) {
   const int K = P.K, V = P.V, t = (int)threadIdx.x - kRecConsumers - 32, lane = t & 31, warp = t >> 5;
   uint32_t bound = info.bound;
   bool listed_ties = ties <= kTies;
@@ -279,53 +306,39 @@ __device__ __forceinline__ void rank_row(const RecordParams& P, RecShared& S, in
     top[place] = x == 0.f ? row_logit<DT>(row, e) : x;       // the key has lost a zero's sign
     ti[place] = e;
   };
-  float extra = 0.f;                         // weights past K, in the order of their places
-  if (n <= kFinThreads) {
-    // a candidate's place: the number of candidates before it
-    if (t == 0) list[n] = 0;                 // the keys are read by twos
-    fin_sync();
-    const unsigned long long mine = t < n ? list[t] : 0;
-    int place = 0;
-    const ulonglong2* pair = reinterpret_cast<const ulonglong2*>(list);
-#pragma unroll 4
-    for (int j = 0; j < (n + 1) / 2; ++j) {
-      const ulonglong2 p = pair[j];
-      place += (p.x > mine) + (p.y > mine);
-    }
-    fin_sync();                              // the list is read: it takes the weights past K, by place
-    float* left = reinterpret_cast<float*>(list);
-    if (t < n) {
-      if (place < K) record(place, mine);
-      else left[place - K] = weight(key_value((uint32_t)(mine >> 32)));
-    }
-    if (n > K) {
-      fin_sync();
-      if (t < n - K) extra = left[t];
-    }
-  } else {
-    // more candidates than finishers are sorted (305: 6000 clocks; counting took 17000)
-    int size = 2 * kFinThreads;
-    while (size < n) size *= 2;
-    for (int i = n + t; i < size; i += kFinThreads) list[i] = 0;
-    fin_sync();
-#pragma unroll 1
-    for (int width = 2; width <= size; width *= 2)
-#pragma unroll 1
-      for (int gap = width / 2; gap > 0; gap /= 2) {
-        for (int p = t; p < size / 2; p += kFinThreads) {
-          const int i = 2 * p - (p & (gap - 1)), j = i + gap;
-          const unsigned long long a = list[i], b = list[j];
-          if ((a < b) == ((i & width) == 0)) { list[i] = b; list[j] = a; }
-        }
-        fin_sync();
+  // A candidate's place: each warp orders a quarter by counting, then each candidate
+  // looks up how many of the other quarters come before it.  (305 candidates: 7000 to 9000
+  // clocks with the outputs; sorting all of them in one go took 14000 to 17000.)
+  const int run = ((n + kFinWarps - 1) / kFinWarps + 1) & ~1;
+  if (t == 0) list[n] = 0;                   // the keys are read by twos
+  fin_sync();
+  auto length = [&](int w) { return n - w * run < 0 ? 0 : n - w * run < run ? n - w * run : run; };
+  if (run <= 32) order_run<1>(list + warp * run, length(warp), spare + warp * run);
+  else if (run <= 64) order_run<2>(list + warp * run, length(warp), spare + warp * run);
+  else order_run<3>(list + warp * run, length(warp), spare + warp * run);
+  fin_sync();                                // the list is read: it takes the weights past K, by place
+  float* past = reinterpret_cast<float*>(list);
+  const int first_step = 1 << (31 - __clz(run));
+  for (int i = t; i < n; i += kFinThreads) {
+    const int w = i / run;
+    const unsigned long long mine = spare[i];
+    int at[kFinWarps - 1] = {};
+    for (int step = first_step; step > 0; step >>= 1)
+#pragma unroll
+      for (int q = 0; q < kFinWarps - 1; ++q) {
+        const int other = (w + 1 + q) % kFinWarps, to = at[q] + step;
+        if (to <= length(other) && spare[other * run + to - 1] > mine) at[q] = to;
       }
-    for (int i = t; i < n; i += kFinThreads) {
-      const unsigned long long key = list[i];
-      if (i < K) record(i, key);
-      else extra += weight(key_value((uint32_t)(key >> 32)));
-    }
+    int place = i - w * run;
+#pragma unroll
+    for (int q = 0; q < kFinWarps - 1; ++q) place += at[q];
+    if (place < K) record(place, mine);
+    else past[place - K] = weight(key_value((uint32_t)(mine >> 32)));
   }
+  float extra = 0.f;                         // weights past K, in the order of their places
   if (n > K) {
+    fin_sync();
+    for (int i = t; i < n - K; i += kFinThreads) extra += past[i];
     extra = warp_sum(extra);
     if (lane == 0) S.part[warp] = extra;
     fin_sync();
@@ -556,7 +569,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
             if (t + q * kFinThreads < ties) list[above + t + q * kFinThreads] = v[q];
           fin_sync();
         }
-        rank_row<DT>(P, S, r, info, above, ties, sum, list);
+        rank_row<DT>(P, S, r, info, above, ties, sum, list, S.list[1]);
       } else {
         const int lb = live & 1, leader = live % CS;
         const uint32_t lturn = (live >> 1) & 1;
@@ -593,7 +606,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
           if (t == 0) S.stop[2] = *waits.failed;
           fin_sync();
           if (S.stop[2]) break;
-          rank_row<DT>(P, S, r, info, total, all_ties, below, S.list[1]);
+          rank_row<DT>(P, S, r, info, total, all_ties, below, S.list[1], S.list[0]);
         }
         ++live;
       }
