@@ -422,13 +422,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constan
   griddep_wait();
   if (blockIdx.x * 32 >= *P.count) return;
   const int tiles = (P.V + kTcTile - 1) / kTcTile;
+  // the maximum of several parts first, then their sums beside it; parts without a finite
+  // logit hold 0 or NaN
   float m = -INFINITY, s = 0.f;
-  auto add = [&](float2 p) {                 // a NaN sum stays
-    const float top = fmaxf(m, p.x);
-    if (top == -INFINITY) s += p.y;          // 0, or NaN
-    else s = s * ex2((m - top) * kLog2eHi) + p.y * ex2((p.x - top) * kLog2eHi);
-    m = top;
-  };
+  auto beside = [](float2 p, float top) { return p.x == -INFINITY ? p.y : p.y * ex2((p.x - top) * kLog2eHi); };
   constexpr int U = 20;                      // loads in flight: a vocabulary of 163840 in one go
   for (int t0 = warp; t0 < tiles; t0 += U * kMergeWarps) {
     float2 p[U];
@@ -437,13 +434,24 @@ __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constan
       const int t = t0 + u * kMergeWarps;
       p[u] = t < tiles ? P.part[(size_t)t * P.n_pad + i] : make_float2(-INFINITY, 0.f);
     }
+    float top = m;
 #pragma unroll
-    for (int u = 0; u < U; ++u) add(p[u]);
+    for (int u = 0; u < U; ++u) top = fmaxf(top, p[u].x);
+    s = beside(make_float2(m, s), top);
+#pragma unroll
+    for (int u = 0; u < U; ++u) s += beside(p[u], top);
+    m = top;
   }
   s_part[warp][lane] = make_float2(m, s);
   __syncthreads();
   if (warp != 0 || i >= *P.count) return;
-  for (int w = 1; w < kMergeWarps; ++w) add(s_part[w][lane]);
+  float all = m;
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) all = fmaxf(all, s_part[w][lane].x);
+  s = beside(make_float2(m, s), all);
+#pragma unroll
+  for (int w = 1; w < kMergeWarps; ++w) s += beside(s_part[w][lane], all);
+  m = all;
   // with the label: lse - z = ln(1 + others / e^z), where z is the larger without lse's rounding
   const float z = P.label_logit[i], top = fmaxf(m, z), nan = __int_as_float(0x7fc00000);
   const float others = m == -INFINITY ? s : s * ex2((m - top) * kLog2eHi);
@@ -541,10 +549,16 @@ cudaError_t launch_after(K kernel, int grid, int threads, size_t smem, cudaStrea
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// The maps of rows and G end with the last stage of rows: what lies behind it is zeros
+// without a read (64 rows of a tile of 256, G read once for each tile of H: 186 us with
+// all of them, 181 without; a map that ends at row n itself is slow, 176 us for 115 of
+// one row).
+static int rows_read(const CeParams& P) { return (P.n + kTcK - 1) / kTcK * kTcK; }
+
 cudaError_t launch_ce_forward(const CeParams& P, int nsm, cudaStream_t s, int* launches) {
   CeMaps M;
   memset(&M, 0, sizeof M);
-  if (!encode(&M.rows, P.rows, P.H, P.row_stride, P.n_pad, kTcHalf) ||
+  if (!encode(&M.rows, P.rows, P.H, P.row_stride, rows_read(P), kTcHalf) ||
       !encode(&M.weight, P.weight, P.H, P.H, P.V, kTcHalf))
     return cudaErrorInvalidValue;
   launch_gather<false>(P, s);
@@ -558,12 +572,12 @@ cudaError_t launch_ce_forward(const CeParams& P, int nsm, cudaStream_t s, int* l
 cudaError_t launch_ce_backward(const CeParams& P, int nsm, cudaStream_t s, int* launches) {
   CeMaps M;
   memset(&M, 0, sizeof M);
-  if (!encode(&M.rows, P.rows, P.H, P.row_stride, P.n_pad, kTcHalf) ||
+  if (!encode(&M.rows, P.rows, P.H, P.row_stride, rows_read(P), kTcHalf) ||
       !encode(&M.weight, P.weight, P.H, P.H, P.V, kTcHalf) ||
-      !encode(&M.soft, P.soft, P.piece, P.piece, P.n_pad, kTcHalf) ||
-      !encode(&M.rows_t, P.rows, P.H, P.row_stride, P.n_pad, kTcK) ||
+      !encode(&M.soft, P.soft, P.piece, P.piece, rows_read(P), kTcHalf) ||
+      !encode(&M.rows_t, P.rows, P.H, P.row_stride, rows_read(P), kTcK) ||
       !encode(&M.weight_t, P.weight, P.H, P.H, P.V, kTcK) ||
-      !encode(&M.soft_t, P.soft, P.piece, P.piece, P.n_pad, kTcK) ||
+      !encode(&M.soft_t, P.soft, P.piece, P.piece, rows_read(P), kTcK) ||
       !encode(&M.soft_out, P.soft, P.piece, P.piece, P.n_pad, 32) ||
       (P.grad_weight && !encode(&M.grad_weight, P.grad_weight, P.H, P.H, P.V, 32)))
     return cudaErrorInvalidValue;
