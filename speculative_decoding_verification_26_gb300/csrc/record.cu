@@ -319,17 +319,24 @@ __device__ __forceinline__ void rank_row(const RecordParams& P, RecShared& S, in
   fin_sync();                                // the list is read: it takes the weights past K, by place
   float* past = reinterpret_cast<float*>(list);
   const int first_step = 1 << (31 - __clz(run));
-  for (int i = t; i < n; i += kFinThreads) {
-    const int w = i / run;
-    const unsigned long long mine = spare[i];
+  const unsigned long long* other[kFinWarps - 1];
+  int others[kFinWarps - 1];
+#pragma unroll
+  for (int q = 0; q < kFinWarps - 1; ++q) {
+    const int w = (warp + 1 + q) % kFinWarps;
+    other[q] = spare + w * run - 1;
+    others[q] = length(w);
+  }
+  for (int i = lane; i < length(warp); i += 32) {
+    const unsigned long long mine = spare[warp * run + i];
     int at[kFinWarps - 1] = {};
     for (int step = first_step; step > 0; step >>= 1)
 #pragma unroll
       for (int q = 0; q < kFinWarps - 1; ++q) {
-        const int other = (w + 1 + q) % kFinWarps, to = at[q] + step;
-        if (to <= length(other) && spare[other * run + to - 1] > mine) at[q] = to;
+        const int to = at[q] + step;
+        if (to <= others[q] && other[q][to] > mine) at[q] = to;
       }
-    int place = i - w * run;
+    int place = i;
 #pragma unroll
     for (int q = 0; q < kFinWarps - 1; ++q) place += at[q];
     if (place < K) record(place, mine);
@@ -462,6 +469,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
       uint32_t marked = 0;
       const int stages = (sh.hi - sh.lo + kRecStageVecs - 1) / kRecStageVecs;
       const int groups = (stages + group - 1) / group * kRecConsumers;
+#pragma unroll 4
       for (int g = t, bit = 0; g < groups; g += kFinThreads, ++bit) {
         const float gm = S.group_max[b][g], gs = S.group_sum[b][g];
         if (gm >= least) marked |= 1u << bit;
