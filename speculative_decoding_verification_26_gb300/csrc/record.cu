@@ -782,9 +782,10 @@ cudaError_t launch_as(const RecordParams& P, int dev, cudaStream_t s) {
 }
 
 // Two CTAs share a row of 256 KB or more even where the rows fill the GPU: the work
-// after the stream is shared, and the last round of rows is shorter (512 x 151936
-// bf16: 43.6 us, 46.4 with one; 600 x 128256 fp32: 119 and 146; but 2048 x 32000
-// bf16, rows of 64 KB: 89 us, 53 with one).
+// after the stream is shared, and the last round of rows is shorter (K = 64: 512 x
+// 151936 bf16 43.4 us, 46.5 with one, 57 with four; 600 x 128256 fp32 65 and 72; K = 256:
+// 600 x 128256 fp32 100 and 116; but 2048 x 32000 bf16, rows of 64 KB: 89 us, 52 with
+// one).
 template <int DT>
 cudaError_t launch_of(const RecordParams& P, int dev, int nsm, cudaStream_t s) {
   int cs = row_cluster(P.n, P.V, RowType<DT>::ES, nsm);
