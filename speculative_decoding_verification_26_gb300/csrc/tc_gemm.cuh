@@ -31,9 +31,13 @@ constexpr int kTcThreads = kTcEpilogue * 32 + 64;
 constexpr int kTcProducer = kTcEpilogue, kTcIssuer = kTcEpilogue + 1;
 constexpr uint32_t kTcColumns = 512;
 
+// Places for the halves' values: a warp that is a tile ahead of its other half writes to
+// one of its own, and its products wait for that half two tiles later at the latest.
+constexpr int kTcTurns = 4;
+
 struct TcShared {
   uint64_t full[kTcStages], empty[kTcStages], done[2], drained[2];
-  uint64_t half[2][kTcEpilogue / 2];
+  uint64_t half[kTcTurns][kTcEpilogue / 2];
   uint32_t tmem;
   int failed;
 };
@@ -101,6 +105,21 @@ __device__ __forceinline__ void tc_load32(float (&v)[32], uint32_t addr) {
   for (int c = 0; c < 32; ++c) v[c] = __uint_as_float(r[c]);
 }
 
+// 16 columns, added to x
+__device__ __forceinline__ void tc_add16(float* x, uint32_t addr) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int c = 0; c < 16; ++c) x[c] += __uint_as_float(r[c]);
+}
+
 // An epilogue warp's stores: 32 rows of 64 bf16 at a time, thread = row, through
 // shared memory (swizzled: no bank conflicts, and whole lines to L2; 16-byte stores
 // by rows halve the write rate).  The map has boxes of 64 columns x 32 rows; what
@@ -152,6 +171,11 @@ __device__ __forceinline__ void tc_stage(uint32_t dst, const TcOperand& o, uint3
 // The persistent kernel.  Work::index(l, pair, pairs) is a pair's l-th tile, -1 after
 // its last; Work::tile(t) gives a tile's operands and the number of stages of k
 // (0: no product); Work::epilogue(t, e) is called by the epilogue threads.
+// With CHUNK > 0 a tile's sum is taken in parts of CHUNK stages, each from 0 in a TMEM
+// buffer of its turn, and the parts are added in registers, rounded to nearest: the
+// tensor cores cut their sums off at every addition, and a part is smaller and has
+// fewer of them.  The epilogue gets the sums, epilogue(t, e, x), of half rows for which
+// Work::counts(t, e) holds; every tile has a product.
 struct TcTile {
   TcOperand a, b;
   int steps;
@@ -164,7 +188,7 @@ struct TcHalfRow {
   bool any;
   float2* halves;                            // of this tile, by row % 128 (in the staging: either is used)
   uint64_t* ready;                           // and the barrier that counts this quarter's 32 of them
-  uint32_t turn, joined;                     // tile mod 2; joins so far mod 2, a bit for each turn
+  uint32_t turn, joined;                     // tile mod kTcTurns; joins so far mod 2, a bit for each turn
   Waits waits;
   TcStore store;
   // The second half's value to the thread of the first half, which gets it (after a
@@ -182,7 +206,7 @@ struct TcHalfRow {
   }
 };
 // `make` gives the work, once the kernel before has ended.
-template <class Make>
+template <int CHUNK, class Make>
 __device__ __forceinline__ void tc_run(Make&& make, long long wait_limit, int* error) {
   extern __shared__ unsigned char tc_smem[];
   const uint32_t base = (smem_u32(tc_smem) + 1023) & ~1023u;
@@ -196,7 +220,7 @@ __device__ __forceinline__ void tc_run(Make&& make, long long wait_limit, int* e
     S.failed = 0;
     for (int i = 0; i < kTcStages; ++i) { mbar_init(&S.full[i], 1); mbar_init(&S.empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&S.done[i], 1); mbar_init(&S.drained[i], 2 * kTcEpilogue); }
-    for (int i = 0; i < kTcEpilogue; ++i) mbar_init(&S.half[i & 1][i >> 1], 32);
+    for (int i = 0; i < kTcTurns * kTcEpilogue / 2; ++i) mbar_init(&S.half[i % kTcTurns][i / kTcTurns], 32);
     fence_mbar_init();
   }
   __syncthreads();
@@ -240,24 +264,29 @@ __device__ __forceinline__ void tc_run(Make&& make, long long wait_limit, int* e
       for (int l = 0, t; ok && (t = work.index(l, pair, pairs)) >= 0; ++l) {
         const TcTile tile = work.tile(t);
         if (tile.steps == 0) continue;
-        const int buf = n & 1;
-        if (!(ok = bounded_wait(&S.drained[buf], ((n >> 1) & 1) ^ 1, waits))) break;
-        tc_fence_after();
-        const uint32_t idesc = tc_idesc(tile.a.k_inner, tile.b.k_inner), d = tmem + buf * kTcTile;
+        const uint32_t idesc = tc_idesc(tile.a.k_inner, tile.b.k_inner);
         const uint32_t sa = tile.a.k_inner ? 32 >> 4 : 2048 >> 4, sb = tile.b.k_inner ? 32 >> 4 : 2048 >> 4;
-        for (int k = 0; k < tile.steps; ++k, ++it) {
-          const int st = it % kTcStages;
-          if (!(ok = bounded_wait(&S.full[st], (it / kTcStages) & 1, waits))) break;
+        int first = 0;
+        do {
+          const int buf = n & 1, end = CHUNK > 0 && first + CHUNK < tile.steps ? first + CHUNK : tile.steps;
+          if (!(ok = bounded_wait(&S.drained[buf], ((n >> 1) & 1) ^ 1, waits))) break;
           tc_fence_after();
-          const uint64_t da = tc_desc(base + st * kTcStage, tile.a.k_inner);
-          const uint64_t db = tc_desc(base + st * kTcStage + kTcOperand, tile.b.k_inner);
+          const uint32_t d = tmem + buf * kTcTile;
+          for (int k = first; k < end; ++k, ++it) {
+            const int st = it % kTcStages;
+            if (!(ok = bounded_wait(&S.full[st], (it / kTcStages) & 1, waits))) break;
+            tc_fence_after();
+            const uint64_t da = tc_desc(base + st * kTcStage, tile.a.k_inner);
+            const uint64_t db = tc_desc(base + st * kTcStage + kTcOperand, tile.b.k_inner);
 #pragma unroll
-          for (int q = 0; q < kTcK / 16; ++q)
-            tc_mma(d, da + (uint64_t)(q * sa), db + (uint64_t)(q * sb), idesc, k > 0 || q > 0);
-          tc_commit(&S.empty[st]);
-        }
-        if (ok) tc_commit(&S.done[buf]);
-        ++n;
+            for (int q = 0; q < kTcK / 16; ++q)
+              tc_mma(d, da + (uint64_t)(q * sa), db + (uint64_t)(q * sb), idesc, k > first || q > 0);
+            tc_commit(&S.empty[st]);
+          }
+          if (ok) tc_commit(&S.done[buf]);
+          ++n;
+          first = end;
+        } while (CHUNK > 0 && ok && first < tile.steps);
       }
     }
   } else {
@@ -268,8 +297,39 @@ __device__ __forceinline__ void tc_run(Make&& make, long long wait_limit, int* e
     e.joined = 0;
     e.waits = waits;
     e.store.box = base + kTcStages * kTcStage + (uint32_t)warp * kTcBox;
+    float2* const halves =
+        reinterpret_cast<float2*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage);
     for (int l = 0, t; (t = work.index(l, pair, pairs)) >= 0; ++l) {
       const int steps = work.tile(t).steps;
+      const int turn = l % kTcTurns;
+      e.halves = halves + turn * kTcHalf;
+      e.ready = &S.half[turn][warp & 3];
+      e.turn = (uint32_t)turn;
+      if constexpr (CHUNK > 0) {
+        float x[kTcHalf];
+        const bool counts = work.counts(t, e);
+        bool ok = true;
+        int buf = 0;
+#pragma unroll
+        for (int c = 0; c < kTcHalf; ++c) x[c] = 0.f;
+        for (int k = 0; k < steps; k += CHUNK, ++n) {
+          buf = n & 1;
+          ok = __all_sync(0xffffffffu, bounded_wait(&S.done[buf], (n >> 1) & 1, waits));
+          if (!ok) break;
+          tc_fence_after();
+          if (counts) {
+            const uint32_t at = tmem + buf * kTcTile + e.col + ((uint32_t)((warp & 3) * 32) << 16);
+#pragma unroll
+            for (int c = 0; c < kTcHalf; c += 16) tc_add16(x + c, at + c);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(map_rank(smem_u32(&S.drained[buf]), 0));
+        }
+        if (!ok) break;
+        if (counts) work.epilogue(t, e, x);
+        continue;
+      }
       const int buf = n & 1;
       if (steps > 0) {
         const bool ok = bounded_wait(&S.done[buf], (n >> 1) & 1, waits);
@@ -278,10 +338,7 @@ __device__ __forceinline__ void tc_run(Make&& make, long long wait_limit, int* e
       }
       e.tmem = tmem + buf * kTcTile + e.col + ((uint32_t)((warp & 3) * 32) << 16);
       e.any = steps > 0;
-      e.halves = reinterpret_cast<float2*>(tc_smem + (base - smem_u32(tc_smem)) + kTcStages * (size_t)kTcStage) + buf * kTcHalf;
-      e.ready = &S.half[buf][warp & 3];
-      e.turn = (uint32_t)buf;
-      work.epilogue(t, e);
+      if constexpr (CHUNK == 0) work.epilogue(t, e);
       if (steps > 0) {
         tc_fence_before();
         __syncwarp();
