@@ -318,7 +318,7 @@ __device__ __forceinline__ void rank_row(const RecordParams& P, RecShared& S, in
   else order_run<3>(list + warp * run, length(warp), spare + warp * run);
   fin_sync();                                // the list is read: it takes the weights past K, by place
   float* past = reinterpret_cast<float*>(list);
-  const int first_step = 1 << (31 - __clz(run));
+  const int first_step = 1 << (31 - __clz(run | 1));       // no run: only ties, none of them listed
   const unsigned long long* other[kFinWarps - 1];
   int others[kFinWarps - 1];
 #pragma unroll
