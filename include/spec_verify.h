@@ -311,8 +311,9 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
  *   tail_lse    [n] or NULL; NULL or -inf: the teacher has no mass outside the
  *     record, p is renormalised over its K logits;
  *   label       [n] int32 or NULL; -1 or NULL: no CE term;
- *   row_weight  [n] fp32 or NULL (= 1); of a row of weight 0 (padding) nothing
- *     is read, its loss, parts and gradient are 0;
+ *   row_weight  [n] fp32 or NULL (= 1); of a row of weight 0 (padding) the
+ *     logits are not read, what its record, label and temperature hold does not
+ *     matter, and its loss, parts and gradient are 0;
  *   temperature [n] fp32 or NULL (= 1), of both distributions;
  *   kl, tv, ce  coefficients, finite; a term of coefficient 0 is left out;
  *   loss        [n] fp32; parts [n, 3] fp32 or NULL: KL, TV, CE (0 without a

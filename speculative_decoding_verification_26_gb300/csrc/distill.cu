@@ -223,9 +223,11 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
     // logits there; the consumers may begin
     auto mark = [&](Record<NJ>& R, const RawRow& W, int r, int b) {
       R.w = W.w;
-      R.skip = W.w == 0.f;                   // a padded row: nothing more of it is read
+      R.skip = W.w == 0.f;                   // a padded row: its logits are not read
       R.st = 0;
       if (R.skip) {
+        // the next row's copies go to the same words, and copies are not ordered among themselves
+        asm volatile("cp.async.wait_all;" ::: "memory");
         if (lane == 0) { S.skip[b] = 1; mbar_arrive(&S.marked[b]); }
         return;
       }

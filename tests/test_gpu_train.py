@@ -283,6 +283,29 @@ def test_distill_masked_rows_and_entries(sv):
     assert (r["grad"][2] == 0).all() and r["loss"][2] == 0 and zero[0] == 99999
 
 
+@pytest.mark.parametrize("grad", [False, True])
+@pytest.mark.parametrize("K", [5, 256])
+def test_distill_runs_of_padded_rows(sv, K, grad):
+    """Many more rows than are at work at once, and runs of padded ones among them, at
+    the start too: the record of a padded row never takes the place of the next one's."""
+    n, V = 2500, 601
+    d = make_distill(n, V, K, torch.bfloat16, 17)
+    g = gen(18)
+    pad = torch.rand(n, generator=g) < 0.7
+    pad[:900] = True
+    pad[1400:1500] = False
+    d["w"][pad] = 0
+    # what a padded row holds would be a valid record for its neighbours
+    d["idx"][pad] = torch.arange(K, dtype=torch.int32)
+    d["top"][pad] = torch.linspace(9, -9, K)
+    a = check_distill(sv, d, 0.7, 1.0, 0.1, grad=grad)
+    assert (a["loss"].cpu()[pad] == 0).all() and (a["parts"].cpu()[pad] == 0).all()
+    for _ in range(5):
+        b = sv.distill_topk(*cuda(d["z"], d["top"], d["idx"], d["tail"]), label=d["label"].cuda(),
+                            row_weight=d["w"].cuda(), temperature=d["T"].cuda(), kl=0.7, tv=1.0, ce=0.1, grad=grad)
+        assert all(torch.equal(a[k], b[k]) for k in a)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_distill_masks_of_the_lowest_value(sv, dtype):
     """Student rows masked with the type's lowest value: runs of it before the first
