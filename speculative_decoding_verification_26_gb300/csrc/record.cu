@@ -459,8 +459,8 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
             if (P.status) P.status[r] = info.st;
           }
         }
+        fin_sync();                          // S.row[b] is read by all: it may take the row after next
         if (t == 0) mbar_arrive(&S.freed[b]);
-        fin_sync();
         continue;
       }
       const float c = scale_split(info.T).c, top = info.m, least = key_value(info.bound);

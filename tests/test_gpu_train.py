@@ -156,6 +156,34 @@ def test_record_row_errors(sv):
     assert torch.equal(r["top_index"][5:].cpu().long(), ok[1])
 
 
+@pytest.mark.parametrize("V,K", [(2, 1), (9, 4), (1200, 200)])
+def test_record_refused_rows_among_short_ones(sv, V, K):
+    """Refused rows between others, and runs of them, many to a CTA: each row gets its
+    own result."""
+    n = 6000
+    x = rows(n, V, torch.float32, V)
+    T = torch.rand(n, generator=gen(19)) + 0.5
+    g = gen(20)
+    bad = torch.rand(n, generator=g) < 0.5
+    bad[2000:3500] = True
+    hot = bad & (torch.rand(n, generator=g) < 0.5)
+    x[hot, 1] = NAN
+    T[bad & ~hot] = 0.0
+    xd, Td = cuda(x, T)
+    first = sv.topk_logits(xd, K, Td)
+    good = ~bad
+    top, idx, tail = TP.record(x[good], K, T[good])
+    st = torch.where(hot, 1, torch.where(bad, 64, 0)).to(torch.int32)
+    assert torch.equal(first["status"].cpu(), st)
+    assert torch.equal(first["top_index"].cpu()[good].long(), idx)
+    assert torch.equal(first["top_logits"].cpu()[good].double(), top)
+    assert ((first["tail_lse"].cpu()[good].double() - tail).abs() <= TOL + 3e-7 * tail.abs()).all()
+    assert (first["top_index"].cpu()[bad] == -1).all() and first["tail_lse"].cpu()[bad].isnan().all()
+    for _ in range(5):
+        r = sv.topk_logits(xd, K, Td)
+        assert all(torch.equal(r[k][good.cuda()], first[k][good.cuda()]) for k in r)
+
+
 def test_record_tail_does_not_cancel(sv):
     """Nearly all of the mass in the record: the tail keeps its precision."""
     x = torch.full((2, 5000), -30.0) + torch.rand(2, 5000, generator=gen(1))
