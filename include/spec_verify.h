@@ -359,7 +359,8 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
  *     backward call leaves out rows with a bad label or an lse that is not finite.
  *   workspace: spec_linear_ce_workspace_bytes(n, H, V, backward) bytes, 256-byte
  *     aligned, no initial contents.  Calls that share one must not overlap on
- *     the device; that holds for captured graphs too.
+ *     the device; that holds for captured graphs too.  A call is several launches:
+ *     host threads that share one make their calls in turn, on one stream too.
  * Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^20], H outside [8, 65536]
  * or not a multiple of 8, V outside [2, 2^28), ceil(n / 256) ceil(V / 256) of
  * 2^30 or more, dtype, NULL required pointers, misalignment, overlap),

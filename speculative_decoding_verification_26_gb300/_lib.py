@@ -481,13 +481,26 @@ def linear_ce_workspace_bytes(n: int, H: int, V: int, backward: bool) -> int:
     return int(lib().spec_linear_ce_workspace_bytes(int(n), int(H), int(V), int(bool(backward))))
 
 
+_ws_locks: dict = {}
+
+
+def _ws_lock(device: int, stream: int):
+    """The lock of a stream's cached workspaces, held from taking one to the end
+    of the C call: a call is several launches, and another host thread on the same
+    stream must not put its own between them."""
+    lock = _ws_locks.get((device, stream))
+    return _ws_locks.setdefault((device, stream), threading.Lock()) if lock is None else lock
+
+
 _ce_ws_cache: dict = {}
 
 
 def linear_ce_workspace(n, H, V, device, *, backward):
     """A cached workspace of linear_ce_forward / linear_ce_backward for these
     sizes (reused by calls on the same stream; calls sharing it must not overlap
-    on the device).  Under stream capture it is new: a graph keeps its own."""
+    on the device, nor be made by several host threads at once: the calls that
+    take it by default see to that).  Under stream capture it is new: a graph
+    keeps its own."""
     h = _hot()
     device = h.torch.device(device)
     need = linear_ce_workspace_bytes(n, H, V, backward)
@@ -516,6 +529,16 @@ def _ce_inputs(h, hidden, weight, label):
     return n, H, V, dev
 
 
+def _ce_call(h, dev, ws, backward, f, hidden, weight, dtype, n, H, V, *rest):
+    """_call with the workspace ws, or the stream's cached one."""
+    if ws is not None:
+        _check(ws, "ws", h.torch.uint8, device=dev)
+        return _call(h, dev, f, hidden, weight, dtype, n, H, V, *rest, ws.data_ptr(), ws.numel())
+    with _ws_lock(dev.index, h.stream(dev.index)):
+        ws = linear_ce_workspace(n, H, V, dev, backward=backward)
+        _call(h, dev, f, hidden, weight, dtype, n, H, V, *rest, ws.data_ptr(), ws.numel())
+
+
 def linear_ce_forward(hidden, weight, label, *, ws=None, out=None):
     """Cross entropy of the projection hidden [n, H] times weight [V, H] (bf16)
     against label [n] int32 (-1: the row takes no part), without its logits.
@@ -525,12 +548,8 @@ def linear_ce_forward(hidden, weight, label, *, ws=None, out=None):
     o = out or {}
     loss, lse = _result(o, "loss", (n,), h.f32, dev), _result(o, "lse", (n,), h.f32, dev)
     st = _result(o, "status", (n,), h.i32, dev)
-    if ws is None:
-        ws = linear_ce_workspace(n, H, V, dev, backward=False)
-    else:
-        _check(ws, "ws", h.torch.uint8, device=dev)
-    _call(h, dev, h.ce_forward, hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
-          loss.data_ptr(), lse.data_ptr(), st.data_ptr(), ws.data_ptr(), ws.numel())
+    _ce_call(h, dev, ws, False, h.ce_forward, hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
+             loss.data_ptr(), lse.data_ptr(), st.data_ptr())
     return {"loss": loss, "lse": lse, "status": st}
 
 
@@ -547,12 +566,8 @@ def linear_ce_backward(hidden, weight, label, lse, grad_loss=None, *, need_hidde
     o = out or {}
     gh = _result(o, "grad_hidden", (n, H), h.bf16, dev) if need_hidden else None
     gw = _result(o, "grad_weight", (V, H), h.bf16, dev) if need_weight else None
-    if ws is None:
-        ws = linear_ce_workspace(n, H, V, dev, backward=True)
-    else:
-        _check(ws, "ws", h.torch.uint8, device=dev)
-    _call(h, dev, h.ce_backward, hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
-          lse.data_ptr(), _addr(grad_loss), _addr(gh), _addr(gw), ws.data_ptr(), ws.numel())
+    _ce_call(h, dev, ws, True, h.ce_backward, hidden.data_ptr(), weight.data_ptr(), BF16, n, H, V, label.data_ptr(),
+             lse.data_ptr(), _addr(grad_loss), _addr(gh), _addr(gw))
     r = {}
     if need_hidden:
         r["grad_hidden"] = gh

@@ -749,6 +749,33 @@ def test_captured_call_has_its_own_workspace(sv):
     assert torch.equal(out["loss"], eager) and not torch.equal(other, eager)
 
 
+def test_threads_on_one_stream(sv):
+    """Host threads that call on the default stream with its cached workspace."""
+    import threading
+    sets = [cuda(*make_ce(n, 72, V, 30 + n)) for n, V in ((300, 3001), (40, 9000), (5, 700))]
+    want = []
+    for h, w, y in sets:
+        f = sv.linear_ce_forward(h, w, y)
+        want.append((f["loss"], f["lse"], *sv.linear_ce_backward(h, w, y, f["lse"]).values()))
+    torch.cuda.synchronize()
+    got = [[] for _ in sets]
+
+    def work(k):
+        h, w, y = sets[k]
+        for _ in range(60):
+            f = sv.linear_ce_forward(h, w, y)
+            got[k] = [f["loss"], f["lse"], *sv.linear_ce_backward(h, w, y, f["lse"]).values()]
+            wrong.extend(k for a, b in zip(want[k], got[k]) if not torch.equal(a, b))
+
+    wrong = []
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(len(sets))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong and all(got)
+
+
 def test_rows_behind_the_last_stay(sv):
     """Outputs are views into larger buffers: what lies behind them stays."""
     d = make_distill(3, 1003, 6, torch.bfloat16, 21)

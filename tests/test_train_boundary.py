@@ -1,6 +1,9 @@
 """The drafter-training calls: host checks (no GPU, nothing is launched), the
 workspace sizes, and the plain implementations against differences."""
 import ctypes
+import threading
+import time
+import types
 
 import pytest
 import torch
@@ -132,3 +135,47 @@ def test_plain_gradients_against_differences():
             d[k] = 1e-6
             d = d.view_as(t)
             assert abs((f(t + d) - f(t - d)) / 2e-6 - gt.view(-1)[k]) < 1e-7
+
+
+def test_threads_take_turns_on_a_cached_workspace(monkeypatch):
+    """Host threads on one stream, with the library's calls replaced: no two of them
+    are in a call with the same workspace, and a thread on another stream has its own."""
+    from speculative_decoding_verification_26_gb300 import _lib as lib
+    stream = threading.local()
+    busy, wrong, seen = set(), [], set()
+
+    def entry(*args):
+        ws = args[-3]
+        if ws in busy:
+            wrong.append(ws)
+        busy.add(ws)
+        seen.add((stream.id, ws))
+        time.sleep(0.002)                  # as ctypes does, without the interpreter's lock
+        busy.discard(ws)
+        return 0
+
+    entry.__name__ = "entry"
+    cuda = types.SimpleNamespace(is_current_stream_capturing=lambda: False)
+    h = types.SimpleNamespace(
+        torch=types.SimpleNamespace(uint8=torch.uint8, device=torch.device, cuda=cuda), empty=torch.empty,
+        f32=torch.float32, i32=torch.int32, bf16=torch.bfloat16, device=lambda: None, stream=lambda i: stream.id,
+        ce_forward=entry, ce_backward=entry)
+    monkeypatch.setattr(lib, "_hot", lambda: h)
+    monkeypatch.setattr(lib, "_check", lambda *a, **k: None)
+    monkeypatch.setattr(lib, "_ce_ws_cache", {})
+    monkeypatch.setattr(lib, "linear_ce_workspace_bytes", lambda n, H, V, b: 256 * (2 if b else 1) * n)
+    x, label = torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32)
+
+    def work(k):
+        stream.id = 7 if k < 4 else 8
+        for n in (2, 4, 3):
+            lse = lib.linear_ce_forward(x[:n], x, label[:n])["lse"]
+            lib.linear_ce_backward(x[:n], x, label[:n], lse)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(5)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert {s for s, _ in seen} == {7, 8}
