@@ -55,7 +55,8 @@
  *     accept_prob and signals NaN.  Other requests are unaffected.
  *   - Given identical inputs the outputs are bit-identical from call to call.
  *   - Calls that share a workspace must not overlap on the device (enqueue
- *     them on one stream, or give each its own workspace).
+ *     them on one stream, or give each its own workspace).  A call may be
+ *     several launches: host threads that share one make their calls in turn.
  */
 #ifndef SPEC_VERIFY_H
 #define SPEC_VERIFY_H

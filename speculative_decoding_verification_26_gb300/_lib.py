@@ -152,12 +152,25 @@ def _check(t, name, dtype=None, shape=None, device=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
+_ws_locks: dict = {}
+
+
+def _ws_lock(device: int, stream: int):
+    """The lock of a stream's cached workspaces, held from taking one to the end
+    of the C call: a call is several launches, and another host thread on the same
+    stream must not put its own between them."""
+    lock = _ws_locks.get((device, stream))
+    return _ws_locks.setdefault((device, stream), threading.Lock()) if lock is None else lock
+
+
 _ws_cache: dict = {}
 
 
 def workspace(B, G, V, device):
     """A cached workspace tensor for these sizes on `device` (reused by calls
-    on the same stream; calls sharing it must not overlap on the device)."""
+    on the same stream; calls sharing it must not overlap on the device, nor be
+    made by several host threads at once: the calls that take it by default see
+    to that)."""
     torch = _torch()
     n = workspace_bytes(B, G, V)
     if n == 0:
@@ -168,6 +181,31 @@ def workspace(B, G, V, device):
         ws = torch.empty(n, dtype=torch.uint8, device=device)
         _ws_cache[key] = ws
     return ws
+
+
+class _Held:
+    """A verification call's workspace while the call is made: the caller's, or
+    the stream's cached one under its lock."""
+    __slots__ = ("ws", "sizes", "dev", "lock")
+
+    def __init__(self, ws, B, G, V, dev):
+        self.ws, self.sizes, self.dev, self.lock = ws, (B, G, V), dev, None
+
+    def __enter__(self):
+        if self.ws is None:
+            lock = _ws_lock(self.dev.index, _torch().cuda.current_stream(self.dev).cuda_stream)
+            lock.acquire()
+            self.lock = lock
+            try:
+                self.ws = workspace(*self.sizes, self.dev)
+            except BaseException:
+                lock.release()
+                raise
+        return self.ws
+
+    def __exit__(self, *exc):
+        if self.lock is not None:
+            self.lock.release()
 
 
 def _out(o, key, make):
@@ -192,9 +230,9 @@ def verify_greedy(target, draft_tokens, gamma=None, *, ws=None, out=None):
     acc = _out(o, "accept_len", lambda: torch.empty(B, dtype=torch.int32, device=dev))
     tok = _out(o, "tokens", lambda: torch.empty(B, G + 1, dtype=torch.int32, device=dev))
     st = _out(o, "status", lambda: torch.empty(B, dtype=torch.int32, device=dev))
-    ws = ws if ws is not None else workspace(B, G, V, dev)
-    rc = lib().spec_verify_greedy(_ptr(target), _dtype_code(target), B, G, V, _ptr(draft_tokens), _ptr(gamma),
-                                  _ptr(acc), _ptr(tok), _ptr(st), _ptr(ws), ws.numel(), _stream(dev))
+    with _Held(ws, B, G, V, dev) as ws:
+        rc = lib().spec_verify_greedy(_ptr(target), _dtype_code(target), B, G, V, _ptr(draft_tokens), _ptr(gamma),
+                                      _ptr(acc), _ptr(tok), _ptr(st), _ptr(ws), ws.numel(), _stream(dev))
     if rc != OK:
         raise SpecVerifyError(rc, "spec_verify_greedy")
     return {"accept_len": acc, "tokens": tok, "status": st}
@@ -219,10 +257,10 @@ def verify_sample(target, draft, draft_tokens, gamma, temperature, uniforms, *, 
     st = _out(o, "status", lambda: torch.empty(B, dtype=torch.int32, device=dev))
     sig = (_out(o, "signals", lambda: torch.empty(B, 4, dtype=torch.float32, device=dev))) if signals else None
     ap = (_out(o, "accept_prob", lambda: torch.empty(B, G, dtype=torch.float32, device=dev))) if accept_prob else None
-    ws = ws if ws is not None else workspace(B, G, V, dev)
-    rc = lib().spec_verify_sample(_ptr(target), _ptr(draft), _dtype_code(target), B, G, V, _ptr(draft_tokens),
-                                  _ptr(gamma), _ptr(temperature), _ptr(uniforms), _ptr(acc), _ptr(tok), _ptr(sig),
-                                  _ptr(ap), _ptr(st), _ptr(ws), ws.numel(), _stream(dev))
+    with _Held(ws, B, G, V, dev) as ws:
+        rc = lib().spec_verify_sample(_ptr(target), _ptr(draft), _dtype_code(target), B, G, V, _ptr(draft_tokens),
+                                      _ptr(gamma), _ptr(temperature), _ptr(uniforms), _ptr(acc), _ptr(tok), _ptr(sig),
+                                      _ptr(ap), _ptr(st), _ptr(ws), ws.numel(), _stream(dev))
     if rc != OK:
         raise SpecVerifyError(rc, "spec_verify_sample")
     r = {"accept_len": acc, "tokens": tok, "status": st}
@@ -249,10 +287,10 @@ def verify_onehot(target, draft_tokens, gamma, temperature, uniforms, *, accept_
     tok = _out(o, "tokens", lambda: torch.empty(B, G + 1, dtype=torch.int32, device=dev))
     st = _out(o, "status", lambda: torch.empty(B, dtype=torch.int32, device=dev))
     ap = (_out(o, "accept_prob", lambda: torch.empty(B, G, dtype=torch.float32, device=dev))) if accept_prob else None
-    ws = ws if ws is not None else workspace(B, G, V, dev)
-    rc = lib().spec_verify_onehot(_ptr(target), _dtype_code(target), B, G, V, _ptr(draft_tokens), _ptr(gamma),
-                                  _ptr(temperature), _ptr(uniforms), _ptr(acc), _ptr(tok), _ptr(ap), _ptr(st),
-                                  _ptr(ws), ws.numel(), _stream(dev))
+    with _Held(ws, B, G, V, dev) as ws:
+        rc = lib().spec_verify_onehot(_ptr(target), _dtype_code(target), B, G, V, _ptr(draft_tokens), _ptr(gamma),
+                                      _ptr(temperature), _ptr(uniforms), _ptr(acc), _ptr(tok), _ptr(ap), _ptr(st),
+                                      _ptr(ws), ws.numel(), _stream(dev))
     if rc != OK:
         raise SpecVerifyError(rc, "spec_verify_onehot")
     r = {"accept_len": acc, "tokens": tok, "status": st}
@@ -338,9 +376,9 @@ def draft_signals(draft, gamma, temperature, *, row_signals=False, ws=None, out=
     sig = _out(o, "signals", lambda: torch.empty(B, 4, dtype=torch.float32, device=dev))
     rs = (_out(o, "row_signals", lambda: torch.empty(B, G, 2, dtype=torch.float32, device=dev))) if row_signals else None
     st = _out(o, "status", lambda: torch.empty(B, dtype=torch.int32, device=dev))
-    ws = ws if ws is not None else workspace(B, G, V, dev)
-    rc = lib().spec_draft_signals(_ptr(draft), _dtype_code(draft), B, G, V, _ptr(gamma), _ptr(temperature),
-                                  _ptr(sig), _ptr(rs), _ptr(st), _ptr(ws), ws.numel(), _stream(dev))
+    with _Held(ws, B, G, V, dev) as ws:
+        rc = lib().spec_draft_signals(_ptr(draft), _dtype_code(draft), B, G, V, _ptr(gamma), _ptr(temperature),
+                                      _ptr(sig), _ptr(rs), _ptr(st), _ptr(ws), ws.numel(), _stream(dev))
     if rc != OK:
         raise SpecVerifyError(rc, "spec_draft_signals")
     r = {"signals": sig, "status": st}
@@ -479,17 +517,6 @@ def distill_topk(logits, top_logits, top_index, tail_lse=None, *, label=None, ro
 
 def linear_ce_workspace_bytes(n: int, H: int, V: int, backward: bool) -> int:
     return int(lib().spec_linear_ce_workspace_bytes(int(n), int(H), int(V), int(bool(backward))))
-
-
-_ws_locks: dict = {}
-
-
-def _ws_lock(device: int, stream: int):
-    """The lock of a stream's cached workspaces, held from taking one to the end
-    of the C call: a call is several launches, and another host thread on the same
-    stream must not put its own between them."""
-    lock = _ws_locks.get((device, stream))
-    return _ws_locks.setdefault((device, stream), threading.Lock()) if lock is None else lock
 
 
 _ce_ws_cache: dict = {}

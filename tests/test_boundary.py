@@ -116,3 +116,56 @@ def test_filter_rejects_bad_arguments(L):
     assert L.spec_filter_top_k_top_p(fake, 1, 0, 1024, None, None, None, None, None) == 1
     assert L.spec_filter_top_k_top_p(fake, 1, 4, 1, None, None, None, None, None) == 1
     assert L.spec_filter_top_k_top_p(P(0x7f0000000001), 1, 4, 1024, None, None, None, None, None) == 1
+
+
+def test_threads_take_turns_on_a_cached_workspace(monkeypatch):
+    """Host threads on one stream, with the library's calls replaced: no two of
+    them are in a call with the same workspace; another stream has its own."""
+    import threading
+    import time
+    import types
+
+    torch = pytest.importorskip("torch")
+    from speculative_decoding_verification_26_gb300 import _lib as lib
+    stream = threading.local()
+    busy, wrong, seen = set(), [], set()
+
+    def entry(*args):
+        ws = args[-3].value
+        if ws in busy:
+            wrong.append(ws)
+        busy.add(ws)
+        seen.add((stream.id, ws))
+        time.sleep(0.002)                  # as ctypes does, without the interpreter's lock
+        busy.discard(ws)
+        return 0
+
+    cuda = types.SimpleNamespace(current_stream=lambda dev: types.SimpleNamespace(cuda_stream=stream.id))
+    fake = types.SimpleNamespace(cuda=cuda, **{k: getattr(torch, k) for k in (
+        "empty", "uint8", "int32", "float32", "bfloat16")})
+    calls = types.SimpleNamespace(**{f"spec_{k}": entry for k in (
+        "verify_greedy", "verify_sample", "verify_onehot", "draft_signals")})
+    monkeypatch.setattr(lib, "_torch", lambda: fake)
+    monkeypatch.setattr(lib, "lib", lambda: calls)
+    monkeypatch.setattr(lib, "_check", lambda *a, **k: None)
+    monkeypatch.setattr(lib, "_ws_cache", {})
+    monkeypatch.setattr(lib, "workspace_bytes", lambda B, G, V: 256 * B)
+    t, d = torch.zeros(4, 3, 8), torch.zeros(4, 2, 8)
+    tok, gam, T, u = (torch.zeros(4, 2, dtype=torch.int32), torch.zeros(4, dtype=torch.int32), torch.ones(4),
+                      torch.zeros(4, 3))
+
+    def work(k):
+        stream.id = 7 if k < 4 else 8
+        for B in (2, 4, 3):
+            lib.verify_greedy(t[:B], tok[:B], gam[:B])
+            lib.verify_sample(t[:B], d[:B], tok[:B], gam[:B], T[:B], u[:B])
+            lib.verify_onehot(t[:B], tok[:B], gam[:B], T[:B], u[:B])
+            lib.draft_signals(d[:B], gam[:B], T[:B])
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in range(5)]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not wrong
+    assert {s for s, _ in seen} == {7, 8}
