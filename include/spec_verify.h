@@ -327,8 +327,8 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
  *     mass): such a row has NaN losses and a gradient of 0.  SPEC_ST_TIMEOUT (an
  *     internal wait hit its time limit): NaN losses, and the gradient of the row
  *     may not have been written.
- * KL is +inf where some q_b = 0 < p_b, CE where q_label = 0; the gradient stays
- * finite.  Without the gradient each row is read once.  With it, pass the
+ * KL is +inf where some q_b = 0 < p_b, CE where q_label = 0 (logits of -inf: the
+ * logarithm of a q_b too small for 32 bits is kept); the gradient stays finite.  Without the gradient each row is read once.  With it, pass the
  * upstream gradient of a row's loss as a factor of row_weight.
  * No workspace.  Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^30], V, K,
  * dtype, coefficients, NULL required pointers, misalignment, overlap),

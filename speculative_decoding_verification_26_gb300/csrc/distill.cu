@@ -56,7 +56,7 @@ struct DisShared {
   // CTA's message is in
   uint64_t marked[2], summed[2], factors[2], fixed[2], written[2], message[2];
   float part_m[2][kDisWarps], part_s[2][kDisWarps];
-  uint4 msg[2][8];                           // maximum, sum, status of each CTA of the cluster
+  uint4 msg[2][8];                           // maximum and sum outside the record, status, of each CTA of the cluster
   float c[2], top[2], factor[2];
   int skip[2], zero[2];
   uint32_t ends[2];                          // marks of the single elements: head from bit 0, tail from bit 8
@@ -360,29 +360,32 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         const float c = S.c[b];
         float m = lane < kDisWarps ? S.part_m[b][lane] : -INFINITY;
         float s = lane < kDisWarps ? S.part_s[b][lane] : 0.f;
-        float mall = fmaxf(R.zmax, warp_max(m));
-        float rest = warp_sum(moved(s, m, mall, c));
+        // The tokens outside the record: their sum stays beside their own maximum, where it is
+        // 1 or more (beside the row's, weights below 2^-126 are 0, and so would q_rest be).
+        float mr = warp_max(m), sum_r = warp_sum(moved(s, m, mr, c));
         st = R.st;
         if constexpr (CS > 1) {
           const int mb = live & 1;
           if (lane == 0) mbar_arrive_expect_tx(&S.message[mb], 16 * CS);
           __syncwarp();
           if (lane < CS)                     // this CTA's sums to each CTA of the cluster
-            send16(&S.msg[mb][rank], &S.message[mb], lane, __float_as_uint(mall), __float_as_uint(rest), (uint32_t)st, 0u);
+            send16(&S.msg[mb][rank], &S.message[mb], lane, __float_as_uint(mr), __float_as_uint(sum_r), (uint32_t)st, 0u);
           bounded_wait(&S.message[mb], (live >> 1) & 1, waits);
           __syncwarp();
           uint4 msg[CS];
 #pragma unroll
           for (int q = 0; q < CS; ++q) {
             msg[q] = S.msg[mb][q];
-            mall = fmaxf(mall, __uint_as_float(msg[q].x));
+            mr = fmaxf(mr, __uint_as_float(msg[q].x));
             st |= (int)msg[q].z;
           }
-          rest = 0.f;
+          sum_r = 0.f;
 #pragma unroll
-          for (int q = 0; q < CS; ++q) rest += moved(__uint_as_float(msg[q].y), __uint_as_float(msg[q].x), mall, c);
+          for (int q = 0; q < CS; ++q) sum_r += moved(__uint_as_float(msg[q].y), __uint_as_float(msg[q].x), mr, c);
         }
         ++live;
+        const float mall = fmaxf(R.zmax, mr), lift_r = mr == -INFINITY ? 0.f : (mr - mall) * c;
+        const float rest = sum_r * ex2(lift_r);
         // every weight is beside mall from here on; the record's own move there by `up`
         const float zy = raw_value<DT>(R.zy), lift = R.zmax == -INFINITY ? 0.f : (R.zmax - mall) * c, up = ex2(lift);
         const float sum = fmaf(R.F, up, rest);
@@ -409,10 +412,11 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
           S.zero[b] = st != 0;
           mbar_arrive(&S.factors[b]);
         }
-        // log2 q_k = (z_k - zmax) c + lift - l2S, and the p_k sum to 1 - p_r
+        // log2 q_k = (z_k - zmax) c + lift - l2S, and the p_k sum to 1 - p_r;
+        // log2 q_r = log2 sum_r + lift_r - l2S
         kl = R.A - (1.f - R.pr) * (lift - l2S);
         if (1.f - R.pr == 0.f) kl = R.A;
-        if (R.pr > 0.f) kl += R.pr * (R.lpr - (log2f(rest) - l2S));
+        if (R.pr > 0.f) kl += R.pr * (R.lpr - (log2f(sum_r) + lift_r - l2S));
         kl *= kLn2;
         tv = 0.5f * (tv + fabsf(R.pr - qr));
         ce = R.y >= 0 ? (l2S - (zy - mall) * c) * kLn2 : 0.f;

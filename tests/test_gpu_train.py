@@ -376,6 +376,65 @@ def test_distill_infinite_losses(sv):
     assert torch.isfinite(r["loss"]).all()
 
 
+def confident(n, V, K, dtype, seed, p_rest, gap, T):
+    """Students whose logits outside the record lie `gap` temperatures or more below all
+    inside it (gap < 0: inside below the largest outside), teachers with a mass of p_rest
+    outside; temperatures of T to 2 T."""
+    d = make_distill(n, V, K, dtype, seed)
+    d["T"] = torch.rand(n, generator=gen(seed + 2)) * T + T
+    lse = torch.logsumexp(d["top"].double() / d["T"].double()[:, None], 1)
+    d["tail"] = (lse + math.log(p_rest / (1 - p_rest))).float()
+    z = d["z"].float()
+    inside = torch.zeros(n, V, dtype=torch.bool).scatter_(1, d["idx"].long(), True)
+    top = torch.where(inside, -INF, z).max(1, keepdim=True).values
+    if gap < 0:
+        low = torch.where(inside, z, -INF).max(1, keepdim=True).values
+    else:
+        low = torch.where(inside, z, INF).min(1, keepdim=True).values
+    d["z"] = torch.where(inside, z - low + top + gap * d["T"][:, None], z).to(dtype)
+    return d
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V,K", [(3, 5003, 16), (40, 20011, 200), (400, 3001, 5)])
+@pytest.mark.parametrize("gap,T,p_rest", [(95, 0.2, 0.1), (300, 0.05, 0.1), (90, 1.0, 0.9), (-300, 0.05, 0.9),
+                                          (-95, 0.3, 0.1)])
+def test_distill_rest_far_from_the_record(sv, n, V, K, dtype, gap, T, p_rest):
+    """One of the two has no weight beside the other in 32 bits (e^-87.3 = 2^-126): KL is
+    finite all the same, its logarithms are."""
+    check_distill(sv, confident(n, V, K, dtype, 50, p_rest, gap, T), 1.0, 0.5, 0.1, grad=False)
+
+
+def test_distill_rest_by_hand(sv):
+    """V = 3, K = 1, T = 0.1, teacher (8, 0, 0), student (10, 0, 0): p_rest = 2 e^-80, q_rest =
+    2 e^-100, KL = 40 e^-80 - (p_rest - q_rest) = 7e-34."""
+    r = sv.distill_topk(torch.tensor([[10.0, 0.0, 0.0]], device="cuda"), torch.tensor([[8.0]], device="cuda"),
+                        torch.zeros(1, 1, dtype=torch.int32, device="cuda"), torch.tensor([math.log(2)], device="cuda"),
+                        temperature=torch.tensor([0.1], device="cuda"))
+    assert r["status"].item() == 0 and abs(r["loss"].item()) <= 1e-6
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V,K", [(5, 1001, 9), (3, 70001, 256), (400, 5000, 40)])
+def test_low_temperatures(sv, n, V, K, dtype):
+    T = torch.rand(n, generator=gen(V)) * 0.2 + 0.01
+    x = rows(n, V, dtype, 53)
+    top, idx, tail = TP.record(x, K, T)
+    r = sv.topk_logits(x.cuda(), K, T.cuda())
+    assert (r["status"] == 0).all() and torch.equal(r["top_index"].cpu().long(), idx)
+    assert torch.equal(r["top_logits"].cpu().double(), top)
+    # A weight below 2^-126 of the row's largest is 0: up to V of them are missing from the tail,
+    # V 2^-126 of its mass beside that weight, so ln(1 - share) of the tail; half of it or more
+    # may be missing near the limit, all of it below.
+    got, share = r["tail_lse"].cpu().double(), V * 2.0 ** -126 / torch.exp(tail - top[:, 0] / T.double())
+    lim = TOL + 3e-7 * tail.abs()
+    assert (got <= tail + lim).all() and (got >= tail - lim - 2 * share)[share < 0.5].all() and (share < 1e-6).any()
+    d = make_distill(n, V, K, dtype, 52)
+    d["T"] = T
+    d.update(top=top.float(), idx=idx.to(torch.int32), tail=tail.float())
+    check_distill(sv, d, 1.0, 1.0, 0.5, grad=False)
+
+
 def test_distill_row_errors(sv):
     d = make_distill(9, 701, 5, torch.float32, 11)
     d["z"][0, 700] = NAN
