@@ -12,7 +12,8 @@
 // losses).  With s_b = sign(q_b - p_b) and S = 1/2 sum_b s_b q_b the gradient is
 //   w/T [ q_v (kl + ce + tv (s_b(v)/2 - S)) - kl p_v - ce [v = y] ]  v recorded,
 //   w/T [ q_v (kl + ce + tv (s_r/2 - S) - kl p_r / q_r) - ce [v = y] ]  else.
-// For a token outside the record it is e^{z_v / T} times one factor of the row.
+// For a token outside the record it is e^{(z_v - m) / T}, m the largest logit outside,
+// times one factor of the row.
 // The sum over the tokens not recorded leaves the others out by a bit map: q_r as
 // 1 - sum q_k would cancel.
 //
@@ -385,8 +386,8 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         }
         ++live;
         const float mall = fmaxf(R.zmax, mr), lift_r = mr == -INFINITY ? 0.f : (mr - mall) * c;
-        const float rest = sum_r * ex2(lift_r);
-        // every weight is beside mall from here on; the record's own move there by `up`
+        const float up_r = ex2(lift_r), rest = sum_r * up_r;
+        // weights are beside mall from here on: the record's own move there by `up`
         const float zy = raw_value<DT>(R.zy), lift = R.zmax == -INFINITY ? 0.f : (R.zmax - mall) * c, up = ex2(lift);
         const float sum = fmaf(R.F, up, rest);
         if (!isfinite(mall) || !isfinite(sum)) st |= SPEC_ST_NONFINITE;
@@ -404,10 +405,14 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
         tv = warp_sum(tv);
         const float mean = warp_sum(sq) + sr * qr;
         const float lce = R.y >= 0 ? P.ce : 0.f, wT = R.w / R.T, base = P.kl + lce - P.tv * mean;
-        // rest = 0: no token of the rest has weight, its factor does not matter
-        const float factor = ((base + P.tv * sr) * rS - (rest > 0.f ? P.kl * R.pr / rest : 0.f)) * wT;
+        // A token of the rest has q_v = e_v up_r rS and the share e_v / sum_r of the teacher's,
+        // e_v = 2^{(z_v - mr) c} <= 1: one factor of e_v, no larger than its terms (pr / rest
+        // would pass 2^128 long before the gradient does).  sum_r = 0: no token of the rest has
+        // weight, its factor does not matter.
+        const float factor = ((base + P.tv * sr) * (up_r * rS) - (sum_r > 0.f ? P.kl * R.pr / sum_r : 0.f)) * wT;
+        const float e0 = mr == -INFINITY ? 0.f : mr;
         if (P.grad && lane == 0) {
-          S.top[b] = mall;
+          S.top[b] = e0;
           S.factor[b] = factor;
           S.zero[b] = st != 0;
           mbar_arrive(&S.factors[b]);
@@ -436,7 +441,7 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
           }
           if (lane == 0) {                   // the label, where it is not recorded
             S.fix_idx[K] = R.recorded ? -1 : R.y;
-            S.fix_g[K] = ex2((zy - mall) * c) * factor - wT * lce;
+            S.fix_g[K] = ex2((zy - e0) * c) * factor - wT * lce;
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&S.fixed[b]);

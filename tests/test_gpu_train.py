@@ -405,6 +405,31 @@ def test_distill_rest_far_from_the_record(sv, n, V, K, dtype, gap, T, p_rest):
     check_distill(sv, confident(n, V, K, dtype, 50, p_rest, gap, T), 1.0, 0.5, 0.1, grad=False)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale", [1.0, 65536.0, -65536.0, 1e-4])
+@pytest.mark.parametrize("n,V,K", [(3, 5003, 16), (400, 3001, 5), (2, 600011, 30)])
+@pytest.mark.parametrize("gap,p_rest", [(80, 0.2), (86, 0.2), (95, 0.2), (200, 0.9), (-200, 0.2)])
+def test_distill_gradient_of_a_rest_far_from_the_record(sv, n, V, K, dtype, scale, gap, p_rest):
+    """The pull towards the rest is there whatever q_rest is, and it is finite under a loss
+    scale: |gradient| <= 2 (kl + tv + ce) w / T."""
+    d = confident(n, V, K, dtype, 51, p_rest, gap, 0.2)
+    d["w"] *= scale
+    kl, tv, ce = 5.0, 0.5, 0.1
+    top, idx, tail, label, w, T = cuda(d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"])
+    r = sv.distill_topk(d["z"].cuda(), top, idx, tail, label=label, row_weight=w, temperature=T, kl=kl, tv=tv, ce=ce,
+                        grad=True)
+    loss, _, g64, size = TP.distill(d["z"], d["top"], d["idx"], d["tail"], d["label"], d["w"], d["T"], kl, tv, ce)
+    assert (r["status"] == 0).all()
+    lim = d["w"].double().abs() * (kl + tv + ce) * 3 * TOL + 4e-6 * loss.abs()
+    assert ((r["loss"].cpu().double() - loss).abs() <= lim).all()
+    # weights below 2^-126 are 0, of q beside the row's largest logit and of the teacher's share
+    # beside the rest's: up to 2^-126 of the terms' coefficients, twice; and an output that is
+    # itself below 2^-126 is rounded to steps of 2^-126 eps (2^-133 in bf16, 2^-149 in fp32)
+    flush = (d["w"].abs() / d["T"]).double()[:, None] * 2 * (kl + tv + ce) * 2.0 ** -126 + 2.0 ** -126 * HALF[dtype]
+    e = (r["grad"].cpu().double() - g64).abs()
+    assert (e <= 1e-4 * size + HALF[dtype] * g64.abs() + flush).all()
+
+
 def test_distill_rest_by_hand(sv):
     """V = 3, K = 1, T = 0.1, teacher (8, 0, 0), student (10, 0, 0): p_rest = 2 e^-80, q_rest =
     2 e^-100, KL = 40 e^-80 - (p_rest - q_rest) = 7e-34."""
