@@ -203,11 +203,17 @@ struct ForwardWork {
 #pragma unroll
     for (int c = 4; c < kTcHalf; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
     const float m = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-    const float ref = m == -INFINITY ? 0.f : -m * kLog2eHi;  // a half past the vocabulary: weights of 0
-    float part[4] = {0.f, 0.f, 0.f, 0.f};
+    // x - m first: m log2(e) of logits masked with the type's lowest value would overflow
+    const float ref = m == -INFINITY ? 0.f : -m;             // a half past the vocabulary: weights of 0
+    const float2 R2 = make_float2(ref, ref), K2 = make_float2(kLog2eHi, kLog2eHi);
+    float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-    for (int c = 0; c < kTcHalf; ++c) part[c & 3] += ex2(fmaf(x[c], kLog2eHi, ref));
-    float s = (part[0] + part[1]) + (part[2] + part[3]);
+    for (int c = 0; c < kTcHalf; c += 2) {
+      const float2 a = __fmul2_rn(__fadd2_rn(make_float2(x[c], x[c + 1]), R2), K2);
+      part[c >> 1 & 1] = __fadd2_rn(part[c >> 1 & 1], make_float2(ex2(a.x), ex2(a.y)));
+    }
+    part[0] = __fadd2_rn(part[0], part[1]);
+    float s = part[0].x + part[0].y;
     const float2 other = e.join(make_float2(m, s));
     if (e.col != 0) return;
     const float both = fmaxf(m, other.x);    // a NaN sum stays
@@ -248,7 +254,8 @@ struct SoftWork {
     // a stage's last rows are zero (G sums over rows in whole stages); later ones are not read
     if (first >= (lt.rows + kTcK - 1) / kTcK * kTcK) return;
     const int at = P.lab[i] - v0;
-    const float g = P.g_c[i], gy = P.label_g[i], ref = -P.lse_c[i] * kLog2eHi;
+    const float g = P.g_c[i], gy = P.label_g[i], lse = P.lse_c[i];
+    const float2 L2 = make_float2(-lse, -lse), K2 = make_float2(kLog2eHi, kLog2eHi);    // l - lse first, as in the forward pass
     for (int c0 = 0; c0 < kTcHalf; c0 += 64) {
       uint4 out[8];
 #pragma unroll
@@ -257,9 +264,12 @@ struct SoftWork {
         tc_load32(x, e.tmem + c0 + 32 * h);
         const int left = P.V - v0 - c0 - 32 * h, mark = at - c0 - 32 * h;
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          x[c] = c < left && g != 0.f ? g * ex2(fmaf(x[c], kLog2eHi, ref)) : 0.f;
+        for (int c = 0; c < 32; c += 2) {
+          const float2 a = __fmul2_rn(__fadd2_rn(make_float2(x[c], x[c + 1]), L2), K2);
+          x[c] = c < left && g != 0.f ? g * ex2(a.x) : 0.f;
+          x[c + 1] = c + 1 < left && g != 0.f ? g * ex2(a.y) : 0.f;
           if (c == mark) x[c] = gy;
+          if (c + 1 == mark) x[c + 1] = gy;
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) out[4 * h + c] = pack8(x + 8 * c);

@@ -685,6 +685,51 @@ def test_ce_vocabulary_masked_by_minus_infinity(sv, V, lo, hi):
     assert (f["status"] == 1).all() and f["loss"].isnan().all() and f["lse"].isnan().all()
 
 
+LOWEST = torch.finfo(torch.bfloat16).min
+
+
+@pytest.mark.parametrize("V,lo,hi", [(1000, 0, 300), (9000, 0, 8700), (9000, 300, 9000), (9000, 0, 256),
+                                     (9000, 8448, 8704), (300, 0, 128)])
+def test_ce_vocabulary_masked_by_the_lowest_value(sv, V, lo, hi):
+    """The same with the type's lowest value, in whole half tiles and tiles: no weight, and
+    no gradient."""
+    h, w, label = make_ce(4, 64, V, 22)
+    h[:, 0] = 1
+    keep = torch.cat([torch.arange(lo), torch.arange(hi, V)])
+    at = label.long() % len(keep)
+    wd = w.clone()
+    wd[lo:hi, 0] = LOWEST
+    y = keep[at].to(torch.int32)
+    f = sv.linear_ce_forward(*cuda(h, wd, y))
+    cut = sv.linear_ce_forward(*cuda(h, w[keep], at.to(torch.int32)))
+    assert (f["status"] == 0).all()
+    lim = ce_tol(h, w[keep]).cuda()
+    for k in ("loss", "lse"):
+        assert ((f[k] - cut[k]).abs() <= 4 * lim + 4e-7 * cut[k].abs()).all()
+    b = sv.linear_ce_backward(*cuda(h, wd, y), f["lse"])
+    c = TP.ce_backward(h, w[keep], at, torch.ones(4), 4 * float(ce_tol(h, w[keep]).max()))
+    check_ce_grads({"grad_weight": b["grad_weight"][keep.cuda()]}, c)
+    assert (b["grad_weight"][lo:hi] == 0).all()
+    check_ce_grads({"grad_hidden": b["grad_hidden"]}, c)
+
+
+def test_ce_every_logit_of_the_lowest_value(sv):
+    """A uniform row so far below 0 that ln V is less than half a step of lse: the loss is ln V,
+    and the gradient is the one of the lse that was given, e^{l - lse} = 1 for each token."""
+    V = 700
+    h, w, label = make_ce(3, 64, V, 23)
+    h[:, 0] = 1
+    w[:, 0] = LOWEST
+    f = sv.linear_ce_forward(*cuda(h, w, label))
+    assert (f["status"] == 0).all() and (f["lse"] == LOWEST).all()
+    assert torch.allclose(f["loss"], torch.full((3,), math.log(V), device="cuda"), rtol=1e-5)
+    b = sv.linear_ce_backward(*cuda(h, w, label), f["lse"], need_hidden=False)["grad_weight"].cpu().double()
+    G = torch.ones(3, V, dtype=torch.double)
+    G[torch.arange(3), label.long()] = 0
+    want = G.t() @ h.double()
+    assert ((b - want).abs() <= 2.0 ** -8 * want.abs() + 1e-5).all()
+
+
 def test_ce_shared_labels(sv):
     """Every row has the same label: its weight row gathers all of them."""
     h, w, label = make_ce(200, 64, 300, 8)
