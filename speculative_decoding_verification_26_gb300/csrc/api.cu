@@ -28,58 +28,77 @@ thread_local uint64_t g_launches = 0;
 std::atomic<long long> g_wait_limit{kWaitLimitCycles};   // spec_set_wait_limit
 thread_local cudaEvent_t g_prof_begin = nullptr, g_prof_end = nullptr;
 
+// Kernels configured together, on the first call that needs them: what one family asks of
+// the device does not hold up, or fail, the calls of another.
+enum Family { kVerification, kRecord, kDistill, kLinearCe, kFamilies };
+
 struct DevState {
-  bool ready = false;
+  bool known = false;
   int sms = 0;        // multiprocessors
   int ctas = 0;       // resident verify CTAs on the device (SMs x CTAs per SM, at most 2 per SM)
-  int status = SPEC_OK;
+  int status = SPEC_OK;                    // whether the device runs the library's code
+  bool ready[kFamilies] = {};
+  int verification = SPEC_OK;              // of a ready kVerification
 };
 DevState g_dev[kMaxDevices];
 std::mutex g_mu;
 
-int device_state(int* ctas) {
+cudaError_t configure(Family f, int dev) {
+  switch (f) {
+    case kRecord: return configure_record(dev);
+    case kDistill: return configure_distill(dev);
+    case kLinearCe: return configure_linear_ce();
+    default: return configure_kernels();
+  }
+}
+
+// The current device, with the kernels of `f` configured.
+int device_for(Family f, int* device, DevState** state) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SPEC_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return SPEC_ERR_UNSUPPORTED;
   std::lock_guard<std::mutex> lk(g_mu);
   DevState& d = g_dev[dev];
-  if (!d.ready) {
-    int major = 0, minor = 0, n = 0;
+  *device = dev;
+  *state = &d;
+  if (!d.known) {
+    int major = 0, minor = 0;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return SPEC_ERR_CUDA;
-    d.sms = n;
-    if (major != 10 || minor != 3) {
-      d.status = SPEC_ERR_UNSUPPORTED;   // the library carries sm_103a code only
-    } else {
-      cudaError_t e = configure_kernels();
-      if (e == cudaSuccess) e = configure_record(dev);
-      if (e == cudaSuccess) e = configure_distill(dev);
-      if (e == cudaSuccess) e = configure_linear_ce();
-      int per_sm = 0;
-      if (e == cudaSuccess) e = verify_blocks_per_sm(&per_sm);
-      if (e != cudaSuccess) return SPEC_ERR_CUDA;
-      if (per_sm < 1) {
-        d.status = SPEC_ERR_UNSUPPORTED;
-      } else {
-        d.status = SPEC_OK;
-        n *= per_sm < 2 ? per_sm : 2;
-      }
-    }
-    d.ctas = n;
-    d.ready = true;
+    if (major != 10 || minor != 3) d.status = SPEC_ERR_UNSUPPORTED;   // the library carries sm_103a code only
+    d.known = true;
   }
-  *ctas = d.ctas;
-  return d.status;
+  if (d.status != SPEC_OK) return d.status;
+  if (!d.ready[f]) {
+    if (configure(f, dev) != cudaSuccess) return SPEC_ERR_CUDA;
+    if (f == kVerification) {
+      int per_sm = 0;
+      if (verify_blocks_per_sm(&per_sm) != cudaSuccess) return SPEC_ERR_CUDA;
+      d.verification = per_sm < 1 ? SPEC_ERR_UNSUPPORTED : SPEC_OK;
+      d.ctas = d.sms * (per_sm < 2 ? per_sm : 2);
+    }
+    d.ready[f] = true;
+  }
+  return f == kVerification ? d.verification : SPEC_OK;
 }
 
-// The current device and its multiprocessors, after a device_state that succeeded.
-int current_sms(int* device) {
+// For the verification calls and those beside them: resident verify CTAs.
+int device_state(int* ctas) {
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) dev = 0;
-  *device = dev;
-  return g_dev[dev].sms;
+  DevState* d = nullptr;
+  const int rc = device_for(kVerification, &dev, &d);
+  if (rc == SPEC_OK) *ctas = d->ctas;
+  return rc;
+}
+
+// For the drafter-training calls: the device and its multiprocessors.
+int training_state(Family f, int* dev, int* sms) {
+  DevState* d = nullptr;
+  const int rc = device_for(f, dev, &d);
+  if (rc == SPEC_OK) *sms = d->sms;
+  return rc;
 }
 
 bool overlap(const void* a, size_t an, const void* b, size_t bn) {
@@ -416,8 +435,8 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
   for (const void* p : ptrs4)
     if (!aligned(p, 4)) return SPEC_ERR_INVALID_ARG;
   if (!aligned(logits, dtype == SPEC_BF16 ? 2 : 4)) return SPEC_ERR_INVALID_ARG;
-  int ctas = 0;
-  const int ds = device_state(&ctas);
+  int dev = 0, sms = 0;
+  const int ds = training_state(kRecord, &dev, &sms);
   if (ds != SPEC_OK) return ds;
   RecordParams P{};
   P.logits = static_cast<const unsigned char*>(logits);
@@ -425,8 +444,6 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
   P.temperature = temperature;
   P.top_logits = top_logits; P.top_index = top_index; P.tail_lse = tail_lse; P.status = status;
   P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
-  int dev = 0;
-  const int sms = current_sms(&dev);
   if (launch_record(P, dev, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
   ++g_launches;
   return SPEC_OK;
@@ -448,8 +465,8 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
   if (grad_logits && grad_logits != logits) {        // in place, or apart
     if (overlap(logits, (size_t)n * V * es, grad_logits, (size_t)n * V * es)) return SPEC_ERR_INVALID_ARG;
   }
-  int ctas = 0;
-  const int ds = device_state(&ctas);
+  int dev = 0, sms = 0;
+  const int ds = training_state(kDistill, &dev, &sms);
   if (ds != SPEC_OK) return ds;
   DistillParams P{};
   P.logits = static_cast<const unsigned char*>(logits);
@@ -460,8 +477,6 @@ int spec_distill_topk(const void* logits, int dtype, int n, int V, int K, const 
   P.loss = loss; P.parts = parts; P.status = status;
   P.grad = static_cast<unsigned char*>(grad_logits);
   P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
-  int dev = 0;
-  const int sms = current_sms(&dev);
   if (launch_distill(P, dev, sms, reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return SPEC_ERR_CUDA;
   ++g_launches;
   return SPEC_OK;
@@ -487,15 +502,15 @@ int spec_linear_ce_forward(const void* hidden, const void* weight, int dtype, in
   P.n = n; P.H = H; P.V = V;
   if (!workspace || workspace_bytes < ce_layout(P, false, workspace)) return SPEC_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SPEC_ERR_INVALID_ARG;
-  int ctas = 0;
-  const int ds = device_state(&ctas);
+  int dev = 0, sms = 0;
+  const int ds = training_state(kLinearCe, &dev, &sms);
   if (ds != SPEC_OK) return ds;
   P.hidden = static_cast<const __nv_bfloat16*>(hidden);
   P.weight = static_cast<const __nv_bfloat16*>(weight);
   P.label = label; P.loss = loss; P.lse = lse; P.status = status;
   P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
-  int launches = 0, dev = 0;
-  const cudaError_t e = launch_ce_forward(P, current_sms(&dev), reinterpret_cast<cudaStream_t>(stream), &launches);
+  int launches = 0;
+  const cudaError_t e = launch_ce_forward(P, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
   g_launches += launches;
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
@@ -522,8 +537,8 @@ int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, i
   P.n = n; P.H = H; P.V = V;
   if (!workspace || workspace_bytes < ce_layout(P, true, workspace)) return SPEC_ERR_WORKSPACE;
   if (!aligned(workspace, 256)) return SPEC_ERR_INVALID_ARG;
-  int ctas = 0;
-  const int ds = device_state(&ctas);
+  int dev = 0, sms = 0;
+  const int ds = training_state(kLinearCe, &dev, &sms);
   if (ds != SPEC_OK) return ds;
   P.hidden = static_cast<const __nv_bfloat16*>(hidden);
   P.weight = static_cast<const __nv_bfloat16*>(weight);
@@ -531,8 +546,8 @@ int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, i
   P.grad_hidden = static_cast<__nv_bfloat16*>(grad_hidden);
   P.grad_weight = static_cast<__nv_bfloat16*>(grad_weight);
   P.wait_limit = g_wait_limit.load(std::memory_order_relaxed);
-  int launches = 0, dev = 0;
-  const cudaError_t e = launch_ce_backward(P, current_sms(&dev), reinterpret_cast<cudaStream_t>(stream), &launches);
+  int launches = 0;
+  const cudaError_t e = launch_ce_backward(P, sms, reinterpret_cast<cudaStream_t>(stream), &launches);
   g_launches += launches;
   return e == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }

@@ -866,6 +866,37 @@ def test_repeated_captured_and_on_two_streams(sv):
             assert torch.equal(p, q)
 
 
+FIRST_CAPTURED = """
+import sys
+import torch
+sys.path.insert(0, "tests")
+import speculative_decoding_verification_26_gb300 as sv
+import test_gpu_train as T
+ins = T.step_inputs(1)
+ws = T.step_ws(sv)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = T.all_calls(sv, *ins, ws)
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in outs]
+assert all(torch.equal(a, b) for a, b in zip(got, T.all_calls(sv, *ins, ws)))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_are_captured(sv):
+    """Kernels are configured on the first call that needs them, in a capture too."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CAPTURED], cwd=root, env={**os.environ, "PYTHONPATH": root},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
 def test_captured_call_has_its_own_workspace(sv):
     h, w, label = cuda(*make_ce(50, 64, 700, 5))
     eager = sv.linear_ce_forward(h, w, label)["loss"].clone()
