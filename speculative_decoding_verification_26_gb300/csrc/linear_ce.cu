@@ -279,6 +279,12 @@ struct SoftWork {
   }
 };
 
+// The gradients' sums are whole up to kWholeSteps stages and joined from parts of kGradChunk
+// beyond (rows for dW, a piece's vocabulary for dh).  The tensor cores cut off at every
+// addition of 16 k, and sums of one sign drift: dW of 131072 rows was off by 2.8e-4, of 2^20
+// rows by 4.4e-3, past its rounding to bf16 (2^-8).
+constexpr int kWholeSteps = 512, kGradChunk = 256;
+
 // Stages of k that a tile of dW takes at least: the time to write it.
 constexpr int kStoreSteps = 6;
 
@@ -328,18 +334,39 @@ struct GradWork {
     const int vb = t / col_tiles, nb = t % col_tiles;
     return {{&M.soft_t, false, vb * kTcTile, 0}, {&M.rows_t, false, nb * kTcTile, 0}, steps_w};
   }
+  // 32 columns from c0 of the half row: in tensor memory, or joined from parts
+  __device__ __forceinline__ static void columns(float (&v)[32], const TcHalfRow& e, int c0) { tc_load32(v, e.tmem + c0); }
+  __device__ __forceinline__ static void columns(float (&v)[32], const float (&x)[kTcHalf], int c0) {
+#pragma unroll
+    for (int c = 0; c < 32; ++c) v[c] = x[c0 + c];
+  }
+  __device__ __forceinline__ bool counts(int t, const TcHalfRow& e) const {      // the same for the warp
+    const int first = e.row - (int)(threadIdx.x & 31);
+    if (t < hidden_tiles) {
+      int mb, nb, sp;
+      hidden_at(t, mb, nb, sp);
+      return mb * kTcTile + first < rows;
+    }
+    return v_begin + (t - hidden_tiles) / col_tiles * kTcTile + first < P.V;
+  }
   __device__ __forceinline__ void epilogue(int t, TcHalfRow& e) const {
+    if (counts(t, e)) store<1>(t, e, e, e.any);
+  }
+  __device__ __forceinline__ void epilogue(int t, TcHalfRow& e, float (&x)[kTcHalf]) const { store<4>(t, e, x, true); }
+  template <int UNROLL, class From>
+  __device__ __forceinline__ void store(int t, TcHalfRow& e, const From& from, bool any) const {
     const int lane = threadIdx.x & 31;
     if (t < hidden_tiles) {
       int mb, nb, sp;
       hidden_at(t, mb, nb, sp);
       const int i = mb * kTcTile + e.row, j0 = nb * kTcTile + e.col;
-      if (i - lane >= rows) return;          // none of the warp's rows counts
       float* out = P.acc + ((size_t)sp * P.n_pad + i) * P.H + j0;
-      for (int c0 = 0; c0 < kTcHalf && j0 + c0 < P.H; c0 += 32) {
+#pragma unroll UNROLL
+      for (int c0 = 0; c0 < kTcHalf; c0 += 32) {
+        if (j0 + c0 >= P.H) break;
         float x[32];
-        if (e.any) {
-          tc_load32(x, e.tmem + c0);
+        if (any) {
+          columns(x, from, c0);
         } else {
 #pragma unroll
           for (int c = 0; c < 32; ++c) x[c] = 0.f;
@@ -362,14 +389,15 @@ struct GradWork {
     t -= hidden_tiles;
     const int vb = t / col_tiles, nb = t % col_tiles, first = v_begin + vb * kTcTile + e.row - lane;
     const int j0 = nb * kTcTile + e.col;
-    if (first >= P.V) return;
-    for (int c0 = 0; c0 < kTcHalf && j0 + c0 < P.H; c0 += 64) {
+#pragma unroll (UNROLL / 2 > 1 ? UNROLL / 2 : 1)
+    for (int c0 = 0; c0 < kTcHalf; c0 += 64) {
+      if (j0 + c0 >= P.H) break;
       uint4 out[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (e.any) {
+        if (any) {
           float x[32];
-          tc_load32(x, e.tmem + c0 + 32 * h);
+          columns(x, from, c0 + 32 * h);
 #pragma unroll
           for (int c = 0; c < 4; ++c) out[4 * h + c] = pack8(x + 8 * c);
         } else {
@@ -401,9 +429,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
                     v_begin};
   }, P.wait_limit, P.count + 1);
 }
+template <int CHUNK>
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     ce_grads(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
-  tc_run<0>([&] {
+  tc_run<CHUNK>([&] {
     const int len = piece_len(P, v_begin), count = *P.count;
     const int rt = (count + kTcTile - 1) / kTcTile, ct = (P.H + kTcTile - 1) / kTcTile;
     const int ht = P.grad_hidden ? rt * ct * P.splits : 0;
@@ -529,7 +558,8 @@ cudaError_t configure_linear_ce() {
   const int smem = (int)kTcSmem;
   e = cudaFuncSetAttribute(ce_forward, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_softmax, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_grads, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_grads<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_grads<kGradChunk>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   return e;
 }
 
@@ -581,12 +611,14 @@ cudaError_t launch_ce_backward(const CeParams& P, int nsm, cudaStream_t s, int* 
       !encode(&M.soft_out, P.soft, P.piece, P.piece, P.n_pad, 32) ||
       (P.grad_weight && !encode(&M.grad_weight, P.grad_weight, P.H, P.H, P.V, 32)))
     return cudaErrorInvalidValue;
+  const bool whole = P.split_steps <= kWholeSteps && P.n <= kWholeSteps * kTcK;
+  const auto grads = whole ? ce_grads<0> : ce_grads<kGradChunk>;
   launch_gather<true>(P, s);
   cudaError_t e = cudaGetLastError();
   int n = 2;
   for (long long v = 0; v < P.V && e == cudaSuccess; v += P.piece, n += 2) {
     e = launch_after(ce_softmax, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M, (int)v);
-    if (e == cudaSuccess) e = launch_after(ce_grads, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M, (int)v);
+    if (e == cudaSuccess) e = launch_after(grads, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M, (int)v);
   }
   if (e == cudaSuccess) e = launch_after(finish_grads, 4 * nsm, 256, 0, s, P);
   *launches = n;

@@ -631,6 +631,48 @@ def test_ce_row_errors(sv):
     assert (r["grad_hidden"][1:4] == 0).all()
 
 
+@pytest.mark.parametrize("n", [1 << 15, 1 << 17, 1 << 20])
+def test_ce_weight_gradient_of_many_rows(sv, n):
+    """Sums of one sign over up to the most rows.  With W = 0 and V = 256, G is -255/256 at the
+    label and 1/256 elsewhere, exact in bf16, so that only the sums of h and the output's
+    rounding are left.  The tensor cores add 16 rows at a time and cut off less than a step of
+    2^-23 of the sum so far; of a sum that grows evenly that is half of it on average, over at
+    most 2048 additions in a row: 2^-13."""
+    H, V = 64, 256
+    g = gen(5)
+    h = ((torch.rand(n, H, generator=g) + 1) * 2 ** (torch.arange(H) / H)).to(torch.bfloat16)
+    hd, wd, ld = cuda(h, torch.zeros(V, H, dtype=torch.bfloat16), torch.full((n,), 3, dtype=torch.int32))
+    lse = sv.linear_ce_forward(hd, wd, ld)["lse"]
+    r = sv.linear_ce_backward(hd, wd, ld, lse)
+    G = torch.full((V, 1), 1 / 256, dtype=torch.double)
+    G[3] = -255 / 256
+    want = G * h.double().sum(0)
+    e = (r["grad_weight"].cpu().double() - want).abs()
+    step = 2.0 ** (torch.floor(torch.log2(want.abs())) - 7)
+    assert (e <= step / 2 + 2.0 ** -13 * want.abs()).all(), ((e - step / 2) / want.abs()).max()
+    assert (r["grad_hidden"] == 0).all()
+
+
+def test_ce_hidden_gradient_over_a_large_vocabulary(sv):
+    """grad_hidden's sum over a piece joined from parts (checked on the GPU)."""
+    n, H, V = 2000, 1288, 65700
+    h, w, label = make_ce(n, H, V, 24)
+    w = w.abs()
+    g = torch.rand(n, generator=gen(10)) / n
+    hd, wd, ld, gd = cuda(h * 0.1, w, label, g)
+    f = sv.linear_ce_forward(hd, wd, ld)
+    r = sv.linear_ce_backward(hd, wd, ld, f["lse"], gd)
+    W = wd.double()
+    p = torch.softmax(hd.double() @ W.t(), 1) * gd.double()[:, None]
+    G = p.clone()
+    G[torch.arange(n, device="cuda"), ld.long()] -= gd.double()
+    off = 2.0 ** -8 * G.abs() + 2e-4 * p                 # see train_plain.ce_backward
+    for got, want, lim in ((r["grad_hidden"], G @ W, off @ W.abs()),
+                           (r["grad_weight"], G.t() @ hd.double(), off.t() @ hd.double().abs())):
+        e = (got.double() - want).abs()
+        assert (e <= lim + 2.0 ** -8 * want.abs() + 1e-37).all(), (e / lim).max()
+
+
 def test_ce_one_gradient_alone(sv):
     h, w, label = make_ce(70, 72, 900, 3)
     g = torch.rand(70, generator=gen(5))
