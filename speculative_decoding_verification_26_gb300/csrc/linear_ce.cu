@@ -234,8 +234,21 @@ __device__ __forceinline__ uint4 pack8(const float* v) {
   return make_uint4(u[0], u[1], u[2], u[3]);
 }
 
+// 32 columns from c0 of a half row: in tensor memory, or joined from parts
+__device__ __forceinline__ void columns(float (&v)[32], const TcHalfRow& e, int c0) { tc_load32(v, e.tmem + c0); }
+__device__ __forceinline__ void columns(float (&v)[32], const float (&x)[kTcHalf], int c0) {
+#pragma unroll
+  for (int c = 0; c < 32; ++c) v[c] = x[c0 + c];
+}
+
 // backward: G of a piece as bf16, its one rounding before the two products that
-// read it; the logits and the softmax are fp32
+// read it; the logits and the softmax are fp32.  Past kWholeLogits stages (H = 2048) the
+// logits are sums of the same parts as the forward call's, to match the lse that they are
+// taken beside: with whole sums and an offset l that all logits of a row share, the rows of
+// G sum to -2e-6 l at H = 2048 (below its rounding while l < 1000), to -4e-5 l at 8192 and
+// -4e-4 l at 65536.  Parts cost 140 us for 135 at H = 1160, where whole sums are used, and
+// nothing to speak of at 2048 and more (4.43 ms for 4.41).
+constexpr int kWholeLogits = 32;
 struct SoftWork {
   const CeParams& P;
   const CeMaps& M;
@@ -247,21 +260,31 @@ struct SoftWork {
     lt.at(t, mb, vt);
     return {{&M.rows, true, mb * kTcTile, 0}, {&M.weight, true, v_begin + vt * kTcTile, 0}, (P.H + kTcK - 1) / kTcK};
   }
+  // a stage's last rows are zero (G sums over rows in whole stages); later ones are not read
+  __device__ __forceinline__ bool counts(int t, const TcHalfRow& e) const {      // the same for the warp
+    int mb, vt;
+    lt.at(t, mb, vt);
+    return mb * kTcTile + e.row - (int)(threadIdx.x & 31) < (lt.rows + kTcK - 1) / kTcK * kTcK;
+  }
   __device__ __forceinline__ void epilogue(int t, TcHalfRow& e) const {
+    if (counts(t, e)) store<1>(t, e, e);
+  }
+  __device__ __forceinline__ void epilogue(int t, TcHalfRow& e, float (&x)[kTcHalf]) const { store<2>(t, e, x); }
+  template <int UNROLL, class From>
+  __device__ __forceinline__ void store(int t, TcHalfRow& e, const From& from) const {
     int mb, vt;
     lt.at(t, mb, vt);
     const int i = mb * kTcTile + e.row, first = i - (int)(threadIdx.x & 31), v0 = v_begin + vt * kTcTile + e.col;
-    // a stage's last rows are zero (G sums over rows in whole stages); later ones are not read
-    if (first >= (lt.rows + kTcK - 1) / kTcK * kTcK) return;
     const int at = P.lab[i] - v0;
     const float g = P.g_c[i], gy = P.label_g[i], lse = P.lse_c[i];
     const float2 L2 = make_float2(-lse, -lse), K2 = make_float2(kLog2eHi, kLog2eHi);    // l - lse first, as in the forward pass
+#pragma unroll UNROLL
     for (int c0 = 0; c0 < kTcHalf; c0 += 64) {
       uint4 out[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float x[32];
-        tc_load32(x, e.tmem + c0 + 32 * h);
+        columns(x, from, c0 + 32 * h);
         const int left = P.V - v0 - c0 - 32 * h, mark = at - c0 - 32 * h;
 #pragma unroll
         for (int c = 0; c < 32; c += 2) {
@@ -333,12 +356,6 @@ struct GradWork {
     t -= hidden_tiles;
     const int vb = t / col_tiles, nb = t % col_tiles;
     return {{&M.soft_t, false, vb * kTcTile, 0}, {&M.rows_t, false, nb * kTcTile, 0}, steps_w};
-  }
-  // 32 columns from c0 of the half row: in tensor memory, or joined from parts
-  __device__ __forceinline__ static void columns(float (&v)[32], const TcHalfRow& e, int c0) { tc_load32(v, e.tmem + c0); }
-  __device__ __forceinline__ static void columns(float (&v)[32], const float (&x)[kTcHalf], int c0) {
-#pragma unroll
-    for (int c = 0; c < 32; ++c) v[c] = x[c0 + c];
   }
   __device__ __forceinline__ bool counts(int t, const TcHalfRow& e) const {      // the same for the warp
     const int first = e.row - (int)(threadIdx.x & 31);
@@ -421,9 +438,10 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     return ForwardWork{P, M, {(count + kTcTile - 1) / kTcTile, (P.V + kTcTile - 1) / kTcTile, count}};
   }, P.wait_limit, P.count + 1);
 }
+template <int CHUNK>
 __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
     ce_softmax(const __grid_constant__ CeParams P, const __grid_constant__ CeMaps M, int v_begin) {
-  tc_run<0>([&] {
+  tc_run<CHUNK>([&] {
     const int count = *P.count;
     return SoftWork{P, M, {(count + kTcTile - 1) / kTcTile, (piece_len(P, v_begin) + kTcTile - 1) / kTcTile, count},
                     v_begin};
@@ -557,7 +575,8 @@ cudaError_t configure_linear_ce() {
   g_encode = reinterpret_cast<EncodeTiled>(f);
   const int smem = (int)kTcSmem;
   e = cudaFuncSetAttribute(ce_forward, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_softmax, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_softmax<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_softmax<kChunk>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_grads<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_grads<kGradChunk>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   return e;
@@ -611,13 +630,14 @@ cudaError_t launch_ce_backward(const CeParams& P, int nsm, cudaStream_t s, int* 
       !encode(&M.soft_out, P.soft, P.piece, P.piece, P.n_pad, 32) ||
       (P.grad_weight && !encode(&M.grad_weight, P.grad_weight, P.H, P.H, P.V, 32)))
     return cudaErrorInvalidValue;
+  const auto softmax = P.H <= kWholeLogits * kTcK ? ce_softmax<0> : ce_softmax<kChunk>;
   const bool whole = P.split_steps <= kWholeSteps && P.n <= kWholeSteps * kTcK;
   const auto grads = whole ? ce_grads<0> : ce_grads<kGradChunk>;
   launch_gather<true>(P, s);
   cudaError_t e = cudaGetLastError();
   int n = 2;
   for (long long v = 0; v < P.V && e == cudaSuccess; v += P.piece, n += 2) {
-    e = launch_after(ce_softmax, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M, (int)v);
+    e = launch_after(softmax, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M, (int)v);
     if (e == cudaSuccess) e = launch_after(grads, nsm / 2 * 2, kTcThreads, kTcSmem, s, P, M, (int)v);
   }
   if (e == cudaSuccess) e = launch_after(finish_grads, 4 * nsm, 256, 0, s, P);

@@ -673,6 +673,36 @@ def test_ce_hidden_gradient_over_a_large_vocabulary(sv):
         assert (e <= lim + 2.0 ** -8 * want.abs() + 1e-37).all(), (e / lim).max()
 
 
+@pytest.mark.parametrize("H,offset", [(1024, 100), (2048, 100), (2056, 100), (8192, 300), (65536, 1000)])
+def test_ce_logits_that_share_an_offset(sv, H, offset):
+    """Logits of one sign, all about `offset`: the backward call's match the lse that they are
+    taken beside.  A column of ones in the weights makes grad_hidden the sum of a row of G, 0 by
+    the formula.  G is rounded to bf16, off by 2^-8 of itself at most and not all one way, so its
+    row sums to that of the rounded G of the formula, within what moves a rounding: the logits'
+    own error.  At most 128 additions in a row, of sums that grow evenly, cut off 128 / 2 steps of
+    2^-23 (whole sums at H <= 2048); the parts' own additions are 2^-24 offset each, in lse and
+    in the logits; and ex2's 2e-6."""
+    n, V = 8, 1000
+    g = gen(6)
+    w = (torch.rand(V, H, generator=g) * 0.2 + 0.9) * offset / H / 1.5
+    w[:, 0] = 1.0
+    w = w.to(torch.bfloat16)
+    h = (torch.rand(n, H, generator=g) + 1).to(torch.bfloat16)
+    label = torch.arange(n, dtype=torch.int32)
+    hd, wd, ld = cuda(h, w, label)
+    f = sv.linear_ce_forward(hd, wd, ld)
+    got = sv.linear_ce_backward(hd, wd, ld, f["lse"])["grad_hidden"][:, 0].double()
+    l = hd.double() @ wd.double().t()
+    G = torch.softmax(l, 1)
+    G[torch.arange(n), label.long()] -= 1
+    rounded = G.to(torch.bfloat16).double().sum(1)
+    parts = max(1, H // 1024)
+    slip = (64 * 2.0 ** -23 + 2 * parts * 2.0 ** -24) * offset * 1.1 + 2e-6
+    # e^slip of all weights, of which sums to 1; and a rounding that goes the other way moves a
+    # weight by a step: those within slip of a border, twice slip of them, by 2^-7 at most
+    assert ((got - rounded).abs() <= slip + 2 * slip + 2.0 ** -8 * rounded.abs()).all(), (got - rounded).abs().max()
+
+
 def test_ce_one_gradient_alone(sv):
     h, w, label = make_ce(70, 72, 900, 3)
     g = torch.rand(70, generator=gen(5))
