@@ -561,6 +561,44 @@ def test_ce_backward(sv, n, H, V):
     check_ce_backward(sv, h, w, label, torch.rand(n, generator=gen(1)) / n)
 
 
+@pytest.mark.parametrize("n,H,V", [(7, 1032, 300), (70, 2048, 513), (300, 2056, 1023), (33, 2560, 777), (5, 4104, 257),
+                                   (129, 8192, 300)])
+def test_ce_wide_hidden_states(sv, n, H, V):
+    """Sums of several parts of 1024 of H, whole and ragged ones, some rows without a label."""
+    h, w, label = make_ce(n, H, V, H + V)
+    label[1::5] = -1
+    check_ce_forward(sv, h, w, label)
+    check_ce_backward(sv, h, w, label, torch.rand(n, generator=gen(1)) / n)
+
+
+@pytest.mark.parametrize("n,H,V", [(4097, 24, 600), (9001, 16, 300), (32769, 8, 300), (70003, 8, 257)])
+def test_ce_many_rows(sv, n, H, V):
+    """More than one group of row tiles (4096 rows), and CTAs that gather 64 rows (32768)."""
+    h, w, label = make_ce(n, H, V, H + V)
+    label[1::5] = -1
+    label[4000:4300] = -1
+    check_ce_forward(sv, h, w, label)
+    check_ce_backward(sv, h, w, label, torch.rand(n, generator=gen(1)) / n)
+
+
+@pytest.mark.parametrize("H", [1024, 2048, 2560])
+def test_ce_small_losses(sv, H):
+    """The label has nearly all of the mass: the loss ln(1 + sum e^{l_v - z}) keeps its precision.
+    It is off by what l_v and z are: others of up to 5 in size, 64 additions of a part cut off by
+    2^-24 of them on average, 1.9e-5, over up to 2.5 parts of which most is chance; z of up to
+    24 from 64 chains joined in nearest, 3e-6; ex2 and the sums, 2e-6."""
+    n, V = 64, 3001
+    _, w, label = make_ce(n, H, V, 77)
+    h = (torch.linspace(2.5, 5.6, n)[:, None] * w[label.long()].float()).to(torch.bfloat16)
+    f = sv.linear_ce_forward(*cuda(h, w, label))
+    l = h.double() @ w.double().t()
+    z = l.gather(1, label.long()[:, None])
+    hot = torch.zeros_like(l).scatter_(1, label.long()[:, None], 1.0)
+    loss = torch.log1p((torch.exp(l - z) * (1 - hot)).sum(1))
+    assert loss.min() < 1e-5 and loss.max() > 1e-2
+    assert ((f["loss"].cpu().double() - loss).abs() <= 4e-5 * loss).all()
+
+
 def test_ce_large_vocabulary_in_several_pieces(sv):
     """A small batch whose G does not fit one piece (checked on a few rows)."""
     n, H, V = 1024, 64, 151936
