@@ -537,7 +537,6 @@ cudaError_t launch_record(const RecordParams& P, int dev, int nsm, cudaStream_t 
 cudaError_t configure_record(int dev);    // resident clusters of the current device `dev`
 
 // Parameters of the distillation kernel (distill.cu).
-constexpr int kDistillMaxV = SPEC_DISTILL_MAX_V;
 struct DistillParams {
   const unsigned char* logits;   // [n, V]
   int dtype, n, V, K;

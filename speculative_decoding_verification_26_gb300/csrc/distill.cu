@@ -48,7 +48,6 @@ constexpr int kDisPer = 4;                                 // vectors of a stage
 constexpr int kDisStageVecs = kDisPer * kDisConsumers;
 constexpr int kDisStage = 16 * kDisStageVecs;
 constexpr int kDisMaxStages = 6;
-constexpr float kLn2 = 0.693147180559945f;
 
 struct DisShared {
   uint64_t full[kDisMaxStages], empty[kDisMaxStages];
@@ -74,16 +73,6 @@ __device__ __forceinline__ void store_logit(unsigned char* row, int e, float v) 
   else reinterpret_cast<float*>(row)[e] = v;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-  return v;
-}
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
 // Weights are 2^{(x - m) c}, m a maximum: m c apart would overflow for rows masked with
 // the type's lowest value.  A sum of weights moved from one maximum to another:
 __device__ __forceinline__ float moved(float sum, float from, float to, float c) {
@@ -108,15 +97,6 @@ __device__ __forceinline__ void mark_of(int o, int& word, int& bit) {
   word = at >> 5;
   bit = at & 31;
 }
-
-// The ring's place: stage and phase.
-struct RingAt {
-  int stage = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int stages) {
-    if (++stage == stages) { stage = 0; phase ^= 1; }
-  }
-};
 
 // A logit as loaded, and its value: a load is not waited for until the latter.
 template <int DT>
@@ -351,7 +331,6 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
       bounded_wait(&S.summed[b], (i >> 1) & 1, waits);
       __syncwarp();
       const unsigned char* row = P.logits + (size_t)r * V * ES;
-      unsigned char* grow = P.grad ? P.grad + (size_t)r * V * ES : nullptr;
       const RowSpan sp = row_span<DT>(row, V);
       const RowShare sh = row_share<CS>(sp, rank);
       const float nan = __int_as_float(0x7fc00000);

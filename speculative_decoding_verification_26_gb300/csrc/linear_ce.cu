@@ -164,8 +164,6 @@ struct LogitTiles {
   }
 };
 
-constexpr float kLn2 = 0.693147180559945f;
-
 // Forward: a tile's maximum and sum of each row, without the label.  The tensor cores
 // cut their sums off (about 1e-5 of a logit of 16 over H = 2048), and where the label
 // has nearly all of the mass its loss is as small as that: the label's logit is summed

@@ -55,7 +55,6 @@ constexpr int kMaxima = 4 * kRecConsumers;
 constexpr int kAbove = 768, kTies = 256, kList = kAbove + kTies;
 static_assert(kMaxGroups * kRecConsumers * 2 <= kList * 8, "a list holds the numbers of all groups");
 static_assert(kMaxGroups * kRecConsumers <= 32 * kFinThreads, "a finisher's marks");
-constexpr float kLn2 = 0.693147180559945f;
 
 // order of a float as an unsigned integer, -0 and +0 alike
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -99,21 +98,6 @@ struct RecShared {
   int stop[3];                               // the finishers' decision after each wait
   int failed;
 };
-
-// The ring's place: stage and phase.
-struct RecRing {
-  int stage = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next(int stages) {
-    if (++stage == stages) { stage = 0; phase ^= 1; }
-  }
-};
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  return v;
-}
 
 // A bound of a share's want-th largest logit from N of its maxima per lane: one of
 // them that `want` or more reach, at most an eighth more where there is one.  Keys are
@@ -416,7 +400,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
 
   if (warp == kRecWarps + 1 + kFinWarps) {   // producer
     if (lane == 0) {
-      RecRing at;
+      RingAt at;
       bool ok = true;
       for (int r = first; r < P.n && ok; r += step) {
         const unsigned char* row = P.logits + (size_t)r * V * ES;
@@ -661,7 +645,7 @@ __global__ void __launch_bounds__(kRecThreads, 2) record_kernel(const __grid_con
       __syncwarp();
     }
   } else {                                   // consumers
-    RecRing at;
+    RingAt at;
     int i = 0;
     float T = first < P.n && P.temperature ? P.temperature[first] : 1.f;      // a row ahead: a load takes 2 us here
     for (int r = first; r < P.n; r += step, ++i) {

@@ -195,6 +195,28 @@ inline cudaError_t resident_clusters(K kernel, int cs, int threads, size_t smem,
   return e;
 }
 
+constexpr float kLn2 = 0.693147180559945f;
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  return v;
+}
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// A place in a ring of stages: the stage, and the phase of its barriers.
+struct RingAt {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next(int stages) {
+    if (++stage == stages) { stage = 0; phase ^= 1; }
+  }
+};
+
 // ---------------------------------------------------------------------------
 // clusters
 
