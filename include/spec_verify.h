@@ -283,14 +283,16 @@ int spec_gamma_select(const float* signals, const float* comp, const float* mode
  *   top_logits [n, K] fp32, top_index [n, K] int32: the K largest logits, the
  *     largest first, equal values (-0 and +0 among them) by ascending token;
  *   tail_lse   [n] fp32: ln sum e^{x_v / T} over the tokens not recorded, -inf
- *     when they have no mass (weights below 2^-126 of the row's largest are 0).
+ *     when they have no mass (weights below 2^-126 of the row's largest, 87 nats
+ *     under it, are 0).
  * A logit of -inf is not recorded: a row with fewer than K others (a filtered
  * row) ends with entries of logit -inf and index -1.
  *   K           1 <= K <= min(V, SPEC_MAX_TOPK);
  *   temperature [n] fp32 or NULL (= 1);
  *   status      0, SPEC_ST_NONFINITE (a NaN or +inf, or no finite logit),
  *     SPEC_ST_BAD_TEMPERATURE or SPEC_ST_TIMEOUT (an internal wait hit its time
- *     limit); such a row has NaN logits, indices -1 and a NaN tail.
+ *     limit; rows of 2^26 logits or more whose large ones sit in few places can
+ *     take that long); such a row has NaN logits, indices -1 and a NaN tail.
  * No workspace.  Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^30], V
  * outside [2, 2^28), K, dtype, NULL required pointers, misalignment),
  * SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
@@ -310,7 +312,8 @@ int spec_topk_logits(const void* logits, int dtype, int n, int V, int K, const f
  *   top_logits, top_index [n, K], 1 <= K <= SPEC_MAX_TOPK: entries in any order;
  *     an entry of index -1 is left out, whatever its logit;
  *   tail_lse    [n] or NULL; NULL or -inf: the teacher has no mass outside the
- *     record, p is renormalised over its K logits;
+ *     record, p is renormalised over its K logits.  It belongs to the temperature
+ *     that the record was taken at, which has to be this call's for the row;
  *   label       [n] int32 or NULL; -1 or NULL: no CE term;
  *   row_weight  [n] fp32 or NULL (= 1); of a row of weight 0 (padding) the
  *     logits are not read, what its record, label and temperature hold does not

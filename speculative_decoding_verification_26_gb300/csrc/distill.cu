@@ -717,7 +717,8 @@ cudaError_t configure_as(int dev) {
   return e;
 }
 
-// Entries per recorder lane: records of up to 64, 128 and 256.
+// Entries per recorder lane: records of up to 64, 128 and 256.  With 8 entries the
+// recorder spills 64 to 204 bytes a thread, a few words of a row's record at a time.
 template <int DT>
 cudaError_t launch_entries(const DistillParams& P, int dev, int nsm, cudaStream_t s) {
   if (P.K <= 64) return launch_of<DT, 2>(P, dev, nsm, s);

@@ -170,7 +170,8 @@ struct LogitTiles {
 // apart (gather_rows), the loss is ln(1 + the others' weights beside the label's), and
 // the others' logits are sums of parts of kChunk stages, 1024 of H (H = 2048: the loss off
 // by 5.8e-6 of itself at most, 1e-5 with whole sums and 3.8e-6 with parts of 512; one row
-// 115.4, 115.2 and 117.9 us; 4096 rows 1.26, 1.25 and 1.34 ms).
+// 115.4, 115.2 and 117.9 us; 4096 rows 1.26, 1.25 and 1.34 ms in short runs, and 1.40 ms
+// with parts of 1024 where the power cap holds).
 constexpr int kChunk = 16;
 struct ForwardWork {
   const CeParams& P;
@@ -303,7 +304,9 @@ struct SoftWork {
 // The gradients' sums are whole up to kWholeSteps stages and joined from parts of kGradChunk
 // beyond (rows for dW, a piece's vocabulary for dh).  The tensor cores cut off at every
 // addition of 16 k, and sums of one sign drift: dW of 131072 rows was off by 2.8e-4, of 2^20
-// rows by 4.4e-3, past its rounding to bf16 (2^-8).
+// rows by 4.4e-3, past its rounding to bf16 (2^-8).  Parts cost 194 us for 183 where tiles
+// are many and short (64 x 1024 x 128256), 132.5 for 134.6 at 333 x 1160 x 40001, and the
+// same at 4096 rows.
 constexpr int kWholeSteps = 512, kGradChunk = 256;
 
 // Stages of k that a tile of dW takes at least: the time to write it.
@@ -458,7 +461,7 @@ __global__ void __cluster_dims__(2) __launch_bounds__(kTcThreads, 1)
 }
 
 // lse and loss of the rows that count: the tiles' maxima and sums, each warp a
-// share of the tiles of 32 rows
+// share of the tiles of 32 rows.  20 loads in flight spill 10 words a thread.
 constexpr int kMergeThreads = 1024, kMergeWarps = kMergeThreads / 32;
 __global__ void __launch_bounds__(kMergeThreads) merge_rows(const __grid_constant__ CeParams P) {
   __shared__ float2 s_part[kMergeWarps][32];
@@ -664,7 +667,8 @@ size_t ce_layout(CeParams& P, bool backward, void* base) {
     P.part = reinterpret_cast<float2*>(place(8ull * P.n_pad * ((P.V + kTcTile - 1) / kTcTile)));
     return at;
   }
-  // G of a piece takes at most about 256 MB, and a piece is a whole number of tiles
+  // G of a piece takes at most 256 MB, and a piece is a whole number of tiles: past 2^19
+  // rows one, and up to 512 MB
   const long long all = (P.V + kTcTile - 1ll) / kTcTile * kTcTile;
   long long piece = (128ll << 20) / P.n_pad / kTcTile * kTcTile;
   if (piece < kTcTile) piece = kTcTile;
