@@ -128,7 +128,7 @@ struct Record {
   int idx[NJ];                               // -1: none
   float p[NJ], f[NJ];                        // teacher's share, student's 2^{(z - zmax) c}
   uint32_t z[NJ], zy;                        // student's logits there and at the label, as loaded
-  float w, T, zmax, F, A, pr, lpr;           // A = sum p (log2 p - (z - zmax) c), F = sum f
+  float w, T, zmax, F, A, in, pr, lpr;       // A = sum p (log2 p - (z - zmax) c), F = sum f, in = sum p
   int y, st;
   bool skip, recorded;
 };
@@ -300,12 +300,15 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
       Z = warp_sum(Z) + er;
       R.F = warp_sum(F);
       const float rZ = 1.f / Z, l2Z = log2f(Z);
+      float in = 0.f;
 #pragma unroll
       for (int j = 0; j < NJ; ++j) {
         R.p[j] *= rZ;
+        in += R.p[j];
         if (R.p[j] > 0.f) A += R.p[j] * ((a[j] - l2Z) - (z[j] - z0) * sc.c);   // +inf where z is -inf
       }
       R.A = warp_sum(A);
+      R.in = warp_sum(in);                   // 1 - pr would cancel beside a lift of thousands
       R.pr = er * rZ;
       R.lpr = lt - top - l2Z;
       R.st = (int)__reduce_or_sync(0xffffffffu, (unsigned)R.st);
@@ -396,10 +399,9 @@ __global__ void __launch_bounds__(kDisThreads, 2) distill_kernel(const __grid_co
           S.zero[b] = st != 0;
           mbar_arrive(&S.factors[b]);
         }
-        // log2 q_k = (z_k - zmax) c + lift - l2S, and the p_k sum to 1 - p_r;
+        // log2 q_k = (z_k - zmax) c + lift - l2S, and the p_k sum to `in`;
         // log2 q_r = log2 sum_r + lift_r - l2S
-        kl = R.A - (1.f - R.pr) * (lift - l2S);
-        if (1.f - R.pr == 0.f) kl = R.A;
+        kl = R.in > 0.f ? R.A - R.in * (lift - l2S) : R.A;
         if (R.pr > 0.f) kl += R.pr * (R.lpr - (log2f(sum_r) + lift_r - l2S));
         kl *= kLn2;
         tv = 0.5f * (tv + fabsf(R.pr - qr));
@@ -718,7 +720,7 @@ cudaError_t configure_as(int dev) {
 }
 
 // Entries per recorder lane: records of up to 64, 128 and 256.  With 8 entries the
-// recorder spills 64 to 204 bytes a thread, a few words of a row's record at a time.
+// recorder spills 72 to 208 bytes a thread, a few words of a row's record at a time.
 template <int DT>
 cudaError_t launch_entries(const DistillParams& P, int dev, int nsm, cudaStream_t s) {
   if (P.K <= 64) return launch_of<DT, 2>(P, dev, nsm, s);

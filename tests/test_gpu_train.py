@@ -398,7 +398,7 @@ def confident(n, V, K, dtype, seed, p_rest, gap, T):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("n,V,K", [(3, 5003, 16), (40, 20011, 200), (400, 3001, 5)])
 @pytest.mark.parametrize("gap,T,p_rest", [(95, 0.2, 0.1), (300, 0.05, 0.1), (90, 1.0, 0.9), (-300, 0.05, 0.9),
-                                          (-95, 0.3, 0.1)])
+                                          (-95, 0.3, 0.1), (-20000, 0.001, 0.99999)])
 def test_distill_rest_far_from_the_record(sv, n, V, K, dtype, gap, T, p_rest):
     """One of the two has no weight beside the other in 32 bits (e^-87.3 = 2^-126): KL is
     finite all the same, its logarithms are."""
