@@ -218,7 +218,8 @@ __device__ __noinline__ void recount(const RecordParams& P, RecShared& S, int r,
     else hi = mid - 1;
   }
   const int ties = count([&](uint32_t k) { return k == lo; });
-  float s = 0.f;
+  // a lane sums V / 32 weights one after another: what each addition rounds off is carried along
+  float s = 0.f, off = 0.f;
   int at = 0;
   for (int e0 = 0; e0 < V; e0 += 32) {
     const int e = e0 + lane;
@@ -229,7 +230,11 @@ __device__ __noinline__ void recount(const RecordParams& P, RecShared& S, int r,
     const int to = at + __popc(vote & ((1u << lane) - 1));
     if (above && to < kAbove) list[to] = candidate(x, e);
     at += __popc(vote);
-    if (e < V && k < lo) s += ex2((x - m) * c);
+    if (e < V && k < lo) {
+      const float w = ex2((x - m) * c) - off, to_s = s + w;
+      off = (to_s - s) - w;
+      s = to_s;
+    }
   }
   s = warp_sum(s);
   __syncwarp();

@@ -136,6 +136,16 @@ def test_record_of_long_rows(sv, n, V, dtype):
     check_record(sv, rows(n, V, dtype, 41), 256, torch.rand(n, generator=gen(6)) + 0.5)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("n,V,K", [(4, 283111, 142), (3, 1 << 20, 64), (320, 70000, 256)])
+def test_record_of_clustered_rows(sv, n, V, K, dtype):
+    """The large logits in few threads' vectors, more of them than are listed: the K-th largest
+    by counting, and a tail of all the others."""
+    x = torch.randn(n, V, generator=gen(43))
+    x[:, torch.arange(V) % 2048 < 8] += 20
+    check_record(sv, x.to(dtype), K, torch.rand(n, generator=gen(7)) + 1.0)
+
+
 @pytest.mark.parametrize("shift", [1, 3, 5])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_record_of_rows_off_alignment(sv, dtype, shift):
