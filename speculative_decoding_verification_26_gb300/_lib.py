@@ -172,14 +172,20 @@ def workspace(B, G, V, device):
     made by several host threads at once: the calls that take it by default see
     to that)."""
     torch = _torch()
+    torch.cuda.init()
+    device = torch.device(device)
+    i = torch.cuda.current_device() if device.index is None else device.index
+    return _cached_ws(B, G, V, device, (i, _raw_stream(i)))
+
+
+def _cached_ws(B, G, V, device, key):
     n = workspace_bytes(B, G, V)
     if n == 0:
         raise ValueError("sizes outside the library limits")
-    key = (str(device), torch.cuda.current_stream(device).cuda_stream)
     ws = _ws_cache.get(key)
     if ws is None or ws.numel() < n:
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        _ws_cache[key] = ws
+        torch = _torch()
+        ws = _ws_cache[key] = torch.empty(n, dtype=torch.uint8, device=device)
     return ws
 
 
@@ -192,16 +198,18 @@ class _Held:
         self.ws, self.sizes, self.dev, self.lock = ws, (B, G, V), dev, None
 
     def __enter__(self):
-        if self.ws is None:
-            lock = _ws_lock(self.dev.index, _torch().cuda.current_stream(self.dev).cuda_stream)
-            lock.acquire()
-            self.lock = lock
-            try:
-                self.ws = workspace(*self.sizes, self.dev)
-            except BaseException:
-                lock.release()
-                raise
-        return self.ws
+        if self.ws is not None:
+            return self.ws
+        i = self.dev.index
+        stream = _raw_stream(i)
+        lock = _ws_lock(i, stream)
+        lock.acquire()
+        self.lock = lock
+        try:
+            return _cached_ws(*self.sizes, self.dev, (i, stream))
+        except BaseException:
+            lock.release()
+            raise
 
     def __exit__(self, *exc):
         if self.lock is not None:
@@ -213,8 +221,13 @@ def _out(o, key, make):
     return make() if t is None else t
 
 
+def _raw_stream(i):
+    """The current stream's handle on device i (torch.cuda.current_stream builds an object)."""
+    return _torch()._C._cuda_getCurrentRawStream(i)
+
+
 def _stream(device):
-    return ctypes.c_void_p(_torch().cuda.current_stream(device).cuda_stream)
+    return ctypes.c_void_p(_raw_stream(device.index))
 
 
 def verify_greedy(target, draft_tokens, gamma=None, *, ws=None, out=None):

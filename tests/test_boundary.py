@@ -140,12 +140,11 @@ def test_threads_take_turns_on_a_cached_workspace(monkeypatch):
         busy.discard(ws)
         return 0
 
-    cuda = types.SimpleNamespace(current_stream=lambda dev: types.SimpleNamespace(cuda_stream=stream.id))
-    fake = types.SimpleNamespace(cuda=cuda, **{k: getattr(torch, k) for k in (
-        "empty", "uint8", "int32", "float32", "bfloat16")})
+    fake = types.SimpleNamespace(**{k: getattr(torch, k) for k in ("empty", "uint8", "int32", "float32", "bfloat16")})
     calls = types.SimpleNamespace(**{f"spec_{k}": entry for k in (
         "verify_greedy", "verify_sample", "verify_onehot", "draft_signals")})
     monkeypatch.setattr(lib, "_torch", lambda: fake)
+    monkeypatch.setattr(lib, "_raw_stream", lambda i: stream.id)
     monkeypatch.setattr(lib, "lib", lambda: calls)
     monkeypatch.setattr(lib, "_check", lambda *a, **k: None)
     monkeypatch.setattr(lib, "_ws_cache", {})
