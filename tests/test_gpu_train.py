@@ -948,6 +948,31 @@ def test_waits_that_run_out(sv):
         assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("n,H,V", [(300, 2568, 3001), (40000, 64, 1500)])
+def test_waits_that_run_out_between_parts(sv, n, H, V):
+    """The same for sums joined from parts: of wide hidden states, and of many rows."""
+    big = cuda(*make_ce(n, H, V, 4))
+    f = sv.linear_ce_forward(*big)
+    b = sv.linear_ce_backward(*big, f["lse"])
+    torch.cuda.synchronize()
+    sv.set_wait_limit(1)
+    try:
+        f1 = sv.linear_ce_forward(*big)
+        b1 = sv.linear_ce_backward(*big, f["lse"])
+        torch.cuda.synchronize()
+    finally:
+        sv.set_wait_limit(0)
+    to = f1["status"] == sv._lib.ST_TIMEOUT
+    assert ((f1["status"] == 0) | to).all()
+    for k in ("loss", "lse"):
+        assert torch.equal(f1[k][~to], f[k][~to]) and f1[k][to].isnan().all()
+    for k in b:
+        assert torch.equal(b1[k], b[k]) or b1[k].isnan().all(), k
+    f2 = sv.linear_ce_forward(*big)
+    b2 = sv.linear_ce_backward(*big, f2["lse"])
+    assert all(torch.equal(f[k], f2[k]) for k in f) and all(torch.equal(b[k], b2[k]) for k in b)
+
+
 def test_repeated_captured_and_on_two_streams(sv):
     """The same bits from a second call, from a replayed graph on new inputs, and
     from two streams at once with a workspace each."""
