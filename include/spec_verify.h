@@ -95,7 +95,10 @@ enum {
                                     are valid                                */
     SPEC_ST_TIMEOUT = 32,        /* an internal wait hit its time limit     */
     SPEC_ST_BAD_TEMPERATURE = 64,/* temperature <= 0 or not finite          */
-    SPEC_ST_BAD_UNIFORM = 128    /* a uniform that was used is not in [0,1) */
+    SPEC_ST_BAD_UNIFORM = 128,   /* a uniform that was used is not in [0,1) */
+    SPEC_ST_BAD_PENALTY = 256,   /* a penalty or bias outside its range     */
+    SPEC_ST_BAD_LENGTH = 512     /* a history or prompt length outside its
+                                    range                                    */
 };
 
 /* Limits checked by the host: 1 <= B <= 65535, 0 <= G <= 31, 2 <= V < 2^28,
@@ -377,6 +380,97 @@ int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, i
                             const int32_t* label, const float* lse, const float* grad_loss,
                             void* grad_hidden, void* grad_weight,
                             void* workspace, size_t workspace_bytes, spec_stream_t stream);
+
+/* The calls below make and prepare the rows that a decode step verifies or
+ * draws from: products with 4-bit weights (a drafter's or a target's vocabulary
+ * projection, or any other linear layer), and penalties, biases and masks on
+ * logit rows.  Calls are enqueued on `stream`, allocate nothing, need no workspace
+ * and give the same bits for the same inputs. */
+
+/* Weights in 4 bits.  A row of H weights is cut into groups of 32, 64 or 128 (the
+ * last of a row may be shorter); a group has a scale s and a zero point z, and a
+ * weight is (q - z) s, 0 <= q <= 15.
+ *   packed [V, H / 2] bytes: 32-bit words of 8 weights of a row in ascending order,
+ *          weight i of a word in the bits 4 p .. 4 p + 3, p = 0, 4, 1, 5, 2, 6, 3, 7
+ *          for i = 0 .. 7;
+ *   scale  [V, ceil(H / group)] bf16;
+ *   zero   [V, ceil(H / group)] uint8, 0 to 15, or NULL: every z is 8.
+ * Sizes: 1 <= V < 2^28, 32 <= H <= 65536, H a multiple of 32; weight and packed
+ * 16-byte aligned.
+ * spec_w4_quantize: for each group of weight [V, H] (SPEC_F32 or SPEC_BF16), with
+ * the quotients' halves rounded to even,
+ *   without zero points  s = max |w| / 7, z = 8;
+ *   with them            lo = min(0, min w), hi = max(0, max w),
+ *                        s = (hi - lo) / 15, z = min(round(-lo / s), 15);
+ *   q = min(max(round(w / s) + z, 0), 15), with s rounded to fp32 and then to bf16.
+ * A scale of 0 gives q = z = 8.  A group with NaN or infinities has the scale NaN
+ * and q = z = 8.  status [V] or NULL: 0, or SPEC_ST_NONFINITE for a row with such a
+ * group.  No output may overlap another or the weights.
+ * spec_w4_dequantize: weight [V, H] = (q - z) s, rounded once to its dtype.
+ * Host errors: SPEC_ERR_INVALID_ARG (sizes, group, dtype, NULL required pointers,
+ * misalignment, overlap), SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
+int spec_w4_quantize(const void* weight, int dtype, int V, int H, int group, uint8_t* packed, void* scale,
+                     uint8_t* zero, int32_t* status, spec_stream_t stream);
+int spec_w4_dequantize(const uint8_t* packed, const void* scale, const uint8_t* zero, int V, int H, int group,
+                       void* weight, int dtype, spec_stream_t stream);
+
+/* logits [n, V] = hidden [n, H] weight^T with 4-bit weights (above): for each group
+ * the products of bf16 hidden states and the whole numbers q - z are summed in fp32,
+ * and the groups' sums, times their scales, in fp32; no weight is rounded.
+ *   hidden [n, H] SPEC_BF16, 16-byte aligned; logits SPEC_F32 or SPEC_BF16, rounded
+ *   once; it may overlap none of the operands.  NaN and infinities of a hidden state
+ *   reach the logits of its row, those of a scale the logits of its column.  If an
+ *   internal wait hits its time limit, the logits that it served are NaN.
+ * Host errors: SPEC_ERR_INVALID_ARG (n outside [1, 2^20], ceil(n / 16) ceil(V / 128)
+ * of 2^30 or more, sizes, group, dtype, NULL required pointers, misalignment,
+ * overlap), SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
+int spec_linear_w4(const void* hidden, int dtype, int n, const uint8_t* packed, const void* scale, const uint8_t* zero,
+                   int V, int H, int group, void* logits, int logits_dtype, spec_stream_t stream);
+
+/* Penalties for repeated tokens, biases and masks on logit rows [B, R, V], before
+ * they are filtered, verified or drawn from.  Row i of request b is the row after
+ * its history and its draft tokens y_0 .. y_{i-1} (each row has the history of its
+ * own candidate prefix: rows 0 .. G of a target, or 0 .. G - 1 of a drafter).  With
+ * c the occurrences of token v among the outputs of the row (the history behind the
+ * prompt, and those drafts):
+ *   x <- x / repetition if x > 0, else x repetition   (v in the history, prompt
+ *        included, or among those drafts)
+ *   x <- x - (c frequency + presence)                 (c > 0)
+ *   x <- x + the biases listed for v, added in their order
+ *   x <- -inf                                         (the mask's bit of v is 0)
+ * in fp32, rounded once.  Logits that nothing of this touches keep their bits, and
+ * a NaN or infinity is taken like any other value.
+ *   logits     [B, R, V], SPEC_F32 or SPEC_BF16; out: the same shape and dtype, or
+ *              `logits` itself (in place); any other overlap is refused;
+ *   history    [B, L] int32, or NULL with L = 0; history_len [B] or NULL (= L), what
+ *              lies behind it does not matter; prompt_len [B] or NULL (= 0): the
+ *              first entries of a history that are its prompt.  -1: no token;
+ *   draft_tokens [B, D] int32, D >= R - 1, or NULL with D = 0 (every row has the
+ *              history alone).  -1: no token;
+ *   gamma      [B] or NULL (= D, or R - 1 without draft tokens): draft tokens from
+ *              y_gamma on are not looked at, rows i > gamma neither read nor written;
+ *   repetition, frequency, presence [B] fp32 or NULL (1, 0, 0), finite, repetition
+ *              above 0;
+ *   bias_index, bias_value [B, biases], or NULL with biases = 0: an index of -1 is
+ *              left out; a value is finite or -inf;
+ *   mask       [B, R, ceil(V / 32)] 32-bit words or NULL: bit v mod 32 of word
+ *              v / 32 is 1 for a token that is allowed.  Rows may be left without one;
+ *   status     [B] or NULL: 0, or bits SPEC_ST_BAD_TOKEN (a token or index outside
+ *              [-1, V)), SPEC_ST_BAD_LENGTH (history_len outside [0, L] or prompt_len
+ *              outside [0, history_len]), SPEC_ST_BAD_GAMMA (gamma outside its range),
+ *              SPEC_ST_BAD_PENALTY (a penalty or a bias outside its range): the rows
+ *              of such a request are left (out of place: copied) unchanged.
+ * Host errors: SPEC_ERR_INVALID_ARG (B outside [1, SPEC_MAX_B], R outside
+ * [1, SPEC_MAX_G + 1], V outside [2, 2^28), L above SPEC_MAX_HISTORY, D or biases
+ * outside their limits, dtype, NULL required pointers, misalignment, out or status on
+ * another argument), SPEC_ERR_CUDA, SPEC_ERR_UNSUPPORTED. */
+#define SPEC_MAX_HISTORY (1 << 28)
+#define SPEC_MAX_BIASES 4096
+int spec_adjust_logits(const void* logits, void* out, int dtype, int B, int R, int V, const int32_t* history, int L,
+                       const int32_t* history_len, const int32_t* prompt_len, const int32_t* draft_tokens, int D,
+                       const int32_t* gamma, const float* repetition, const float* frequency, const float* presence,
+                       const int32_t* bias_index, const float* bias_value, int biases, const uint32_t* mask,
+                       int32_t* status, spec_stream_t stream);
 
 /* Size of the library-owned scratch used by spec_verify_sample_static: 8 MiB.
  * It holds the workspace of spec_workspace_bytes(B, G, V) <= this value, e.g.

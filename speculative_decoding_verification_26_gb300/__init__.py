@@ -17,3 +17,6 @@ from ._lib import (  # noqa: F401
     DISTILL_MAX_V, MAX_TOPK, distill_topk, linear_ce_backward, linear_ce_forward, linear_ce_workspace,
     linear_ce_workspace_bytes, topk_logits,
 )
+from ._lib import (  # noqa: F401
+    MAX_BIASES, MAX_HISTORY, W4_GROUPS, adjust_logits, dequantize_w4, linear_w4, quantize_w4,
+)

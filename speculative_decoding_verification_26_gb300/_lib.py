@@ -19,6 +19,7 @@ F32, BF16 = 0, 1
 OK, ERR_INVALID_ARG, ERR_WORKSPACE, ERR_CUDA, ERR_UNSUPPORTED = 0, 1, 2, 3, 4
 ST_NONFINITE, ST_BAD_TOKEN, ST_BAD_GAMMA, ST_ZERO_RESIDUAL = 1, 2, 4, 8
 ST_GUARDED, ST_TIMEOUT, ST_BAD_TEMPERATURE, ST_BAD_UNIFORM = 16, 32, 64, 128
+ST_BAD_PENALTY, ST_BAD_LENGTH = 256, 512
 
 _lock = threading.Lock()
 _lib = None
@@ -79,6 +80,14 @@ def lib(path: str | None = None) -> ctypes.CDLL:
         L.spec_linear_ce_forward.restype = I
         L.spec_linear_ce_backward.argtypes = [P, P, I, I, I, I, P, P, P, P, P, P, SZ, P]
         L.spec_linear_ce_backward.restype = I
+        L.spec_w4_quantize.argtypes = [P, I, I, I, I, P, P, P, P, P]
+        L.spec_w4_quantize.restype = I
+        L.spec_w4_dequantize.argtypes = [P, P, P, I, I, I, P, I, P]
+        L.spec_w4_dequantize.restype = I
+        L.spec_linear_w4.argtypes = [P, I, I, P, P, P, I, I, I, P, I, P]
+        L.spec_linear_w4.restype = I
+        L.spec_adjust_logits.argtypes = [P, P, I, I, I, I, P, I, P, P, P, I, P, P, P, P, P, P, I, P, P, P]
+        L.spec_adjust_logits.restype = I
         if path is None:
             _lib = L
         return L
@@ -419,6 +428,9 @@ class _Hot:
         self.device, self.stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         self.topk, self.distill = L.spec_topk_logits, L.spec_distill_topk
         self.ce_forward, self.ce_backward = L.spec_linear_ce_forward, L.spec_linear_ce_backward
+        self.quantize, self.dequantize = L.spec_w4_quantize, L.spec_w4_dequantize
+        self.linear_w4, self.adjust = L.spec_linear_w4, L.spec_adjust_logits
+        self.u8 = torch.uint8
 
 
 _hot_state = None
@@ -614,6 +626,153 @@ def linear_ce_backward(hidden, weight, label, lse, grad_loss=None, *, need_hidde
     if need_weight:
         r["grad_weight"] = gw
     return r
+
+
+W4_GROUPS = (32, 64, 128)
+MAX_HISTORY, MAX_BIASES = 1 << 28, 4096
+
+
+def _code(h, t):
+    code = h.code.get(t.dtype)
+    return _dtype_code(t) if code is None else code
+
+
+def _w4_weights(h, packed, scale, zero, group):
+    """(V, H) of 4-bit weights, checked."""
+    if packed.dim() != 2:
+        raise ValueError("packed is [V, H / 2]")
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
+    V, H = packed.shape
+    H *= 2
+    dev = packed.device
+    _check(packed, "packed", h.u8)
+    per = (V, -(-H // group))
+    _want(scale, "scale", h.bf16, per, dev)
+    _want(zero, "zero", h.u8, per, dev)
+    return V, H
+
+
+def quantize_w4(weight, group=128, *, zero=False, out=None):
+    """weight [V, H] (fp32 or bf16, H a multiple of 32) in 4 bits, with a bf16
+    scale and, with `zero`, a zero point for each `group` of 32, 64 or 128
+    weights of a row.  Returns {"packed": [V, H / 2] uint8, "scale": [V,
+    ceil(H / group)] bf16, "status": [V]} and "zero" ([V, ceil(H / group)]
+    uint8) (see spec_w4_quantize)."""
+    h = _hot()
+    if weight.dim() != 2:
+        raise ValueError("weight is [V, H]")
+    if group not in W4_GROUPS:
+        raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
+    V, H = weight.shape
+    dev = weight.device
+    _check(weight, "weight")
+    o = out or {}
+    per = (V, -(-H // group))
+    packed, scale = _result(o, "packed", (V, H // 2), h.u8, dev), _result(o, "scale", per, h.bf16, dev)
+    z = _result(o, "zero", per, h.u8, dev) if zero else None
+    st = _result(o, "status", (V,), h.i32, dev)
+    _call(h, dev, h.quantize, weight.data_ptr(), _code(h, weight), V, H, group, packed.data_ptr(), scale.data_ptr(),
+          _addr(z), st.data_ptr())
+    r = {"packed": packed, "scale": scale, "status": st}
+    if zero:
+        r["zero"] = z
+    return r
+
+
+def dequantize_w4(packed, scale, zero=None, *, group=128, dtype=None, out=None):
+    """The weights [V, H] that quantize_w4's results stand for, in `dtype` (bf16
+    by default, or fp32).  Returns {"weight": [V, H]} (see spec_w4_dequantize)."""
+    h = _hot()
+    V, H = _w4_weights(h, packed, scale, zero, group)
+    dev = packed.device
+    w = _result(out or {}, "weight", (V, H), dtype or h.bf16, dev)
+    _call(h, dev, h.dequantize, packed.data_ptr(), scale.data_ptr(), _addr(zero), V, H, group, w.data_ptr(), _code(h, w))
+    return {"weight": w}
+
+
+def linear_w4(hidden, packed, scale, zero=None, *, group=128, dtype=None, out=None):
+    """hidden [..., H] (bf16) times 4-bit weights (quantize_w4), transposed:
+    {"logits": [..., V]} in `dtype` (bf16 by default, or fp32) (see spec_linear_w4)."""
+    h = _hot()
+    V, H = _w4_weights(h, packed, scale, zero, group)
+    dev = packed.device
+    shape = hidden.shape
+    if len(shape) < 1 or shape[-1] != H:
+        raise ValueError(f"hidden must have shape [..., {H}], got {tuple(shape)}")
+    _check(hidden, "hidden", h.bf16, device=dev)
+    dtype = dtype or h.bf16
+    if out is None:
+        y = h.empty((*shape[:-1], V), dtype=dtype, device=dev)
+    else:
+        y = _result(out, "logits", (*shape[:-1], V), dtype, dev)
+    _call(h, dev, h.linear_w4, hidden.data_ptr(), BF16, hidden.numel() // H, packed.data_ptr(), scale.data_ptr(),
+          _addr(zero), V, H, group, y.data_ptr(), _code(h, y))
+    return {"logits": y}
+
+
+def adjust_logits(logits, history=None, history_len=None, *, prompt_len=None, draft_tokens=None, gamma=None,
+                  repetition=None, frequency=None, presence=None, bias_index=None, bias_value=None, mask=None, out=None):
+    """Penalties for repeated tokens, biases and masks on the rows of logits
+    [B, R, V] (fp32 or bf16), in place unless out={"logits": other} is given: row
+    i has the history of request b (history [B, L] int32, history_len [B]; the
+    first prompt_len [B] entries are its prompt) and its draft tokens y_0 ..
+    y_{i-1} (draft_tokens [B, D], D >= R - 1, gamma [B] of them).  repetition,
+    frequency, presence [B] fp32; bias_index [B, N] int32 with bias_value [B, N]
+    fp32; mask [B, R, ceil(V / 32)] int32, bit v % 32 of word v // 32 for token v,
+    1 where it is allowed; each optional.  Returns {"logits", "status": [B]} (see
+    spec_adjust_logits)."""
+    h = _hot()
+    f32, i32 = h.f32, h.i32
+    if logits.dim() != 3:
+        raise ValueError("logits is [B, R, V]")
+    B, R, V = logits.shape
+    dev = logits.device
+    _check(logits, "logits")
+    L = D = N = 0
+    per = (B,)
+    if history is not None:
+        if history.dim() != 2:
+            raise ValueError("history is [B, L]")
+        L = history.shape[1]
+        _want(history, "history", i32, (B, L), dev)
+    elif history_len is not None or prompt_len is not None:
+        raise ValueError("history_len and prompt_len are those of a history")
+    if draft_tokens is not None:
+        if draft_tokens.dim() != 2:
+            raise ValueError("draft_tokens is [B, D]")
+        D = draft_tokens.shape[1]
+        _want(draft_tokens, "draft_tokens", i32, (B, D), dev)
+        if 0 < D < R - 1 or D == 0 and R > 1:
+            raise ValueError(f"draft_tokens has {D} tokens for {R} rows")
+    if (bias_index is None) != (bias_value is None):
+        raise ValueError("bias_index and bias_value go together")
+    if bias_index is not None:
+        if bias_index.dim() != 2:
+            raise ValueError("bias_index is [B, N]")
+        N = bias_index.shape[1]
+        _want(bias_index, "bias_index", i32, (B, N), dev)
+        _want(bias_value, "bias_value", f32, (B, N), dev)
+    _want(history_len, "history_len", i32, per, dev)
+    _want(prompt_len, "prompt_len", i32, per, dev)
+    _want(gamma, "gamma", i32, per, dev)
+    _want(repetition, "repetition", f32, per, dev)
+    _want(frequency, "frequency", f32, per, dev)
+    _want(presence, "presence", f32, per, dev)
+    _want(mask, "mask", i32, (B, R, (V + 31) // 32), dev)
+    if out is None:
+        y, st = logits, h.empty(per, dtype=i32, device=dev)
+    else:
+        y = out.get("logits")
+        if y is None:
+            y = logits
+        elif y is not logits:
+            _want(y, "out['logits']", logits.dtype, logits.shape, dev)
+        st = _result(out, "status", per, i32, dev)
+    _call(h, dev, h.adjust, logits.data_ptr(), y.data_ptr(), _code(h, logits), B, R, V, _addr(history), L,
+          _addr(history_len), _addr(prompt_len), _addr(draft_tokens), D, _addr(gamma), _addr(repetition),
+          _addr(frequency), _addr(presence), _addr(bias_index), _addr(bias_value), N, _addr(mask), st.data_ptr())
+    return {"logits": y, "status": st}
 
 
 STATIC_WORKSPACE_BYTES = 8 << 20

@@ -18,7 +18,7 @@
 #include <cstdint>
 #include <mutex>
 
-#include "common.cuh"
+#include "serve.cuh"
 
 using namespace sv;
 
@@ -52,12 +52,11 @@ cudaError_t configure(Family f, int dev) {
   }
 }
 
-// The current device, with the kernels of `f` configured.
-int device_for(Family f, int* device, DevState** state) {
+// The state of the current device, known to run the library's code or not; under g_mu.
+int known_device(int* device, DevState** state) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SPEC_ERR_CUDA;
   if (dev < 0 || dev >= kMaxDevices) return SPEC_ERR_UNSUPPORTED;
-  std::lock_guard<std::mutex> lk(g_mu);
   DevState& d = g_dev[dev];
   *device = dev;
   *state = &d;
@@ -70,9 +69,17 @@ int device_for(Family f, int* device, DevState** state) {
     if (major != 10 || minor != 3) d.status = SPEC_ERR_UNSUPPORTED;   // the library carries sm_103a code only
     d.known = true;
   }
-  if (d.status != SPEC_OK) return d.status;
+  return d.status;
+}
+
+// The current device, with the kernels of `f` configured.
+int device_for(Family f, int* device, DevState** state) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  const int rc = known_device(device, state);
+  if (rc != SPEC_OK) return rc;
+  DevState& d = **state;
   if (!d.ready[f]) {
-    if (configure(f, dev) != cudaSuccess) return SPEC_ERR_CUDA;
+    if (configure(f, *device) != cudaSuccess) return SPEC_ERR_CUDA;
     if (f == kVerification) {
       int per_sm = 0;
       if (verify_blocks_per_sm(&per_sm) != cudaSuccess) return SPEC_ERR_CUDA;
@@ -257,6 +264,20 @@ int static_workspace(void** out) {
 
 }  // namespace
 
+namespace sv {
+
+int current_device(int* dev, int* sms) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  DevState* d = nullptr;
+  const int rc = known_device(dev, &d);
+  if (rc == SPEC_OK) *sms = d->sms;
+  return rc;
+}
+void count_launches(int n) { g_launches += n; }
+long long current_wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
+}  // namespace sv
+
 extern "C" {
 
 size_t spec_workspace_bytes(int B, int G, int V) {
@@ -288,6 +309,8 @@ const char* spec_request_status_string(int bit) {
     case SPEC_ST_TIMEOUT: return "internal wait timed out";
     case SPEC_ST_BAD_TEMPERATURE: return "temperature not positive and finite";
     case SPEC_ST_BAD_UNIFORM: return "uniform outside [0, 1)";
+    case SPEC_ST_BAD_PENALTY: return "penalty or bias outside its range";
+    case SPEC_ST_BAD_LENGTH: return "history or prompt length outside its range";
     default: break;
   }
   return "unknown status bit";
