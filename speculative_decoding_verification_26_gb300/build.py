@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspec_verify.so")
 SOURCES = ["api.cu", "verify.cu", "divergence.cu", "gamma.cu", "filter.cu", "record.cu",
-           "distill.cu", "linear_ce.cu", "api_serve.cu", "w4.cu", "adjust.cu"]
+           "distill.cu", "linear_ce.cu", "api_serve.cu", "w4.cu", "w4_linear.cu", "adjust.cu"]
 HEADERS = ["common.cuh", "rows.cuh", "tc_gemm.cuh", "serve.cuh", "exp2_table.cuh", os.path.join("..", "..", "include", "spec_verify.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

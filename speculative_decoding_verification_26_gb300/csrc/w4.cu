@@ -1,5 +1,4 @@
-// w4.cu -- weights in 4 bits with a scale for each group, read back, and products
-// with them.
+// w4.cu -- weights in 4 bits with a scale for each group, and read back.
 //
 // A row of H weights is cut into groups of 32, 64 or 128 (the last may be shorter).
 // A group has a scale s (bf16) and a zero point z (0 to 15; 8 without zero points),
@@ -136,44 +135,6 @@ __global__ void __launch_bounds__(kW4Threads) dequantize_kernel(const W4Params P
   }
 }
 
-// A warp takes a row of weights and 8 rows of hidden states at a time.
-constexpr int kRowsAtOnce = 8;
-template <int DT>
-__global__ void __launch_bounds__(kW4Threads) linear_kernel(const W4Params P) {
-  const int lane = threadIdx.x & 31, words = P.H / 8, per = P.group / 8;
-  for (long long v = (blockIdx.x * (long long)kW4Threads + threadIdx.x) / 32; v < P.V; v += gridDim.x * (kW4Threads / 32ll)) {
-    for (int r0 = 0; r0 < P.n; r0 += kRowsAtOnce) {
-      float sum[kRowsAtOnce] = {};
-      for (int k = lane; k < words; k += 32) {
-        const int g = k / per;
-        const uint32_t word = P.packed[v * words + k];
-        const float s = __bfloat162float(P.scale[v * P.groups + g]), z = P.zero ? (float)P.zero[v * P.groups + g] : 8.f;
-        float w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = weight_of(word, j, z) * s;
-#pragma unroll
-        for (int r = 0; r < kRowsAtOnce; ++r) {
-          if (r0 + r < P.n) {
-            float x[8];
-            load8<SPEC_BF16>(x, reinterpret_cast<const unsigned char*>(P.hidden + (size_t)(r0 + r) * P.H + 8 * k));
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum[r] = __fmaf_rn(w[j], x[j], sum[r]);
-          }
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < kRowsAtOnce; ++r) {
-        const float y = warp_sum(sum[r]);
-        if (lane == 0 && r0 + r < P.n) {
-          const size_t o = (size_t)(r0 + r) * P.V + v;
-          if constexpr (DT == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(y);
-          else reinterpret_cast<float*>(P.out)[o] = y;
-        }
-      }
-    }
-  }
-}
-
 int row_grid(int V, int nsm) {
   const long long most = 8ll * nsm, need = (V + kW4Threads / 32 - 1) / (kW4Threads / 32);
   return (int)(need < most ? need : most);
@@ -199,15 +160,6 @@ cudaError_t launch_w4_dequantize(const W4Params& P, int nsm, cudaStream_t s) {
   const int grid = row_grid(P.V, nsm);
   if (P.dtype == SPEC_BF16) dequantize_kernel<SPEC_BF16><<<grid, kW4Threads, 0, s>>>(P);
   else dequantize_kernel<SPEC_F32><<<grid, kW4Threads, 0, s>>>(P);
-  return cudaGetLastError();
-}
-
-cudaError_t configure_w4() { return cudaSuccess; }
-
-cudaError_t launch_w4_linear(const W4Params& P, int nsm, cudaStream_t s) {
-  const int grid = row_grid(P.V, nsm);
-  if (P.dtype == SPEC_BF16) linear_kernel<SPEC_BF16><<<grid, kW4Threads, 0, s>>>(P);
-  else linear_kernel<SPEC_F32><<<grid, kW4Threads, 0, s>>>(P);
   return cudaGetLastError();
 }
 

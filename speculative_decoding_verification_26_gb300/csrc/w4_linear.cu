@@ -1,0 +1,420 @@
+// w4_linear.cu -- products with 4-bit weights on the tensor cores of sm_103a.
+//
+// logits[r, v] = sum over groups g of s[v, g] sum_{k in g} (q[v, k] - z[v, g]) h[r, k].
+//
+// The inner sums are products of bf16 with small whole numbers, which bf16 holds exactly:
+// tcgen05.mma takes them, the weights as the operand A of 128 vocabulary rows in tensor
+// memory and the hidden states as the operand B in shared memory, and starts a sum for each
+// group.  Its fp32 sum is read back and added, times the group's scale, to registers.  No
+// weight is rounded, and a sum of the tensor cores, which cut off at every addition, is at
+// most 128 long.
+//
+// A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states.  Roles:
+//   warps 0-7    weights from shared memory to bf16 in tensor memory: thread = vocabulary row
+//                (32 (w % 4) on), half of each 128 k (w / 4);
+//   warps 8-11   groups' sums to registers and out (8-15, each half of the columns, for NT = 128);
+//   then one warp each: copies of weights (256 k a stage), copies of hidden states (128 k a
+//   slot), products.
+// Where there are fewer tiles than SMs, a cluster of CTAs splits the k of a tile, and the
+// parts are joined through distributed shared memory in the order of their ranks.
+#include "serve.cuh"
+#include "tc_gemm.cuh"
+
+namespace sv {
+namespace {
+
+constexpr int kRows = 128;                   // vocabulary rows of a tile
+constexpr int kStageK = 256, kSlotK = 128;   // k of a stage of weights, of a slot
+constexpr int kWeightStage = kRows * kStageK / 2;        // 16 KB
+constexpr int kUnpackWarps = 8;
+constexpr int kASlots = 4, kAColumns = kSlotK / 2;       // tensor-memory columns of a slot of A
+constexpr int kDColumn = kASlots * kAColumns;            // where the sums begin
+constexpr int kMaxSplit = 8;
+
+template <int NT>
+struct Shape {
+  static constexpr int WS = NT <= 32 ? 8 : NT == 64 ? 6 : 5;     // stages of weights
+  static constexpr int XS = NT <= 32 ? 8 : NT == 64 ? 6 : 4;     // slots of hidden states
+  static constexpr int DS = NT == 128 ? 2 : NT == 64 ? 4 : 8;    // sums
+  static constexpr int XSlot = NT * kSlotK * 2, XBox = NT * 128; // bytes
+  static constexpr int SumWarps = NT == 128 ? 8 : 4, Columns = NT / (SumWarps / 4);   // of a thread
+  static constexpr int Threads = (kUnpackWarps + SumWarps + 3) * 32;
+  static constexpr int Ring = WS * kWeightStage + XS * XSlot;
+};
+template <int NT>
+struct W4Shared {
+  using Z = Shape<NT>;
+  uint64_t w_full[Z::WS], w_empty[Z::WS], x_full[Z::XS], x_empty[Z::XS], a_full[kASlots], a_empty[kASlots], d_full[Z::DS],
+      d_empty[Z::DS];
+  uint32_t tmem;
+  int failed;
+};
+template <int NT>
+constexpr size_t linear_smem() { return Shape<NT>::Ring + 1024 + sizeof(W4Shared<NT>); }
+
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
+                   "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+               : "memory");
+}
+// A in tensor memory, B in shared memory
+__device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+               "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+               : "memory");
+}
+__device__ __forceinline__ void commit_to(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void store32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+      "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]),
+      "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void load16(float (&v)[16], uint32_t addr) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+#pragma unroll
+  for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(r[c]);
+}
+__device__ __forceinline__ uint4 shared16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+// a word of 8 weights as bf16 pairs of q - z; less = 128 + z in both halves.  128 + q is q in the
+// last bits of the mantissa; the difference is exact.
+__device__ __forceinline__ void unpack8(uint32_t* out, uint32_t word, __nv_bfloat162 less) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const uint32_t u = (word >> 4 * p & 0x000F000Fu) | 0x43004300u;
+    __nv_bfloat162 x;
+    memcpy(&x, &u, 4);
+    x = __hsub2(x, less);
+    memcpy(out + p, &x, 4);
+  }
+}
+
+struct W4Maps {
+  CUtensorMap weight, hidden;
+};
+
+// What a CTA does: its tiles, and of each the slots [first, first + slots) of 128 k.
+struct Plan {
+  int items, step, row_tiles, first, slots;
+  __device__ __forceinline__ int row0(int item, int nt) const { return item % row_tiles * nt; }
+  __device__ __forceinline__ int col0(int item) const { return item / row_tiles * kRows; }
+};
+
+template <int NT, int DT>
+__global__ void __launch_bounds__(Shape<NT>::Threads, 1)
+linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps M, int split) {
+  using Z = Shape<NT>;
+  extern __shared__ unsigned char w4_smem[];
+  const uint32_t base = (smem_u32(w4_smem) + 1023) & ~1023u;
+  unsigned char* const ring = w4_smem + (base - smem_u32(w4_smem));
+  W4Shared<NT>& S = *reinterpret_cast<W4Shared<NT>*>(ring + Z::Ring);
+  const uint32_t w_ring = base, x_ring = base + Z::WS * kWeightStage;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kWeightCopies = kUnpackWarps + Z::SumWarps, kHiddenCopies = kWeightCopies + 1, kProducts = kWeightCopies + 2;
+  const Waits waits{&S.failed, P.wait_limit};
+
+  Plan plan;
+  plan.row_tiles = (P.n + NT - 1) / NT;
+  plan.items = plan.row_tiles * ((P.V + kRows - 1) / kRows);
+  const int rank = blockIdx.x % split, item0 = blockIdx.x / split;
+  plan.step = gridDim.x / split;
+  {
+    const int stages = (P.H + kStageK - 1) / kStageK, lo = rank * stages / split, hi = (rank + 1) * stages / split;
+    const int end = min(hi * (kStageK / kSlotK), (P.H + kSlotK - 1) / kSlotK);
+    plan.first = lo * (kStageK / kSlotK);
+    plan.slots = end - plan.first;
+  }
+  const int per_slot = kSlotK / P.group;     // groups
+
+  if (threadIdx.x == 0) {
+    S.failed = 0;
+    for (int i = 0; i < Z::WS; ++i) { mbar_init(&S.w_full[i], 1); mbar_init(&S.w_empty[i], kUnpackWarps); }
+    for (int i = 0; i < Z::XS; ++i) { mbar_init(&S.x_full[i], 1); mbar_init(&S.x_empty[i], 1); }
+    for (int i = 0; i < kASlots; ++i) { mbar_init(&S.a_full[i], kUnpackWarps); mbar_init(&S.a_empty[i], 1); }
+    for (int i = 0; i < Z::DS; ++i) { mbar_init(&S.d_full[i], 1); mbar_init(&S.d_empty[i], Z::SumWarps); }
+    fence_mbar_init();
+  }
+  if (warp == kProducts) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(kTcColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = S.tmem;
+
+  float acc[Z::Columns];
+  bool ok = true;
+  if (warp < kUnpackWarps) {
+    const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kAColumns / 2);
+    RingAt w, a;
+    for (int item = item0; ok && item < plan.items; item += plan.step) {
+      const size_t per = (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
+      for (int j = 0; ok && j < plan.slots; ++j) {
+        const int k0 = (plan.first + j) * kSlotK + half * (kSlotK / 2);
+        uint32_t z[2] = {8, 8};
+        if (P.zero) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c) z[c] = P.zero[per + min((k0 + 32 * c) / P.group, P.groups - 1)];
+        }
+        if (!(ok = __all_sync(0xffffffffu, bounded_wait(&S.w_full[w.stage], w.phase, waits)))) break;
+        const uint32_t at = w_ring + w.stage * kWeightStage + row * 128;
+        uint32_t r[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint4 v = shared16(at + (uint32_t)((((j & 1) * 4 + half * 2 + c) ^ (row & 7)) << 4));
+          const uint32_t less = (0x4300u | z[c]) * 0x10001u;
+          __nv_bfloat162 l;
+          memcpy(&l, &less, 4);
+          unpack8(r + 16 * c, v.x, l);
+          unpack8(r + 16 * c + 4, v.y, l);
+          unpack8(r + 16 * c + 8, v.z, l);
+          unpack8(r + 16 * c + 12, v.w, l);
+        }
+        if ((j & 1) || j + 1 == plan.slots) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&S.w_empty[w.stage]);
+          w.next(Z::WS);
+        }
+        if (!(ok = __all_sync(0xffffffffu, bounded_wait(&S.a_empty[a.stage], a.phase ^ 1, waits)))) break;
+        tc_fence_after();
+        store32(lanes + a.stage * kAColumns, r);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.a_full[a.stage]);
+        a.next(kASlots);
+      }
+    }
+  } else if (warp < kWeightCopies) {
+    const int quarter = warp & 3, part = (warp - kUnpackWarps) >> 2, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + kDColumn + part * Z::Columns;
+    RingAt d;
+    for (int item = item0; item < plan.items; item += plan.step) {
+      const int v = plan.col0(item) + row;
+      const __nv_bfloat16* scale = P.scale + (size_t)min(v, P.V - 1) * P.groups;
+#pragma unroll
+      for (int c = 0; c < Z::Columns; ++c) acc[c] = 0.f;
+      const int g0 = plan.first * per_slot, g1 = min((plan.first + plan.slots) * per_slot, P.groups);
+      for (int g = g0; ok && g < g1; ++g) {
+        const float s = __bfloat162float(scale[g]);
+        if (!(ok = __all_sync(0xffffffffu, bounded_wait(&S.d_full[d.stage], d.phase, waits)))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int c = 0; c < Z::Columns; c += 16) {
+          float x[16];
+          load16(x, lanes + d.stage * NT + c);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) acc[c + i] = __fmaf_rn(s, x[i], acc[c + i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&S.d_empty[d.stage]);
+        d.next(Z::DS);
+      }
+      if (!ok) {
+#pragma unroll
+        for (int c = 0; c < Z::Columns; ++c) acc[c] = NAN;
+      }
+      if (split == 1 && v < P.V) {
+        const int r0 = plan.row0(item, NT) + part * Z::Columns;
+#pragma unroll
+        for (int c = 0; c < Z::Columns; ++c) {
+          if (r0 + c < P.n) {
+            const size_t o = (size_t)(r0 + c) * P.V + v;
+            if constexpr (DT == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(acc[c]);
+            else reinterpret_cast<float*>(P.out)[o] = acc[c];
+          }
+        }
+      }
+    }
+  } else if (warp == kWeightCopies) {
+    if (lane == 0) {
+      RingAt w;
+      for (int item = item0; ok && item < plan.items; item += plan.step) {
+        for (int j = 0; j < plan.slots; j += kStageK / kSlotK) {
+          if (!(ok = bounded_wait(&S.w_empty[w.stage], w.phase ^ 1, waits))) break;
+          mbar_arrive_expect_tx(&S.w_full[w.stage], kWeightStage);
+          copy_box(w_ring + w.stage * kWeightStage, &M.weight, (plan.first + j) * (kSlotK / 2), plan.col0(item), &S.w_full[w.stage]);
+          w.next(Z::WS);
+        }
+      }
+    }
+  } else if (warp == kHiddenCopies) {
+    if (lane == 0) {
+      RingAt x;
+      for (int item = item0; ok && item < plan.items; item += plan.step) {
+        for (int j = 0; j < plan.slots; ++j) {
+          if (!(ok = bounded_wait(&S.x_empty[x.stage], x.phase ^ 1, waits))) break;
+          mbar_arrive_expect_tx(&S.x_full[x.stage], Z::XSlot);
+          const int k = (plan.first + j) * kSlotK;
+          copy_box(x_ring + x.stage * Z::XSlot, &M.hidden, k, plan.row0(item, NT), &S.x_full[x.stage]);
+          copy_box(x_ring + x.stage * Z::XSlot + Z::XBox, &M.hidden, k + 64, plan.row0(item, NT), &S.x_full[x.stage]);
+          x.next(Z::XS);
+        }
+      }
+    }
+  } else if (lane == 0) {
+    constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(NT >> 3) << 17 | (uint32_t)(kRows >> 4) << 24;
+    RingAt x, a, d;
+    const int steps = P.group / 16;
+    for (int item = item0; ok && item < plan.items; item += plan.step) {
+      for (int j = 0; ok && j < plan.slots; ++j) {
+        if (!(ok = bounded_wait(&S.x_full[x.stage], x.phase, waits) && bounded_wait(&S.a_full[a.stage], a.phase, waits))) break;
+        tc_fence_after();
+        const uint32_t at = tmem + a.stage * kAColumns, xs = x_ring + x.stage * Z::XSlot;
+        const int left = P.groups - (plan.first + j) * per_slot, groups = left < per_slot ? left : per_slot;
+        for (int g = 0; g < groups; ++g) {
+          if (!(ok = bounded_wait(&S.d_empty[d.stage], d.phase ^ 1, waits))) break;
+          tc_fence_after();
+          for (int q = 0; q < steps; ++q) {
+            const int k = g * steps + q;     // 16 k each, 4 to a box
+            product(tmem + kDColumn + d.stage * NT, at + k * 8, tc_desc(xs + (k >> 2) * Z::XBox + (k & 3) * 32, true), idesc, q > 0);
+          }
+          commit_to(&S.d_full[d.stage]);
+          d.next(Z::DS);
+        }
+        commit_to(&S.a_empty[a.stage]);
+        commit_to(&S.x_empty[x.stage]);
+        a.next(kASlots);
+        x.next(Z::XS);
+      }
+    }
+  }
+  __syncwarp();
+  const bool failed = any_failed(waits);
+  if (failed) drain_after_failure();         // copies or products may still be in flight
+  __syncwarp();
+
+  if (split > 1) {
+    // every copy has landed and every product is done (or NaN stands for them): the ring is free
+    float* const parts = reinterpret_cast<float*>(ring);           // [NT][128]
+    const bool sums = warp >= kUnpackWarps && warp < kWeightCopies;
+    const int row = (warp & 3) * 32 + lane, part = (warp - kUnpackWarps) >> 2;
+    __syncthreads();
+    if (sums) {
+#pragma unroll
+      for (int c = 0; c < Z::Columns; ++c) parts[(part * Z::Columns + c) * kRows + row] = acc[c];
+    }
+    cluster_sync();
+    if (sums) {
+      const int v = plan.col0(item0) + row, r0 = plan.row0(item0, NT);
+      for (int c = rank + part * split; c < NT && r0 + c < P.n; c += split * (Z::SumWarps / 4)) {
+        float sum = 0.f;
+        for (int k = 0; k < split; ++k) {
+          float x;
+          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(map_rank(base + (uint32_t)(c * kRows + row) * 4, k)) : "memory");
+          sum += x;
+        }
+        if (v < P.V) {
+          const size_t o = (size_t)(r0 + c) * P.V + v;
+          if constexpr (DT == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(sum);
+          else reinterpret_cast<float*>(P.out)[o] = sum;
+        }
+      }
+    }
+    cluster_sync();                          // a part is read until here
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kProducts)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcColumns) : "memory");
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled g_encode_w4 = nullptr;           // set once by configure_w4
+
+// rows of `width` elements of `size` bytes, boxes of 128 bytes x `box` rows
+bool encode(CUtensorMap* map, CUtensorMapDataType type, int size, const void* p, uint64_t width, uint64_t height, uint32_t box) {
+  const cuuint64_t dims[2] = {width, height}, strides[1] = {width * size};
+  const cuuint32_t boxes[2] = {(cuuint32_t)(128 / size), box}, ones[2] = {1, 1};
+  return g_encode_w4(map, type, 2, const_cast<void*>(p), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+template <int NT, int DT>
+cudaError_t run(const W4Params& P, int nsm, cudaStream_t s) {
+  W4Maps M;
+  if (!encode(&M.weight, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, P.packed, P.H / 2, P.V, kRows) ||
+      !encode(&M.hidden, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, P.hidden, P.H, P.n, NT))
+    return cudaErrorInvalidValue;
+  const long long items = ((P.n + NT - 1ll) / NT) * ((P.V + kRows - 1ll) / kRows);
+  const int stages = (P.H + kStageK - 1) / kStageK;
+  int split = 1;
+  while (split < kMaxSplit && 2 * split <= stages && 2 * split * items <= nsm) split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(split > 1 ? items * split : items < nsm ? items : nsm));
+  cfg.blockDim = dim3(Shape<NT>::Threads);
+  cfg.dynamicSmemBytes = linear_smem<NT>();
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {(unsigned)split, 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_kernel<NT, DT>, P, M, split);
+}
+template <int NT>
+cudaError_t of_type(const W4Params& P, int nsm, cudaStream_t s) {
+  return P.dtype == SPEC_BF16 ? run<NT, SPEC_BF16>(P, nsm, s) : run<NT, SPEC_F32>(P, nsm, s);
+}
+template <int NT>
+cudaError_t allow() {
+  static_assert(linear_smem<NT>() <= 232448, "shared memory of a CTA");
+  static_assert(kDColumn + Shape<NT>::DS * NT <= (int)kTcColumns, "tensor memory");
+  static_assert(Shape<NT>::Ring >= NT * kRows * 4, "parts of a split tile");
+  const int smem = (int)linear_smem<NT>();
+  cudaError_t e = cudaFuncSetAttribute(linear_kernel<NT, SPEC_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_kernel<NT, SPEC_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t configure_w4() {
+  cudaDriverEntryPointQueryResult found;
+  void* f = nullptr;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return e;
+  if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+  g_encode_w4 = reinterpret_cast<EncodeTiled>(f);
+  e = allow<16>();
+  if (e == cudaSuccess) e = allow<32>();
+  if (e == cudaSuccess) e = allow<64>();
+  if (e == cudaSuccess) e = allow<128>();
+  return e;
+}
+
+cudaError_t launch_w4_linear(const W4Params& P, int nsm, cudaStream_t s) {
+  if (P.n <= 16) return of_type<16>(P, nsm, s);
+  if (P.n <= 32) return of_type<32>(P, nsm, s);
+  if (P.n <= 64) return of_type<64>(P, nsm, s);
+  return of_type<128>(P, nsm, s);
+}
+
+}  // namespace sv
