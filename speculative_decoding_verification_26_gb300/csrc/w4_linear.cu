@@ -57,6 +57,36 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
                    "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
                : "memory");
 }
+// bounded_wait of a barrier that only this CTA arrives on, all lanes of a warp alike; mostly
+// the phase is over already
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const Waits& waits) {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+               : "=r"(ok)
+               : "r"(smem_u32(bar)), "r"(parity)
+               : "memory");
+  if (__all_sync(0xffffffffu, ok)) return true;
+  long long t0 = 0;
+  for (;;) {
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(waits.limit < kSleepNs ? (uint32_t)waits.limit : kSleepNs)
+        : "memory");
+    if (__all_sync(0xffffffffu, ok)) return true;
+    const long long t = clock64();
+    if (t0 == 0) t0 = t;
+    if (__any_sync(0xffffffffu, *waits.failed || t - t0 > waits.limit)) {
+      *waits.failed = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
+  return one != 0;
+}
 // A in tensor memory, B in shared memory
 __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile("{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
@@ -119,7 +149,7 @@ struct Plan {
   __device__ __forceinline__ int col0(int item) const { return item / row_tiles * kRows; }
 };
 
-template <int NT, int DT>
+template <int NT, int GROUP>
 __global__ void __launch_bounds__(Shape<NT>::Threads, 1)
 linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps M, int split) {
   using Z = Shape<NT>;
@@ -128,7 +158,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   unsigned char* const ring = w4_smem + (base - smem_u32(w4_smem));
   W4Shared<NT>& S = *reinterpret_cast<W4Shared<NT>*>(ring + Z::Ring);
   const uint32_t w_ring = base, x_ring = base + Z::WS * kWeightStage;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   constexpr int kWeightCopies = kUnpackWarps + Z::SumWarps, kHiddenCopies = kWeightCopies + 1, kProducts = kWeightCopies + 2;
   const Waits waits{&S.failed, P.wait_limit};
 
@@ -143,7 +173,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     plan.first = lo * (kStageK / kSlotK);
     plan.slots = end - plan.first;
   }
-  const int per_slot = kSlotK / P.group;     // groups
+  constexpr int per_slot = kSlotK / GROUP;   // groups
 
   if (threadIdx.x == 0) {
     S.failed = 0;
@@ -176,9 +206,9 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         uint32_t z[2] = {8, 8};
         if (P.zero) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) z[c] = P.zero[per + min((k0 + 32 * c) / P.group, P.groups - 1)];
+          for (int c = 0; c < 2; ++c) z[c] = P.zero[per + min((k0 + 32 * c) / GROUP, P.groups - 1)];
         }
-        if (!(ok = __all_sync(0xffffffffu, bounded_wait(&S.w_full[w.stage], w.phase, waits)))) break;
+        if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits))) break;
         const uint32_t at = w_ring + w.stage * kWeightStage + row * 128;
         uint32_t r[32];
 #pragma unroll
@@ -197,7 +227,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
           if (lane == 0) mbar_arrive(&S.w_empty[w.stage]);
           w.next(Z::WS);
         }
-        if (!(ok = __all_sync(0xffffffffu, bounded_wait(&S.a_empty[a.stage], a.phase ^ 1, waits)))) break;
+        if (!(ok = wait_for(&S.a_empty[a.stage], a.phase ^ 1, waits))) break;
         tc_fence_after();
         store32(lanes + a.stage * kAColumns, r);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -217,9 +247,16 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
 #pragma unroll
       for (int c = 0; c < Z::Columns; ++c) acc[c] = 0.f;
       const int g0 = plan.first * per_slot, g1 = min((plan.first + plan.slots) * per_slot, P.groups);
+      constexpr int kAhead = 4;              // scales on their way
+      __nv_bfloat16 next[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) next[i] = scale[min(g0 + i, P.groups - 1)];
       for (int g = g0; ok && g < g1; ++g) {
-        const float s = __bfloat162float(scale[g]);
-        if (!(ok = __all_sync(0xffffffffu, bounded_wait(&S.d_full[d.stage], d.phase, waits)))) break;
+        const float s = __bfloat162float(next[0]);
+#pragma unroll
+        for (int i = 1; i < kAhead; ++i) next[i - 1] = next[i];
+        next[kAhead - 1] = scale[min(g + kAhead, P.groups - 1)];
+        if (!(ok = wait_for(&S.d_full[d.stage], d.phase, waits))) break;
         tc_fence_after();
 #pragma unroll
         for (int c = 0; c < Z::Columns; c += 16) {
@@ -243,60 +280,66 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         for (int c = 0; c < Z::Columns; ++c) {
           if (r0 + c < P.n) {
             const size_t o = (size_t)(r0 + c) * P.V + v;
-            if constexpr (DT == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(acc[c]);
+            if (P.dtype == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(acc[c]);
             else reinterpret_cast<float*>(P.out)[o] = acc[c];
           }
         }
       }
     }
   } else if (warp == kWeightCopies) {
-    if (lane == 0) {
-      RingAt w;
-      for (int item = item0; ok && item < plan.items; item += plan.step) {
-        for (int j = 0; j < plan.slots; j += kStageK / kSlotK) {
-          if (!(ok = bounded_wait(&S.w_empty[w.stage], w.phase ^ 1, waits))) break;
+    RingAt w;
+    for (int item = item0; ok && item < plan.items; item += plan.step) {
+      for (int j = 0; j < plan.slots; j += kStageK / kSlotK) {
+        if (!(ok = wait_for(&S.w_empty[w.stage], w.phase ^ 1, waits))) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&S.w_full[w.stage], kWeightStage);
           copy_box(w_ring + w.stage * kWeightStage, &M.weight, (plan.first + j) * (kSlotK / 2), plan.col0(item), &S.w_full[w.stage]);
-          w.next(Z::WS);
         }
+        w.next(Z::WS);
       }
     }
   } else if (warp == kHiddenCopies) {
-    if (lane == 0) {
-      RingAt x;
-      for (int item = item0; ok && item < plan.items; item += plan.step) {
-        for (int j = 0; j < plan.slots; ++j) {
-          if (!(ok = bounded_wait(&S.x_empty[x.stage], x.phase ^ 1, waits))) break;
+    RingAt x;
+    for (int item = item0; ok && item < plan.items; item += plan.step) {
+      for (int j = 0; j < plan.slots; ++j) {
+        if (!(ok = wait_for(&S.x_empty[x.stage], x.phase ^ 1, waits))) break;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&S.x_full[x.stage], Z::XSlot);
           const int k = (plan.first + j) * kSlotK;
           copy_box(x_ring + x.stage * Z::XSlot, &M.hidden, k, plan.row0(item, NT), &S.x_full[x.stage]);
           copy_box(x_ring + x.stage * Z::XSlot + Z::XBox, &M.hidden, k + 64, plan.row0(item, NT), &S.x_full[x.stage]);
-          x.next(Z::XS);
         }
+        x.next(Z::XS);
       }
     }
-  } else if (lane == 0) {
+  } else {
     constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(NT >> 3) << 17 | (uint32_t)(kRows >> 4) << 24;
     RingAt x, a, d;
-    const int steps = P.group / 16;
     for (int item = item0; ok && item < plan.items; item += plan.step) {
       for (int j = 0; ok && j < plan.slots; ++j) {
-        if (!(ok = bounded_wait(&S.x_full[x.stage], x.phase, waits) && bounded_wait(&S.a_full[a.stage], a.phase, waits))) break;
-        tc_fence_after();
-        const uint32_t at = tmem + a.stage * kAColumns, xs = x_ring + x.stage * Z::XSlot;
+        if (!(ok = wait_for(&S.x_full[x.stage], x.phase, waits) && wait_for(&S.a_full[a.stage], a.phase, waits))) break;
+        const uint32_t at = tmem + a.stage * kAColumns;
+        const uint64_t desc = tc_desc(x_ring + x.stage * Z::XSlot, true);
         const int left = P.groups - (plan.first + j) * per_slot, groups = left < per_slot ? left : per_slot;
         for (int g = 0; g < groups; ++g) {
-          if (!(ok = bounded_wait(&S.d_empty[d.stage], d.phase ^ 1, waits))) break;
+          if (!(ok = wait_for(&S.d_empty[d.stage], d.phase ^ 1, waits))) break;
           tc_fence_after();
-          for (int q = 0; q < steps; ++q) {
-            const int k = g * steps + q;     // 16 k each, 4 to a box
-            product(tmem + kDColumn + d.stage * NT, at + k * 8, tc_desc(xs + (k >> 2) * Z::XBox + (k & 3) * 32, true), idesc, q > 0);
+          if (elect_one()) {
+            const uint32_t to = tmem + kDColumn + d.stage * NT;
+#pragma unroll
+            for (int q = 0; q < GROUP / 16; ++q) {
+              const int k = g * (GROUP / 16) + q;      // 16 k each, 4 to a box
+              product(to, at + k * 8, desc + (uint64_t)((k >> 2) * (Z::XBox >> 4) + (k & 3) * 2), idesc, q > 0);
+            }
+            commit_to(&S.d_full[d.stage]);
+            if (g + 1 == groups) {
+              commit_to(&S.a_empty[a.stage]);
+              commit_to(&S.x_empty[x.stage]);
+            }
           }
-          commit_to(&S.d_full[d.stage]);
+          __syncwarp();
           d.next(Z::DS);
         }
-        commit_to(&S.a_empty[a.stage]);
-        commit_to(&S.x_empty[x.stage]);
         a.next(kASlots);
         x.next(Z::XS);
       }
@@ -329,7 +372,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         }
         if (v < P.V) {
           const size_t o = (size_t)(r0 + c) * P.V + v;
-          if constexpr (DT == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(sum);
+          if (P.dtype == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(sum);
           else reinterpret_cast<float*>(P.out)[o] = sum;
         }
       }
@@ -357,7 +400,7 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int size, const void* p,
          CUDA_SUCCESS;
 }
 
-template <int NT, int DT>
+template <int NT, int GROUP>
 cudaError_t run(const W4Params& P, int nsm, cudaStream_t s) {
   W4Maps M;
   if (!encode(&M.weight, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, P.packed, P.H / 2, P.V, kRows) ||
@@ -377,11 +420,11 @@ cudaError_t run(const W4Params& P, int nsm, cudaStream_t s) {
   attr[0].val.clusterDim = {(unsigned)split, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<NT, DT>, P, M, split);
+  return cudaLaunchKernelEx(&cfg, linear_kernel<NT, GROUP>, P, M, split);
 }
 template <int NT>
-cudaError_t of_type(const W4Params& P, int nsm, cudaStream_t s) {
-  return P.dtype == SPEC_BF16 ? run<NT, SPEC_BF16>(P, nsm, s) : run<NT, SPEC_F32>(P, nsm, s);
+cudaError_t of_group(const W4Params& P, int nsm, cudaStream_t s) {
+  return P.group == 128 ? run<NT, 128>(P, nsm, s) : P.group == 64 ? run<NT, 64>(P, nsm, s) : run<NT, 32>(P, nsm, s);
 }
 template <int NT>
 cudaError_t allow() {
@@ -389,8 +432,9 @@ cudaError_t allow() {
   static_assert(kDColumn + Shape<NT>::DS * NT <= (int)kTcColumns, "tensor memory");
   static_assert(Shape<NT>::Ring >= NT * kRows * 4, "parts of a split tile");
   const int smem = (int)linear_smem<NT>();
-  cudaError_t e = cudaFuncSetAttribute(linear_kernel<NT, SPEC_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_kernel<NT, SPEC_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = cudaFuncSetAttribute(linear_kernel<NT, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_kernel<NT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_kernel<NT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   return e;
 }
 
@@ -411,10 +455,10 @@ cudaError_t configure_w4() {
 }
 
 cudaError_t launch_w4_linear(const W4Params& P, int nsm, cudaStream_t s) {
-  if (P.n <= 16) return of_type<16>(P, nsm, s);
-  if (P.n <= 32) return of_type<32>(P, nsm, s);
-  if (P.n <= 64) return of_type<64>(P, nsm, s);
-  return of_type<128>(P, nsm, s);
+  if (P.n <= 16) return of_group<16>(P, nsm, s);
+  if (P.n <= 32) return of_group<32>(P, nsm, s);
+  if (P.n <= 64) return of_group<64>(P, nsm, s);
+  return of_group<128>(P, nsm, s);
 }
 
 }  // namespace sv
