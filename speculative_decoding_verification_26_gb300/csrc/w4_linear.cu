@@ -26,46 +26,53 @@ namespace {
 constexpr int kRows = 128;                   // vocabulary rows of a tile
 constexpr int kStageK = 256, kSlotK = 128;   // k of a stage of weights, of a slot
 constexpr int kWeightStage = kRows * kStageK / 2;        // 16 KB
-constexpr int kUnpackWarps = 8;
-constexpr int kASlots = 4, kAColumns = kSlotK / 2;       // tensor-memory columns of a slot of A
-constexpr int kDColumn = kASlots * kAColumns;            // where the sums begin
+constexpr int kAColumns = kSlotK / 2;        // tensor-memory columns of a slot of A
 constexpr int kMaxSplit = 8;
 
-template <int NT>
+// Tensor memory holds AS slots of A and DS units of sums; a unit is the sums of UG groups,
+// handed over together: at most 128 columns.
+template <int NT, int GROUP>
 struct Shape {
   static constexpr int WS = NT <= 32 ? 8 : NT == 64 ? 6 : 5;     // stages of weights
   static constexpr int XS = NT <= 32 ? 8 : NT == 64 ? 6 : 4;     // slots of hidden states
-  static constexpr int DS = NT == 128 ? 2 : NT == 64 ? 4 : 8;    // sums
+  static constexpr int PerSlot = kSlotK / GROUP;                 // groups
+  static constexpr int UG = PerSlot * NT <= 128 ? PerSlot : 128 / NT, Unit = UG * NT;
+  static constexpr int AS = Unit <= 64 ? 4 : 2, DColumn = AS * kAColumns;
+  static constexpr int DS = Unit <= 32 ? 8 : Unit == 64 ? 4 : 3;
   static constexpr int XSlot = NT * kSlotK * 2, XBox = NT * 128; // bytes
-  static constexpr int SumWarps = NT == 128 ? 8 : 4, Columns = NT / (SumWarps / 4);   // of a thread
-  static constexpr int Threads = (kUnpackWarps + SumWarps + 3) * 32;
+  static constexpr int UnpackWarps = 8, SumWarps = NT == 128 ? 8 : 4, Columns = NT / (SumWarps / 4);   // of a thread
+  static constexpr int Threads = (UnpackWarps + SumWarps + 3) * 32;
   static constexpr int Ring = WS * kWeightStage + XS * XSlot;
 };
-template <int NT>
+template <class Z>
 struct W4Shared {
-  using Z = Shape<NT>;
-  uint64_t w_full[Z::WS], w_empty[Z::WS], x_full[Z::XS], x_empty[Z::XS], a_full[kASlots], a_empty[kASlots], d_full[Z::DS],
+  uint64_t w_full[Z::WS], w_empty[Z::WS], x_full[Z::XS], x_empty[Z::XS], a_full[Z::AS], a_empty[Z::AS], d_full[Z::DS],
       d_empty[Z::DS];
   uint32_t tmem;
   int failed;
 };
-template <int NT>
-constexpr size_t linear_smem() { return Shape<NT>::Ring + 1024 + sizeof(W4Shared<NT>); }
+template <class Z>
+constexpr size_t linear_smem() { return Z::Ring + 1024 + sizeof(W4Shared<Z>); }
 
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::
                    "r"(dst), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
                : "memory");
 }
-// bounded_wait of a barrier that only this CTA arrives on, all lanes of a warp alike; mostly
-// the phase is over already
-__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const Waits& waits) {
+// Whether a phase of a barrier is over.
+__device__ __forceinline__ uint32_t over(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
                : "=r"(ok)
                : "r"(smem_u32(bar)), "r"(parity)
                : "memory");
-  if (__all_sync(0xffffffffu, ok)) return true;
+  return ok;
+}
+// bounded_wait of a barrier that only this CTA arrives on, all lanes of a warp alike; `seen` is
+// what over() said before (a test takes about 130 clocks from issue to use)
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const Waits& waits, uint32_t seen = 0) {
+  if (__all_sync(0xffffffffu, seen)) return true;
+  uint32_t ok;
   long long t0 = 0;
   for (;;) {
     asm volatile(
@@ -96,7 +103,7 @@ __device__ __forceinline__ void product(uint32_t d, uint32_t a, uint64_t b, uint
 __device__ __forceinline__ void commit_to(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void store32(uint32_t addr, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void store32(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
@@ -138,6 +145,31 @@ __device__ __forceinline__ void unpack8(uint32_t* out, uint32_t word, __nv_bfloa
   }
 }
 
+// acc[c] += s * column c of a group's sums
+template <int N>
+__device__ __forceinline__ void add_unit(float (&acc)[N], uint32_t from, float s) {
+#pragma unroll
+  for (int c = 0; c < N; c += (N < 32 ? 16 : 32)) {
+    if constexpr (N < 32) {
+      float x[16];
+      load16(x, from + c);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) acc[c + i] = __fmaf_rn(s, x[i], acc[c + i]);
+    } else {
+      float x[32];
+      tc_load32(x, from + c);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) acc[c + i] = __fmaf_rn(s, x[i], acc[c + i]);
+    }
+  }
+}
+// asks `count` elements from p + at on into L2
+template <class T>
+__device__ __forceinline__ void ahead(const T* p, size_t at, int count) {
+  for (int i = 0; i < count; i += 128 / (int)sizeof(T))
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at + i));
+}
+
 struct W4Maps {
   CUtensorMap weight, hidden;
 };
@@ -150,16 +182,16 @@ struct Plan {
 };
 
 template <int NT, int GROUP>
-__global__ void __launch_bounds__(Shape<NT>::Threads, 1)
+__global__ void __launch_bounds__(Shape<NT, GROUP>::Threads, 1)
 linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps M, int split) {
-  using Z = Shape<NT>;
+  using Z = Shape<NT, GROUP>;
   extern __shared__ unsigned char w4_smem[];
   const uint32_t base = (smem_u32(w4_smem) + 1023) & ~1023u;
   unsigned char* const ring = w4_smem + (base - smem_u32(w4_smem));
-  W4Shared<NT>& S = *reinterpret_cast<W4Shared<NT>*>(ring + Z::Ring);
+  W4Shared<Z>& S = *reinterpret_cast<W4Shared<Z>*>(ring + Z::Ring);
   const uint32_t w_ring = base, x_ring = base + Z::WS * kWeightStage;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  constexpr int kWeightCopies = kUnpackWarps + Z::SumWarps, kHiddenCopies = kWeightCopies + 1, kProducts = kWeightCopies + 2;
+  constexpr int kWeightCopies = Z::UnpackWarps + Z::SumWarps, kHiddenCopies = kWeightCopies + 1, kProducts = kWeightCopies + 2;
   const Waits waits{&S.failed, P.wait_limit};
 
   Plan plan;
@@ -173,13 +205,12 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     plan.first = lo * (kStageK / kSlotK);
     plan.slots = end - plan.first;
   }
-  constexpr int per_slot = kSlotK / GROUP;   // groups
 
   if (threadIdx.x == 0) {
     S.failed = 0;
-    for (int i = 0; i < Z::WS; ++i) { mbar_init(&S.w_full[i], 1); mbar_init(&S.w_empty[i], kUnpackWarps); }
+    for (int i = 0; i < Z::WS; ++i) { mbar_init(&S.w_full[i], 1); mbar_init(&S.w_empty[i], Z::UnpackWarps); }
     for (int i = 0; i < Z::XS; ++i) { mbar_init(&S.x_full[i], 1); mbar_init(&S.x_empty[i], 1); }
-    for (int i = 0; i < kASlots; ++i) { mbar_init(&S.a_full[i], kUnpackWarps); mbar_init(&S.a_empty[i], 1); }
+    for (int i = 0; i < Z::AS; ++i) { mbar_init(&S.a_full[i], Z::UnpackWarps / 2); mbar_init(&S.a_empty[i], 1); }
     for (int i = 0; i < Z::DS; ++i) { mbar_init(&S.d_full[i], 1); mbar_init(&S.d_empty[i], Z::SumWarps); }
     fence_mbar_init();
   }
@@ -195,80 +226,114 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
 
   float acc[Z::Columns];
   bool ok = true;
-  if (warp < kUnpackWarps) {
-    const int quarter = warp & 3, half = warp >> 2, row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + half * (kAColumns / 2);
+  if (warp < Z::UnpackWarps) {
+    // warps 0-3 the first slot of a stage, 4-7 the second
+    const int quarter = warp & 3, team = warp >> 2, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     RingAt w, a;
+    if (team) a.next(Z::AS);
+    uint32_t w_seen = 0;
     for (int item = item0; ok && item < plan.items; item += plan.step) {
       const size_t per = (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
-      for (int j = 0; ok && j < plan.slots; ++j) {
-        const int k0 = (plan.first + j) * kSlotK + half * (kSlotK / 2);
-        uint32_t z[2] = {8, 8};
-        if (P.zero) {
+      uint32_t z[4] = {8, 8, 8, 8};
+      if (P.zero) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) z[c] = P.zero[per + min((k0 + 32 * c) / GROUP, P.groups - 1)];
-        }
-        if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits))) break;
+        for (int c = 0; c < 4; ++c) z[c] = P.zero[per + min(((plan.first + team) * kSlotK + 32 * c) / GROUP, P.groups - 1)];
+        ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
+      }
+      for (int j = team; ok && j < plan.slots + team; j += 2) {
+        if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen))) break;
+        uint64_t* const emptied = &S.w_empty[w.stage];
         const uint32_t at = w_ring + w.stage * kWeightStage + row * 128;
-        uint32_t r[32];
+        w.next(Z::WS);
+        if (j >= plan.slots) {
+          // a tile's last stage may be one slot, of the others: an empty one after it keeps each team at
+          // its own slots of A (a team that went on by three of two would take a phase for the one before)
+          if (!(ok = wait_for(&S.a_empty[a.stage], a.phase ^ 1, waits))) break;
+          if (lane == 0) {
+            mbar_arrive(&S.a_full[a.stage]);
+            mbar_arrive(emptied);
+          }
+          a.next(Z::AS);
+          a.next(Z::AS);
+          w_seen = 0;
+          break;
+        }
+        uint4 v[4];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 v = shared16(at + (uint32_t)((((j & 1) * 4 + half * 2 + c) ^ (row & 7)) << 4));
+        for (int c = 0; c < 4; ++c) v[c] = shared16(at + (uint32_t)(((team * 4 + c) ^ (row & 7)) << 4));
+        const uint32_t a_seen = over(&S.a_empty[a.stage], a.phase ^ 1);
+        w_seen = over(&S.w_full[w.stage], w.phase);
+        uint32_t r[64];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
           const uint32_t less = (0x4300u | z[c]) * 0x10001u;
           __nv_bfloat162 l;
           memcpy(&l, &less, 4);
-          unpack8(r + 16 * c, v.x, l);
-          unpack8(r + 16 * c + 4, v.y, l);
-          unpack8(r + 16 * c + 8, v.z, l);
-          unpack8(r + 16 * c + 12, v.w, l);
+          unpack8(r + 16 * c, v[c].x, l);
+          unpack8(r + 16 * c + 4, v[c].y, l);
+          unpack8(r + 16 * c + 8, v[c].z, l);
+          unpack8(r + 16 * c + 12, v[c].w, l);
         }
-        if ((j & 1) || j + 1 == plan.slots) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&S.w_empty[w.stage]);
-          w.next(Z::WS);
+        if (P.zero) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) z[c] = P.zero[per + min(((plan.first + j + 2) * kSlotK + 32 * c) / GROUP, P.groups - 1)];
         }
-        if (!(ok = wait_for(&S.a_empty[a.stage], a.phase ^ 1, waits))) break;
+        if (!(ok = wait_for(&S.a_empty[a.stage], a.phase ^ 1, waits, a_seen))) break;
         tc_fence_after();
         store32(lanes + a.stage * kAColumns, r);
+        store32(lanes + a.stage * kAColumns + 32, r + 32);
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.a_full[a.stage]);
-        a.next(kASlots);
+        if (lane == 0) {
+          mbar_arrive(&S.a_full[a.stage]);
+          // only here: the loads above are sure to be done once what they gave has been stored (an
+          // arrival before the stores has let the next copy into the stage under them)
+          mbar_arrive(emptied);
+        }
+        a.next(Z::AS);
+        a.next(Z::AS);
       }
     }
   } else if (warp < kWeightCopies) {
-    const int quarter = warp & 3, part = (warp - kUnpackWarps) >> 2, row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + kDColumn + part * Z::Columns;
+    const int quarter = warp & 3, part = (warp - Z::UnpackWarps) >> 2, row = quarter * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + Z::DColumn + part * Z::Columns;
     RingAt d;
+    uint32_t seen = 0;
     for (int item = item0; item < plan.items; item += plan.step) {
       const int v = plan.col0(item) + row;
       const __nv_bfloat16* scale = P.scale + (size_t)min(v, P.V - 1) * P.groups;
+      ahead(P.scale, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
 #pragma unroll
       for (int c = 0; c < Z::Columns; ++c) acc[c] = 0.f;
-      const int g0 = plan.first * per_slot, g1 = min((plan.first + plan.slots) * per_slot, P.groups);
-      constexpr int kAhead = 4;              // scales on their way
-      __nv_bfloat16 next[kAhead];
+      const int g0 = plan.first * Z::PerSlot, g1 = min((plan.first + plan.slots) * Z::PerSlot, P.groups);
+      constexpr int kAhead = 2;              // units whose scales are on their way
+      __nv_bfloat16 next[kAhead][Z::UG];
 #pragma unroll
-      for (int i = 0; i < kAhead; ++i) next[i] = scale[min(g0 + i, P.groups - 1)];
-      for (int g = g0; ok && g < g1; ++g) {
-        const float s = __bfloat162float(next[0]);
+      for (int i = 0; i < kAhead * Z::UG; ++i) next[i / Z::UG][i % Z::UG] = scale[min(g0 + i, P.groups - 1)];
+      for (int g = g0; ok && g < g1; g += Z::UG) {
+        float s[Z::UG];
 #pragma unroll
-        for (int i = 1; i < kAhead; ++i) next[i - 1] = next[i];
-        next[kAhead - 1] = scale[min(g + kAhead, P.groups - 1)];
-        if (!(ok = wait_for(&S.d_full[d.stage], d.phase, waits))) break;
+        for (int i = 0; i < Z::UG; ++i) {
+          s[i] = __bfloat162float(next[0][i]);
+#pragma unroll
+          for (int u = 1; u < kAhead; ++u) next[u - 1][i] = next[u][i];
+          next[kAhead - 1][i] = scale[min(g + kAhead * Z::UG + i, P.groups - 1)];
+        }
+        if (!(ok = wait_for(&S.d_full[d.stage], d.phase, waits, seen))) break;
         tc_fence_after();
+        const uint32_t from = lanes + d.stage * Z::Unit;
 #pragma unroll
-        for (int c = 0; c < Z::Columns; c += 16) {
-          float x[16];
-          load16(x, lanes + d.stage * NT + c);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) acc[c + i] = __fmaf_rn(s, x[i], acc[c + i]);
+        for (int i = 0; i < Z::UG; ++i) {
+          if (i > 0 && g + i >= g1) break;   // the last unit of a row may have fewer groups
+          add_unit<Z::Columns>(acc, from + i * NT, s[i]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&S.d_empty[d.stage]);
         d.next(Z::DS);
+        seen = over(&S.d_full[d.stage], d.phase);
       }
       if (!ok) {
 #pragma unroll
@@ -315,33 +380,51 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   } else {
     constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(NT >> 3) << 17 | (uint32_t)(kRows >> 4) << 24;
     RingAt x, a, d;
+    uint32_t seen = 0;
     for (int item = item0; ok && item < plan.items; item += plan.step) {
       for (int j = 0; ok && j < plan.slots; ++j) {
-        if (!(ok = wait_for(&S.x_full[x.stage], x.phase, waits) && wait_for(&S.a_full[a.stage], a.phase, waits))) break;
+        if (!(ok = wait_for(&S.x_full[x.stage], x.phase, waits, seen) && wait_for(&S.a_full[a.stage], a.phase, waits, seen))) break;
         const uint32_t at = tmem + a.stage * kAColumns;
         const uint64_t desc = tc_desc(x_ring + x.stage * Z::XSlot, true);
-        const int left = P.groups - (plan.first + j) * per_slot, groups = left < per_slot ? left : per_slot;
-        for (int g = 0; g < groups; ++g) {
-          if (!(ok = wait_for(&S.d_empty[d.stage], d.phase ^ 1, waits))) break;
-          tc_fence_after();
-          if (elect_one()) {
-            const uint32_t to = tmem + kDColumn + d.stage * NT;
+        uint64_t *a_done = &S.a_empty[a.stage], *x_done = &S.x_empty[x.stage];
+        const int left = P.groups - (plan.first + j) * Z::PerSlot, groups = left < Z::PerSlot ? left : Z::PerSlot;
+        a.next(Z::AS);
+        x.next(Z::XS);
 #pragma unroll
-            for (int q = 0; q < GROUP / 16; ++q) {
+        for (int g = 0; g < Z::PerSlot; g += Z::UG) {
+          if (g > 0 && g >= groups) break;
+          if (!(ok = wait_for(&S.d_empty[d.stage], d.phase ^ 1, waits, seen))) break;
+          tc_fence_after();
+          const uint32_t to = tmem + Z::DColumn + d.stage * Z::Unit;
+          uint64_t* d_done = &S.d_full[d.stage];
+          d.next(Z::DS);
+          // what the next products wait for, asked while these are issued
+          seen = over(&S.d_empty[d.stage], d.phase ^ 1);
+          const bool last = g + Z::UG >= groups;
+          if (last) seen &= over(&S.x_full[x.stage], x.phase) & over(&S.a_full[a.stage], a.phase);
+          if (elect_one()) {
+#pragma unroll
+            for (int q = 0; q < Z::UG * GROUP / 16; ++q) {
               const int k = g * (GROUP / 16) + q;      // 16 k each, 4 to a box
-              product(to, at + k * 8, desc + (uint64_t)((k >> 2) * (Z::XBox >> 4) + (k & 3) * 2), idesc, q > 0);
+              if (q % (GROUP / 16) == 0 && q > 0 && g + q / (GROUP / 16) >= groups) break;
+              product(to + q / (GROUP / 16) * NT, at + k * 8, desc + (uint64_t)((k >> 2) * (Z::XBox >> 4) + (k & 3) * 2), idesc,
+                      q % (GROUP / 16) > 0);
             }
-            commit_to(&S.d_full[d.stage]);
-            if (g + 1 == groups) {
-              commit_to(&S.a_empty[a.stage]);
-              commit_to(&S.x_empty[x.stage]);
+            commit_to(d_done);
+            if (last) {
+              commit_to(a_done);
+              commit_to(x_done);
             }
           }
           __syncwarp();
-          d.next(Z::DS);
         }
-        a.next(kASlots);
-        x.next(Z::XS);
+      }
+      if (ok && (plan.slots & 1)) {          // the empty slot after the last
+        if (!(ok = wait_for(&S.a_full[a.stage], a.phase, waits))) break;
+        if (elect_one()) commit_to(&S.a_empty[a.stage]);
+        __syncwarp();
+        a.next(Z::AS);
+        seen = 0;
       }
     }
   }
@@ -353,8 +436,8 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   if (split > 1) {
     // every copy has landed and every product is done (or NaN stands for them): the ring is free
     float* const parts = reinterpret_cast<float*>(ring);           // [NT][128]
-    const bool sums = warp >= kUnpackWarps && warp < kWeightCopies;
-    const int row = (warp & 3) * 32 + lane, part = (warp - kUnpackWarps) >> 2;
+    const bool sums = warp >= Z::UnpackWarps && warp < kWeightCopies;
+    const int row = (warp & 3) * 32 + lane, part = (warp - Z::UnpackWarps) >> 2;
     __syncthreads();
     if (sums) {
 #pragma unroll
@@ -412,8 +495,8 @@ cudaError_t run(const W4Params& P, int nsm, cudaStream_t s) {
   while (split < kMaxSplit && 2 * split <= stages && 2 * split * items <= nsm) split *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split > 1 ? items * split : items < nsm ? items : nsm));
-  cfg.blockDim = dim3(Shape<NT>::Threads);
-  cfg.dynamicSmemBytes = linear_smem<NT>();
+  cfg.blockDim = dim3(Shape<NT, GROUP>::Threads);
+  cfg.dynamicSmemBytes = linear_smem<Shape<NT, GROUP>>();
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -426,15 +509,19 @@ template <int NT>
 cudaError_t of_group(const W4Params& P, int nsm, cudaStream_t s) {
   return P.group == 128 ? run<NT, 128>(P, nsm, s) : P.group == 64 ? run<NT, 64>(P, nsm, s) : run<NT, 32>(P, nsm, s);
 }
-template <int NT>
+template <int NT, int GROUP>
 cudaError_t allow() {
-  static_assert(linear_smem<NT>() <= 232448, "shared memory of a CTA");
-  static_assert(kDColumn + Shape<NT>::DS * NT <= (int)kTcColumns, "tensor memory");
-  static_assert(Shape<NT>::Ring >= NT * kRows * 4, "parts of a split tile");
-  const int smem = (int)linear_smem<NT>();
-  cudaError_t e = cudaFuncSetAttribute(linear_kernel<NT, 32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_kernel<NT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(linear_kernel<NT, 128>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  using Z = Shape<NT, GROUP>;
+  static_assert(linear_smem<Z>() <= 232448, "shared memory of a CTA");
+  static_assert(Z::DColumn + Z::DS * Z::Unit <= (int)kTcColumns, "tensor memory");
+  static_assert(Z::Ring >= NT * kRows * 4, "parts of a split tile");
+  return cudaFuncSetAttribute(linear_kernel<NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)linear_smem<Z>());
+}
+template <int NT>
+cudaError_t allow_all() {
+  cudaError_t e = allow<NT, 32>();
+  if (e == cudaSuccess) e = allow<NT, 64>();
+  if (e == cudaSuccess) e = allow<NT, 128>();
   return e;
 }
 
@@ -447,10 +534,10 @@ cudaError_t configure_w4() {
   if (e != cudaSuccess) return e;
   if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
   g_encode_w4 = reinterpret_cast<EncodeTiled>(f);
-  e = allow<16>();
-  if (e == cudaSuccess) e = allow<32>();
-  if (e == cudaSuccess) e = allow<64>();
-  if (e == cudaSuccess) e = allow<128>();
+  e = allow_all<16>();
+  if (e == cudaSuccess) e = allow_all<32>();
+  if (e == cudaSuccess) e = allow_all<64>();
+  if (e == cudaSuccess) e = allow_all<128>();
   return e;
 }
 
