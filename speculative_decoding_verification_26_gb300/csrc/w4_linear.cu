@@ -9,12 +9,16 @@
 // weight is rounded, and a sum of the tensor cores, which cut off at every addition, is at
 // most 128 long.
 //
-// A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states.  Roles:
+// A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states.  The k of a
+// tile goes by stages of 256 (16 KB of weights), cut into slots of whole groups: a slot has its
+// own columns of tensor memory for A and for the sums of its groups, and two barriers, "ready"
+// (unpacked, and the sums of its last use taken) and "done" (products finished): one wait and
+// one commit of the issuing warp a slot.  With barriers of their own for A, hidden states and
+// sums at every 128 k the issuing warp took 800 clocks for what HBM brings in 360.  Roles:
 //   warps 0-7    weights from shared memory to bf16 in tensor memory: thread = vocabulary row
-//                (32 (w % 4) on), half of each 128 k (w / 4);
-//   warps 8-11   groups' sums to registers and out (8-15, each half of the columns, for NT = 128);
-//   then one warp each: copies of weights (256 k a stage), copies of hidden states (128 k a
-//   slot), products.
+//                (32 (w % 4) on); warps 0-3 and 4-7 share a stage (0-3 alone for NT = 128);
+//   the next 4   groups' sums to registers and out (8, each half of the columns, for NT = 128);
+//   then one warp each: copies of weights, copies of hidden states, products.
 // Where there are fewer tiles than SMs, a cluster of CTAs splits the k of a tile, and the
 // parts are joined through distributed shared memory in the order of their ranks.
 #include "serve.cuh"
@@ -24,30 +28,30 @@ namespace sv {
 namespace {
 
 constexpr int kRows = 128;                   // vocabulary rows of a tile
-constexpr int kStageK = 256, kSlotK = 128;   // k of a stage of weights, of a slot
+constexpr int kStageK = 256;                 // k of a stage of weights
 constexpr int kWeightStage = kRows * kStageK / 2;        // 16 KB
-constexpr int kAColumns = kSlotK / 2;        // tensor-memory columns of a slot of A
 constexpr int kMaxSplit = 8;
 
-// Tensor memory holds AS slots of A and DS units of sums; a unit is the sums of UG groups,
-// handed over together: at most 128 columns.
 template <int NT, int GROUP>
 struct Shape {
-  static constexpr int WS = NT <= 32 ? 8 : NT == 64 ? 6 : 5;     // stages of weights
-  static constexpr int XS = NT <= 32 ? 8 : NT == 64 ? 6 : 4;     // slots of hidden states
-  static constexpr int PerSlot = kSlotK / GROUP;                 // groups
-  static constexpr int UG = PerSlot * NT <= 128 ? PerSlot : 128 / NT, Unit = UG * NT;
-  static constexpr int AS = Unit <= 64 ? 4 : 2, DColumn = AS * kAColumns;
-  static constexpr int DS = Unit <= 32 ? 8 : Unit == 64 ? 4 : 3;
-  static constexpr int XSlot = NT * kSlotK * 2, XBox = NT * 128; // bytes
-  static constexpr int UnpackWarps = 8, SumWarps = NT == 128 ? 8 : 4, Columns = NT / (SumWarps / 4);   // of a thread
+  // a slot: GS groups, their sums in at most 128 columns
+  static constexpr int Most = NT >= 128 ? 1 : 128 / NT, GS = kStageK / GROUP < Most ? kStageK / GROUP : Most;
+  static constexpr int SlotK = GS * GROUP, Subs = kStageK / SlotK, ACols = SlotK / 2, DCols = GS * NT;
+  static constexpr int Fit = (int)kTcColumns / (ACols + DCols), Slots = Fit < 4 ? Fit : 4;
+  static constexpr int DColumn = Slots * ACols;                  // where the sums begin
+  // unpacking: a team of four warps takes half of each slot, or every other slot; or there is one team
+  static constexpr int Teams = NT == 128 ? 1 : 2, Parts = Teams == 2 && Subs == 1 ? 2 : 1;
+  static constexpr int Chunks = SlotK / Parts / 32, Share = 8 / Teams;   // of 16 bytes of a row: of a part, of a team in a stage
+  static constexpr int WS = NT == 16 ? 9 : NT == 32 ? 8 : NT == 64 ? 7 : 5;      // stages of weights
+  static constexpr int XK = NT == 128 ? 128 : 256, XS = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 3 : 4;   // of hidden states
+  static constexpr int XSlot = NT * XK * 2, XBox = NT * 128;     // bytes
+  static constexpr int UnpackWarps = 4 * Teams, SumWarps = NT == 128 ? 8 : 4, Columns = NT / (SumWarps / 4);   // of a thread
   static constexpr int Threads = (UnpackWarps + SumWarps + 3) * 32;
   static constexpr int Ring = WS * kWeightStage + XS * XSlot;
 };
 template <class Z>
 struct W4Shared {
-  uint64_t w_full[Z::WS], w_empty[Z::WS], x_full[Z::XS], x_empty[Z::XS], a_full[Z::AS], a_empty[Z::AS], d_full[Z::DS],
-      d_empty[Z::DS];
+  uint64_t w_full[Z::WS], w_empty[Z::WS], x_full[Z::XS], x_empty[Z::XS], ready[Z::Slots], done[Z::Slots];
   uint32_t tmem;
   int failed;
 };
@@ -114,6 +118,14 @@ __device__ __forceinline__ void store32(uint32_t addr, const uint32_t* r) {
       "r"(addr)
       : "memory");
 }
+__device__ __forceinline__ void store16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+      "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
 __device__ __forceinline__ void load16(float (&v)[16], uint32_t addr) {
   uint32_t r[16];
   asm volatile(
@@ -174,9 +186,9 @@ struct W4Maps {
   CUtensorMap weight, hidden;
 };
 
-// What a CTA does: its tiles, and of each the slots [first, first + slots) of 128 k.
+// What a CTA does: its tiles, and of each the stages [first, first + stages) of 256 k.
 struct Plan {
-  int items, step, row_tiles, first, slots;
+  int items, step, row_tiles, first, stages;
   __device__ __forceinline__ int row0(int item, int nt) const { return item % row_tiles * nt; }
   __device__ __forceinline__ int col0(int item) const { return item / row_tiles * kRows; }
 };
@@ -200,18 +212,16 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   const int rank = blockIdx.x % split, item0 = blockIdx.x / split;
   plan.step = gridDim.x / split;
   {
-    const int stages = (P.H + kStageK - 1) / kStageK, lo = rank * stages / split, hi = (rank + 1) * stages / split;
-    const int end = min(hi * (kStageK / kSlotK), (P.H + kSlotK - 1) / kSlotK);
-    plan.first = lo * (kStageK / kSlotK);
-    plan.slots = end - plan.first;
+    const int stages = (P.H + kStageK - 1) / kStageK;
+    plan.first = rank * stages / split;
+    plan.stages = (rank + 1) * stages / split - plan.first;
   }
 
   if (threadIdx.x == 0) {
     S.failed = 0;
     for (int i = 0; i < Z::WS; ++i) { mbar_init(&S.w_full[i], 1); mbar_init(&S.w_empty[i], Z::UnpackWarps); }
     for (int i = 0; i < Z::XS; ++i) { mbar_init(&S.x_full[i], 1); mbar_init(&S.x_empty[i], 1); }
-    for (int i = 0; i < Z::AS; ++i) { mbar_init(&S.a_full[i], Z::UnpackWarps / 2); mbar_init(&S.a_empty[i], 1); }
-    for (int i = 0; i < Z::DS; ++i) { mbar_init(&S.d_full[i], 1); mbar_init(&S.d_empty[i], Z::SumWarps); }
+    for (int i = 0; i < Z::Slots; ++i) { mbar_init(&S.ready[i], 4 * Z::Parts + Z::SumWarps); mbar_init(&S.done[i], 1); }
     fence_mbar_init();
   }
   if (warp == kProducts) {
@@ -227,78 +237,87 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   float acc[Z::Columns];
   bool ok = true;
   if (warp < Z::UnpackWarps) {
-    // warps 0-3 the first slot of a stage, 4-7 the second
     const int quarter = warp & 3, team = warp >> 2, row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (Z::Parts == 2 ? team * (Z::ACols / 2) : 0);
+    // chunk i of a team's share of a stage is chunk `chunk(i)` of the row's eight
+    constexpr bool kTurns = Z::Teams == 2 && Z::Parts == 1;      // the teams take slots in turn
+    const auto chunk = [&](int i) { return kTurns ? (i / Z::Chunks * 2 + team) * Z::Chunks + i % Z::Chunks : team * Z::Share + i; };
     RingAt w, a;
-    if (team) a.next(Z::AS);
+    if (kTurns && team) a.next(Z::Slots);
+    uint32_t z[Z::Share];
+    uint4 v[Z::Share];
+    const auto zeros = [&](int item, int stage) {
+      if (!P.zero) return;
+      const uint8_t* p = P.zero + (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
+#pragma unroll
+      for (int i = 0; i < Z::Share; ++i) z[i] = p[min(((plan.first + stage) * kStageK + 32 * chunk(i)) / GROUP, P.groups - 1)];
+    };
+    const auto weights = [&] {
+      const uint32_t at = w_ring + w.stage * kWeightStage + row * 128;
+#pragma unroll
+      for (int i = 0; i < Z::Share; ++i) v[i] = shared16(at + (uint32_t)((chunk(i) ^ (row & 7)) << 4));
+    };
+#pragma unroll
+    for (int i = 0; i < Z::Share; ++i) z[i] = 8;
+    int item = item0, stage = 0;
+    if (item < plan.items) {
+      zeros(item, stage);
+      ok = wait_for(&S.w_full[w.stage], w.phase, waits);
+      weights();
+    }
     uint32_t w_seen = 0;
-    for (int item = item0; ok && item < plan.items; item += plan.step) {
-      const size_t per = (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
-      uint32_t z[4] = {8, 8, 8, 8};
-      if (P.zero) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) z[c] = P.zero[per + min(((plan.first + team) * kSlotK + 32 * c) / GROUP, P.groups - 1)];
-        ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
+    while (ok && item < plan.items) {
+      uint64_t* const emptied = &S.w_empty[w.stage];
+      w.next(Z::WS);
+      if (P.zero && stage == 0) ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
+      if (++stage == plan.stages) {
+        stage = 0;
+        item += plan.step;
       }
-      for (int j = team; ok && j < plan.slots + team; j += 2) {
-        if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen))) break;
-        uint64_t* const emptied = &S.w_empty[w.stage];
-        const uint32_t at = w_ring + w.stage * kWeightStage + row * 128;
-        w.next(Z::WS);
-        if (j >= plan.slots) {
-          // a tile's last stage may be one slot, of the others: an empty one after it keeps each team at
-          // its own slots of A (a team that went on by three of two would take a phase for the one before)
-          if (!(ok = wait_for(&S.a_empty[a.stage], a.phase ^ 1, waits))) break;
-          if (lane == 0) {
-            mbar_arrive(&S.a_full[a.stage]);
-            mbar_arrive(emptied);
-          }
-          a.next(Z::AS);
-          a.next(Z::AS);
-          w_seen = 0;
-          break;
-        }
-        uint4 v[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) v[c] = shared16(at + (uint32_t)(((team * 4 + c) ^ (row & 7)) << 4));
-        const uint32_t a_seen = over(&S.a_empty[a.stage], a.phase ^ 1);
-        w_seen = over(&S.w_full[w.stage], w.phase);
-        uint32_t r[64];
+      for (int i = 0; i < Z::Share; i += Z::Chunks) {
+        const uint32_t a_seen = over(&S.done[a.stage], a.phase ^ 1);
+        if (i == 0) w_seen = over(&S.w_full[w.stage], w.phase);
+        uint32_t r[16 * Z::Chunks];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t less = (0x4300u | z[c]) * 0x10001u;
+        for (int c = 0; c < Z::Chunks; ++c) {
+          const uint32_t less = (0x4300u | z[i + c]) * 0x10001u;
           __nv_bfloat162 l;
           memcpy(&l, &less, 4);
-          unpack8(r + 16 * c, v[c].x, l);
-          unpack8(r + 16 * c + 4, v[c].y, l);
-          unpack8(r + 16 * c + 8, v[c].z, l);
-          unpack8(r + 16 * c + 12, v[c].w, l);
+          unpack8(r + 16 * c, v[i + c].x, l);
+          unpack8(r + 16 * c + 4, v[i + c].y, l);
+          unpack8(r + 16 * c + 8, v[i + c].z, l);
+          unpack8(r + 16 * c + 12, v[i + c].w, l);
         }
-        if (P.zero) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) z[c] = P.zero[per + min(((plan.first + j + 2) * kSlotK + 32 * c) / GROUP, P.groups - 1)];
-        }
-        if (!(ok = wait_for(&S.a_empty[a.stage], a.phase ^ 1, waits, a_seen))) break;
+        if (!(ok = wait_for(&S.done[a.stage], a.phase ^ 1, waits, a_seen))) break;
         tc_fence_after();
-        store32(lanes + a.stage * kAColumns, r);
-        store32(lanes + a.stage * kAColumns + 32, r + 32);
+        const uint32_t to = lanes + a.stage * Z::ACols;
+        if constexpr (Z::Chunks == 1) store16(to, r);
+#pragma unroll
+        for (int c = 0; c + 1 < Z::Chunks; c += 2) store32(to + 16 * c, r + 16 * c);
+        const bool last = i + Z::Chunks == Z::Share;
+        if (last && item < plan.items) {     // the next stage's, while the stores go out
+          zeros(item, stage);
+          if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen))) break;
+          weights();
+        }
         asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&S.a_full[a.stage]);
-          // only here: the loads above are sure to be done once what they gave has been stored (an
-          // arrival before the stores has let the next copy into the stage under them)
-          mbar_arrive(emptied);
+          mbar_arrive(&S.ready[a.stage]);
+          // only here: the loads from the stage are sure to be done once what they gave has been
+          // stored (an arrival before the stores has let the next copy into the stage under them)
+          if (last) mbar_arrive(emptied);
         }
-        a.next(Z::AS);
-        a.next(Z::AS);
+        a.next(Z::Slots);
+        if (kTurns) a.next(Z::Slots);
       }
     }
   } else if (warp < kWeightCopies) {
     const int quarter = warp & 3, part = (warp - Z::UnpackWarps) >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + Z::DColumn + part * Z::Columns;
+    if (lane < Z::Slots) mbar_arrive(&S.ready[lane]);            // nothing to take of the first use
     RingAt d;
     uint32_t seen = 0;
     for (int item = item0; item < plan.items; item += plan.step) {
@@ -307,33 +326,33 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
       ahead(P.scale, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
 #pragma unroll
       for (int c = 0; c < Z::Columns; ++c) acc[c] = 0.f;
-      const int g0 = plan.first * Z::PerSlot, g1 = min((plan.first + plan.slots) * Z::PerSlot, P.groups);
-      constexpr int kAhead = 2;              // units whose scales are on their way
-      __nv_bfloat16 next[kAhead][Z::UG];
+      const int g0 = plan.first * (kStageK / GROUP), g1 = (plan.first + plan.stages) * (kStageK / GROUP);
+      constexpr int kAhead = 2;              // slots whose scales are on their way
+      __nv_bfloat16 next[kAhead][Z::GS];
 #pragma unroll
-      for (int i = 0; i < kAhead * Z::UG; ++i) next[i / Z::UG][i % Z::UG] = scale[min(g0 + i, P.groups - 1)];
-      for (int g = g0; ok && g < g1; g += Z::UG) {
-        float s[Z::UG];
+      for (int i = 0; i < kAhead * Z::GS; ++i) next[i / Z::GS][i % Z::GS] = scale[min(g0 + i, P.groups - 1)];
+      for (int g = g0; ok && g < g1; g += Z::GS) {
+        float s[Z::GS];
 #pragma unroll
-        for (int i = 0; i < Z::UG; ++i) {
+        for (int i = 0; i < Z::GS; ++i) {
           s[i] = __bfloat162float(next[0][i]);
 #pragma unroll
           for (int u = 1; u < kAhead; ++u) next[u - 1][i] = next[u][i];
-          next[kAhead - 1][i] = scale[min(g + kAhead * Z::UG + i, P.groups - 1)];
+          next[kAhead - 1][i] = scale[min(g + kAhead * Z::GS + i, P.groups - 1)];
         }
-        if (!(ok = wait_for(&S.d_full[d.stage], d.phase, waits, seen))) break;
+        if (!(ok = wait_for(&S.done[d.stage], d.phase, waits, seen))) break;
         tc_fence_after();
-        const uint32_t from = lanes + d.stage * Z::Unit;
+        const uint32_t from = lanes + d.stage * Z::DCols;
 #pragma unroll
-        for (int i = 0; i < Z::UG; ++i) {
-          if (i > 0 && g + i >= g1) break;   // the last unit of a row may have fewer groups
+        for (int i = 0; i < Z::GS; ++i) {
+          if (g + i >= P.groups) break;      // behind the row's end
           add_unit<Z::Columns>(acc, from + i * NT, s[i]);
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.d_empty[d.stage]);
-        d.next(Z::DS);
-        seen = over(&S.d_full[d.stage], d.phase);
+        if (lane == 0) mbar_arrive(&S.ready[d.stage]);
+        d.next(Z::Slots);
+        seen = over(&S.done[d.stage], d.phase);
       }
       if (!ok) {
 #pragma unroll
@@ -354,11 +373,11 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   } else if (warp == kWeightCopies) {
     RingAt w;
     for (int item = item0; ok && item < plan.items; item += plan.step) {
-      for (int j = 0; j < plan.slots; j += kStageK / kSlotK) {
+      for (int j = 0; j < plan.stages; ++j) {
         if (!(ok = wait_for(&S.w_empty[w.stage], w.phase ^ 1, waits))) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&S.w_full[w.stage], kWeightStage);
-          copy_box(w_ring + w.stage * kWeightStage, &M.weight, (plan.first + j) * (kSlotK / 2), plan.col0(item), &S.w_full[w.stage]);
+          copy_box(w_ring + w.stage * kWeightStage, &M.weight, (plan.first + j) * (kStageK / 2), plan.col0(item), &S.w_full[w.stage]);
         }
         w.next(Z::WS);
       }
@@ -366,65 +385,51 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   } else if (warp == kHiddenCopies) {
     RingAt x;
     for (int item = item0; ok && item < plan.items; item += plan.step) {
-      for (int j = 0; j < plan.slots; ++j) {
+      for (int k = plan.first * kStageK; k < (plan.first + plan.stages) * kStageK; k += Z::XK) {
         if (!(ok = wait_for(&S.x_empty[x.stage], x.phase ^ 1, waits))) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&S.x_full[x.stage], Z::XSlot);
-          const int k = (plan.first + j) * kSlotK;
-          copy_box(x_ring + x.stage * Z::XSlot, &M.hidden, k, plan.row0(item, NT), &S.x_full[x.stage]);
-          copy_box(x_ring + x.stage * Z::XSlot + Z::XBox, &M.hidden, k + 64, plan.row0(item, NT), &S.x_full[x.stage]);
+#pragma unroll
+          for (int c = 0; c < Z::XK / 64; ++c)
+            copy_box(x_ring + x.stage * Z::XSlot + c * Z::XBox, &M.hidden, k + 64 * c, plan.row0(item, NT), &S.x_full[x.stage]);
         }
         x.next(Z::XS);
       }
     }
   } else {
     constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(NT >> 3) << 17 | (uint32_t)(kRows >> 4) << 24;
-    RingAt x, a, d;
-    uint32_t seen = 0;
+    constexpr int kSteps = GROUP / 16;       // 16 k each, 4 to a box
+    RingAt x, a;
+    uint32_t a_seen = 0, x_seen = 0;
     for (int item = item0; ok && item < plan.items; item += plan.step) {
-      for (int j = 0; ok && j < plan.slots; ++j) {
-        if (!(ok = wait_for(&S.x_full[x.stage], x.phase, waits, seen) && wait_for(&S.a_full[a.stage], a.phase, waits, seen))) break;
-        const uint32_t at = tmem + a.stage * kAColumns;
-        const uint64_t desc = tc_desc(x_ring + x.stage * Z::XSlot, true);
-        uint64_t *a_done = &S.a_empty[a.stage], *x_done = &S.x_empty[x.stage];
-        const int left = P.groups - (plan.first + j) * Z::PerSlot, groups = left < Z::PerSlot ? left : Z::PerSlot;
-        a.next(Z::AS);
-        x.next(Z::XS);
+      for (int j = 0; ok && j < plan.stages; ++j) {
 #pragma unroll
-        for (int g = 0; g < Z::PerSlot; g += Z::UG) {
-          if (g > 0 && g >= groups) break;
-          if (!(ok = wait_for(&S.d_empty[d.stage], d.phase ^ 1, waits, seen))) break;
+        for (int sub = 0; sub < Z::Subs; ++sub) {
+          constexpr int kPer = Z::XK / Z::SlotK;               // slots to a copy of hidden states
+          const bool first = sub % kPer == 0, last = sub % kPer == kPer - 1;
+          if (first && !(ok = wait_for(&S.x_full[x.stage], x.phase, waits, x_seen))) break;
+          if (!(ok = wait_for(&S.ready[a.stage], a.phase, waits, a_seen))) break;
           tc_fence_after();
-          const uint32_t to = tmem + Z::DColumn + d.stage * Z::Unit;
-          uint64_t* d_done = &S.d_full[d.stage];
-          d.next(Z::DS);
+          const uint32_t at = tmem + a.stage * Z::ACols, to = tmem + Z::DColumn + a.stage * Z::DCols;
+          const uint64_t desc = tc_desc(x_ring + x.stage * Z::XSlot, true);
+          uint64_t *const done = &S.done[a.stage], *const x_done = &S.x_empty[x.stage];
+          a.next(Z::Slots);
+          if (last) x.next(Z::XS);
           // what the next products wait for, asked while these are issued
-          seen = over(&S.d_empty[d.stage], d.phase ^ 1);
-          const bool last = g + Z::UG >= groups;
-          if (last) seen &= over(&S.x_full[x.stage], x.phase) & over(&S.a_full[a.stage], a.phase);
+          a_seen = over(&S.ready[a.stage], a.phase);
+          if (last) x_seen = over(&S.x_full[x.stage], x.phase);
           if (elect_one()) {
 #pragma unroll
-            for (int q = 0; q < Z::UG * GROUP / 16; ++q) {
-              const int k = g * (GROUP / 16) + q;      // 16 k each, 4 to a box
-              if (q % (GROUP / 16) == 0 && q > 0 && g + q / (GROUP / 16) >= groups) break;
-              product(to + q / (GROUP / 16) * NT, at + k * 8, desc + (uint64_t)((k >> 2) * (Z::XBox >> 4) + (k & 3) * 2), idesc,
-                      q % (GROUP / 16) > 0);
+            for (int q = 0; q < Z::GS * kSteps; ++q) {
+              const int k = sub % kPer * (Z::GS * kSteps) + q;
+              product(to + q / kSteps * NT, at + q * 8, desc + (uint64_t)((k >> 2) * (Z::XBox >> 4) + (k & 3) * 2), idesc,
+                      q % kSteps > 0);
             }
-            commit_to(d_done);
-            if (last) {
-              commit_to(a_done);
-              commit_to(x_done);
-            }
+            commit_to(done);
+            if (last) commit_to(x_done);
           }
           __syncwarp();
         }
-      }
-      if (ok && (plan.slots & 1)) {          // the empty slot after the last
-        if (!(ok = wait_for(&S.a_full[a.stage], a.phase, waits))) break;
-        if (elect_one()) commit_to(&S.a_empty[a.stage]);
-        __syncwarp();
-        a.next(Z::AS);
-        seen = 0;
       }
     }
   }
@@ -513,7 +518,8 @@ template <int NT, int GROUP>
 cudaError_t allow() {
   using Z = Shape<NT, GROUP>;
   static_assert(linear_smem<Z>() <= 232448, "shared memory of a CTA");
-  static_assert(Z::DColumn + Z::DS * Z::Unit <= (int)kTcColumns, "tensor memory");
+  static_assert(Z::Slots >= 2 && Z::DColumn + Z::Slots * Z::DCols <= (int)kTcColumns, "tensor memory");
+  static_assert(Z::Subs % Z::Teams == 0 || Z::Parts == 2, "slots of a stage");
   static_assert(Z::Ring >= NT * kRows * 4, "parts of a split tile");
   return cudaFuncSetAttribute(linear_kernel<NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)linear_smem<Z>());
 }
