@@ -215,6 +215,10 @@ struct RingAt {
   __device__ __forceinline__ void next(int stages) {
     if (++stage == stages) { stage = 0; phase ^= 1; }
   }
+  __device__ __forceinline__ void skip(int n, int stages) {      // n <= stages
+    stage += n;
+    if (stage >= stages) { stage -= stages; phase ^= 1; }
+  }
 };
 
 // ---------------------------------------------------------------------------

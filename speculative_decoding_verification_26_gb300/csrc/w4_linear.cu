@@ -34,19 +34,25 @@ constexpr int kMaxSplit = 8;
 
 template <int NT, int GROUP>
 struct Shape {
-  // a slot: GS groups, their sums in at most 128 columns
-  static constexpr int Most = NT >= 128 ? 1 : 128 / NT, GS = kStageK / GROUP < Most ? kStageK / GROUP : Most;
-  static constexpr int SlotK = GS * GROUP, Subs = kStageK / SlotK, ACols = SlotK / 2, DCols = GS * NT;
-  static constexpr int Fit = (int)kTcColumns / (ACols + DCols), Slots = Fit < 4 ? Fit : 4;
+  // warps: teams of four unpack, each taking every Teams-th slot
+  static constexpr int Teams = NT <= 32 ? 4 : 2, UnpackWarps = 4 * Teams, SumWarps = NT >= 64 ? 8 : 4;
+  static constexpr int Columns = NT / (SumWarps / 4);            // of a thread
+  static constexpr int Issuers = 2, Threads = (UnpackWarps + SumWarps + 2 + Issuers) * 32;   // an issuer takes every other slot
+  // a slot: whole groups, at most 128 k; as many as leave tensor memory for a slot of each team.
+  // Whoever takes every n-th slot, stage or copy of a ring has a ring of a multiple of n: it waits
+  // for every phase of the barriers that it waits for, and so never takes one for another.
+  static constexpr int cost(int k) { return k / 2 + k / GROUP * NT; }
+  static constexpr int SlotK = GROUP >= 128 || Teams * cost(128) <= (int)kTcColumns ? 128
+                               : GROUP >= 64 || Teams * cost(64) <= (int)kTcColumns ? 64 : 32;
+  static constexpr int GS = SlotK / GROUP, Subs = kStageK / SlotK, ACols = SlotK / 2, DCols = GS * NT;
+  static constexpr int Fit = (int)kTcColumns / (ACols + DCols), Slots = (Fit < 6 ? Fit : 6) / Teams * Teams;
   static constexpr int DColumn = Slots * ACols;                  // where the sums begin
-  // unpacking: a team of four warps takes half of each slot, or every other slot; or there is one team
-  static constexpr int Teams = NT == 128 ? 1 : 2, Parts = Teams == 2 && Subs == 1 ? 2 : 1;
-  static constexpr int Chunks = SlotK / Parts / 32, Share = 8 / Teams;   // of 16 bytes of a row: of a part, of a team in a stage
-  static constexpr int WS = NT == 16 ? 9 : NT == 32 ? 8 : NT == 64 ? 7 : 5;      // stages of weights
+  static constexpr int Chunks = SlotK / 32;                      // of 16 bytes of a row
+  static constexpr int Sharing = Teams < Subs ? Teams : Subs;    // teams that read a stage
+  static constexpr int Turns = Subs / Sharing, Skip = Teams / Sharing;   // of a team in a stage; stages to its next
+  static constexpr int WS = NT <= 32 ? 8 : NT == 64 ? 7 : 5;      // stages of weights
   static constexpr int XK = NT == 128 ? 128 : 256, XS = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 3 : 4;   // of hidden states
   static constexpr int XSlot = NT * XK * 2, XBox = NT * 128;     // bytes
-  static constexpr int UnpackWarps = 4 * Teams, SumWarps = NT == 128 ? 8 : 4, Columns = NT / (SumWarps / 4);   // of a thread
-  static constexpr int Threads = (UnpackWarps + SumWarps + 3) * 32;
   static constexpr int Ring = WS * kWeightStage + XS * XSlot;
 };
 template <class Z>
@@ -130,14 +136,19 @@ __device__ __forceinline__ void load16(float (&v)[16], uint32_t addr) {
   uint32_t r[16];
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
         "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
 #pragma unroll
   for (int c = 0; c < 16; ++c) v[c] = __uint_as_float(r[c]);
+}
+// once loads have been issued: what they give may be used after wait_loads and keep
+__device__ __forceinline__ void wait_loads() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void keep(float (&v)[16]) {
+#pragma unroll
+  for (int c = 0; c < 16; ++c) asm volatile("" : "+f"(v[c]));
 }
 __device__ __forceinline__ uint4 shared16(uint32_t addr) {
   uint4 v;
@@ -161,10 +172,12 @@ __device__ __forceinline__ void unpack8(uint32_t* out, uint32_t word, __nv_bfloa
 template <int N>
 __device__ __forceinline__ void add_unit(float (&acc)[N], uint32_t from, float s) {
 #pragma unroll
-  for (int c = 0; c < N; c += (N < 32 ? 16 : 32)) {
-    if constexpr (N < 32) {
+  for (int c = 0; c < N; c += (N == 32 ? 32 : 16)) {
+    if constexpr (N != 32) {
       float x[16];
       load16(x, from + c);
+      wait_loads();
+      keep(x);
 #pragma unroll
       for (int i = 0; i < 16; ++i) acc[c + i] = __fmaf_rn(s, x[i], acc[c + i]);
     } else {
@@ -219,9 +232,9 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
 
   if (threadIdx.x == 0) {
     S.failed = 0;
-    for (int i = 0; i < Z::WS; ++i) { mbar_init(&S.w_full[i], 1); mbar_init(&S.w_empty[i], Z::UnpackWarps); }
-    for (int i = 0; i < Z::XS; ++i) { mbar_init(&S.x_full[i], 1); mbar_init(&S.x_empty[i], 1); }
-    for (int i = 0; i < Z::Slots; ++i) { mbar_init(&S.ready[i], 4 * Z::Parts + Z::SumWarps); mbar_init(&S.done[i], 1); }
+    for (int i = 0; i < Z::WS; ++i) { mbar_init(&S.w_full[i], 1); mbar_init(&S.w_empty[i], 4 * Z::Sharing); }
+    for (int i = 0; i < Z::XS; ++i) { mbar_init(&S.x_full[i], 1); mbar_init(&S.x_empty[i], Z::XK / Z::SlotK); }
+    for (int i = 0; i < Z::Slots; ++i) { mbar_init(&S.ready[i], 4 + Z::SumWarps); mbar_init(&S.done[i], 1); }
     fence_mbar_init();
   }
   if (warp == kProducts) {
@@ -238,81 +251,91 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   bool ok = true;
   if (warp < Z::UnpackWarps) {
     const int quarter = warp & 3, team = warp >> 2, row = quarter * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + (Z::Parts == 2 ? team * (Z::ACols / 2) : 0);
-    // chunk i of a team's share of a stage is chunk `chunk(i)` of the row's eight
-    constexpr bool kTurns = Z::Teams == 2 && Z::Parts == 1;      // the teams take slots in turn
-    const auto chunk = [&](int i) { return kTurns ? (i / Z::Chunks * 2 + team) * Z::Chunks + i % Z::Chunks : team * Z::Share + i; };
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     RingAt w, a;
-    if (kTurns && team) a.next(Z::Slots);
-    uint32_t z[Z::Share];
-    uint4 v[Z::Share];
-    const auto zeros = [&](int item, int stage) {
+    int item = item0, stage = 0, turn = 0;
+    const auto skip = [&](int stages) {
+      for (int i = 0; i < stages; ++i) {
+        w.next(Z::WS);
+        if (++stage == plan.stages) {
+          stage = 0;
+          item += plan.step;
+        }
+      }
+    };
+    skip(team / Z::Sharing);
+    a.skip(team, Z::Slots);
+    uint32_t z[Z::Chunks];
+    uint4 v[Z::Chunks];
+    // the current slot's zero points and weights: chunk c of the slot is chunk first + c of the row's eight
+    const auto zeros = [&](int first) {
       if (!P.zero) return;
       const uint8_t* p = P.zero + (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
 #pragma unroll
-      for (int i = 0; i < Z::Share; ++i) z[i] = p[min(((plan.first + stage) * kStageK + 32 * chunk(i)) / GROUP, P.groups - 1)];
+      for (int c = 0; c < Z::Chunks; ++c) z[c] = p[min(((plan.first + stage) * kStageK + 32 * (first + c)) / GROUP, P.groups - 1)];
     };
-    const auto weights = [&] {
+    const auto weights = [&](int first) {
       const uint32_t at = w_ring + w.stage * kWeightStage + row * 128;
 #pragma unroll
-      for (int i = 0; i < Z::Share; ++i) v[i] = shared16(at + (uint32_t)((chunk(i) ^ (row & 7)) << 4));
+      for (int c = 0; c < Z::Chunks; ++c) v[c] = shared16(at + (uint32_t)(((first + c) ^ (row & 7)) << 4));
     };
+    const auto first = [&] { return (team % Z::Sharing + turn * Z::Sharing) * Z::Chunks; };
 #pragma unroll
-    for (int i = 0; i < Z::Share; ++i) z[i] = 8;
-    int item = item0, stage = 0;
+    for (int c = 0; c < Z::Chunks; ++c) z[c] = 8;
     if (item < plan.items) {
-      zeros(item, stage);
+      zeros(first());
       ok = wait_for(&S.w_full[w.stage], w.phase, waits);
-      weights();
+      weights(first());
     }
-    uint32_t w_seen = 0;
     while (ok && item < plan.items) {
       uint64_t* const emptied = &S.w_empty[w.stage];
-      w.next(Z::WS);
-      if (P.zero && stage == 0) ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
-      if (++stage == plan.stages) {
-        stage = 0;
-        item += plan.step;
+      const bool last = ++turn == Z::Turns;
+      if (P.zero && stage < Z::Skip) ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
+      const uint32_t a_seen = over(&S.done[a.stage], a.phase ^ 1);
+      uint32_t w_seen = 1;
+      if (last) {
+        turn = 0;
+        skip(Z::Skip);
+        w_seen = over(&S.w_full[w.stage], w.phase);
       }
+      const uint32_t to = lanes + a.stage * Z::ACols;
+      constexpr int kAtOnce = Z::Chunks < 2 ? 1 : 2;
 #pragma unroll
-      for (int i = 0; i < Z::Share; i += Z::Chunks) {
-        const uint32_t a_seen = over(&S.done[a.stage], a.phase ^ 1);
-        if (i == 0) w_seen = over(&S.w_full[w.stage], w.phase);
-        uint32_t r[16 * Z::Chunks];
+      for (int c = 0; c < Z::Chunks; c += kAtOnce) {
+        uint32_t r[16 * kAtOnce];
 #pragma unroll
-        for (int c = 0; c < Z::Chunks; ++c) {
-          const uint32_t less = (0x4300u | z[i + c]) * 0x10001u;
+        for (int u = 0; u < kAtOnce; ++u) {
+          const uint32_t less = (0x4300u | z[c + u]) * 0x10001u;
           __nv_bfloat162 l;
           memcpy(&l, &less, 4);
-          unpack8(r + 16 * c, v[i + c].x, l);
-          unpack8(r + 16 * c + 4, v[i + c].y, l);
-          unpack8(r + 16 * c + 8, v[i + c].z, l);
-          unpack8(r + 16 * c + 12, v[i + c].w, l);
+          unpack8(r + 16 * u, v[c + u].x, l);
+          unpack8(r + 16 * u + 4, v[c + u].y, l);
+          unpack8(r + 16 * u + 8, v[c + u].z, l);
+          unpack8(r + 16 * u + 12, v[c + u].w, l);
         }
-        if (!(ok = wait_for(&S.done[a.stage], a.phase ^ 1, waits, a_seen))) break;
-        tc_fence_after();
-        const uint32_t to = lanes + a.stage * Z::ACols;
-        if constexpr (Z::Chunks == 1) store16(to, r);
-#pragma unroll
-        for (int c = 0; c + 1 < Z::Chunks; c += 2) store32(to + 16 * c, r + 16 * c);
-        const bool last = i + Z::Chunks == Z::Share;
-        if (last && item < plan.items) {     // the next stage's, while the stores go out
-          zeros(item, stage);
-          if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen))) break;
-          weights();
+        if (c == 0) {
+          if (!(ok = wait_for(&S.done[a.stage], a.phase ^ 1, waits, a_seen))) break;
+          tc_fence_after();
         }
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&S.ready[a.stage]);
-          // only here: the loads from the stage are sure to be done once what they gave has been
-          // stored (an arrival before the stores has let the next copy into the stage under them)
-          if (last) mbar_arrive(emptied);
-        }
-        a.next(Z::Slots);
-        if (kTurns) a.next(Z::Slots);
+        if constexpr (kAtOnce == 1) store16(to, r);
+        else store32(to + 16 * c, r);
       }
+      if (ok && item < plan.items) {         // the next slot's, while the stores go out
+        zeros(first());
+        ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen);
+        weights(first());
+      }
+      if (!ok) break;
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&S.ready[a.stage]);
+        // only here: the loads from the stage are sure to be done once what they gave has been
+        // stored (an arrival before the stores has let the next copy into the stage under them)
+        if (last) mbar_arrive(emptied);
+      }
+      a.skip(Z::Teams, Z::Slots);
     }
   } else if (warp < kWeightCopies) {
     const int quarter = warp & 3, part = (warp - Z::UnpackWarps) >> 2, row = quarter * 32 + lane;
@@ -327,31 +350,58 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
 #pragma unroll
       for (int c = 0; c < Z::Columns; ++c) acc[c] = 0.f;
       const int g0 = plan.first * (kStageK / GROUP), g1 = (plan.first + plan.stages) * (kStageK / GROUP);
-      constexpr int kAhead = 2;              // slots whose scales are on their way
-      __nv_bfloat16 next[kAhead][Z::GS];
+      constexpr int kBoth = Z::Columns * Z::GS <= 16 ? 2 : 1, kGroups = kBoth * Z::GS;      // slots taken at once
+      constexpr int kAhead = kGroups <= 2 ? 2 : 1;                 // times their groups' scales are on their way
+      __nv_bfloat16 next[kAhead][kGroups];
 #pragma unroll
-      for (int i = 0; i < kAhead * Z::GS; ++i) next[i / Z::GS][i % Z::GS] = scale[min(g0 + i, P.groups - 1)];
-      for (int g = g0; ok && g < g1; g += Z::GS) {
-        float s[Z::GS];
+      for (int i = 0; i < kAhead * kGroups; ++i) next[i / kGroups][i % kGroups] = scale[min(g0 + i, P.groups - 1)];
+      for (int g = g0; ok && g < g1; g += kGroups) {
+        float s[kGroups];
 #pragma unroll
-        for (int i = 0; i < Z::GS; ++i) {
+        for (int i = 0; i < kGroups; ++i) {
           s[i] = __bfloat162float(next[0][i]);
 #pragma unroll
           for (int u = 1; u < kAhead; ++u) next[u - 1][i] = next[u][i];
-          next[kAhead - 1][i] = scale[min(g + kAhead * Z::GS + i, P.groups - 1)];
+          next[kAhead - 1][i] = scale[min(g + kAhead * kGroups + i, P.groups - 1)];
         }
-        if (!(ok = wait_for(&S.done[d.stage], d.phase, waits, seen))) break;
-        tc_fence_after();
-        const uint32_t from = lanes + d.stage * Z::DCols;
+        uint32_t from[kBoth];
+        uint64_t* taken[kBoth];
 #pragma unroll
-        for (int i = 0; i < Z::GS; ++i) {
-          if (g + i >= P.groups) break;      // behind the row's end
-          add_unit<Z::Columns>(acc, from + i * NT, s[i]);
+        for (int u = 0; u < kBoth; ++u) {
+          ok = ok && wait_for(&S.done[d.stage], d.phase, waits, u == 0 ? seen : 0);
+          from[u] = lanes + d.stage * Z::DCols;
+          taken[u] = &S.ready[d.stage];
+          d.next(Z::Slots);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        constexpr int kOnce = Z::Columns < 32 ? 32 / Z::Columns : 1;       // groups read at once
+#pragma unroll
+        for (int i = 0; i < kGroups; i += kOnce) {
+          if (i > 0 && g + i >= P.groups) break;       // behind the row's end
+          if constexpr (Z::Columns == 16 && kGroups > 1) {
+            float x[2][16];
+            load16(x[0], from[i / Z::GS] + i % Z::GS * NT);
+            load16(x[1], from[(i + 1) / Z::GS] + (i + 1) % Z::GS * NT);
+            wait_loads();
+            keep(x[0]);
+            keep(x[1]);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) acc[c] = __fmaf_rn(s[i], x[0][c], acc[c]);
+            if (g + i + 1 < P.groups) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) acc[c] = __fmaf_rn(s[i + 1], x[1][c], acc[c]);
+            }
+          } else {
+            add_unit<Z::Columns>(acc, from[i / Z::GS] + i % Z::GS * NT, s[i]);
+          }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&S.ready[d.stage]);
-        d.next(Z::Slots);
+        if (lane == 0) {
+#pragma unroll
+          for (int u = 0; u < kBoth; ++u) mbar_arrive(taken[u]);
+        }
         seen = over(&S.done[d.stage], d.phase);
       }
       if (!ok) {
@@ -399,38 +449,33 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   } else {
     constexpr uint32_t idesc = 1u << 4 | 1u << 7 | 1u << 10 | (uint32_t)(NT >> 3) << 17 | (uint32_t)(kRows >> 4) << 24;
     constexpr int kSteps = GROUP / 16;       // 16 k each, 4 to a box
+    // an issuer's slots: every Issuers-th of the CTA's, the copies of hidden states likewise
+    constexpr int kPer = Z::XK / Z::SlotK;                       // slots to a copy
+    const int mine = warp - kProducts;
     RingAt x, a;
-    uint32_t a_seen = 0, x_seen = 0;
-    for (int item = item0; ok && item < plan.items; item += plan.step) {
-      for (int j = 0; ok && j < plan.stages; ++j) {
+    a.skip(mine, Z::Slots);
+    x.skip(mine / kPer, Z::XS);
+    int sub = mine % kPer;
+    uint32_t a_seen = 0;
+    const int tiles = item0 < plan.items ? (plan.items - 1 - item0) / plan.step + 1 : 0;
+    for (long long slot = mine, slots = (long long)tiles * plan.stages * Z::Subs; slot < slots; slot += Z::Issuers) {
+      if (!(ok = wait_for(&S.x_full[x.stage], x.phase, waits) && wait_for(&S.ready[a.stage], a.phase, waits, a_seen))) break;
+      tc_fence_after();
+      const uint32_t at = tmem + a.stage * Z::ACols, to = tmem + Z::DColumn + a.stage * Z::DCols;
+      const uint64_t desc = tc_desc(x_ring + x.stage * Z::XSlot + sub * Z::SlotK / 64 * Z::XBox + sub * Z::SlotK % 64 * 2, true);
+      if (elect_one()) {
 #pragma unroll
-        for (int sub = 0; sub < Z::Subs; ++sub) {
-          constexpr int kPer = Z::XK / Z::SlotK;               // slots to a copy of hidden states
-          const bool first = sub % kPer == 0, last = sub % kPer == kPer - 1;
-          if (first && !(ok = wait_for(&S.x_full[x.stage], x.phase, waits, x_seen))) break;
-          if (!(ok = wait_for(&S.ready[a.stage], a.phase, waits, a_seen))) break;
-          tc_fence_after();
-          const uint32_t at = tmem + a.stage * Z::ACols, to = tmem + Z::DColumn + a.stage * Z::DCols;
-          const uint64_t desc = tc_desc(x_ring + x.stage * Z::XSlot, true);
-          uint64_t *const done = &S.done[a.stage], *const x_done = &S.x_empty[x.stage];
-          a.next(Z::Slots);
-          if (last) x.next(Z::XS);
-          // what the next products wait for, asked while these are issued
-          a_seen = over(&S.ready[a.stage], a.phase);
-          if (last) x_seen = over(&S.x_full[x.stage], x.phase);
-          if (elect_one()) {
-#pragma unroll
-            for (int q = 0; q < Z::GS * kSteps; ++q) {
-              const int k = sub % kPer * (Z::GS * kSteps) + q;
-              product(to + q / kSteps * NT, at + q * 8, desc + (uint64_t)((k >> 2) * (Z::XBox >> 4) + (k & 3) * 2), idesc,
-                      q % kSteps > 0);
-            }
-            commit_to(done);
-            if (last) commit_to(x_done);
-          }
-          __syncwarp();
-        }
+        for (int q = 0; q < Z::GS * kSteps; ++q)
+          product(to + q / kSteps * NT, at + q * 8, desc + (uint64_t)((q >> 2) * (Z::XBox >> 4) + (q & 3) * 2), idesc, q % kSteps > 0);
+        commit_to(&S.done[a.stage]);
+        commit_to(&S.x_empty[x.stage]);
       }
+      __syncwarp();
+      a.skip(Z::Issuers, Z::Slots);
+      a_seen = over(&S.ready[a.stage], a.phase);
+      sub += Z::Issuers;
+      x.skip(sub / kPer, Z::XS);
+      sub %= kPer;
     }
   }
   __syncwarp();
@@ -518,8 +563,9 @@ template <int NT, int GROUP>
 cudaError_t allow() {
   using Z = Shape<NT, GROUP>;
   static_assert(linear_smem<Z>() <= 232448, "shared memory of a CTA");
-  static_assert(Z::Slots >= 2 && Z::DColumn + Z::Slots * Z::DCols <= (int)kTcColumns, "tensor memory");
-  static_assert(Z::Subs % Z::Teams == 0 || Z::Parts == 2, "slots of a stage");
+  static_assert(Z::Slots % Z::Teams == 0 && Z::Slots % Z::Issuers == 0 && Z::WS % Z::Skip == 0 &&
+                (Z::XK > Z::SlotK || Z::XS % Z::Issuers == 0), "phases");
+  static_assert(Z::Slots >= Z::Teams && Z::DColumn + Z::Slots * Z::DCols <= (int)kTcColumns, "tensor memory");
   static_assert(Z::Ring >= NT * kRows * 4, "parts of a split tile");
   return cudaFuncSetAttribute(linear_kernel<NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)linear_smem<Z>());
 }
