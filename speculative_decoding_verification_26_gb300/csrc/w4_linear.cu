@@ -155,17 +155,16 @@ __device__ __forceinline__ uint4 shared16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// a word of 8 weights as bf16 pairs of q - z; less = 128 + z in both halves.  128 + q is q in the
-// last bits of the mantissa; the difference is exact.
-__device__ __forceinline__ void unpack8(uint32_t* out, uint32_t word, __nv_bfloat162 less) {
+// 128 + z as bf16 in both halves
+__device__ __forceinline__ uint32_t less_of(uint32_t z) { return (0x4300u | z) * 0x10001u; }
+// a word of 8 weights as bf16 pairs of q - z; less = less_of(z).  128 + q is q in the last bits of
+// the mantissa; the difference is exact.
+__device__ __forceinline__ void unpack8(uint32_t* out, uint32_t word, uint32_t less) {
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const uint32_t u = (word >> 4 * p & 0x000F000Fu) | 0x43004300u;
-    __nv_bfloat162 x;
-    memcpy(&x, &u, 4);
-    x = __hsub2(x, less);
-    memcpy(out + p, &x, 4);
-  }
+  for (int p = 0; p < 4; ++p)
+    asm("{\n .reg .b32 u;\n lop3.b32 u, %1, 0x000F000F, 0x43004300, 0xEA;\n sub.rn.bf16x2 %0, u, %2;\n}\n"
+        : "=r"(out[p])
+        : "r"(word >> 4 * p), "r"(less));
 }
 
 // acc[c] += s * column c of a group's sums
@@ -206,7 +205,7 @@ struct Plan {
   __device__ __forceinline__ int col0(int item) const { return item / row_tiles * kRows; }
 };
 
-template <int NT, int GROUP>
+template <int NT, int GROUP, bool ZERO>
 __global__ void __launch_bounds__(Shape<NT, GROUP>::Threads, 1)
 linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps M, int split) {
   using Z = Shape<NT, GROUP>;
@@ -247,57 +246,65 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   tc_fence_after();
   const uint32_t tmem = S.tmem;
 
+  const int tiles = item0 < plan.items ? (plan.items - 1 - item0) / plan.step + 1 : 0;
   float acc[Z::Columns];
   bool ok = true;
   if (warp < Z::UnpackWarps) {
     const int quarter = warp & 3, team = warp >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    // the team's next slot of weights, and where it goes
     RingAt w, a;
-    int item = item0, stage = 0, turn = 0;
-    const auto skip = [&](int stages) {
-      for (int i = 0; i < stages; ++i) {
-        w.next(Z::WS);
-        if (++stage == plan.stages) {
-          stage = 0;
+    w.skip(team / Z::Sharing, Z::WS);
+    a.skip(team, Z::Slots);
+    int turn = 0, stage = team / Z::Sharing, item = item0;
+    // chunk first + c of the row's eight, at (first + c) ^ (row % 8) times 16 bytes
+    const uint32_t mine = row * 128 + (((team % Z::Sharing * Z::Chunks) ^ (row & 7)) << 4);
+    uint4 v[Z::Chunks];
+    const auto weights = [&] {
+      const uint32_t at = (w_ring + w.stage * kWeightStage + mine) ^ (Z::Turns > 1 ? turn * (Z::Sharing * Z::Chunks * 16) : 0);
+#pragma unroll
+      for (int c = 0; c < Z::Chunks; ++c) v[c] = shared16(at ^ (c * 16));
+    };
+    uint32_t less[ZERO ? Z::Chunks : 1];
+    if constexpr (!ZERO) less[0] = less_of(8);
+    const uint8_t* zero = nullptr;
+    const auto zeros = [&] {                 // of the next slot
+      if constexpr (ZERO) {
+        const int at = (plan.first + stage) * kStageK + 32 * Z::Chunks * (team % Z::Sharing + turn * Z::Sharing);
+#pragma unroll
+        for (int c = 0; c < Z::Chunks; ++c) less[c] = zero[min((at + 32 * c) / GROUP, P.groups - 1)];
+      }
+    };
+    const auto tile = [&] {
+      if constexpr (ZERO) {
+        while (stage >= plan.stages) {
+          stage -= plan.stages;
           item += plan.step;
         }
+        zero = P.zero + (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
+        ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
       }
     };
-    skip(team / Z::Sharing);
-    a.skip(team, Z::Slots);
-    uint32_t z[Z::Chunks];
-    uint4 v[Z::Chunks];
-    // the current slot's zero points and weights: chunk c of the slot is chunk first + c of the row's eight
-    const auto zeros = [&](int first) {
-      if (!P.zero) return;
-      const uint8_t* p = P.zero + (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
-#pragma unroll
-      for (int c = 0; c < Z::Chunks; ++c) z[c] = p[min(((plan.first + stage) * kStageK + 32 * (first + c)) / GROUP, P.groups - 1)];
-    };
-    const auto weights = [&](int first) {
-      const uint32_t at = w_ring + w.stage * kWeightStage + row * 128;
-#pragma unroll
-      for (int c = 0; c < Z::Chunks; ++c) v[c] = shared16(at + (uint32_t)(((first + c) ^ (row & 7)) << 4));
-    };
-    const auto first = [&] { return (team % Z::Sharing + turn * Z::Sharing) * Z::Chunks; };
-#pragma unroll
-    for (int c = 0; c < Z::Chunks; ++c) z[c] = 8;
-    if (item < plan.items) {
-      zeros(first());
+    int left = (tiles * plan.stages - team / Z::Sharing + Z::Skip - 1) / Z::Skip * Z::Turns;       // the team's slots
+    if (left > 0) {
+      tile();
+      zeros();
       ok = wait_for(&S.w_full[w.stage], w.phase, waits);
-      weights(first());
+      weights();
     }
-    while (ok && item < plan.items) {
+    while (ok && left > 0) {
       uint64_t* const emptied = &S.w_empty[w.stage];
-      const bool last = ++turn == Z::Turns;
-      if (P.zero && stage < Z::Skip) ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
       const uint32_t a_seen = over(&S.done[a.stage], a.phase ^ 1);
-      uint32_t w_seen = 1;
+      const bool last = Z::Turns == 1 || ++turn == Z::Turns;     // of the stage
       if (last) {
         turn = 0;
-        skip(Z::Skip);
-        w_seen = over(&S.w_full[w.stage], w.phase);
+        w.skip(Z::Skip, Z::WS);
+        if constexpr (ZERO) {
+          stage += Z::Skip;
+          if (stage >= plan.stages && left > 1) tile();
+        }
       }
+      const uint32_t w_seen = over(&S.w_full[w.stage], w.phase);
       const uint32_t to = lanes + a.stage * Z::ACols;
       constexpr int kAtOnce = Z::Chunks < 2 ? 1 : 2;
 #pragma unroll
@@ -305,9 +312,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         uint32_t r[16 * kAtOnce];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-          const uint32_t less = (0x4300u | z[c + u]) * 0x10001u;
-          __nv_bfloat162 l;
-          memcpy(&l, &less, 4);
+          const uint32_t l = ZERO ? less_of(less[ZERO ? c + u : 0]) : less[0];
           unpack8(r + 16 * u, v[c + u].x, l);
           unpack8(r + 16 * u + 4, v[c + u].y, l);
           unpack8(r + 16 * u + 8, v[c + u].z, l);
@@ -320,10 +325,10 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         if constexpr (kAtOnce == 1) store16(to, r);
         else store32(to + 16 * c, r);
       }
-      if (ok && item < plan.items) {         // the next slot's, while the stores go out
-        zeros(first());
+      if (ok && --left > 0) {                // the next slot's, while the stores go out
+        zeros();
         ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen);
-        weights(first());
+        weights();
       }
       if (!ok) break;
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -457,7 +462,6 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     x.skip(mine / kPer, Z::XS);
     int sub = mine % kPer;
     uint32_t a_seen = 0;
-    const int tiles = item0 < plan.items ? (plan.items - 1 - item0) / plan.step + 1 : 0;
     for (long long slot = mine, slots = (long long)tiles * plan.stages * Z::Subs; slot < slots; slot += Z::Issuers) {
       if (!(ok = wait_for(&S.x_full[x.stage], x.phase, waits) && wait_for(&S.ready[a.stage], a.phase, waits, a_seen))) break;
       tc_fence_after();
@@ -534,7 +538,7 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int size, const void* p,
 }
 
 template <int NT, int GROUP>
-cudaError_t run(const W4Params& P, int nsm, cudaStream_t s) {
+cudaError_t launch(const W4Params& P, int nsm, cudaStream_t s) {
   W4Maps M;
   if (!encode(&M.weight, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, P.packed, P.H / 2, P.V, kRows) ||
       !encode(&M.hidden, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, P.hidden, P.H, P.n, NT))
@@ -553,11 +557,12 @@ cudaError_t run(const W4Params& P, int nsm, cudaStream_t s) {
   attr[0].val.clusterDim = {(unsigned)split, 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_kernel<NT, GROUP>, P, M, split);
+  return P.zero ? cudaLaunchKernelEx(&cfg, linear_kernel<NT, GROUP, true>, P, M, split)
+                : cudaLaunchKernelEx(&cfg, linear_kernel<NT, GROUP, false>, P, M, split);
 }
 template <int NT>
 cudaError_t of_group(const W4Params& P, int nsm, cudaStream_t s) {
-  return P.group == 128 ? run<NT, 128>(P, nsm, s) : P.group == 64 ? run<NT, 64>(P, nsm, s) : run<NT, 32>(P, nsm, s);
+  return P.group == 128 ? launch<NT, 128>(P, nsm, s) : P.group == 64 ? launch<NT, 64>(P, nsm, s) : launch<NT, 32>(P, nsm, s);
 }
 template <int NT, int GROUP>
 cudaError_t allow() {
@@ -567,7 +572,9 @@ cudaError_t allow() {
                 (Z::XK > Z::SlotK || Z::XS % Z::Issuers == 0), "phases");
   static_assert(Z::Slots >= Z::Teams && Z::DColumn + Z::Slots * Z::DCols <= (int)kTcColumns, "tensor memory");
   static_assert(Z::Ring >= NT * kRows * 4, "parts of a split tile");
-  return cudaFuncSetAttribute(linear_kernel<NT, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)linear_smem<Z>());
+  const int smem = (int)linear_smem<Z>();
+  const cudaError_t e = cudaFuncSetAttribute(linear_kernel<NT, GROUP, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(linear_kernel<NT, GROUP, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 template <int NT>
 cudaError_t allow_all() {
