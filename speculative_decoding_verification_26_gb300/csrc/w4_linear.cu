@@ -167,6 +167,18 @@ __device__ __forceinline__ void unpack8(uint32_t* out, uint32_t word, uint32_t l
         : "r"(word >> 4 * p), "r"(less));
 }
 
+// A scale on its way, and as a number once it is needed.  Both stay where they are written: a
+// conversion that the compiler moves up to its load makes every turn wait for memory (500 clocks).
+__device__ __forceinline__ uint32_t scale_bits(const __nv_bfloat16* p) {
+  uint32_t v;
+  asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float scale_of_bits(uint32_t v) {
+  float f;
+  asm volatile("shl.b32 %0, %1, 16;" : "=f"(f) : "r"(v));
+  return f;
+}
 // acc[c] += s * column c of a group's sums
 template <int N>
 __device__ __forceinline__ void add_unit(float (&acc)[N], uint32_t from, float s) {
@@ -348,27 +360,42 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     if (lane < Z::Slots) mbar_arrive(&S.ready[lane]);            // nothing to take of the first use
     RingAt d;
     uint32_t seen = 0;
+    const int g0 = plan.first * (kStageK / GROUP), g1 = (plan.first + plan.stages) * (kStageK / GROUP);
+    constexpr int kBoth = Z::Columns * Z::GS <= 16 ? 2 : 1, kGroups = kBoth * Z::GS;      // slots taken at once
+    constexpr int kAhead = kGroups <= 2 ? 2 : 1;                 // times their groups' scales are on their way
+    // scales are asked for in the order of use, over the ends of tiles
+    uint32_t next[kAhead][kGroups];
+    int ask_item = item0, ask = g0;
+    const __nv_bfloat16* scale = nullptr;
+    const auto seek = [&] {
+      scale = P.scale + (size_t)min(plan.col0(ask_item) + row, P.V - 1) * P.groups;
+      ahead(P.scale, (size_t)min(plan.col0(ask_item + plan.step) + row, P.V - 1) * P.groups, P.groups);
+    };
+    const auto fetch = [&](uint32_t (&to)[kGroups]) {
+#pragma unroll
+      for (int i = 0; i < kGroups; ++i) to[i] = scale_bits(scale + min(ask + i, P.groups - 1));
+      if ((ask += kGroups) >= g1) {
+        ask = g0;
+        ask_item += plan.step;
+        seek();
+      }
+    };
+    seek();
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) fetch(next[u]);
     for (int item = item0; item < plan.items; item += plan.step) {
       const int v = plan.col0(item) + row;
-      const __nv_bfloat16* scale = P.scale + (size_t)min(v, P.V - 1) * P.groups;
-      ahead(P.scale, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
 #pragma unroll
       for (int c = 0; c < Z::Columns; ++c) acc[c] = 0.f;
-      const int g0 = plan.first * (kStageK / GROUP), g1 = (plan.first + plan.stages) * (kStageK / GROUP);
-      constexpr int kBoth = Z::Columns * Z::GS <= 16 ? 2 : 1, kGroups = kBoth * Z::GS;      // slots taken at once
-      constexpr int kAhead = kGroups <= 2 ? 2 : 1;                 // times their groups' scales are on their way
-      __nv_bfloat16 next[kAhead][kGroups];
-#pragma unroll
-      for (int i = 0; i < kAhead * kGroups; ++i) next[i / kGroups][i % kGroups] = scale[min(g0 + i, P.groups - 1)];
       for (int g = g0; ok && g < g1; g += kGroups) {
         float s[kGroups];
 #pragma unroll
         for (int i = 0; i < kGroups; ++i) {
-          s[i] = __bfloat162float(next[0][i]);
+          s[i] = scale_of_bits(next[0][i]);
 #pragma unroll
           for (int u = 1; u < kAhead; ++u) next[u - 1][i] = next[u][i];
-          next[kAhead - 1][i] = scale[min(g + kAhead * kGroups + i, P.groups - 1)];
         }
+        fetch(next[kAhead - 1]);
         uint32_t from[kBoth];
         uint64_t* taken[kBoth];
 #pragma unroll
@@ -414,14 +441,18 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         for (int c = 0; c < Z::Columns; ++c) acc[c] = NAN;
       }
       if (split == 1 && v < P.V) {
-        const int r0 = plan.row0(item, NT) + part * Z::Columns;
+        const int r0 = plan.row0(item, NT) + part * Z::Columns, rows = P.n - r0;
+        const size_t o = (size_t)r0 * P.V + v;
+        if (P.dtype == SPEC_BF16) {
+          __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(P.out) + o;
 #pragma unroll
-        for (int c = 0; c < Z::Columns; ++c) {
-          if (r0 + c < P.n) {
-            const size_t o = (size_t)(r0 + c) * P.V + v;
-            if (P.dtype == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(P.out)[o] = __float2bfloat16_rn(acc[c]);
-            else reinterpret_cast<float*>(P.out)[o] = acc[c];
-          }
+          for (int c = 0; c < Z::Columns; ++c, to += P.V)
+            if (c < rows) *to = __float2bfloat16_rn(acc[c]);
+        } else {
+          float* to = reinterpret_cast<float*>(P.out) + o;
+#pragma unroll
+          for (int c = 0; c < Z::Columns; ++c, to += P.V)
+            if (c < rows) *to = acc[c];
         }
       }
     }
