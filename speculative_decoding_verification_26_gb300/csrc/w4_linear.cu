@@ -34,24 +34,23 @@ constexpr int kMaxSplit = 8;
 
 template <int NT, int GROUP>
 struct Shape {
-  // warps: teams of four unpack, each taking every Teams-th slot
-  static constexpr int Teams = NT <= 32 ? 4 : 2, UnpackWarps = 4 * Teams, SumWarps = NT >= 64 ? 8 : 4;
-  static constexpr int Columns = NT / (SumWarps / 4);            // of a thread
-  static constexpr int Issuers = 2, Threads = (UnpackWarps + SumWarps + 2 + Issuers) * 32;   // an issuer takes every other slot
-  // a slot: whole groups, at most 128 k; as many as leave tensor memory for a slot of each team.
-  // Whoever takes every n-th slot, stage or copy of a ring has a ring of a multiple of n: it waits
-  // for every phase of the barriers that it waits for, and so never takes one for another.
+  // a slot: whole groups, as many k as leave tensor memory for two slots (the sums of a group of a slot
+  // take NT columns, the weights of 2 k one)
   static constexpr int cost(int k) { return k / 2 + k / GROUP * NT; }
-  static constexpr int SlotK = GROUP >= 128 || Teams * cost(128) <= (int)kTcColumns ? 128
-                               : GROUP >= 64 || Teams * cost(64) <= (int)kTcColumns ? 64 : 32;
+  static constexpr int SlotK = 2 * cost(256) <= (int)kTcColumns ? 256 : GROUP >= 128 || 2 * cost(128) <= (int)kTcColumns ? 128
+                               : GROUP >= 64 || 2 * cost(64) <= (int)kTcColumns ? 64 : 32;
   static constexpr int GS = SlotK / GROUP, Subs = kStageK / SlotK, ACols = SlotK / 2, DCols = GS * NT;
-  static constexpr int Fit = (int)kTcColumns / (ACols + DCols), Slots = (Fit < 6 ? Fit : 6) / Teams * Teams;
+  static constexpr int Fit = (int)kTcColumns / (ACols + DCols), Slots = NT == 128 || Fit < 3 ? 2 : 3;
   static constexpr int DColumn = Slots * ACols;                  // where the sums begin
   static constexpr int Chunks = SlotK / 32;                      // of 16 bytes of a row
-  static constexpr int Sharing = Teams < Subs ? Teams : Subs;    // teams that read a stage
-  static constexpr int Turns = Subs / Sharing, Skip = Teams / Sharing;   // of a team in a stage; stages to its next
-  static constexpr int WS = NT <= 32 ? 8 : NT == 64 ? 7 : 5;      // stages of weights
-  static constexpr int XK = NT == 128 ? 128 : 256, XS = NT == 16 ? 6 : NT == 32 ? 5 : NT == 64 ? 3 : 4;   // of hidden states
+  // warps: teams of four unpack, and take slots in turn, as the issuers do
+  static constexpr int Teams = Slots == 3 ? 3 : 2, UnpackWarps = 4 * Teams, Issuers = Slots == 3 ? 1 : 2;
+  static constexpr int Columns = NT == 128 ? 64 : NT < 32 ? NT : 32, SumWarps = 4 * NT / Columns;       // columns of a thread
+  static constexpr int Threads = (UnpackWarps + SumWarps + 2 + Issuers) * 32;
+  // Whoever takes every n-th slot, stage or copy of a ring has a ring of a multiple of n: it waits
+  // for every phase of the barriers that it waits for, and so never takes one for another.
+  static constexpr int WS = NT > 16 ? 6 : Teams == 3 ? 9 : 8;     // stages of weights
+  static constexpr int XK = NT == 128 ? 128 : 256, XS = NT <= 32 ? 6 : 4;   // of hidden states
   static constexpr int XSlot = NT * XK * 2, XBox = NT * 128;     // bytes
   static constexpr int Ring = WS * kWeightStage + XS * XSlot;
 };
@@ -243,7 +242,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
 
   if (threadIdx.x == 0) {
     S.failed = 0;
-    for (int i = 0; i < Z::WS; ++i) { mbar_init(&S.w_full[i], 1); mbar_init(&S.w_empty[i], 4 * Z::Sharing); }
+    for (int i = 0; i < Z::WS; ++i) { mbar_init(&S.w_full[i], 1); mbar_init(&S.w_empty[i], 4 * Z::Subs); }
     for (int i = 0; i < Z::XS; ++i) { mbar_init(&S.x_full[i], 1); mbar_init(&S.x_empty[i], Z::XK / Z::SlotK); }
     for (int i = 0; i < Z::Slots; ++i) { mbar_init(&S.ready[i], 4 + Z::SumWarps); mbar_init(&S.done[i], 1); }
     fence_mbar_init();
@@ -264,59 +263,57 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   if (warp < Z::UnpackWarps) {
     const int quarter = warp & 3, team = warp >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    // the team's next slot of weights, and where it goes
+    // the team's next slot: `sub` of a stage, and where it goes
     RingAt w, a;
-    w.skip(team / Z::Sharing, Z::WS);
+    int sub = team, stage = 0, item = item0;
+    const auto whole = [&] {                 // sub back into a stage
+#pragma unroll
+      for (int i = 0; i < (Z::Teams + Z::Subs - 1) / Z::Subs; ++i) {
+        if (sub >= Z::Subs) {
+          sub -= Z::Subs;
+          ++stage;
+          w.next(Z::WS);
+        }
+      }
+    };
+    whole();
     a.skip(team, Z::Slots);
-    int turn = 0, stage = team / Z::Sharing, item = item0;
-    // chunk first + c of the row's eight, at (first + c) ^ (row % 8) times 16 bytes
-    const uint32_t mine = row * 128 + (((team % Z::Sharing * Z::Chunks) ^ (row & 7)) << 4);
     uint4 v[Z::Chunks];
+    // chunk c of a row's eight lies at c ^ (row % 8) times 16 bytes
+    const uint32_t mine = w_ring + row * 128 + ((row & 7) << 4);
     const auto weights = [&] {
-      const uint32_t at = (w_ring + w.stage * kWeightStage + mine) ^ (Z::Turns > 1 ? turn * (Z::Sharing * Z::Chunks * 16) : 0);
+      const uint32_t at = (mine + w.stage * kWeightStage) ^ (sub * (Z::Chunks * 16));
 #pragma unroll
       for (int c = 0; c < Z::Chunks; ++c) v[c] = shared16(at ^ (c * 16));
     };
     uint32_t less[ZERO ? Z::Chunks : 1];
     if constexpr (!ZERO) less[0] = less_of(8);
     const uint8_t* zero = nullptr;
-    const auto zeros = [&] {                 // of the next slot
-      if constexpr (ZERO) {
-        const int at = (plan.first + stage) * kStageK + 32 * Z::Chunks * (team % Z::Sharing + turn * Z::Sharing);
+    const auto seek = [&] {                  // the tile of the next slot
+      while (stage >= plan.stages) {
+        stage -= plan.stages;
+        item += plan.step;
+      }
+      zero = P.zero + (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
+      ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
+    };
+    const auto zeros = [&] {
+      const int at = (plan.first + stage) * kStageK + 32 * Z::Chunks * sub;
 #pragma unroll
-        for (int c = 0; c < Z::Chunks; ++c) less[c] = zero[min((at + 32 * c) / GROUP, P.groups - 1)];
-      }
+      for (int c = 0; c < Z::Chunks; ++c) less[ZERO ? c : 0] = zero[min((at + 32 * c) / GROUP, P.groups - 1)];
     };
-    const auto tile = [&] {
-      if constexpr (ZERO) {
-        while (stage >= plan.stages) {
-          stage -= plan.stages;
-          item += plan.step;
-        }
-        zero = P.zero + (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
-        ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
-      }
-    };
-    int left = (tiles * plan.stages - team / Z::Sharing + Z::Skip - 1) / Z::Skip * Z::Turns;       // the team's slots
+    int left = (tiles * plan.stages * Z::Subs - team + Z::Teams - 1) / Z::Teams;      // the team's slots
     if (left > 0) {
-      tile();
-      zeros();
+      if constexpr (ZERO) {
+        seek();
+        zeros();
+      }
       ok = wait_for(&S.w_full[w.stage], w.phase, waits);
       weights();
     }
     while (ok && left > 0) {
       uint64_t* const emptied = &S.w_empty[w.stage];
       const uint32_t a_seen = over(&S.done[a.stage], a.phase ^ 1);
-      const bool last = Z::Turns == 1 || ++turn == Z::Turns;     // of the stage
-      if (last) {
-        turn = 0;
-        w.skip(Z::Skip, Z::WS);
-        if constexpr (ZERO) {
-          stage += Z::Skip;
-          if (stage >= plan.stages && left > 1) tile();
-        }
-      }
-      const uint32_t w_seen = over(&S.w_full[w.stage], w.phase);
       const uint32_t to = lanes + a.stage * Z::ACols;
       constexpr int kAtOnce = Z::Chunks < 2 ? 1 : 2;
 #pragma unroll
@@ -337,20 +334,26 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         if constexpr (kAtOnce == 1) store16(to, r);
         else store32(to + 16 * c, r);
       }
-      if (ok && --left > 0) {                // the next slot's, while the stores go out
-        zeros();
-        ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen);
-        weights();
-      }
       if (!ok) break;
+      sub += Z::Teams;
+      whole();
+      const uint32_t w_seen = over(&S.w_full[w.stage], w.phase);
+      if (ZERO && --left > 0) {
+        if (stage >= plan.stages) seek();
+        zeros();
+      }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(&S.ready[a.stage]);
-        // only here: the loads from the stage are sure to be done once what they gave has been
+        // only here: the loads of a slot are sure to be done once what they gave has been
         // stored (an arrival before the stores has let the next copy into the stage under them)
-        if (last) mbar_arrive(emptied);
+        mbar_arrive(emptied);
+      }
+      if ((ZERO ? left : --left) > 0) {
+        if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen))) break;
+        weights();
       }
       a.skip(Z::Teams, Z::Slots);
     }
@@ -361,7 +364,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     RingAt d;
     uint32_t seen = 0;
     const int g0 = plan.first * (kStageK / GROUP), g1 = (plan.first + plan.stages) * (kStageK / GROUP);
-    constexpr int kBoth = Z::Columns * Z::GS <= 16 ? 2 : 1, kGroups = kBoth * Z::GS;      // slots taken at once
+    constexpr int kBoth = Z::Columns * Z::GS <= 16 && Z::Slots >= 4 ? 2 : 1, kGroups = kBoth * Z::GS;      // slots taken at once
     constexpr int kAhead = kGroups <= 2 ? 2 : 1;                 // times their groups' scales are on their way
     // scales are asked for in the order of use, over the ends of tiles
     uint32_t next[kAhead][kGroups];
@@ -599,8 +602,8 @@ template <int NT, int GROUP>
 cudaError_t allow() {
   using Z = Shape<NT, GROUP>;
   static_assert(linear_smem<Z>() <= 232448, "shared memory of a CTA");
-  static_assert(Z::Slots % Z::Teams == 0 && Z::Slots % Z::Issuers == 0 && Z::WS % Z::Skip == 0 &&
-                (Z::XK > Z::SlotK || Z::XS % Z::Issuers == 0), "phases");
+  static_assert(Z::Slots % Z::Teams == 0 && Z::Slots % Z::Issuers == 0 && Z::WS * Z::Subs % Z::Teams == 0 &&
+                (Z::XK >= Z::Issuers * Z::SlotK || Z::XS % Z::Issuers == 0), "phases");
   static_assert(Z::Slots >= Z::Teams && Z::DColumn + Z::Slots * Z::DCols <= (int)kTcColumns, "tensor memory");
   static_assert(Z::Ring >= NT * kRows * 4, "parts of a split tile");
   const int smem = (int)linear_smem<Z>();
