@@ -3,13 +3,18 @@
 // Row i of request b is the row after the request's history and its draft tokens
 // y_0 .. y_{i-1}.  With c(v) the occurrences of v among the outputs (the history
 // behind the prompt, and those drafts), and v "seen" when it occurs anywhere,
-//   x <- seen ? (x > 0 ? x / rep : x rep) : x;   x <- x - c freq - [c > 0] pres;
+//   x <- seen ? (x > 0 ? x / rep : x rep) : x;   x <- x - (c freq + pres) where c > 0;
 //   x <- x + sum of the biases listed for v;     x <- -inf where the mask has 0,
 // in fp32, rounded once to the row's type.  Logits that nothing touches keep their bits.
 //
-// A CTA takes a range of the vocabulary for all R rows of a request: it counts the
+// A CTA takes a range of the vocabulary for all R rows of a request.  It counts the
 // history's tokens of its range in shared memory (whole numbers: the order of the
-// atomics does not matter) and goes over its part of the rows.
+// atomics does not matter) and lists those that anything touches.  It then goes over
+// its part of the rows in 16-byte vectors, which are copied and masked (in place: left
+// alone, or written without a read where the mask removes all of one), and last over
+// the listed tokens of each row, one logit each.  With both in one pass the code of a
+// touched logit, a vector's worth of it unrolled, did not fit the instruction cache:
+// 186 us for the batch of 64 x 8 x 151936 logits.  HBM bounds the passes over the rows.
 #include "rows.cuh"
 #include "serve.cuh"
 
@@ -17,143 +22,317 @@ namespace sv {
 namespace {
 
 constexpr int kAdjustThreads = 256;
-constexpr int kRange = 4096;                 // tokens of a CTA
-constexpr uint32_t kInPrompt = 0x80000000u;  // of a count: the token is in the prompt
+constexpr int kMaxRange = 4096, kMinRange = 1024;        // tokens of a CTA
+constexpr uint32_t kInPrompt = 0x80000000u, kInDraft = 0x40000000u, kTouched = 0x20000000u,
+                   kCount = 0x1FFFFFFFu;   // of a count word
 
-template <int DT>
-__device__ __forceinline__ void put_logit(unsigned char* row, int e, float x) {
-  if constexpr (DT == SPEC_BF16) reinterpret_cast<__nv_bfloat16*>(row)[e] = __float2bfloat16_rn(x);
-  else reinterpret_cast<float*>(row)[e] = x;
-}
-template <int DT>
-__device__ __forceinline__ void copy_logit(unsigned char* to, const unsigned char* from, int e) {
-  if constexpr (DT == SPEC_BF16) reinterpret_cast<uint16_t*>(to)[e] = reinterpret_cast<const uint16_t*>(from)[e];
-  else reinterpret_cast<uint32_t*>(to)[e] = reinterpret_cast<const uint32_t*>(from)[e];
-}
-
+// In shared memory: this, counts [range], biases [range] (with biases), the touched
+// tokens' places in the range.
 struct AdjustShared {
-  uint32_t count[kRange];
-  float bias[kRange];
-  uint32_t biased[kRange / 32];
   int draft[SPEC_MAX_G + 1];
-  int bad;
+  int bad, listed;
+  int pad[2];
+};
+__host__ __device__ constexpr size_t adjust_smem_bytes(int range, bool any, bool biases) {
+  return sizeof(AdjustShared) + (any ? (size_t)range * (biases ? 10 : 6) : 0);
+}
+
+struct Penalties {
+  float rep, freq, pres;
 };
 
+// A touched logit of row i; c is its count word.
+__device__ __forceinline__ float adjusted(float x, uint32_t c, int v, int i, const AdjustShared& S, const Penalties& p) {
+  uint32_t n = c & kCount;
+  bool seen = n != 0 || (c & kInPrompt) != 0;
+  if (c & kInDraft) {
+    for (int j = 0; j < i; ++j) n += S.draft[j] == v;
+    seen = seen || n != 0;
+  }
+  if (seen) x = x > 0.f ? __fdiv_rn(x, p.rep) : x * p.rep;
+  if (n != 0) x -= __fmaf_rn((float)n, p.freq, p.pres);
+  return x;
+}
+
+// whether v is among the drafts before row i
+__device__ __forceinline__ bool drafted(uint32_t c, int v, int i, const AdjustShared& S) {
+  bool yes = false;
+  if (c & kInDraft)
+    for (int j = 0; j < i; ++j) yes |= S.draft[j] == v;
+  return yes;
+}
+
 template <int DT>
-__global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const AdjustParams P, int splits) {
-  extern __shared__ __align__(16) unsigned char adjust_smem[];
-  AdjustShared& S = *reinterpret_cast<AdjustShared*>(adjust_smem);
-  const int b = blockIdx.x / splits, part = blockIdx.x % splits, t = threadIdx.x;
-  const int lo = part * kRange, hi = min(P.V, lo + kRange);
+struct Logit;
+template <>
+struct Logit<SPEC_BF16> {
+  using Bits = uint16_t;
+  static constexpr uint32_t kFull = 0xFF;
+  static __device__ __forceinline__ Bits pack(float x) { return __bfloat16_as_ushort(__float2bfloat16_rn(x)); }
+  static __device__ __forceinline__ float value(Bits b) { return __uint_as_float((uint32_t)b << 16); }
+};
+template <>
+struct Logit<SPEC_F32> {
+  using Bits = uint32_t;
+  static constexpr uint32_t kFull = 0xF;
+  static __device__ __forceinline__ Bits pack(float x) { return __float_as_uint(x); }
+  static __device__ __forceinline__ float value(Bits b) { return __uint_as_float(b); }
+};
 
-  if (t == 0) S.bad = 0;
-  for (int e = t; e < kRange; e += kAdjustThreads) { S.count[e] = 0; S.bias[e] = 0.f; }
-  for (int e = t; e < kRange / 32; e += kAdjustThreads) S.biased[e] = 0;
-  __syncthreads();
+__device__ __forceinline__ uint4 load_vec(const unsigned char* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ void store_vec(unsigned char* p, const uint4& v) {
+  asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
 
-  int bad = 0;
-  const int len = P.history_len ? P.history_len[b] : P.L, prompt = P.prompt_len ? P.prompt_len[b] : 0;
-  if (len < 0 || len > P.L || prompt < 0 || prompt > len) bad |= SPEC_ST_BAD_LENGTH;
-  else {
-    const int32_t* h = P.history + (size_t)b * P.L;
-    for (int e = t; e < len; e += kAdjustThreads) {
-      const int v = h[e];
-      if (v < -1 || v >= P.V) bad |= SPEC_ST_BAD_TOKEN;
-      else if (v >= lo && v < hi) {
-        if (e < prompt) atomicOr(&S.count[v - lo], kInPrompt);
-        else atomicAdd(&S.count[v - lo], 1u);
-      }
+// The bits of a vector's tokens that the mask allows; the vector starts at token v.
+template <int PER, bool ALIGNED>
+__device__ __forceinline__ uint32_t allowed(const uint32_t* mask, int v, uint32_t full) {
+  const uint32_t* m = mask + (v >> 5);
+  const int bit = v & 31;
+  if constexpr (ALIGNED) return __ldg(m) >> bit & full;
+  const uint32_t w0 = __ldg(m), w1 = bit + PER > 32 ? __ldg(m + 1) : 0;
+  return __funnelshift_r(w0, w1, bit) & full;
+}
+// Logits whose bit of `keep` is 0 become -inf.
+template <int DT>
+__device__ __forceinline__ void remove_others(uint4& x, uint32_t keep) {
+  uint32_t* const w = &x.x;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (DT == SPEC_BF16) {
+      const uint32_t gone = ~keep >> 2 * k & 3u, cover = (gone & 1u) * 0xFFFFu | (gone >> 1) * 0xFFFF0000u;
+      w[k] = (w[k] & ~cover) | (0xFF80FF80u & cover);
+    } else {
+      if (!(keep >> k & 1)) w[k] = 0xFF800000u;
     }
   }
+}
+
+// ALIGNED: every row starts on a 16-byte boundary.
+template <int DT, bool ALIGNED>
+__global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_constant__ AdjustParams P, int splits, int shift) {
+  using Lg = Logit<DT>;
+  using Bits = typename Lg::Bits;
+  constexpr int ES = RowType<DT>::ES, PER = RowType<DT>::PER;
+  extern __shared__ __align__(16) unsigned char adjust_smem[];
+  AdjustShared& S = *reinterpret_cast<AdjustShared*>(adjust_smem);
+  const int range = 1 << shift;
+  uint32_t* const count = reinterpret_cast<uint32_t*>(adjust_smem + sizeof(AdjustShared));
+  float* const bias = reinterpret_cast<float*>(count + range);
+  uint16_t* const list = reinterpret_cast<uint16_t*>(count + range * (P.biases > 0 ? 2 : 1));
+  const int b = blockIdx.x / splits, part = blockIdx.x % splits, t = threadIdx.x;
+  const int lo = part << shift, hi = min(P.V, lo + range);
+  const bool counts = P.L > 0 || P.D > 0, any = counts || P.biases > 0;
+
+  // what a request has that is out of its range; every CTA of it finds the same
+  int bad = 0;
+  const int len = P.history_len ? P.history_len[b] : P.L, prompt = P.prompt_len ? P.prompt_len[b] : 0;
+  const bool lengths = len >= 0 && len <= P.L && prompt >= 0 && prompt <= len;
+  if (!lengths) bad |= SPEC_ST_BAD_LENGTH;
   const int most = P.D > 0 ? P.D : P.R - 1;
   int gamma = P.gamma ? P.gamma[b] : most;
   if (gamma < 0 || gamma > most) { bad |= SPEC_ST_BAD_GAMMA; gamma = most; }
-  if (t < P.D) {
-    const int v = t < gamma ? P.draft[(size_t)b * P.D + t] : -1;
-    if (v < -1 || v >= P.V) bad |= SPEC_ST_BAD_TOKEN;
-    S.draft[t] = v;
-  }
-  const float rep = P.repetition ? P.repetition[b] : 1.f, freq = P.frequency ? P.frequency[b] : 0.f,
-              pres = P.presence ? P.presence[b] : 0.f;
-  if (!(rep > 0.f) || !isfinite(rep) || !isfinite(freq) || !isfinite(pres)) bad |= SPEC_ST_BAD_PENALTY;
-  if (t < 32) {
-    // biases of one token are added in the order of the list: a warp takes 32 at a
-    // time, the first lane of a token its sum
-    for (int e0 = 0; e0 < P.biases; e0 += 32) {
-      const int e = e0 + t;
-      int v = -1;
-      float x = 0.f;
-      if (e < P.biases) {
-        v = P.bias_index[(size_t)b * P.biases + e];
-        x = P.bias_value[(size_t)b * P.biases + e];
+  Penalties p;
+  p.rep = P.repetition ? P.repetition[b] : 1.f;
+  p.freq = P.frequency ? P.frequency[b] : 0.f;
+  p.pres = P.presence ? P.presence[b] : 0.f;
+  if (!(p.rep > 0.f) || !isfinite(p.rep) || !isfinite(p.freq) || !isfinite(p.pres)) bad |= SPEC_ST_BAD_PENALTY;
+
+  if (any) {
+    if (t == 0) S.bad = S.listed = 0;
+    // (the counts of a request without history or drafts are read for its biases)
+    for (int e = t; e < range; e += kAdjustThreads) count[e] = 0;
+    if (P.biases > 0)
+      for (int e = t; e < range; e += kAdjustThreads) bias[e] = 0.f;
+    __syncthreads();
+    const auto touch = [&](int at, uint32_t old) {       // old: its count word before
+      if (old & (kTouched | kInPrompt | kInDraft | kCount)) return;
+      list[atomicAdd(&S.listed, 1)] = (uint16_t)at;
+    };
+    if (lengths) {
+      const int32_t* h = P.history + (size_t)b * P.L;
+      const auto told = [&](int e, int v) {
         if (v < -1 || v >= P.V) bad |= SPEC_ST_BAD_TOKEN;
-        if (v != -1 && !(x < INFINITY)) bad |= SPEC_ST_BAD_PENALTY;
+        else if (v >= lo && v < hi) {
+          touch(v - lo, e < prompt ? atomicOr(&count[v - lo], kInPrompt) : atomicAdd(&count[v - lo], 1u));
+        }
+      };
+      int e = t;
+      for (; e + 3 * kAdjustThreads < len; e += 4 * kAdjustThreads) {
+        int v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[u] = __ldg(h + e + u * kAdjustThreads);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) told(e + u * kAdjustThreads, v[u]);
       }
-      const bool mine = v >= lo && v < hi;
-      const uint32_t same = __match_any_sync(0xffffffffu, v);
-      float sum = mine ? S.bias[v - lo] : 0.f;
-      for (int k = 0; k < 32; ++k) {
-        const float y = __shfl_sync(0xffffffffu, x, k);
-        if (same >> k & 1) sum += y;
-      }
-      if (mine && (same & ((1u << t) - 1)) == 0) {
-        S.bias[v - lo] = sum;
-        atomicOr(&S.biased[(v - lo) >> 5], 1u << ((v - lo) & 31));
-      }
-      __syncwarp();
+      for (; e < len; e += kAdjustThreads) told(e, __ldg(h + e));
     }
+    if (t < P.D) {
+      const int v = t < gamma ? P.draft[(size_t)b * P.D + t] : -1;
+      S.draft[t] = v;
+      if (v < -1 || v >= P.V) bad |= SPEC_ST_BAD_TOKEN;
+      else if (v >= lo && v < hi) touch(v - lo, atomicOr(&count[v - lo], kInDraft));
+    }
+    if (t >= kAdjustThreads - 32) {
+      // biases of one token are added in the order of the list: the last warp takes 32 at a
+      // time, the first lane of a token its sum
+      const int lane = t & 31;
+      for (int e0 = 0; e0 < P.biases; e0 += 32) {
+        const int e = e0 + lane;
+        int v = -1;
+        float x = 0.f;
+        if (e < P.biases) {
+          v = P.bias_index[(size_t)b * P.biases + e];
+          x = P.bias_value[(size_t)b * P.biases + e];
+          if (v < -1 || v >= P.V) bad |= SPEC_ST_BAD_TOKEN;
+          if (v != -1 && !(x < INFINITY)) bad |= SPEC_ST_BAD_PENALTY;
+        }
+        const bool mine = v >= lo && v < hi;
+        if (__any_sync(0xffffffffu, mine)) {
+          const uint32_t same = __match_any_sync(0xffffffffu, mine ? v : -1 - lane);
+          const bool leads = mine && (same & ((1u << lane) - 1)) == 0;
+          float sum = mine ? bias[v - lo] + x : 0.f;
+          if (__any_sync(0xffffffffu, mine && same != 1u << lane)) {
+            sum = mine ? bias[v - lo] : 0.f;
+            for (int k = 0; k < 32; ++k) {
+              const float y = __shfl_sync(0xffffffffu, x, k);
+              if (same >> k & 1) sum += y;
+            }
+          }
+          __syncwarp();
+          if (leads) {
+            bias[v - lo] = sum;
+            touch(v - lo, atomicOr(&count[v - lo], kTouched));
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (bad) atomicOr(&S.bad, bad);
+    __syncthreads();
+    bad = S.bad;
   }
-  if (bad) atomicOr(&S.bad, bad);
-  __syncthreads();
-  bad = S.bad;
   if (part == 0 && t == 0 && P.status) P.status[b] = bad;
 
   const int W = (P.V + 31) / 32, rows = min(P.R, gamma + 1);
-  constexpr int ES = RowType<DT>::ES;
-  for (int i = 0; i < rows; ++i) {
-    const size_t r = (size_t)b * P.R + i;
-    const unsigned char* in = P.in + r * P.V * ES;
-    unsigned char* out = P.out + r * P.V * ES;
-    for (int v = lo + t; v < hi; v += kAdjustThreads) {
-      uint32_t c = S.count[v - lo];
-      if (!bad) {
-        for (int j = 0; j < i && j < P.D; ++j) c += S.draft[j] == v;
-        if (P.mask && !(P.mask[r * W + (v >> 5)] >> (v & 31) & 1)) {
-          put_logit<DT>(out, v, -INFINITY);
-          continue;
-        }
-        const bool biased = S.biased[(v - lo) >> 5] >> ((v - lo) & 31) & 1;
-        if (c != 0 || biased) {
-          float x = row_logit<DT>(in, v);
-          if (c != 0) {
-            x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
-            c &= ~kInPrompt;
-            if (c != 0) x -= __fmaf_rn((float)c, freq, pres);
+  const bool apart = P.out != P.in, marks = any && !bad, masks = P.mask && !bad;
+  if (!apart && !marks && !masks) return;
+  const uint32_t* const mask = P.mask + (masks ? (size_t)b * P.R * W : 0);
+  const size_t first = (size_t)b * P.R * P.V + lo, row_bytes = (size_t)P.V * ES;        // element of row 0
+  const unsigned char* const in0 = P.in + first * ES;
+  unsigned char* const out0 = P.out + first * ES;
+  const int size = hi - lo;
+
+  if (apart || masks) {
+    // one logit of row i, at lo + at
+    const auto single = [&](int i, int at) {
+      Bits* out = reinterpret_cast<Bits*>(out0 + i * row_bytes) + at;
+      if (masks && !(mask[(size_t)i * W + ((lo + at) >> 5)] >> ((lo + at) & 31) & 1)) *out = Lg::pack(-INFINITY);
+      else if (apart) *out = reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at];
+    };
+    if (!ALIGNED && ((reinterpret_cast<uintptr_t>(P.in) ^ reinterpret_cast<uintptr_t>(P.out)) & 15)) {
+      for (int i = 0; i < rows; ++i)
+        for (int at = t; at < size; at += kAdjustThreads) single(i, at);
+    } else {
+      // vector k of kRows rows at a time; with fewer vectors than threads, rows side by side
+      constexpr int kRows = 4;
+      const int vecs = range / PER, abreast = vecs < kAdjustThreads ? vecs : kAdjustThreads;
+      const auto head_of = [&](int i) { return ALIGNED ? 0 : (int)(-(reinterpret_cast<uintptr_t>(in0) + i * row_bytes) & 15) / ES; };
+      for (int k = t & (abreast - 1); k * PER < size; k += abreast) {
+        for (int i0 = t / abreast * kRows; i0 < rows; i0 += kAdjustThreads / abreast * kRows) {
+          uint4 x[kRows];
+          uint32_t keep[kRows];
+          int at[kRows];
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            at[r] = -1;
+            keep[r] = Lg::kFull;
+            if (i0 + r >= rows) continue;
+            const int a = head_of(i0 + r) + k * PER;
+            if (a + PER > size) continue;
+            at[r] = a;
+            if (apart) x[r] = load_vec(in0 + (i0 + r) * row_bytes + (size_t)a * ES);
+            if (masks) keep[r] = allowed<PER, ALIGNED>(mask + (size_t)(i0 + r) * W, lo + a, Lg::kFull);
           }
-          if (biased) x += S.bias[v - lo];
-          put_logit<DT>(out, v, x);
-          continue;
+          if (!apart) {
+            // in place: nothing to do, or nothing to read
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) {
+              if (keep[r] == Lg::kFull) at[r] = -1;
+              x[r] = make_uint4(0, 0, 0, 0);
+              if (at[r] >= 0 && keep[r] != 0) x[r] = load_vec(in0 + (i0 + r) * row_bytes + (size_t)at[r] * ES);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < kRows; ++r) {
+            if (at[r] < 0) continue;
+            if (keep[r] != Lg::kFull) remove_others<DT>(x[r], keep[r]);
+            store_vec(out0 + (i0 + r) * row_bytes + (size_t)at[r] * ES, x[r]);
+          }
         }
       }
-      if (out != in) copy_logit<DT>(out, in, v);
+      // the ends of a row's part, fewer than PER logits each
+      for (int item = t; item < rows * 2 * PER; item += kAdjustThreads) {
+        const int i = item / (2 * PER), e = item % (2 * PER), head = min(head_of(i), size);
+        const int at = e < PER ? e : head + (size - head) / PER * PER + e - PER;
+        if (e < PER ? e < head : at < size) single(i, at);
+      }
     }
+  }
+  if (!marks) return;
+  __syncthreads();
+  const int listed = S.listed;
+  if (listed == 0) return;
+  // (row, token): the rows as they came in hold the logits, in place too: a mask's place is not read
+  for (int item = t; item < listed * rows; item += kAdjustThreads) {
+    const int i = item / listed, at = list[item - i * listed], v = lo + at;
+    if (masks && !(__ldg(mask + (size_t)i * W + (v >> 5)) >> (v & 31) & 1)) continue;
+    const uint32_t c = count[at];
+    const Bits old = reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at];
+    float x = adjusted(Lg::value(old), c, v, i, S, p);
+    if (P.biases > 0 && (c & kTouched)) x += bias[at];
+    else if ((c & (kInPrompt | kCount)) == 0 && !drafted(c, v, i, S)) continue;          // a draft of a later row alone
+    reinterpret_cast<Bits*>(out0 + i * row_bytes)[at] = Lg::pack(x);
   }
 }
 
 }  // namespace
 
+template <int DT, bool ALIGNED>
+static cudaError_t allow() {
+  return cudaFuncSetAttribute(adjust_kernel<DT, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              (int)adjust_smem_bytes(kMaxRange, true, true));
+}
 cudaError_t configure_adjust() {
-  const int smem = (int)sizeof(AdjustShared);
-  cudaError_t e = cudaFuncSetAttribute(adjust_kernel<SPEC_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(adjust_kernel<SPEC_F32>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e = allow<SPEC_BF16, true>();
+  if (e == cudaSuccess) e = allow<SPEC_BF16, false>();
+  if (e == cudaSuccess) e = allow<SPEC_F32, true>();
+  if (e == cudaSuccess) e = allow<SPEC_F32, false>();
   return e;
 }
 
-cudaError_t launch_adjust(const AdjustParams& P, int, cudaStream_t s) {
-  const int splits = (P.V + kRange - 1) / kRange;
-  const dim3 grid((unsigned)(splits * P.B));
-  if (P.dtype == SPEC_BF16) adjust_kernel<SPEC_BF16><<<grid, kAdjustThreads, sizeof(AdjustShared), s>>>(P, splits);
-  else adjust_kernel<SPEC_F32><<<grid, kAdjustThreads, sizeof(AdjustShared), s>>>(P, splits);
+cudaError_t launch_adjust(const AdjustParams& P, int nsm, cudaStream_t s) {
+  // the largest range that still gives every SM four CTAs
+  int shift = 12;
+  static_assert(kMaxRange == 1 << 12 && kMinRange == 1 << 10, "ranges");
+  const auto splits_of = [&](int sh) { return (P.V + (1ll << sh) - 1) >> sh; };
+  while (shift > 10 && splits_of(shift) * P.B < 4ll * nsm) --shift;
+  const int splits = (int)splits_of(shift);
+  const size_t smem = adjust_smem_bytes(1 << shift, P.L > 0 || P.D > 0 || P.biases > 0, P.biases > 0);
+  const unsigned grid = (unsigned)(splits * (long long)P.B);
+  const int es = P.dtype == SPEC_BF16 ? 2 : 4;
+  const bool aligned = ((size_t)P.V * es) % 16 == 0 && reinterpret_cast<uintptr_t>(P.in) % 16 == 0 && reinterpret_cast<uintptr_t>(P.out) % 16 == 0;
+  if (P.dtype == SPEC_BF16) {
+    if (aligned) adjust_kernel<SPEC_BF16, true><<<grid, kAdjustThreads, smem, s>>>(P, splits, shift);
+    else adjust_kernel<SPEC_BF16, false><<<grid, kAdjustThreads, smem, s>>>(P, splits, shift);
+  } else {
+    if (aligned) adjust_kernel<SPEC_F32, true><<<grid, kAdjustThreads, smem, s>>>(P, splits, shift);
+    else adjust_kernel<SPEC_F32, false><<<grid, kAdjustThreads, smem, s>>>(P, splits, shift);
+  }
   return cudaGetLastError();
 }
 
