@@ -27,14 +27,14 @@ constexpr uint32_t kInPrompt = 0x80000000u, kInDraft = 0x40000000u, kTouched = 0
                    kCount = 0x1FFFFFFFu;   // of a count word
 
 // In shared memory: this, counts [range], biases [range] (with biases), the touched
-// tokens' places in the range.
+// tokens' places in the range, and the rows' masks of the range (a word more each).
 struct AdjustShared {
   int draft[SPEC_MAX_G + 1];
   int bad, listed;
   int pad[2];
 };
-__host__ __device__ constexpr size_t adjust_smem_bytes(int range, bool any, bool biases) {
-  return sizeof(AdjustShared) + (any ? (size_t)range * (biases ? 10 : 6) : 0);
+__host__ __device__ constexpr size_t adjust_smem_bytes(int range, bool any, bool biases, int masked_rows) {
+  return sizeof(AdjustShared) + (any ? (size_t)range * (biases ? 10 : 6) : 0) + (size_t)masked_rows * (range / 8 + 4);
 }
 
 struct Penalties {
@@ -88,27 +88,34 @@ __device__ __forceinline__ void store_vec(unsigned char* p, const uint4& v) {
   asm volatile("st.global.L1::no_allocate.v4.b32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// The bits of a vector's tokens that the mask allows; the vector starts at token v.
+// The bits of the PER tokens from `at` on, of a row's mask in shared memory.
 template <int PER, bool ALIGNED>
-__device__ __forceinline__ uint32_t allowed(const uint32_t* mask, int v, uint32_t full) {
-  const uint32_t* m = mask + (v >> 5);
-  const int bit = v & 31;
-  if constexpr (ALIGNED) return __ldg(m) >> bit & full;
-  const uint32_t w0 = __ldg(m), w1 = bit + PER > 32 ? __ldg(m + 1) : 0;
-  return __funnelshift_r(w0, w1, bit) & full;
+__device__ __forceinline__ uint32_t allowed(const uint32_t* mask, int at, uint32_t full) {
+  if constexpr (ALIGNED) {                   // `at` is a multiple of PER
+    const uint32_t byte = reinterpret_cast<const uint8_t*>(mask)[at >> 3];
+    return PER == 8 ? byte : byte >> (at & 4) & full;
+  }
+  return __funnelshift_r(mask[at >> 5], mask[(at >> 5) + 1], at & 31) & full;
 }
-// Logits whose bit of `keep` is 0 become -inf.
+// Logits whose bit of `keep` is 0 become -inf.  A product spreads four bits to the top bits of
+// four bytes, which prmt repeats over the bytes of their logits.
+__device__ __forceinline__ uint32_t spread(uint32_t four) { return four * 0x10204080u; }
+template <uint32_t SELECT>
+__device__ __forceinline__ uint32_t kept(uint32_t w, uint32_t bits, uint32_t gone) {
+  uint32_t m;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(m) : "r"(bits), "n"(SELECT));
+  return (w & m) | (gone & ~m);
+}
 template <int DT>
 __device__ __forceinline__ void remove_others(uint4& x, uint32_t keep) {
-  uint32_t* const w = &x.x;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if constexpr (DT == SPEC_BF16) {
-      const uint32_t gone = ~keep >> 2 * k & 3u, cover = (gone & 1u) * 0xFFFFu | (gone >> 1) * 0xFFFF0000u;
-      w[k] = (w[k] & ~cover) | (0xFF80FF80u & cover);
-    } else {
-      if (!(keep >> k & 1)) w[k] = 0xFF800000u;
-    }
+  if constexpr (DT == SPEC_BF16) {
+    const uint32_t a = spread(keep & 15u), b = spread(keep >> 4);
+    x = make_uint4(kept<0x9988>(x.x, a, 0xFF80FF80u), kept<0xBBAA>(x.y, a, 0xFF80FF80u), kept<0x9988>(x.z, b, 0xFF80FF80u),
+                   kept<0xBBAA>(x.w, b, 0xFF80FF80u));
+  } else {
+    const uint32_t a = spread(keep);
+    x = make_uint4(kept<0x8888>(x.x, a, 0xFF800000u), kept<0x9999>(x.y, a, 0xFF800000u), kept<0xAAAA>(x.z, a, 0xFF800000u),
+                   kept<0xBBBB>(x.w, a, 0xFF800000u));
   }
 }
 
@@ -127,6 +134,29 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
   const int b = blockIdx.x / splits, part = blockIdx.x % splits, t = threadIdx.x;
   const int lo = part << shift, hi = min(P.V, lo + range);
   const bool counts = P.L > 0 || P.D > 0, any = counts || P.biases > 0;
+
+  const int W = (P.V + 31) / 32, pitch = range / 32 + 1;
+  uint32_t* const masks_here = reinterpret_cast<uint32_t*>(adjust_smem + adjust_smem_bytes(range, any, P.biases > 0, 0));
+  const size_t first = (size_t)b * P.R * P.V + lo, row_bytes = (size_t)P.V * ES;        // element of row 0
+  const unsigned char* const in0 = P.in + first * ES;
+  unsigned char* const out0 = P.out + first * ES;
+  const int size = hi - lo;
+  const bool apart = P.out != P.in;
+  // asked for first: the rows into L2 while the history is counted, and the masks of this range
+  if (apart && t < P.R) {
+    const uintptr_t from = (reinterpret_cast<uintptr_t>(in0) + t * row_bytes + 15) & ~(uintptr_t)15,
+                    to = (reinterpret_cast<uintptr_t>(in0) + t * row_bytes + (size_t)size * ES) & ~(uintptr_t)15;
+    if (to > from)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
+  }
+  if (P.mask) {
+    const uint32_t* m = P.mask + (size_t)b * P.R * W + (lo >> 5);
+    const int here = min(pitch - 1, W - (lo >> 5));
+    for (int e = t; e < P.R << (shift - 5); e += kAdjustThreads) {
+      const int i = e >> (shift - 5), k = e & (pitch - 2);
+      if (k < here) masks_here[i * pitch + k] = __ldg(m + (size_t)i * W + k);
+    }
+  }
 
   // what a request has that is out of its range; every CTA of it finds the same
   int bad = 0;
@@ -213,25 +243,19 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
       }
     }
     if (bad) atomicOr(&S.bad, bad);
-    __syncthreads();
-    bad = S.bad;
   }
+  __syncthreads();
+  if (any) bad = S.bad;
   if (part == 0 && t == 0 && P.status) P.status[b] = bad;
 
-  const int W = (P.V + 31) / 32, rows = min(P.R, gamma + 1);
-  const bool apart = P.out != P.in, marks = any && !bad, masks = P.mask && !bad;
-  if (!apart && !marks && !masks) return;
-  const uint32_t* const mask = P.mask + (masks ? (size_t)b * P.R * W : 0);
-  const size_t first = (size_t)b * P.R * P.V + lo, row_bytes = (size_t)P.V * ES;        // element of row 0
-  const unsigned char* const in0 = P.in + first * ES;
-  unsigned char* const out0 = P.out + first * ES;
-  const int size = hi - lo;
+  const int rows = min(P.R, gamma + 1);
+  const bool marks = any && !bad, masks = P.mask && !bad;
 
   if (apart || masks) {
     // one logit of row i, at lo + at
     const auto single = [&](int i, int at) {
       Bits* out = reinterpret_cast<Bits*>(out0 + i * row_bytes) + at;
-      if (masks && !(mask[(size_t)i * W + ((lo + at) >> 5)] >> ((lo + at) & 31) & 1)) *out = Lg::pack(-INFINITY);
+      if (masks && !(masks_here[i * pitch + (at >> 5)] >> (at & 31) & 1)) *out = Lg::pack(-INFINITY);
       else if (apart) *out = reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at];
     };
     if (!ALIGNED && ((reinterpret_cast<uintptr_t>(P.in) ^ reinterpret_cast<uintptr_t>(P.out)) & 15)) {
@@ -242,36 +266,38 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
       constexpr int kRows = 4;
       const int vecs = range / PER, abreast = vecs < kAdjustThreads ? vecs : kAdjustThreads;
       const auto head_of = [&](int i) { return ALIGNED ? 0 : (int)(-(reinterpret_cast<uintptr_t>(in0) + i * row_bytes) & 15) / ES; };
+      const ptrdiff_t to_out = out0 - in0;
+      const int step = kAdjustThreads / abreast * kRows;
       for (int k = t & (abreast - 1); k * PER < size; k += abreast) {
-        for (int i0 = t / abreast * kRows; i0 < rows; i0 += kAdjustThreads / abreast * kRows) {
+        const int i1 = t / abreast * kRows;
+        const unsigned char* row = in0 + i1 * row_bytes + k * 16;
+        for (int i0 = i1; i0 < rows; i0 += step, row += step * row_bytes) {
           uint4 x[kRows];
-          uint32_t keep[kRows];
-          int at[kRows];
+          uint32_t keep[kRows], live = 0;
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
-            at[r] = -1;
+            const int head = ALIGNED ? 0 : head_of(i0 + r);
             keep[r] = Lg::kFull;
-            if (i0 + r >= rows) continue;
-            const int a = head_of(i0 + r) + k * PER;
-            if (a + PER > size) continue;
-            at[r] = a;
-            if (apart) x[r] = load_vec(in0 + (i0 + r) * row_bytes + (size_t)a * ES);
-            if (masks) keep[r] = allowed<PER, ALIGNED>(mask + (size_t)(i0 + r) * W, lo + a, Lg::kFull);
+            if (i0 + r < rows && head + (k + 1) * PER <= size) {
+              live |= 1u << r;
+              if (apart) x[r] = load_vec(row + r * row_bytes + head * ES);
+              if (masks) keep[r] = allowed<PER, ALIGNED>(masks_here + (i0 + r) * pitch, head + k * PER, Lg::kFull);
+            }
           }
           if (!apart) {
             // in place: nothing to do, or nothing to read
 #pragma unroll
             for (int r = 0; r < kRows; ++r) {
-              if (keep[r] == Lg::kFull) at[r] = -1;
               x[r] = make_uint4(0, 0, 0, 0);
-              if (at[r] >= 0 && keep[r] != 0) x[r] = load_vec(in0 + (i0 + r) * row_bytes + (size_t)at[r] * ES);
+              if (keep[r] == Lg::kFull) live &= ~(1u << r);
+              else if (keep[r] != 0) x[r] = load_vec(row + r * row_bytes + (ALIGNED ? 0 : head_of(i0 + r)) * ES);
             }
           }
 #pragma unroll
           for (int r = 0; r < kRows; ++r) {
-            if (at[r] < 0) continue;
+            if (!(live >> r & 1)) continue;
             if (keep[r] != Lg::kFull) remove_others<DT>(x[r], keep[r]);
-            store_vec(out0 + (i0 + r) * row_bytes + (size_t)at[r] * ES, x[r]);
+            store_vec(const_cast<unsigned char*>(row) + to_out + r * row_bytes + (ALIGNED ? 0 : head_of(i0 + r)) * ES, x[r]);
           }
         }
       }
@@ -290,7 +316,7 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
   // (row, token): the rows as they came in hold the logits, in place too: a mask's place is not read
   for (int item = t; item < listed * rows; item += kAdjustThreads) {
     const int i = item / listed, at = list[item - i * listed], v = lo + at;
-    if (masks && !(__ldg(mask + (size_t)i * W + (v >> 5)) >> (v & 31) & 1)) continue;
+    if (masks && !(masks_here[i * pitch + (at >> 5)] >> (at & 31) & 1)) continue;
     const uint32_t c = count[at];
     const Bits old = reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at];
     float x = adjusted(Lg::value(old), c, v, i, S, p);
@@ -305,7 +331,7 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
 template <int DT, bool ALIGNED>
 static cudaError_t allow() {
   return cudaFuncSetAttribute(adjust_kernel<DT, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)adjust_smem_bytes(kMaxRange, true, true));
+                              (int)adjust_smem_bytes(kMaxRange, true, true, SPEC_MAX_G + 1));
 }
 cudaError_t configure_adjust() {
   cudaError_t e = allow<SPEC_BF16, true>();
@@ -322,7 +348,7 @@ cudaError_t launch_adjust(const AdjustParams& P, int nsm, cudaStream_t s) {
   const auto splits_of = [&](int sh) { return (P.V + (1ll << sh) - 1) >> sh; };
   while (shift > 10 && splits_of(shift) * P.B < 4ll * nsm) --shift;
   const int splits = (int)splits_of(shift);
-  const size_t smem = adjust_smem_bytes(1 << shift, P.L > 0 || P.D > 0 || P.biases > 0, P.biases > 0);
+  const size_t smem = adjust_smem_bytes(1 << shift, P.L > 0 || P.D > 0 || P.biases > 0, P.biases > 0, P.mask ? P.R : 0);
   const unsigned grid = (unsigned)(splits * (long long)P.B);
   const int es = P.dtype == SPEC_BF16 ? 2 : 4;
   const bool aligned = ((size_t)P.V * es) % 16 == 0 && reinterpret_cast<uintptr_t>(P.in) % 16 == 0 && reinterpret_cast<uintptr_t>(P.out) % 16 == 0;
