@@ -9,12 +9,14 @@
 //
 // A CTA takes a range of the vocabulary for all R rows of a request.  It counts the
 // history's tokens of its range in shared memory (whole numbers: the order of the
-// atomics does not matter) and lists those that anything touches.  It then goes over
-// its part of the rows in 16-byte vectors, which are copied and masked (in place: left
-// alone, or written without a read where the mask removes all of one), and last over
-// the listed tokens of each row, one logit each.  With both in one pass the code of a
-// touched logit, a vector's worth of it unrolled, did not fit the instruction cache:
-// 186 us for the batch of 64 x 8 x 151936 logits.  HBM bounds the passes over the rows.
+// atomics does not matter), lists those that anything touches, and adjusts them one by one.
+//   Out of place its part of the rows is copied and masked first, in 16-byte vectors (and
+// copied again for a request that the counting finds at fault).
+//   In place most logits are neither read nor written: vectors that the mask removes whole
+// are written without a read, those that it leaves whole are left alone.
+// The adjustment of a listed token stays out of the vector loops: unrolled over a vector's
+// logits it did not fit the instruction cache (64 x 8 x 151936 bf16 logits: 186 us).  Rows by bulk
+// copies through shared memory took 81 us, counting before copying 71 us.  HBM bounds both.
 #include "rows.cuh"
 #include "serve.cuh"
 
@@ -22,7 +24,8 @@ namespace sv {
 namespace {
 
 constexpr int kAdjustThreads = 256;
-constexpr int kMaxRange = 4096, kMinRange = 1024;        // tokens of a CTA
+constexpr int kMaxRange = 2048, kMinRange = 1024;        // tokens of a CTA
+constexpr int kRows = 2;                     // rows taken at once
 constexpr uint32_t kInPrompt = 0x80000000u, kInDraft = 0x40000000u, kTouched = 0x20000000u,
                    kCount = 0x1FFFFFFFu;   // of a count word
 
@@ -34,7 +37,7 @@ struct AdjustShared {
   int pad[2];
 };
 __host__ __device__ constexpr size_t adjust_smem_bytes(int range, bool any, bool biases, int masked_rows) {
-  return sizeof(AdjustShared) + (any ? (size_t)range * (biases ? 10 : 6) : 0) + (size_t)masked_rows * (range / 8 + 4);
+  return sizeof(AdjustShared) + (any ? (size_t)range * (biases ? 10 : 6) : 0) + ((size_t)masked_rows * (range / 8 + 4) + 15) / 16 * 16;
 }
 
 struct Penalties {
@@ -121,7 +124,7 @@ __device__ __forceinline__ void remove_others(uint4& x, uint32_t keep) {
 
 // ALIGNED: every row starts on a 16-byte boundary.
 template <int DT, bool ALIGNED>
-__global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_constant__ AdjustParams P, int splits, int shift) {
+__global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_constant__ AdjustParams P, int splits, int shift) {
   using Lg = Logit<DT>;
   using Bits = typename Lg::Bits;
   constexpr int ES = RowType<DT>::ES, PER = RowType<DT>::PER;
@@ -142,13 +145,16 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
   unsigned char* const out0 = P.out + first * ES;
   const int size = hi - lo;
   const bool apart = P.out != P.in;
-  // asked for first: the rows into L2 while the history is counted, and the masks of this range
-  if (apart && t < P.R) {
-    const uintptr_t from = (reinterpret_cast<uintptr_t>(in0) + t * row_bytes + 15) & ~(uintptr_t)15,
-                    to = (reinterpret_cast<uintptr_t>(in0) + t * row_bytes + (size_t)size * ES) & ~(uintptr_t)15;
-    if (to > from)
-      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
-  }
+  const int most = P.D > 0 ? P.D : P.R - 1;
+  // row i's elements [0, head) and [tail, size) are fewer than a vector each; those between start on a
+  // 16-byte boundary
+  const auto head_of = [&](int i) {
+    return ALIGNED ? 0 : min((int)(-(reinterpret_cast<uintptr_t>(in0) + i * row_bytes) & 15) / ES, size);
+  };
+  const auto tail_of = [&](int i) {
+    const int head = head_of(i);
+    return head + (size - head) / PER * PER;
+  };
   if (P.mask) {
     const uint32_t* m = P.mask + (size_t)b * P.R * W + (lo >> 5);
     const int here = min(pitch - 1, W - (lo >> 5));
@@ -163,7 +169,6 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
   const int len = P.history_len ? P.history_len[b] : P.L, prompt = P.prompt_len ? P.prompt_len[b] : 0;
   const bool lengths = len >= 0 && len <= P.L && prompt >= 0 && prompt <= len;
   if (!lengths) bad |= SPEC_ST_BAD_LENGTH;
-  const int most = P.D > 0 ? P.D : P.R - 1;
   int gamma = P.gamma ? P.gamma[b] : most;
   if (gamma < 0 || gamma > most) { bad |= SPEC_ST_BAD_GAMMA; gamma = most; }
   Penalties p;
@@ -178,7 +183,60 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
     for (int e = t; e < range; e += kAdjustThreads) count[e] = 0;
     if (P.biases > 0)
       for (int e = t; e < range; e += kAdjustThreads) bias[e] = 0.f;
-    __syncthreads();
+  }
+  __syncthreads();
+
+  const int rows = min(P.R, gamma + 1);
+  const auto removed = [&](int i, int at) { return P.mask && !(masks_here[i * pitch + (at >> 5)] >> (at & 31) & 1); };
+  const bool alike = ((reinterpret_cast<uintptr_t>(P.in) ^ reinterpret_cast<uintptr_t>(P.out)) & 15) == 0;
+  // vectors k of kRows rows at a time; with fewer vectors than threads, rows side by side
+  const int vecs = range / PER, abreast = vecs < kAdjustThreads ? vecs : kAdjustThreads;
+  const int side = t / abreast * kRows, step = kAdjustThreads / abreast * kRows;
+  const ptrdiff_t to_out = out0 - in0;
+  const auto copy_rows = [&](bool masked) {
+    if (!alike) {
+      for (int i = 0; i < rows; ++i)
+        for (int at = t; at < size; at += kAdjustThreads)
+          reinterpret_cast<Bits*>(out0 + i * row_bytes)[at] =
+              masked && removed(i, at) ? Lg::pack(-INFINITY) : reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at];
+      return;
+    }
+    for (int k = t & (abreast - 1); k * PER < size; k += abreast) {
+      const unsigned char* row = in0 + side * row_bytes + k * 16;
+      for (int i0 = side; i0 < rows; i0 += step, row += step * row_bytes) {
+        uint4 x[kRows];
+        uint32_t live = 0;
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          const int head = head_of(i0 + r);
+          if (i0 + r < rows && head + (k + 1) * PER <= size) {
+            live |= 1u << r;
+            x[r] = load_vec(row + r * row_bytes + head * ES);
+          }
+        }
+#pragma unroll
+        for (int r = 0; r < kRows; ++r) {
+          if (!(live >> r & 1)) continue;
+          const int head = head_of(i0 + r);
+          if (masked) {
+            const uint32_t keep = allowed<PER, ALIGNED>(masks_here + (i0 + r) * pitch, head + k * PER, Lg::kFull);
+            if (keep != Lg::kFull) remove_others<DT>(x[r], keep);
+          }
+          store_vec(const_cast<unsigned char*>(row) + to_out + r * row_bytes + head * ES, x[r]);
+        }
+      }
+    }
+    // the ends of a row's part
+    for (int item = t; item < rows * 2 * PER; item += kAdjustThreads) {
+      const int i = item / (2 * PER), e = item % (2 * PER), at = e < PER ? e : tail_of(i) + e - PER;
+      if (e < PER ? e < head_of(i) : at < size)
+        reinterpret_cast<Bits*>(out0 + i * row_bytes)[at] =
+            masked && removed(i, at) ? Lg::pack(-INFINITY) : reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at];
+    }
+  };
+  if (apart) copy_rows(P.mask != nullptr);
+
+  if (any) {
     const auto touch = [&](int at, uint32_t old) {       // old: its count word before
       if (old & (kTouched | kInPrompt | kInDraft | kCount)) return;
       list[atomicAdd(&S.listed, 1)] = (uint16_t)at;
@@ -186,20 +244,25 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
     if (lengths) {
       const int32_t* h = P.history + (size_t)b * P.L;
       const auto told = [&](int e, int v) {
-        if (v < -1 || v >= P.V) bad |= SPEC_ST_BAD_TOKEN;
-        else if (v >= lo && v < hi) {
-          touch(v - lo, e < prompt ? atomicOr(&count[v - lo], kInPrompt) : atomicAdd(&count[v - lo], 1u));
-        }
+        bad |= (unsigned)(v + 1) > (unsigned)P.V;          // SPEC_ST_BAD_TOKEN is set below
+        const unsigned at = (unsigned)(v - lo);
+        if (at < (unsigned)size) touch((int)at, e < prompt ? atomicOr(&count[at], kInPrompt) : atomicAdd(&count[at], 1u));
       };
+      static_assert(SPEC_ST_BAD_TOKEN == 2, "bit 0 below stands for it");
+      const int whole = (reinterpret_cast<uintptr_t>(h) & 15) == 0 ? len / 4 : 0;
       int e = t;
-      for (; e + 3 * kAdjustThreads < len; e += 4 * kAdjustThreads) {
-        int v[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) v[u] = __ldg(h + e + u * kAdjustThreads);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) told(e + u * kAdjustThreads, v[u]);
+      for (; e + kAdjustThreads < whole; e += 2 * kAdjustThreads) {
+        const int4 v = __ldg(reinterpret_cast<const int4*>(h) + e), w = __ldg(reinterpret_cast<const int4*>(h) + e + kAdjustThreads);
+        told(4 * e, v.x); told(4 * e + 1, v.y); told(4 * e + 2, v.z); told(4 * e + 3, v.w);
+        const int f = 4 * (e + kAdjustThreads);
+        told(f, w.x); told(f + 1, w.y); told(f + 2, w.z); told(f + 3, w.w);
       }
-      for (; e < len; e += kAdjustThreads) told(e, __ldg(h + e));
+      if (e < whole) {
+        const int4 v = __ldg(reinterpret_cast<const int4*>(h) + e);
+        told(4 * e, v.x); told(4 * e + 1, v.y); told(4 * e + 2, v.z); told(4 * e + 3, v.w);
+      }
+      for (e = 4 * whole + t; e < len; e += kAdjustThreads) told(e, __ldg(h + e));
+      bad = (bad & ~1) | (bad & 1) * SPEC_ST_BAD_TOKEN;
     }
     if (t < P.D) {
       const int v = t < gamma ? P.draft[(size_t)b * P.D + t] : -1;
@@ -248,80 +311,51 @@ __global__ void __launch_bounds__(kAdjustThreads) adjust_kernel(const __grid_con
   if (any) bad = S.bad;
   if (part == 0 && t == 0 && P.status) P.status[b] = bad;
 
-  const int rows = min(P.R, gamma + 1);
-  const bool marks = any && !bad, masks = P.mask && !bad;
-
-  if (apart || masks) {
-    // one logit of row i, at lo + at
-    const auto single = [&](int i, int at) {
-      Bits* out = reinterpret_cast<Bits*>(out0 + i * row_bytes) + at;
-      if (masks && !(masks_here[i * pitch + (at >> 5)] >> (at & 31) & 1)) *out = Lg::pack(-INFINITY);
-      else if (apart) *out = reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at];
-    };
-    if (!ALIGNED && ((reinterpret_cast<uintptr_t>(P.in) ^ reinterpret_cast<uintptr_t>(P.out)) & 15)) {
-      for (int i = 0; i < rows; ++i)
-        for (int at = t; at < size; at += kAdjustThreads) single(i, at);
-    } else {
-      // vector k of kRows rows at a time; with fewer vectors than threads, rows side by side
-      constexpr int kRows = 4;
-      const int vecs = range / PER, abreast = vecs < kAdjustThreads ? vecs : kAdjustThreads;
-      const auto head_of = [&](int i) { return ALIGNED ? 0 : (int)(-(reinterpret_cast<uintptr_t>(in0) + i * row_bytes) & 15) / ES; };
-      const ptrdiff_t to_out = out0 - in0;
-      const int step = kAdjustThreads / abreast * kRows;
-      for (int k = t & (abreast - 1); k * PER < size; k += abreast) {
-        const int i1 = t / abreast * kRows;
-        const unsigned char* row = in0 + i1 * row_bytes + k * 16;
-        for (int i0 = i1; i0 < rows; i0 += step, row += step * row_bytes) {
-          uint4 x[kRows];
-          uint32_t keep[kRows], live = 0;
+  if (bad) {
+    if (apart && P.mask) copy_rows(false);
+    return;
+  }
+  if (!apart && P.mask) {
+    for (int k = t & (abreast - 1); k * PER < size; k += abreast) {
+      unsigned char* row = out0 + side * row_bytes + k * 16;
+      for (int i0 = side; i0 < rows; i0 += step, row += step * row_bytes) {
+        uint4 x[kRows];
+        uint32_t keep[kRows];
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            const int head = ALIGNED ? 0 : head_of(i0 + r);
-            keep[r] = Lg::kFull;
-            if (i0 + r < rows && head + (k + 1) * PER <= size) {
-              live |= 1u << r;
-              if (apart) x[r] = load_vec(row + r * row_bytes + head * ES);
-              if (masks) keep[r] = allowed<PER, ALIGNED>(masks_here + (i0 + r) * pitch, head + k * PER, Lg::kFull);
-            }
-          }
-          if (!apart) {
-            // in place: nothing to do, or nothing to read
+        for (int r = 0; r < kRows; ++r) {
+          const int head = head_of(i0 + r);
+          keep[r] = Lg::kFull;
+          if (i0 + r < rows && head + (k + 1) * PER <= size)
+            keep[r] = allowed<PER, ALIGNED>(masks_here + (i0 + r) * pitch, head + k * PER, Lg::kFull);
+        }
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-              x[r] = make_uint4(0, 0, 0, 0);
-              if (keep[r] == Lg::kFull) live &= ~(1u << r);
-              else if (keep[r] != 0) x[r] = load_vec(row + r * row_bytes + (ALIGNED ? 0 : head_of(i0 + r)) * ES);
-            }
-          }
+        for (int r = 0; r < kRows; ++r) {
+          x[r] = make_uint4(0, 0, 0, 0);
+          if (keep[r] != Lg::kFull && keep[r] != 0) x[r] = load_vec(row + r * row_bytes + head_of(i0 + r) * ES);
+        }
 #pragma unroll
-          for (int r = 0; r < kRows; ++r) {
-            if (!(live >> r & 1)) continue;
-            if (keep[r] != Lg::kFull) remove_others<DT>(x[r], keep[r]);
-            store_vec(const_cast<unsigned char*>(row) + to_out + r * row_bytes + (ALIGNED ? 0 : head_of(i0 + r)) * ES, x[r]);
-          }
+        for (int r = 0; r < kRows; ++r) {
+          if (keep[r] == Lg::kFull) continue;
+          remove_others<DT>(x[r], keep[r]);
+          store_vec(row + r * row_bytes + head_of(i0 + r) * ES, x[r]);
         }
       }
-      // the ends of a row's part, fewer than PER logits each
-      for (int item = t; item < rows * 2 * PER; item += kAdjustThreads) {
-        const int i = item / (2 * PER), e = item % (2 * PER), head = min(head_of(i), size);
-        const int at = e < PER ? e : head + (size - head) / PER * PER + e - PER;
-        if (e < PER ? e < head : at < size) single(i, at);
-      }
     }
+    for (int item = t; item < rows * 2 * PER; item += kAdjustThreads) {
+      const int i = item / (2 * PER), e = item % (2 * PER), at = e < PER ? e : tail_of(i) + e - PER;
+      if ((e < PER ? e < head_of(i) : at < size) && removed(i, at))
+        reinterpret_cast<Bits*>(out0 + i * row_bytes)[at] = Lg::pack(-INFINITY);
+    }
+    __syncthreads();                         // vectors with listed tokens have been written
   }
-  if (!marks) return;
-  __syncthreads();
-  const int listed = S.listed;
-  if (listed == 0) return;
-  // (row, token): the rows as they came in hold the logits, in place too: a mask's place is not read
+  const int listed = any ? S.listed : 0;
   for (int item = t; item < listed * rows; item += kAdjustThreads) {
-    const int i = item / listed, at = list[item - i * listed], v = lo + at;
-    if (masks && !(masks_here[i * pitch + (at >> 5)] >> (at & 31) & 1)) continue;
+    const int i = item / listed, at = list[item - i * listed];
+    if (removed(i, at)) continue;
     const uint32_t c = count[at];
-    const Bits old = reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at];
-    float x = adjusted(Lg::value(old), c, v, i, S, p);
+    float x = adjusted(Lg::value(reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at]), c, lo + at, i, S, p);
     if (P.biases > 0 && (c & kTouched)) x += bias[at];
-    else if ((c & (kInPrompt | kCount)) == 0 && !drafted(c, v, i, S)) continue;          // a draft of a later row alone
+    else if ((c & (kInPrompt | kCount)) == 0 && !drafted(c, lo + at, i, S)) continue;       // a draft of a later row alone
     reinterpret_cast<Bits*>(out0 + i * row_bytes)[at] = Lg::pack(x);
   }
 }
@@ -343,8 +377,8 @@ cudaError_t configure_adjust() {
 
 cudaError_t launch_adjust(const AdjustParams& P, int nsm, cudaStream_t s) {
   // the largest range that still gives every SM four CTAs
-  int shift = 12;
-  static_assert(kMaxRange == 1 << 12 && kMinRange == 1 << 10, "ranges");
+  int shift = 11;
+  static_assert(kMaxRange == 1 << 11 && kMinRange == 1 << 10, "ranges");
   const auto splits_of = [&](int sh) { return (P.V + (1ll << sh) - 1) >> sh; };
   while (shift > 10 && splits_of(shift) * P.B < 4ll * nsm) --shift;
   const int splits = (int)splits_of(shift);
