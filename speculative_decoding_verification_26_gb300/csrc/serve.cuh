@@ -14,6 +14,19 @@ namespace sv {
 // pair of 16-bit values.
 __host__ __device__ constexpr int nibble_of(int i) { return (i >> 1) + 4 * (i & 1); }
 
+// 128 + z as bf16 in both halves
+__device__ __forceinline__ uint32_t less_of(uint32_t z) { return (0x4300u | z) * 0x10001u; }
+// a word of 8 weights as bf16 pairs of q - z; less = less_of(z).  128 + q is q in the last bits of
+// the mantissa; the difference is exact.
+__device__ __forceinline__ void unpack8(uint32_t* out, uint32_t word, uint32_t less) {
+#pragma unroll
+  for (int p = 0; p < 4; ++p)
+    asm("{\n .reg .b32 u;\n lop3.b32 u, %1, 0x000F000F, 0x43004300, 0xEA;\n sub.rn.bf16x2 %0, u, %2;\n}\n"
+        : "=r"(out[p])
+        : "r"(word >> 4 * p), "r"(less));
+}
+
+
 struct W4Params {
   const unsigned char* weight;   // quantise: [V, H] of `dtype`
   int dtype, n, H, V, group, groups;     // groups of a row

@@ -154,18 +154,6 @@ __device__ __forceinline__ uint4 shared16(uint32_t addr) {
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
   return v;
 }
-// 128 + z as bf16 in both halves
-__device__ __forceinline__ uint32_t less_of(uint32_t z) { return (0x4300u | z) * 0x10001u; }
-// a word of 8 weights as bf16 pairs of q - z; less = less_of(z).  128 + q is q in the last bits of
-// the mantissa; the difference is exact.
-__device__ __forceinline__ void unpack8(uint32_t* out, uint32_t word, uint32_t less) {
-#pragma unroll
-  for (int p = 0; p < 4; ++p)
-    asm("{\n .reg .b32 u;\n lop3.b32 u, %1, 0x000F000F, 0x43004300, 0xEA;\n sub.rn.bf16x2 %0, u, %2;\n}\n"
-        : "=r"(out[p])
-        : "r"(word >> 4 * p), "r"(less));
-}
-
 // A scale on its way, and as a number once it is needed.  Both stay where they are written: a
 // conversion that the compiler moves up to its load makes every turn wait for memory (500 clocks).
 __device__ __forceinline__ uint32_t scale_bits(const __nv_bfloat16* p) {
