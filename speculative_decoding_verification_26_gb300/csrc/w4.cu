@@ -51,162 +51,191 @@ __device__ __forceinline__ float over(float a, float more = 0.f) {
   return __fmaf_rn(__fmaf_rn(-q, (float)D, a) + more, c, q);
 }
 
-// 8 weights in place k8 of a row
+// 8 weights of a row
 template <int DT>
 struct Eight {
-  uint4 v[DT == SPEC_BF16 ? 1 : 2];
-  __device__ __forceinline__ void load(const unsigned char* row, int k8) {
-    const uint4* p = reinterpret_cast<const uint4*>(row) + (size_t)k8 * (DT == SPEC_BF16 ? 1 : 2);
-#pragma unroll
-    for (uint4& x : v)
+  uint32_t w[DT == SPEC_BF16 ? 4 : 8];
+  __device__ __forceinline__ void load(const unsigned char* p) {
+    if constexpr (DT == SPEC_BF16)
       asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0, %1, %2, %3}, [%4];"
-                   : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                   : "l"(p++));
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                   : "l"(p));
+    else if (reinterpret_cast<uintptr_t>(p) & 31) {      // the same for all: rows are whole lines
+#pragma unroll
+      for (int i = 0; i < 8; i += 4)
+        asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
+                     : "l"(p + 4 * i));
+    } else                                   // 32 bytes at once: two loads would take a sector each twice
+      asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                   : "l"(p));
   }
   __device__ __forceinline__ void zero() {
 #pragma unroll
-    for (uint4& x : v) x = make_uint4(0, 0, 0, 0);
+    for (uint32_t& x : w) x = 0;
   }
   __device__ __forceinline__ float at(int j) const {
-    if constexpr (DT == SPEC_BF16) {
-      const uint32_t w[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
-      return j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
-    } else {
-      const uint4& x = v[j / 4];
-      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-      return __uint_as_float(w[j & 3]);
-    }
+    if constexpr (DT == SPEC_BF16) return j & 1 ? bf16_hi(w[j / 2]) : bf16_lo(w[j / 2]);
+    else return __uint_as_float(w[j]);
   }
   // the largest magnitude as bits of fp32, which order like the numbers, infinities and NaN above all
   __device__ __forceinline__ uint32_t most() const {
     if constexpr (DT == SPEC_BF16) {
       const uint32_t m = 0x7FFF7FFFu;
-      const uint32_t t = __vmaxu2(__vmaxu2(v[0].x & m, v[0].y & m), __vmaxu2(v[0].z & m, v[0].w & m));
+      const uint32_t t = __vmaxu2(__vmaxu2(w[0] & m, w[1] & m), __vmaxu2(w[2] & m, w[3] & m));
       return max(t << 16, t & 0xFFFF0000u);
     } else {
       uint32_t t = 0;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t = max(t, __float_as_uint(at(j)) & 0x7FFFFFFFu);
+      for (int j = 0; j < 8; ++j) t = max(t, w[j] & 0x7FFFFFFFu);
       return t;
     }
   }
 };
 
-// A group's scale, zero point and reciprocal; LANES lanes hold it.
-struct Group {
-  float s, zero, inv, up;                    // up: what weights and scale are multiplied by first
-  bool none, odd, slow;                      // no scale; NaN or infinities; not for the quick way
+// What the lanes of a group agree on: the largest magnitude, and with zero points the range.
+struct Range {
+  uint32_t most;
+  float lo, hi;
 };
 template <int DT, int LANES, bool ZERO>
-__device__ __forceinline__ Group group_of(const Eight<DT>& w) {
-  Group g;
-  uint32_t most = w.most();
-#pragma unroll
-  for (int off = LANES / 2; off >= 1; off >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
-  g.odd = most >= 0x7F800000u;
-  const float big = __uint_as_float(most);
-  const bool plain = big > 1e-25f && big < 1e37f;
-  float lo = 0.f, hi = 0.f, s;
+__device__ __forceinline__ Range range_of(const Eight<DT>& w) {
+  Range r;
+  r.most = w.most();
+  r.lo = r.hi = 0.f;
   if constexpr (ZERO) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      lo = fminf(lo, w.at(j));
-      hi = fmaxf(hi, w.at(j));
+      r.lo = fminf(r.lo, w.at(j));
+      r.hi = fmaxf(r.hi, w.at(j));
     }
+  }
 #pragma unroll
-    for (int off = LANES / 2; off >= 1; off >>= 1) {
-      lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, off));
-      hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+  for (int off = LANES / 2; off >= 1; off >>= 1) {
+    r.most = max(r.most, __shfl_xor_sync(0xffffffffu, r.most, off));
+    if constexpr (ZERO) {
+      r.lo = fminf(r.lo, __shfl_xor_sync(0xffffffffu, r.lo, off));
+      r.hi = fmaxf(r.hi, __shfl_xor_sync(0xffffffffu, r.hi, off));
     }
-    // (hi - lo) / 15 rounded to fp32 from the whole difference d + err
-    const float down = plain ? 1.f : big < 1e37f ? 1.f : 1.f / 256, a = hi * down, b = -lo * down;       // no overflow
-    const float d = a + b, back = d - a, err = (a - (d - back)) + (b - back);
-    if (plain) {
-      s = over<15>(d, err);
-    } else {
-      const float q = __fdiv_rn(d, 15.f);
-      s = (q + (__fmaf_rn(-q, 15.f, d) + err) / 15.f) * (1.f / down);
-    }
-  } else {
-    s = plain ? over<7>(big) : __fdiv_rn(big, 7.f);
   }
-  s = __bfloat162float(__float2bfloat16_rn(s));
-  g.none = !(s > 0.f) || !(s < INFINITY) || g.odd;
-  // scales whose reciprocal would overflow: everything times 2^64
-  g.up = s < 1e-30f ? 18446744073709551616.f : 1.f;
-  g.slow = !plain || g.none;
-  g.s = s;
-  g.inv = g.none ? 0.f : __frcp_rn(s * g.up);
-  g.zero = 8.f;
+  return r;
+}
+// A group's scale and zero point, and a lane's word.
+struct Coded {
+  float s, zero;
+  uint32_t word;
+};
+__device__ __forceinline__ float as_bf16(float s) { return __bfloat162float(__float2bfloat16_rn(s)); }
+
+// Any group: magnitudes near the ends of fp32's range, scales of 0, NaN and infinities, quotients
+// of fp32 weights next to a half.
+template <int DT, bool ZERO>
+__device__ __noinline__ Coded code_slowly(const Eight<DT> w, const Range r) {
+  Coded c;
+  const bool odd = r.most >= 0x7F800000u;
+  c.zero = 8.f;
   if constexpr (ZERO) {
-    if (!g.none) {
-      const float grid = on_grid(-lo, g.inv), m = at_magic(grid);
-      g.zero = fminf(g.slow || (DT == SPEC_F32 && near_half(grid, m)) ? whole_quotient(-lo * g.up, s * g.up, g.inv) : m - kMagic, 15.f);
-    }
+    // (hi - lo) / 15 rounded to fp32 from the whole difference d + err, without overflow
+    const float down = __uint_as_float(r.most) < 1e37f ? 1.f : 1.f / 256, a = r.hi * down, b = -r.lo * down;
+    const float d = a + b, back = d - a, err = (a - (d - back)) + (b - back), q = __fdiv_rn(d, 15.f);
+    c.s = (q + (__fmaf_rn(-q, 15.f, d) + err) / 15.f) * (1.f / down);
+  } else {
+    c.s = __fdiv_rn(__uint_as_float(r.most), 7.f);
   }
-  return g;
+  c.s = as_bf16(c.s);
+  const bool none = !(c.s > 0.f) || !(c.s < INFINITY) || odd;
+  // scales whose reciprocal would overflow: everything times 2^64
+  const float up = c.s < 1e-30f ? 18446744073709551616.f : 1.f, s = c.s * up, inv = 1.f / s;
+  if (ZERO && !none) c.zero = fminf(whole_quotient(-r.lo * up, s, inv), 15.f);
+  c.word = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float q = none ? c.zero : fminf(fmaxf(whole_quotient(w.at(j) * up, s, inv) + c.zero, 0.f), 15.f);
+    c.word |= (uint32_t)q << 4 * nibble_of(j);
+  }
+  if (odd) c.s = NAN;
+  return c;
+}
+// The others, 4 instructions a weight; false where the slow way has to be taken.
+template <int DT, bool ZERO>
+__device__ __forceinline__ bool code_quickly(const Eight<DT>& w, const Range& r, Coded& c) {
+  const float big = __uint_as_float(r.most);
+  bool quick = big > 1e-25f && big < 1e37f;
+  if constexpr (ZERO) {
+    const float b = -r.lo, d = r.hi + b, back = d - r.hi, err = (r.hi - (d - back)) + (b - back);
+    c.s = over<15>(d, err);
+  } else {
+    c.s = over<7>(big);
+  }
+  c.s = as_bf16(c.s);
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(c.s));
+  c.zero = 8.f;
+  if constexpr (ZERO) {
+    const float grid = on_grid(-r.lo, inv), m = at_magic(grid);
+    if constexpr (DT == SPEC_F32) quick = quick && !near_half(grid, m);
+    c.zero = fminf(m - kMagic, 15.f);
+  }
+  // the sum of (kMagicBits + n) << 4 p, and of z - kMagicBits: (n + z) << 4 p
+  const float least = kMagic - c.zero, most = kMagic + 15.f - c.zero;
+  uint32_t word = ZERO ? ((uint32_t)(int)c.zero - kMagicBits) * 0x11111111u : (8u - kMagicBits) * 0x11111111u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float grid = on_grid(w.at(j), inv);
+    float m = at_magic(grid);
+    if constexpr (DT == SPEC_F32) quick = quick && !near_half(grid, m);
+    if constexpr (ZERO) m = fminf(fmaxf(m, least), most);
+    word += __float_as_uint(m) << 4 * nibble_of(j);
+  }
+  c.word = word;
+  return quick;
 }
 
 // A warp takes ROWS rows, LANES lanes a group, a lane 8 weights.
 template <int DT, int LANES, bool ZERO, int ROWS>
 __global__ void __launch_bounds__(kW4Threads) quantize_kernel(const __grid_constant__ W4Params P) {
-  constexpr int PER = 32 / LANES, ES = RowType<DT>::ES;
+  constexpr int PER = 32 / LANES, BYTES = 8 * RowType<DT>::ES;
   const int lane = threadIdx.x & 31, words = P.H / 8;
   const long long v0 = (blockIdx.x * (long long)(kW4Threads / 32) + (threadIdx.x >> 5)) * ROWS;
   if (v0 >= P.V) return;
   const int rows = (int)min((long long)ROWS, P.V - v0);
-  bool bad[ROWS] = {};
-  for (int g0 = 0; g0 < P.groups; g0 += PER) {
-    const int g = g0 + lane / LANES, k = g0 * LANES + lane;
-    const bool live = k < words;
+  const unsigned char* from = P.weight + (v0 * words + lane) * BYTES;
+  uint32_t* to = P.packed + v0 * words + lane;
+  const long long at = v0 * P.groups + lane / LANES;
+  const bool leads = lane % LANES == 0;
+  uint32_t bad = 0;                          // a bit a row
+  for (int g0 = 0; g0 < P.groups; g0 += PER, from += 32 * BYTES, to += 32) {
+    const bool live = g0 * LANES + lane < words;
     Eight<DT> w[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      if (live && r < rows) w[r].load(P.weight + (v0 + r) * P.H * ES, k);
-      else w[r].zero();
+      w[r].zero();
+      if (live && r < rows) w[r].load(from + (size_t)(r * words) * BYTES);
     }
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      const Group G = group_of<DT, LANES, ZERO>(w[r]);
-      uint32_t word = 0;
-      bool slow = G.slow;
-      // sum of (kMagicBits + n) << 4 p, and of z - kMagicBits: (n + z) << 4 p
-      const float least = kMagic - G.zero, most = kMagic + 15.f - G.zero;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float grid = on_grid(w[r].at(j), G.inv);
-        float m = at_magic(grid);
-        if constexpr (DT == SPEC_F32) slow |= near_half(grid, m);
-        if constexpr (ZERO) m = fminf(fmaxf(m, least), most);
-        word += __float_as_uint(m) << 4 * nibble_of(j);
-      }
-      word += ((uint32_t)(int)G.zero - kMagicBits) * 0x11111111u;
-      if (__any_sync(0xffffffffu, slow)) {
-        if (slow) {
-          word = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float q = G.none ? G.zero : fminf(fmaxf(whole_quotient(w[r].at(j) * G.up, G.s * G.up, G.inv) + G.zero, 0.f), 15.f);
-            word |= (uint32_t)q << 4 * nibble_of(j);
-          }
-        }
+      const Range range = range_of<DT, LANES, ZERO>(w[r]);
+      Coded c;
+      const bool quick = code_quickly<DT, ZERO>(w[r], range, c);
+      if (!__all_sync(0xffffffffu, quick)) {
+        if (!quick) c = code_slowly<DT, ZERO>(w[r], range);
+        if (live && range.most >= 0x7F800000u) bad |= 1u << r;
+        // (the lanes of a group agree on its scale and zero point whichever way they took)
       }
       if (live && r < rows) {
-        P.packed[(v0 + r) * words + k] = word;
-        if (lane % LANES == 0) {
-          P.scale[(v0 + r) * P.groups + g] = __float2bfloat16_rn(G.odd ? NAN : G.s);
-          if (ZERO) P.zero[(v0 + r) * P.groups + g] = (uint8_t)G.zero;
+        to[r * words] = c.word;
+        if (leads) {
+          const long long o = at + g0 + (long long)r * P.groups;
+          P.scale[o] = __float2bfloat16_rn(c.s);
+          if (ZERO) P.zero[o] = (uint8_t)c.zero;
         }
-        bad[r] |= G.odd;
       }
     }
   }
   if (P.status) {
-#pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const bool any = __any_sync(0xffffffffu, bad[r]);
-      if (lane == 0 && r < rows) P.status[v0 + r] = any ? SPEC_ST_NONFINITE : SPEC_ST_OK;
-    }
+    bad = __reduce_or_sync(0xffffffffu, bad);
+    if (lane < rows) P.status[v0 + lane] = bad >> lane & 1 ? SPEC_ST_NONFINITE : SPEC_ST_OK;
   }
 }
 
@@ -215,17 +244,18 @@ __global__ void __launch_bounds__(kW4Threads) quantize_kernel(const __grid_const
 
 template <int DT, bool ZERO, int ROWS>
 __global__ void __launch_bounds__(kW4Threads) dequantize_kernel(const __grid_constant__ W4Params P, int log_per) {
+  constexpr int EACH = DT == SPEC_BF16 ? 1 : 2;          // lanes a word: a lane writes 16 bytes
   const int lane = threadIdx.x & 31, words = P.H / 8;
   const long long v0 = (blockIdx.x * (long long)(kW4Threads / 32) + (threadIdx.x >> 5)) * ROWS;
   if (v0 >= P.V) return;
   const int rows = (int)min((long long)ROWS, P.V - v0);
-  for (int k = lane; k < words; k += 32) {
-    const int g = k >> log_per;
+  for (int k = lane; k < words * EACH; k += 32) {
+    const int at = k / EACH, g = at >> log_per;
     uint32_t word[ROWS], s[ROWS], z[ROWS];
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
       const long long v = v0 + (r < rows ? r : 0);
-      word[r] = __ldg(P.packed + v * words + k);
+      word[r] = __ldg(P.packed + v * words + at);
       s[r] = __ldg(reinterpret_cast<const uint16_t*>(P.scale) + v * P.groups + g);
       z[r] = ZERO ? __ldg(P.zero + v * P.groups + g) : 8u;
     }
@@ -233,21 +263,21 @@ __global__ void __launch_bounds__(kW4Threads) dequantize_kernel(const __grid_con
     for (int r = 0; r < ROWS; ++r) {
       if (r >= rows) continue;
       uint32_t q[4];
-      unpack8(q, word[r], less_of(z[r]));
+      uint4 o;
       if constexpr (DT == SPEC_BF16) {
+        unpack8(q, word[r], less_of(z[r]));
         const uint32_t both = s[r] * 0x10001u;
-        uint4 o;
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(q[0]), "r"(both));
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(q[1]), "r"(both));
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.z) : "r"(q[2]), "r"(both));
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.w) : "r"(q[3]), "r"(both));
-        reinterpret_cast<uint4*>(P.out)[(v0 + r) * words + k] = o;
       } else {
+        unpack8(q, word[r] >> (k & 1) * 8, less_of(z[r]));       // the pairs 0 and 1, or 2 and 3
         const float f = __uint_as_float(s[r] << 16);
-        float4* o = reinterpret_cast<float4*>(P.out) + 2 * ((v0 + r) * words + k);
-        o[0] = make_float4(bf16_lo(q[0]) * f, bf16_hi(q[0]) * f, bf16_lo(q[1]) * f, bf16_hi(q[1]) * f);
-        o[1] = make_float4(bf16_lo(q[2]) * f, bf16_hi(q[2]) * f, bf16_lo(q[3]) * f, bf16_hi(q[3]) * f);
+        o = make_uint4(__float_as_uint(bf16_lo(q[0]) * f), __float_as_uint(bf16_hi(q[0]) * f), __float_as_uint(bf16_lo(q[1]) * f),
+                       __float_as_uint(bf16_hi(q[1]) * f));
       }
+      reinterpret_cast<uint4*>(P.out)[(v0 + r) * words * EACH + k] = o;
     }
   }
 }

@@ -122,6 +122,26 @@ def test_quantize_at_the_edges(sv, dtype, zero):
         check_quantize(sv, w.to(dtype), group, zero)
 
 
+@pytest.mark.parametrize("zero", [False, True])
+def test_quantize_large_and_offset(sv, zero):
+    """Several rows a warp, and weights that start on an odd 16-byte boundary."""
+    for dtype, V, H, group in ((BF, 20000, 160, 64), (F32, 12000, 96, 32), (F32, 12000, 288, 128), (BF, 10001, 544, 128)):
+        w = (torch.randn(V, H, generator=gen(V)) * torch.rand(V, 1, generator=gen(H))).to(dtype)
+        w[5], w[V - 1, 3], w[7] = 0, INF, w[7] * 1e-38
+        buf = torch.zeros(w.numel() + 16, dtype=dtype, device="cuda")
+        off = 16 // dtype.itemsize
+        dev = buf[off:off + w.numel()].view(V, H)
+        dev.copy_(w)
+        assert dev.data_ptr() % 32 == 16
+        q, scale, z = SP.quantize(w, group, zero)
+        r = sv.quantize_w4(dev, group, zero=zero)
+        assert torch.equal(SP.unpack(r["packed"].cpu()), q)
+        assert torch.equal(r["scale"].cpu().view(torch.int16).bitwise_and(0x7FC0) == 0x7FC0, torch.isnan(scale))
+        assert torch.equal(torch.nan_to_num(r["scale"].cpu().float()), torch.nan_to_num(scale.float()))
+        assert not zero or torch.equal(r["zero"].cpu(), z)
+        assert r["status"].cpu().nonzero().flatten().tolist() == [V - 1]
+
+
 def weights_of(V, H, group, zero, seed):
     g = gen(seed)
     q = torch.randint(0, 16, (V, H), generator=g)
