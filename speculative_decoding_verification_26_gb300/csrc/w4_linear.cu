@@ -44,7 +44,7 @@ struct Shape {
   static constexpr int DColumn = Slots * ACols;                  // where the sums begin
   static constexpr int Chunks = SlotK / 32;                      // of 16 bytes of a row
   // warps: teams of four unpack, and take slots in turn, as the issuers do
-  static constexpr int Teams = Slots == 3 ? 3 : 2, UnpackWarps = 4 * Teams, Issuers = Slots == 3 ? 1 : 2;
+  static constexpr int Teams = NT == 128 ? 1 : Slots == 3 ? 3 : 2, UnpackWarps = 4 * Teams, Issuers = Slots == 3 ? 1 : 2;
   static constexpr int Columns = NT == 128 ? 64 : NT < 32 ? NT : 32, SumWarps = 4 * NT / Columns;       // columns of a thread
   static constexpr int Threads = (UnpackWarps + SumWarps + 2 + Issuers) * 32;
   // Whoever takes every n-th slot, stage or copy of a ring has a ring of a multiple of n: it waits
@@ -160,6 +160,14 @@ __device__ __forceinline__ uint32_t scale_bits(const __nv_bfloat16* p) {
   uint32_t v;
   asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
+}
+// 2, 4 or 8 scales, two in each even place (a single one has no pairs)
+template <int N>
+__device__ __forceinline__ void scale_pairs(uint32_t (&to)[N], const __nv_bfloat16* p) {
+  if constexpr (N == 2) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(to[0]) : "l"(p));
+  else if constexpr (N == 4) asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(to[0]), "=r"(to[2]) : "l"(p));
+  else if constexpr (N == 8)
+    asm volatile("ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(to[0]), "=r"(to[2]), "=r"(to[4]), "=r"(to[6]) : "l"(p));
 }
 __device__ __forceinline__ float scale_of_bits(uint32_t v) {
   float f;
@@ -303,32 +311,29 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
       uint64_t* const emptied = &S.w_empty[w.stage];
       const uint32_t a_seen = over(&S.done[a.stage], a.phase ^ 1);
       const uint32_t to = lanes + a.stage * Z::ACols;
-      constexpr int kAtOnce = Z::Chunks < 2 ? 1 : 2;
-#pragma unroll
-      for (int c = 0; c < Z::Chunks; c += kAtOnce) {
-        uint32_t r[16 * kAtOnce];
+      // two chunks at a time; where there are registers, four before the slot's last use is waited for
+      constexpr int kAtOnce = Z::Chunks < 2 ? 1 : 2, kFirst = Z::Chunks >= 4 && Z::Threads <= 512 ? 2 : 1;
+      uint32_t r[kFirst][16 * kAtOnce];
+      const auto unpack = [&](int c, uint32_t (&to)[16 * kAtOnce]) {
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
           const uint32_t l = ZERO ? less_of(less[ZERO ? c + u : 0]) : less[0];
-          unpack8(r + 16 * u, v[c + u].x, l);
-          unpack8(r + 16 * u + 4, v[c + u].y, l);
-          unpack8(r + 16 * u + 8, v[c + u].z, l);
-          unpack8(r + 16 * u + 12, v[c + u].w, l);
+          unpack8(to + 16 * u, v[c + u].x, l);
+          unpack8(to + 16 * u + 4, v[c + u].y, l);
+          unpack8(to + 16 * u + 8, v[c + u].z, l);
+          unpack8(to + 16 * u + 12, v[c + u].w, l);
         }
-        if (c == 0) {
-          if (!(ok = wait_for(&S.done[a.stage], a.phase ^ 1, waits, a_seen))) break;
-          tc_fence_after();
-        }
-        if constexpr (kAtOnce == 1) store16(to, r);
-        else store32(to + 16 * c, r);
-      }
-      if (!ok) break;
-      sub += Z::Teams;
-      whole();
-      const uint32_t w_seen = over(&S.w_full[w.stage], w.phase);
-      if (ZERO && --left > 0) {
-        if (stage >= plan.stages) seek();
-        zeros();
+      };
+#pragma unroll
+      for (int i = 0; i < kFirst; ++i) unpack(i * kAtOnce, r[i]);
+      if (!(ok = wait_for(&S.done[a.stage], a.phase ^ 1, waits, a_seen))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int c = 0; c < Z::Chunks; c += kAtOnce) {
+        const int i = c / kAtOnce;
+        if (i >= kFirst) unpack(c, r[i % kFirst]);
+        if constexpr (kAtOnce == 1) store16(to, r[0]);
+        else store32(to + 16 * c, r[i % kFirst]);
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_fence_before();
@@ -339,8 +344,14 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         // stored (an arrival before the stores has let the next copy into the stage under them)
         mbar_arrive(emptied);
       }
-      if ((ZERO ? left : --left) > 0) {
-        if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits, w_seen))) break;
+      sub += Z::Teams;
+      whole();
+      if (--left > 0) {
+        if constexpr (ZERO) {
+          if (stage >= plan.stages) seek();
+          zeros();
+        }
+        if (!(ok = wait_for(&S.w_full[w.stage], w.phase, waits))) break;
         weights();
       }
       a.skip(Z::Teams, Z::Slots);
@@ -352,20 +363,26 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     RingAt d;
     uint32_t seen = 0;
     const int g0 = plan.first * (kStageK / GROUP), g1 = (plan.first + plan.stages) * (kStageK / GROUP);
-    constexpr int kBoth = Z::Columns * Z::GS <= 16 && Z::Slots >= 4 ? 2 : 1, kGroups = kBoth * Z::GS;      // slots taken at once
-    constexpr int kAhead = kGroups <= 2 ? 2 : 1;                 // times their groups' scales are on their way
-    // scales are asked for in the order of use, over the ends of tiles
-    uint32_t next[kAhead][kGroups];
+    constexpr int kAhead = Z::GS <= 2 && NT < 128 ? 2 : 1;   // slots whose scales are on their way
+    // Scales are asked for in the order of use, over the ends of tiles: a slot's at once, where its
+    // groups' 2 GS bytes are aligned (then as pairs in the even places), or one by one.
+    const bool pairs = Z::GS > 1 && P.groups % Z::GS == 0 && reinterpret_cast<uintptr_t>(P.scale) % (2 * Z::GS) == 0;
+    const bool even = P.V % 2 == 0 && reinterpret_cast<uintptr_t>(P.out) % 4 == 0;
+    uint32_t next[kAhead][Z::GS];
     int ask_item = item0, ask = g0;
     const __nv_bfloat16* scale = nullptr;
     const auto seek = [&] {
       scale = P.scale + (size_t)min(plan.col0(ask_item) + row, P.V - 1) * P.groups;
       ahead(P.scale, (size_t)min(plan.col0(ask_item + plan.step) + row, P.V - 1) * P.groups, P.groups);
     };
-    const auto fetch = [&](uint32_t (&to)[kGroups]) {
+    const auto fetch = [&](uint32_t (&to)[Z::GS]) {
+      if (pairs) {
+        scale_pairs(to, scale + min(ask, P.groups - Z::GS));
+      } else {
 #pragma unroll
-      for (int i = 0; i < kGroups; ++i) to[i] = scale_bits(scale + min(ask + i, P.groups - 1));
-      if ((ask += kGroups) >= g1) {
+        for (int i = 0; i < Z::GS; ++i) to[i] = scale_bits(scale + min(ask + i, P.groups - 1));
+      }
+      if ((ask += Z::GS) >= g1) {
         ask = g0;
         ask_item += plan.step;
         seek();
@@ -378,34 +395,26 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
       const int v = plan.col0(item) + row;
 #pragma unroll
       for (int c = 0; c < Z::Columns; ++c) acc[c] = 0.f;
-      for (int g = g0; ok && g < g1; g += kGroups) {
-        float s[kGroups];
+      for (int g = g0; ok && g < g1; g += Z::GS) {
+        float s[Z::GS];
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-          s[i] = scale_of_bits(next[0][i]);
+        for (int i = 0; i < Z::GS; ++i)
+          s[i] = pairs && (i & 1) ? scale_of_bits(next[0][i & ~1] >> 16) : scale_of_bits(next[0][i]);
 #pragma unroll
-          for (int u = 1; u < kAhead; ++u) next[u - 1][i] = next[u][i];
-        }
+        for (int u = 1; u < kAhead; ++u)
+#pragma unroll
+          for (int i = 0; i < Z::GS; ++i) next[u - 1][i] = next[u][i];
         fetch(next[kAhead - 1]);
-        uint32_t from[kBoth];
-        uint64_t* taken[kBoth];
-#pragma unroll
-        for (int u = 0; u < kBoth; ++u) {
-          ok = ok && wait_for(&S.done[d.stage], d.phase, waits, u == 0 ? seen : 0);
-          from[u] = lanes + d.stage * Z::DCols;
-          taken[u] = &S.ready[d.stage];
-          d.next(Z::Slots);
-        }
-        if (!ok) break;
+        if (!(ok = wait_for(&S.done[d.stage], d.phase, waits, seen))) break;
         tc_fence_after();
-        constexpr int kOnce = Z::Columns < 32 ? 32 / Z::Columns : 1;       // groups read at once
+        const uint32_t from = lanes + d.stage * Z::DCols;
 #pragma unroll
-        for (int i = 0; i < kGroups; i += kOnce) {
-          if (i > 0 && g + i >= P.groups) break;       // behind the row's end
-          if constexpr (Z::Columns == 16 && kGroups > 1) {
+        for (int i = 0; i < Z::GS; i += Z::Columns == 16 && Z::GS > 1 ? 2 : 1) {
+          if (g + i >= P.groups) break;      // behind the row's end
+          if constexpr (Z::Columns == 16 && Z::GS > 1) {
             float x[2][16];
-            load16(x[0], from[i / Z::GS] + i % Z::GS * NT);
-            load16(x[1], from[(i + 1) / Z::GS] + (i + 1) % Z::GS * NT);
+            load16(x[0], from + i * NT);
+            load16(x[1], from + (i + 1) * NT);
             wait_loads();
             keep(x[0]);
             keep(x[1]);
@@ -416,34 +425,43 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
               for (int c = 0; c < 16; ++c) acc[c] = __fmaf_rn(s[i + 1], x[1][c], acc[c]);
             }
           } else {
-            add_unit<Z::Columns>(acc, from[i / Z::GS] + i % Z::GS * NT, s[i]);
+            add_unit<Z::Columns>(acc, from + i * NT, s[i]);
           }
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-#pragma unroll
-          for (int u = 0; u < kBoth; ++u) mbar_arrive(taken[u]);
-        }
+        if (lane == 0) mbar_arrive(&S.ready[d.stage]);
+        d.next(Z::Slots);
         seen = over(&S.done[d.stage], d.phase);
       }
       if (!ok) {
 #pragma unroll
         for (int c = 0; c < Z::Columns; ++c) acc[c] = NAN;
       }
-      if (split == 1 && v < P.V) {
+      if (split == 1) {
         const int r0 = plan.row0(item, NT) + part * Z::Columns, rows = P.n - r0;
         const size_t o = (size_t)r0 * P.V + v;
-        if (P.dtype == SPEC_BF16) {
-          __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(P.out) + o;
+        if (P.dtype == SPEC_BF16 && even) {
+          // two lanes exchange columns: each stores two neighbours of a row at once
+          __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(P.out) + o + (lane & 1 ? (ptrdiff_t)P.V - 1 : 0);
 #pragma unroll
-          for (int c = 0; c < Z::Columns; ++c, to += P.V)
-            if (c < rows) *to = __float2bfloat16_rn(acc[c]);
-        } else {
-          float* to = reinterpret_cast<float*>(P.out) + o;
+          for (int c = 0; c < Z::Columns; c += 2, to += 2 * (size_t)P.V) {
+            const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? acc[c] : acc[c + 1], 1);
+            const __nv_bfloat162 two = lane & 1 ? __floats2bfloat162_rn(other, acc[c + 1]) : __floats2bfloat162_rn(acc[c], other);
+            if (c + (lane & 1) < rows && v < P.V) *reinterpret_cast<__nv_bfloat162*>(to) = two;
+          }
+        } else if (v < P.V) {
+          if (P.dtype == SPEC_BF16) {
+            __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(P.out) + o;
 #pragma unroll
-          for (int c = 0; c < Z::Columns; ++c, to += P.V)
-            if (c < rows) *to = acc[c];
+            for (int c = 0; c < Z::Columns; ++c, to += P.V)
+              if (c < rows) *to = __float2bfloat16_rn(acc[c]);
+          } else {
+            float* to = reinterpret_cast<float*>(P.out) + o;
+#pragma unroll
+            for (int c = 0; c < Z::Columns; ++c, to += P.V)
+              if (c < rows) *to = acc[c];
+          }
         }
       }
     }
