@@ -6,8 +6,8 @@
 //
 // Both kernels read and write each value once: HBM bounds them, and the instructions
 // of a weight come next (4 for a bf16 weight, from its bits to its place in a word).  A
-// warp takes kRows rows, 32 words of 8 weights of each at a time, so that their loads are
-// on their way together.
+// warp takes several rows, or several stretches of one, so that their loads are on their way
+// together.
 #include "rows.cuh"
 #include "serve.cuh"
 
@@ -192,8 +192,8 @@ __device__ __forceinline__ bool code_quickly(const Eight<DT>& w, const Range& r,
   return quick;
 }
 
-// A warp takes ROWS rows, LANES lanes a group, a lane 8 weights.
-template <int DT, int LANES, bool ZERO, int ROWS>
+// A warp takes ROWS rows, COLS times 32 words of each at a time; LANES lanes a group, a lane 8 weights.
+template <int DT, int LANES, bool ZERO, int ROWS, int COLS>
 __global__ void __launch_bounds__(kW4Threads) quantize_kernel(const __grid_constant__ W4Params P) {
   constexpr int PER = 32 / LANES, BYTES = 8 * RowType<DT>::ES;
   const int lane = threadIdx.x & 31, words = P.H / 8;
@@ -205,33 +205,38 @@ __global__ void __launch_bounds__(kW4Threads) quantize_kernel(const __grid_const
   const long long at = v0 * P.groups + lane / LANES;
   const bool leads = lane % LANES == 0;
   uint32_t bad = 0;                          // a bit a row
-  for (int g0 = 0; g0 < P.groups; g0 += PER, from += 32 * BYTES, to += 32) {
-    const bool live = g0 * LANES + lane < words;
-    Eight<DT> w[ROWS];
+  for (int g0 = 0; g0 < P.groups; g0 += PER * COLS, from += COLS * 32 * BYTES, to += COLS * 32) {
+    Eight<DT> w[ROWS][COLS];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      w[r].zero();
-      if (live && r < rows) w[r].load(from + (size_t)(r * words) * BYTES);
-    }
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const Range range = range_of<DT, LANES, ZERO>(w[r]);
-      Coded c;
-      const bool quick = code_quickly<DT, ZERO>(w[r], range, c);
-      if (!__all_sync(0xffffffffu, quick)) {
-        if (!quick) c = code_slowly<DT, ZERO>(w[r], range);
-        if (live && range.most >= 0x7F800000u) bad |= 1u << r;
-        // (the lanes of a group agree on its scale and zero point whichever way they took)
+      for (int c = 0; c < COLS; ++c) {
+        w[r][c].zero();
+        if (g0 * LANES + c * 32 + lane < words && r < rows) w[r][c].load(from + (size_t)(r * words + c * 32) * BYTES);
       }
-      if (live && r < rows) {
-        to[r * words] = c.word;
-        if (leads) {
-          const long long o = at + g0 + (long long)r * P.groups;
-          P.scale[o] = __float2bfloat16_rn(c.s);
-          if (ZERO) P.zero[o] = (uint8_t)c.zero;
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        if (COLS > 1 && g0 + c * PER >= P.groups) break;
+        const bool live = g0 * LANES + c * 32 + lane < words;
+        const Range range = range_of<DT, LANES, ZERO>(w[r][c]);
+        Coded code;
+        const bool quick = code_quickly<DT, ZERO>(w[r][c], range, code);
+        // (the lanes of a group agree on its scale and zero point whichever way they take)
+        if (!__all_sync(0xffffffffu, quick)) {
+          if (!quick) code = code_slowly<DT, ZERO>(w[r][c], range);
+          if (live && range.most >= 0x7F800000u) bad |= 1u << r;
+        }
+        if (live && r < rows) {
+          to[r * words + c * 32] = code.word;
+          if (leads) {
+            const long long o = at + g0 + c * PER + (long long)r * P.groups;
+            P.scale[o] = __float2bfloat16_rn(code.s);
+            if (ZERO) P.zero[o] = (uint8_t)code.zero;
+          }
         }
       }
-    }
   }
   if (P.status) {
     bad = __reduce_or_sync(0xffffffffu, bad);
@@ -242,47 +247,52 @@ __global__ void __launch_bounds__(kW4Threads) quantize_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 // read back: exact whole numbers times the scale, rounded once
 
-template <int DT, bool ZERO, int ROWS>
+template <int DT, bool ZERO, int ROWS, int COLS>
 __global__ void __launch_bounds__(kW4Threads) dequantize_kernel(const __grid_constant__ W4Params P, int log_per) {
   constexpr int EACH = DT == SPEC_BF16 ? 1 : 2;          // lanes a word: a lane writes 16 bytes
   const int lane = threadIdx.x & 31, words = P.H / 8;
   const long long v0 = (blockIdx.x * (long long)(kW4Threads / 32) + (threadIdx.x >> 5)) * ROWS;
   if (v0 >= P.V) return;
   const int rows = (int)min((long long)ROWS, P.V - v0);
-  for (int k = lane; k < words * EACH; k += 32) {
-    const int at = k / EACH, g = at >> log_per;
-    uint32_t word[ROWS], s[ROWS], z[ROWS];
+  for (int k0 = lane; k0 < words * EACH; k0 += 32 * COLS) {
+    uint32_t word[ROWS][COLS], s[ROWS][COLS], z[ROWS][COLS];
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      const long long v = v0 + (r < rows ? r : 0);
-      word[r] = __ldg(P.packed + v * words + at);
-      s[r] = __ldg(reinterpret_cast<const uint16_t*>(P.scale) + v * P.groups + g);
-      z[r] = ZERO ? __ldg(P.zero + v * P.groups + g) : 8u;
-    }
+    for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-    for (int r = 0; r < ROWS; ++r) {
-      if (r >= rows) continue;
-      uint32_t q[4];
-      uint4 o;
-      if constexpr (DT == SPEC_BF16) {
-        unpack8(q, word[r], less_of(z[r]));
-        const uint32_t both = s[r] * 0x10001u;
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(q[0]), "r"(both));
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(q[1]), "r"(both));
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.z) : "r"(q[2]), "r"(both));
-        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.w) : "r"(q[3]), "r"(both));
-      } else {
-        unpack8(q, word[r] >> (k & 1) * 8, less_of(z[r]));       // the pairs 0 and 1, or 2 and 3
-        const float f = __uint_as_float(s[r] << 16);
-        o = make_uint4(__float_as_uint(bf16_lo(q[0]) * f), __float_as_uint(bf16_hi(q[0]) * f), __float_as_uint(bf16_lo(q[1]) * f),
-                       __float_as_uint(bf16_hi(q[1]) * f));
+      for (int c = 0; c < COLS; ++c) {
+        const long long v = v0 + (r < rows ? r : 0);
+        const int at = min(k0 + 32 * c, words * EACH - 1) / EACH, g = at >> log_per;
+        word[r][c] = __ldg(P.packed + v * words + at);
+        s[r][c] = __ldg(reinterpret_cast<const uint16_t*>(P.scale) + v * P.groups + g);
+        z[r][c] = ZERO ? __ldg(P.zero + v * P.groups + g) : 8u;
       }
-      reinterpret_cast<uint4*>(P.out)[(v0 + r) * words * EACH + k] = o;
-    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) {
+        const int k = k0 + 32 * c;
+        if (r >= rows || (COLS > 1 && k >= words * EACH)) continue;
+        uint32_t q[4];
+        uint4 o;
+        if constexpr (DT == SPEC_BF16) {
+          unpack8(q, word[r][c], less_of(z[r][c]));
+          const uint32_t both = s[r][c] * 0x10001u;
+          asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.x) : "r"(q[0]), "r"(both));
+          asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.y) : "r"(q[1]), "r"(both));
+          asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.z) : "r"(q[2]), "r"(both));
+          asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(o.w) : "r"(q[3]), "r"(both));
+        } else {
+          unpack8(q, word[r][c] >> (k & 1) * 8, less_of(z[r][c]));       // the pairs 0 and 1, or 2 and 3
+          const float f = __uint_as_float(s[r][c] << 16);
+          o = make_uint4(__float_as_uint(bf16_lo(q[0]) * f), __float_as_uint(bf16_hi(q[0]) * f), __float_as_uint(bf16_lo(q[1]) * f),
+                         __float_as_uint(bf16_hi(q[1]) * f));
+        }
+        reinterpret_cast<uint4*>(P.out)[(v0 + r) * words * EACH + k] = o;
+      }
   }
 }
 
-// Rows of a warp: as many as leave every SM 16 warps.
+// A warp takes kRows rows at once where that leaves every SM 16 warps, else as much of one row.
 template <int MOST>
 bool few(int V, int nsm) { return V < 16ll * nsm * MOST; }
 int blocks(int V, int rows) { return (int)((V + (kW4Threads / 32) * (long long)rows - 1) / (kW4Threads / 32 * rows)); }
@@ -290,8 +300,8 @@ int blocks(int V, int rows) { return (int)((V + (kW4Threads / 32) * (long long)r
 template <int DT, int LANES, bool ZERO>
 void quantize(const W4Params& P, int nsm, cudaStream_t s) {
   constexpr int kRows = DT == SPEC_BF16 ? 4 : 2;
-  if (few<kRows>(P.V, nsm)) quantize_kernel<DT, LANES, ZERO, 1><<<blocks(P.V, 1), kW4Threads, 0, s>>>(P);
-  else quantize_kernel<DT, LANES, ZERO, kRows><<<blocks(P.V, kRows), kW4Threads, 0, s>>>(P);
+  if (few<kRows>(P.V, nsm)) quantize_kernel<DT, LANES, ZERO, 1, kRows><<<blocks(P.V, 1), kW4Threads, 0, s>>>(P);
+  else quantize_kernel<DT, LANES, ZERO, kRows, 1><<<blocks(P.V, kRows), kW4Threads, 0, s>>>(P);
 }
 template <int LANES>
 void quantize_of(const W4Params& P, int nsm, cudaStream_t s) {
@@ -301,8 +311,8 @@ void quantize_of(const W4Params& P, int nsm, cudaStream_t s) {
 template <int DT, bool ZERO>
 void dequantize(const W4Params& P, int nsm, cudaStream_t s) {
   const int log_per = P.group == 128 ? 4 : P.group == 64 ? 3 : 2;
-  if (few<4>(P.V, nsm)) dequantize_kernel<DT, ZERO, 1><<<blocks(P.V, 1), kW4Threads, 0, s>>>(P, log_per);
-  else dequantize_kernel<DT, ZERO, 4><<<blocks(P.V, 4), kW4Threads, 0, s>>>(P, log_per);
+  if (few<4>(P.V, nsm)) dequantize_kernel<DT, ZERO, 1, 4><<<blocks(P.V, 1), kW4Threads, 0, s>>>(P, log_per);
+  else dequantize_kernel<DT, ZERO, 4, 1><<<blocks(P.V, 4), kW4Threads, 0, s>>>(P, log_per);
 }
 
 }  // namespace

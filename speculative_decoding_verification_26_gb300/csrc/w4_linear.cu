@@ -30,7 +30,7 @@ namespace {
 constexpr int kRows = 128;                   // vocabulary rows of a tile
 constexpr int kStageK = 256;                 // k of a stage of weights
 constexpr int kWeightStage = kRows * kStageK / 2;        // 16 KB
-constexpr int kMaxSplit = 8;
+constexpr int kMaxSplit = 4, kSplitStages = 16;          // of a tile's k, from so many stages on
 
 template <int NT, int GROUP>
 struct Shape {
@@ -585,8 +585,10 @@ cudaError_t launch(const W4Params& P, int nsm, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const long long items = ((P.n + NT - 1ll) / NT) * ((P.V + kRows - 1ll) / kRows);
   const int stages = (P.H + kStageK - 1) / kStageK;
+  // V = 2048, 8 rows: 12.3 us in one part and 8.2 in four for 16 stages, 18.5 and 10.3 for 32; 8.2 either way
+  // for 8 (64 rows: 10.3 and 11.9), where the joining costs what it saves
   int split = 1;
-  while (split < kMaxSplit && 2 * split <= stages && 2 * split * items <= nsm) split *= 2;
+  while (split < kMaxSplit && stages >= kSplitStages && 2 * split * items <= nsm) split *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(split > 1 ? items * split : items < nsm ? items : nsm));
   cfg.blockDim = dim3(Shape<NT, GROUP>::Threads);
