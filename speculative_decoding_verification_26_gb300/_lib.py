@@ -637,20 +637,24 @@ def _code(h, t):
     return _dtype_code(t) if code is None else code
 
 
-def _w4_weights(h, packed, scale, zero, group):
-    """(V, H) of 4-bit weights, checked."""
+def _take(t, name, dtype, shape, dev):
+    """The address of a tensor of this dtype and shape on `dev`, checked; None of None."""
+    if t is None:
+        return None
+    if not (t.dtype is dtype and t.shape == shape and t.get_device() == dev.index and t.is_contiguous()):
+        _check(t, name, dtype, shape, dev)
+    return t.data_ptr()
+
+
+def _w4_sizes(packed, group):
+    """(V, H, the shape of scales) of 4-bit weights."""
     if packed.dim() != 2:
         raise ValueError("packed is [V, H / 2]")
     if group not in W4_GROUPS:
         raise ValueError(f"group must be one of {W4_GROUPS}, got {group}")
     V, H = packed.shape
     H *= 2
-    dev = packed.device
-    _check(packed, "packed", h.u8)
-    per = (V, -(-H // group))
-    _want(scale, "scale", h.bf16, per, dev)
-    _want(zero, "zero", h.u8, per, dev)
-    return V, H
+    return V, H, (V, -(-H // group))
 
 
 def quantize_w4(weight, group=128, *, zero=False, out=None):
@@ -667,11 +671,16 @@ def quantize_w4(weight, group=128, *, zero=False, out=None):
     V, H = weight.shape
     dev = weight.device
     _check(weight, "weight")
-    o = out or {}
     per = (V, -(-H // group))
-    packed, scale = _result(o, "packed", (V, H // 2), h.u8, dev), _result(o, "scale", per, h.bf16, dev)
-    z = _result(o, "zero", per, h.u8, dev) if zero else None
-    st = _result(o, "status", (V,), h.i32, dev)
+    if out is None:
+        empty = h.empty
+        packed, scale = empty((V, H // 2), dtype=h.u8, device=dev), empty(per, dtype=h.bf16, device=dev)
+        z = empty(per, dtype=h.u8, device=dev) if zero else None
+        st = empty((V,), dtype=h.i32, device=dev)
+    else:
+        packed, scale = _result(out, "packed", (V, H // 2), h.u8, dev), _result(out, "scale", per, h.bf16, dev)
+        z = _result(out, "zero", per, h.u8, dev) if zero else None
+        st = _result(out, "status", (V,), h.i32, dev)
     _call(h, dev, h.quantize, weight.data_ptr(), _code(h, weight), V, H, group, packed.data_ptr(), scale.data_ptr(),
           _addr(z), st.data_ptr())
     r = {"packed": packed, "scale": scale, "status": st}
@@ -684,10 +693,13 @@ def dequantize_w4(packed, scale, zero=None, *, group=128, dtype=None, out=None):
     """The weights [V, H] that quantize_w4's results stand for, in `dtype` (bf16
     by default, or fp32).  Returns {"weight": [V, H]} (see spec_w4_dequantize)."""
     h = _hot()
-    V, H = _w4_weights(h, packed, scale, zero, group)
+    V, H, per = _w4_sizes(packed, group)
     dev = packed.device
-    w = _result(out or {}, "weight", (V, H), dtype or h.bf16, dev)
-    _call(h, dev, h.dequantize, packed.data_ptr(), scale.data_ptr(), _addr(zero), V, H, group, w.data_ptr(), _code(h, w))
+    _check(packed, "packed", h.u8)
+    s, z = _take(scale, "scale", h.bf16, per, dev), _take(zero, "zero", h.u8, per, dev)
+    dtype = dtype or h.bf16
+    w = h.empty((V, H), dtype=dtype, device=dev) if out is None else _result(out, "weight", (V, H), dtype, dev)
+    _call(h, dev, h.dequantize, packed.data_ptr(), s, z, V, H, group, w.data_ptr(), _code(h, w))
     return {"weight": w}
 
 
@@ -695,19 +707,22 @@ def linear_w4(hidden, packed, scale, zero=None, *, group=128, dtype=None, out=No
     """hidden [..., H] (bf16) times 4-bit weights (quantize_w4), transposed:
     {"logits": [..., V]} in `dtype` (bf16 by default, or fp32) (see spec_linear_w4)."""
     h = _hot()
-    V, H = _w4_weights(h, packed, scale, zero, group)
+    V, H, per = _w4_sizes(packed, group)
     dev = packed.device
+    _check(packed, "packed", h.u8)
+    s, z = _take(scale, "scale", h.bf16, per, dev), _take(zero, "zero", h.u8, per, dev)
     shape = hidden.shape
     if len(shape) < 1 or shape[-1] != H:
         raise ValueError(f"hidden must have shape [..., {H}], got {tuple(shape)}")
-    _check(hidden, "hidden", h.bf16, device=dev)
+    if not (hidden.dtype is h.bf16 and hidden.get_device() == dev.index and hidden.is_contiguous()):
+        _check(hidden, "hidden", h.bf16, device=dev)
     dtype = dtype or h.bf16
     if out is None:
         y = h.empty((*shape[:-1], V), dtype=dtype, device=dev)
     else:
         y = _result(out, "logits", (*shape[:-1], V), dtype, dev)
-    _call(h, dev, h.linear_w4, hidden.data_ptr(), BF16, hidden.numel() // H, packed.data_ptr(), scale.data_ptr(),
-          _addr(zero), V, H, group, y.data_ptr(), _code(h, y))
+    _call(h, dev, h.linear_w4, hidden.data_ptr(), BF16, hidden.numel() // H, packed.data_ptr(), s, z, V, H, group,
+          y.data_ptr(), _code(h, y))
     return {"logits": y}
 
 
@@ -730,20 +745,21 @@ def adjust_logits(logits, history=None, history_len=None, *, prompt_len=None, dr
     dev = logits.device
     _check(logits, "logits")
     L = D = N = 0
+    told = drafts = index = value = None
     per = (B,)
     if history is not None:
         if history.dim() != 2:
             raise ValueError("history is [B, L]")
         L = history.shape[1]
-        _want(history, "history", i32, (B, L), dev)
+        told = _take(history, "history", i32, (B, L), dev)
     elif history_len is not None or prompt_len is not None:
         raise ValueError("history_len and prompt_len are those of a history")
     if draft_tokens is not None:
         if draft_tokens.dim() != 2:
             raise ValueError("draft_tokens is [B, D]")
         D = draft_tokens.shape[1]
-        _want(draft_tokens, "draft_tokens", i32, (B, D), dev)
-        if 0 < D < R - 1 or D == 0 and R > 1:
+        drafts = _take(draft_tokens, "draft_tokens", i32, (B, D), dev)
+        if D < R - 1:
             raise ValueError(f"draft_tokens has {D} tokens for {R} rows")
     if (bias_index is None) != (bias_value is None):
         raise ValueError("bias_index and bias_value go together")
@@ -751,27 +767,19 @@ def adjust_logits(logits, history=None, history_len=None, *, prompt_len=None, dr
         if bias_index.dim() != 2:
             raise ValueError("bias_index is [B, N]")
         N = bias_index.shape[1]
-        _want(bias_index, "bias_index", i32, (B, N), dev)
-        _want(bias_value, "bias_value", f32, (B, N), dev)
-    _want(history_len, "history_len", i32, per, dev)
-    _want(prompt_len, "prompt_len", i32, per, dev)
-    _want(gamma, "gamma", i32, per, dev)
-    _want(repetition, "repetition", f32, per, dev)
-    _want(frequency, "frequency", f32, per, dev)
-    _want(presence, "presence", f32, per, dev)
-    _want(mask, "mask", i32, (B, R, (V + 31) // 32), dev)
-    if out is None:
-        y, st = logits, h.empty(per, dtype=i32, device=dev)
-    else:
-        y = out.get("logits")
-        if y is None:
-            y = logits
-        elif y is not logits:
-            _want(y, "out['logits']", logits.dtype, logits.shape, dev)
-        st = _result(out, "status", per, i32, dev)
-    _call(h, dev, h.adjust, logits.data_ptr(), y.data_ptr(), _code(h, logits), B, R, V, _addr(history), L,
-          _addr(history_len), _addr(prompt_len), _addr(draft_tokens), D, _addr(gamma), _addr(repetition),
-          _addr(frequency), _addr(presence), _addr(bias_index), _addr(bias_value), N, _addr(mask), st.data_ptr())
+        index, value = _take(bias_index, "bias_index", i32, (B, N), dev), _take(bias_value, "bias_value", f32, (B, N), dev)
+    y = None if out is None else out.get("logits")
+    if y is None:
+        y = logits
+    to = logits.data_ptr() if y is logits else _take(y, "out['logits']", logits.dtype, logits.shape, dev)
+    st = None if out is None else out.get("status")
+    if st is None:
+        st = h.empty(per, dtype=i32, device=dev)
+    _call(h, dev, h.adjust, logits.data_ptr(), to, _code(h, logits), B, R, V, told, L,
+          _take(history_len, "history_len", i32, per, dev), _take(prompt_len, "prompt_len", i32, per, dev), drafts, D,
+          _take(gamma, "gamma", i32, per, dev), _take(repetition, "repetition", f32, per, dev),
+          _take(frequency, "frequency", f32, per, dev), _take(presence, "presence", f32, per, dev), index, value, N,
+          _take(mask, "mask", i32, (B, R, (V + 31) // 32), dev), _take(st, "status", i32, per, dev))
     return {"logits": y, "status": st}
 
 

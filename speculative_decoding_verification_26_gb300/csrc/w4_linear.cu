@@ -9,18 +9,28 @@
 // weight is rounded, and a sum of the tensor cores, which cut off at every addition, is at
 // most 128 long.
 //
-// A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states.  The k of a
-// tile goes by stages of 256 (16 KB of weights), cut into slots of whole groups: a slot has its
-// own columns of tensor memory for A and for the sums of its groups, and two barriers, "ready"
-// (unpacked, and the sums of its last use taken) and "done" (products finished): one wait and
-// one commit of the issuing warp a slot.  With barriers of their own for A, hidden states and
-// sums at every 128 k the issuing warp took 800 clocks for what HBM brings in 360.  Roles:
-//   warps 0-7    weights from shared memory to bf16 in tensor memory: thread = vocabulary row
-//                (32 (w % 4) on); warps 0-3 and 4-7 share a stage (0-3 alone for NT = 128);
-//   the next 4   groups' sums to registers and out (8, each half of the columns, for NT = 128);
-//   then one warp each: copies of weights, copies of hidden states, products.
-// Where there are fewer tiles than SMs, a cluster of CTAs splits the k of a tile, and the
-// parts are joined through distributed shared memory in the order of their ranks.
+// A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states (16 to 128, the
+// least that holds them: 39 us for 1 to 16 rows against 151936 x 2048 weights in groups of 128, 41
+// for 32, 48 for 64, 70 for 128, 253 for 512).  The k of a tile goes by stages of 256 (16 KB of
+// weights), cut into slots of whole groups: a slot has its own columns of tensor memory for A and
+// for the sums of its groups, and two barriers, "ready" (unpacked, and the sums of its last use
+// taken) and "done" (products finished): one wait and one commit of the issuing warp a slot.
+// Roles, in warps:
+//   teams of four  weights from shared memory to bf16 in tensor memory, thread = vocabulary row;
+//                  the teams take slots in turn;
+//   four or eight  groups' sums to registers, and out;
+//   one each       copies of weights, copies of hidden states;
+//   one or two     products, in turn.
+// Where there are few tiles and much k, a cluster of CTAs splits the k of a tile, and the parts
+// are joined through distributed shared memory in the order of their ranks.
+//
+// What bounds it: for few rows the hand-overs between the roles.  The weights alone stream through
+// the ring in 28 us (5.8 TB/s), and with hand-overs but without unpacking, products and sums a call
+// takes 33 to 37; unpacking has 2.75 instructions a pair of weights.  For many rows the warps that
+// take the sums (64 columns of each group to a thread).  With barriers of their own for A, hidden
+// states and sums at every 128 k one row took 54 us; with products issued by a single lane of a
+// diverged warp 132.  mma.sync with the weights straight in registers took 108 us for up to 8 rows
+// (its m16n8k16 goes out every 20 clocks of a scheduler, and needs the scales of 16 rows a warp).
 #include "serve.cuh"
 #include "tc_gemm.cuh"
 
@@ -298,7 +308,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
 #pragma unroll
       for (int c = 0; c < Z::Chunks; ++c) less[ZERO ? c : 0] = zero[min((at + 32 * c) / GROUP, P.groups - 1)];
     };
-    int left = (tiles * plan.stages * Z::Subs - team + Z::Teams - 1) / Z::Teams;      // the team's slots
+    long long left = ((long long)tiles * plan.stages * Z::Subs - team + Z::Teams - 1) / Z::Teams;       // the team's slots
     if (left > 0) {
       if constexpr (ZERO) {
         seek();

@@ -191,6 +191,31 @@ def test_linear_large(sv, n, V, H, group):
     check_linear(sv, n, V, H, group, n == 3, F32)
 
 
+@pytest.mark.parametrize("n", [1, 20, 64, 65, 200])
+@pytest.mark.parametrize("V,H", [(130, 4096), (2500, 4352), (5000, 8192), (19000, 4160), (25000, 2080)])
+def test_linear_split(sv, V, H, n):
+    """Tiles whose k is split over two or four CTAs, or not, with a ragged end."""
+    check_linear(sv, n, V, H, (32, 64, 128)[n % 3], V % 2 == 0, F32)
+
+
+@pytest.mark.parametrize("n", [3, 70])
+def test_linear_odd_starts(sv, n):
+    """Outputs and scales off their vector boundaries, odd vocabularies."""
+    H, group = 512, 64
+    for V in (1001, 1002):
+        q, scale, z = weights_of(V, H, group, True, 3)
+        x = torch.randn(n, H, generator=gen(n)).to(BF)
+        sbuf = torch.zeros(scale.numel() + 1, dtype=BF, device="cuda")
+        sc = sbuf[1:].view(scale.shape)
+        sc.copy_(scale)
+        want = sv.linear_w4(x.cuda(), SP.pack(q).cuda(), scale.cuda(), z.cuda(), group=group)["logits"]
+        for elems in (1, 2, 3):
+            out, guard = guarded((n, V), BF, elems)
+            sv.linear_w4(x.cuda(), SP.pack(q).cuda(), sc, z.cuda(), group=group, out={"logits": out})
+            guard()
+            assert torch.equal(out, want)
+
+
 def test_linear_long_rows(sv):
     check_linear(sv, 2, 40, 65536, 128, True, F32)
     check_linear(sv, 70, 5, 32768, 32, False, F32)
@@ -246,10 +271,10 @@ def test_linear_offsets_past_32_bits(sv):
     assert ((got - want).abs() <= 16 * 2.0 ** -23 * mag + HALF[BF] * want.abs()).all()
 
 
-@pytest.mark.parametrize("n,V", [(1, 500), (8, 30000), (100, 30000)])
-def test_linear_waits_that_run_out(sv, n, V):
-    """With a limit of one cycle a call ends, and a logit is right or NaN; the next call is right."""
-    H = 1024
+@pytest.mark.parametrize("n,V,H", [(1, 500, 1024), (8, 30000, 1024), (100, 30000, 1024), (5, 700, 8192), (60, 300, 4096)])
+def test_linear_waits_that_run_out(sv, n, V, H):
+    """With a limit of one cycle a call ends, and a logit is right or NaN; the next call is right
+    (the last two split their k over a cluster)."""
     q, scale, _ = weights_of(V, H, 128, False, 9)
     packed, sc, x = SP.pack(q).cuda(), scale.cuda(), torch.randn(n, H, generator=gen(2)).to(BF).cuda()
     want = sv.linear_w4(x, packed, sc, dtype=F32)["logits"]
