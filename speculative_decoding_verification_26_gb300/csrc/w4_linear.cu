@@ -184,6 +184,17 @@ __device__ __forceinline__ float scale_of_bits(uint32_t v) {
   asm volatile("shl.b32 %0, %1, 16;" : "=f"(f) : "r"(v));
   return f;
 }
+// Zero points on their way: one, or 1, 2, 4 or 8 as bytes.
+__device__ __forceinline__ void zero_byte(uint32_t& to, const uint8_t* p) { asm volatile("ld.global.nc.u8 %0, [%1];" : "=r"(to) : "l"(p)); }
+template <int N>
+__device__ __forceinline__ void zero_bytes(uint32_t* to, const uint8_t* p) {
+  if constexpr (N == 1) zero_byte(to[0], p);
+  else if constexpr (N == 2) asm volatile("ld.global.nc.u16 %0, [%1];" : "=r"(to[0]) : "l"(p));
+  else if constexpr (N == 4) asm volatile("ld.global.nc.b32 %0, [%1];" : "=r"(to[0]) : "l"(p));
+  else asm volatile("ld.global.nc.v2.b32 {%0, %1}, [%2];" : "=r"(to[0]), "=r"(to[1]) : "l"(p));
+}
+// less_of(byte i of z): the byte, 0x43, the byte, 0x43
+__device__ __forceinline__ uint32_t less_of_byte(uint32_t z, int i) { return __byte_perm(z, 0x43u, 0x4040u | (uint32_t)i * 0x0101u); }
 // acc[c] += s * column c of a group's sums
 template <int N>
 __device__ __forceinline__ void add_unit(float (&acc)[N], uint32_t from, float s) {
@@ -292,21 +303,38 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
 #pragma unroll
       for (int c = 0; c < Z::Chunks; ++c) v[c] = shared16(at ^ (c * 16));
     };
-    uint32_t less[ZERO ? Z::Chunks : 1];
-    if constexpr (!ZERO) less[0] = less_of(8);
-    const uint8_t* zero = nullptr;
+    // zero points of the next slot's groups: all at once, GS bytes in zero[0] and zero[1], where those are
+    // aligned, or one by one
+    constexpr int kZeros = ZERO ? (Z::GS < 2 ? 2 : Z::GS) : 1;
+    uint32_t zero[kZeros];
+    const bool packed = ZERO && P.groups % Z::GS == 0 && reinterpret_cast<uintptr_t>(P.zero) % Z::GS == 0;
+    const uint8_t* zeros_of = nullptr;
     const auto seek = [&] {                  // the tile of the next slot
       while (stage >= plan.stages) {
         stage -= plan.stages;
         item += plan.step;
       }
-      zero = P.zero + (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
+      zeros_of = P.zero + (size_t)min(plan.col0(item) + row, P.V - 1) * P.groups;
       ahead(P.zero, (size_t)min(plan.col0(item + plan.step) + row, P.V - 1) * P.groups, P.groups);
     };
     const auto zeros = [&] {
-      const int at = (plan.first + stage) * kStageK + 32 * Z::Chunks * sub;
+      if constexpr (ZERO) {
+        const int g = (plan.first + stage) * (kStageK / GROUP) + sub * Z::GS;
+        if (packed) {
+          zero_bytes<Z::GS>(zero, zeros_of + min(g, P.groups - Z::GS));
+        } else {
 #pragma unroll
-      for (int c = 0; c < Z::Chunks; ++c) less[ZERO ? c : 0] = zero[min((at + 32 * c) / GROUP, P.groups - 1)];
+          for (int i = 0; i < Z::GS; ++i) zero_byte(zero[i], zeros_of + min(g + i, P.groups - 1));
+        }
+      }
+    };
+    const auto less = [&](int c) {           // of chunk c
+      if constexpr (!ZERO) {
+        return less_of(8);
+      } else {
+        const int i = c * 32 / GROUP;
+        return packed ? less_of_byte(zero[i / 4], i % 4) : less_of(zero[i]);
+      }
     };
     long long left = ((long long)tiles * plan.stages * Z::Subs - team + Z::Teams - 1) / Z::Teams;       // the team's slots
     if (left > 0) {
@@ -327,7 +355,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
       const auto unpack = [&](int c, uint32_t (&to)[16 * kAtOnce]) {
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) {
-          const uint32_t l = ZERO ? less_of(less[ZERO ? c + u : 0]) : less[0];
+          const uint32_t l = less(c + u);
           unpack8(to + 16 * u, v[c + u].x, l);
           unpack8(to + 16 * u + 4, v[c + u].y, l);
           unpack8(to + 16 * u + 8, v[c + u].z, l);
