@@ -16,7 +16,11 @@
 // are written without a read, those that it leaves whole are left alone.
 // The adjustment of a listed token stays out of the vector loops: unrolled over a vector's
 // logits it did not fit the instruction cache (64 x 8 x 151936 bf16 logits: 186 us).  Rows by bulk
-// copies through shared memory took 81 us, counting before copying 71 us.  HBM bounds both.
+// copies through shared memory took 81 us, counting before copying 71 us.
+//   What bounds it, in 64 x 8 x 151936 bf16 logits: the copy alone takes 51 us (6.1 TB/s), masks 3 us
+// more, histories of 2048 tokens 9 to 11: counting 2, the listed tokens' logits 4, their
+// stores of 2 bytes 5.  In place a mask that leaves 2 % takes 44 us, 30 of them its stores, the
+// rest the vectors that it leaves in part (84 MB of reads in 64-byte pieces).
 #include "rows.cuh"
 #include "serve.cuh"
 
@@ -250,8 +254,8 @@ __global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_
     if (lengths) {
       const int32_t* h = P.history + (size_t)b * P.L;
       const auto told = [&](int e, int v) {
-        bad |= (unsigned)(v + 1) > (unsigned)P.V;          // SPEC_ST_BAD_TOKEN is set below
-        const unsigned at = (unsigned)(v - lo);
+        bad |= (unsigned)v + 1u > (unsigned)P.V;           // SPEC_ST_BAD_TOKEN is set below
+        const unsigned at = (unsigned)v - (unsigned)lo;
         if (at < (unsigned)size) touch((int)at, e < prompt ? atomicOr(&count[at], kInPrompt) : atomicAdd(&count[at], 1u));
       };
       static_assert(SPEC_ST_BAD_TOKEN == 2, "bit 0 below stands for it");
@@ -359,10 +363,11 @@ __global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_
     const int i = item / listed, at = list[item - i * listed];
     if (removed(i, at)) continue;
     const uint32_t c = count[at];
-    float x = adjusted(Lg::value(reinterpret_cast<const Bits*>(in0 + i * row_bytes)[at]), c, lo + at, i, S, p);
+    Bits* const to = reinterpret_cast<Bits*>(out0 + i * row_bytes) + at;       // the logit, copied: it is in L2
+    float x = adjusted(Lg::value(*to), c, lo + at, i, S, p);
     if (P.biases > 0 && (c & kTouched)) x += bias[at];
     else if ((c & (kInPrompt | kCount)) == 0 && !drafted(c, lo + at, i, S)) continue;       // a draft of a later row alone
-    reinterpret_cast<Bits*>(out0 + i * row_bytes)[at] = Lg::pack(x);
+    *to = Lg::pack(x);
   }
 }
 
