@@ -10,8 +10,8 @@
 // most 128 long.
 //
 // A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states (16 to 128, the
-// least that holds them: 39 us for 1 to 16 rows against 151936 x 2048 weights in groups of 128, 41
-// for 32, 48 for 64, 70 for 128, 253 for 512).  The k of a tile goes by stages of 256 (16 KB of
+// least that holds them: 36 us for one row and 37 for 16 against 151936 x 2048 weights in groups of
+// 128, 40 for 32, 48 for 64, 70 for 128, 252 for 512).  The k of a tile goes by stages of 256 (16 KB of
 // weights), cut into slots of whole groups: a slot has its own columns of tensor memory for A and
 // for the sums of its groups, and two barriers, "ready" (unpacked, and the sums of its last use
 // taken) and "done" (products finished): one wait and one commit of the issuing warp a slot.
@@ -517,11 +517,12 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     }
   } else if (warp == kHiddenCopies) {
     RingAt x;
+    const uint32_t box_bytes = min(P.n, NT) * 128;
     for (int item = item0; ok && item < plan.items; item += plan.step) {
       for (int k = plan.first * kStageK; k < (plan.first + plan.stages) * kStageK; k += Z::XK) {
         if (!(ok = wait_for(&S.x_empty[x.stage], x.phase ^ 1, waits))) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(&S.x_full[x.stage], Z::XSlot);
+          mbar_arrive_expect_tx(&S.x_full[x.stage], box_bytes * (Z::XK / 64));
 #pragma unroll
           for (int c = 0; c < Z::XK / 64; ++c)
             copy_box(x_ring + x.stage * Z::XSlot + c * Z::XBox, &M.hidden, k + 64 * c, plan.row0(item, NT), &S.x_full[x.stage]);
@@ -619,7 +620,9 @@ template <int NT, int GROUP>
 cudaError_t launch(const W4Params& P, int nsm, cudaStream_t s) {
   W4Maps M;
   if (!encode(&M.weight, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, P.packed, P.H / 2, P.V, kRows) ||
-      !encode(&M.hidden, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, P.hidden, P.H, P.n, NT))
+      // boxes of no more rows than there are: 36.4 us for one row, 39 with a box of 16 that TMA fills
+      // up with zeros.  What the other rows of a tile hold reaches columns of the sums that nothing takes.
+      !encode(&M.hidden, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, P.hidden, P.H, P.n, P.n < NT ? P.n : NT))
     return cudaErrorInvalidValue;
   const long long items = ((P.n + NT - 1ll) / NT) * ((P.V + kRows - 1ll) / kRows);
   const int stages = (P.H + kStageK - 1) / kStageK;
