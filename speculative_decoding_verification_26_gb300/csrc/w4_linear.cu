@@ -11,7 +11,7 @@
 //
 // A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states (16 to 128, the
 // least that holds them: 36 us for one row and 37 for 16 against 151936 x 2048 weights in groups of
-// 128, 40 for 32, 48 for 64, 70 for 128, 252 for 512).  The k of a tile goes by stages of 256 (16 KB of
+// 128, 40 for 32, 46 for 64, 69 for 128, 247 for 512).  The k of a tile goes by stages of 256 (16 KB of
 // weights), cut into slots of whole groups: a slot has its own columns of tensor memory for A and
 // for the sums of its groups, and two barriers, "ready" (unpacked, and the sums of its last use
 // taken) and "done" (products finished): one wait and one commit of the issuing warp a slot.
@@ -195,24 +195,24 @@ __device__ __forceinline__ void zero_bytes(uint32_t* to, const uint8_t* p) {
 }
 // less_of(byte i of z): the byte, 0x43, the byte, 0x43
 __device__ __forceinline__ uint32_t less_of_byte(uint32_t z, int i) { return __byte_perm(z, 0x43u, 0x4040u | (uint32_t)i * 0x0101u); }
+// a += s x, two at once: each rounded once, as by fmaf
+__device__ __forceinline__ void add_two(float* a, float s, const float* x) {
+  asm("{\n .reg .b64 a, x, s;\n mov.b64 a, {%0, %1};\n mov.b64 x, {%3, %4};\n mov.b64 s, {%2, %2};\n"
+      " fma.rn.f32x2 a, x, s, a;\n mov.b64 {%0, %1}, a;\n}\n"
+      : "+f"(a[0]), "+f"(a[1])
+      : "f"(s), "f"(x[0]), "f"(x[1]));
+}
 // acc[c] += s * column c of a group's sums
 template <int N>
 __device__ __forceinline__ void add_unit(float (&acc)[N], uint32_t from, float s) {
 #pragma unroll
-  for (int c = 0; c < N; c += (N == 32 ? 32 : 16)) {
-    if constexpr (N != 32) {
-      float x[16];
-      load16(x, from + c);
-      wait_loads();
-      keep(x);
+  for (int c = 0; c < N; c += 16) {          // (32 at once left too few registers: 64 rows, groups of 32: 113 us, here 100)
+    float x[16];
+    load16(x, from + c);
+    wait_loads();
+    keep(x);
 #pragma unroll
-      for (int i = 0; i < 16; ++i) acc[c + i] = __fmaf_rn(s, x[i], acc[c + i]);
-    } else {
-      float x[32];
-      tc_load32(x, from + c);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) acc[c + i] = __fmaf_rn(s, x[i], acc[c + i]);
-    }
+    for (int i = 0; i < 16; i += 2) add_two(acc + c + i, s, x + i);
   }
 }
 // asks `count` elements from p + at on into L2
@@ -275,7 +275,6 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   const uint32_t tmem = S.tmem;
 
   const int tiles = item0 < plan.items ? (plan.items - 1 - item0) / plan.step + 1 : 0;
-  float acc[Z::Columns];
   bool ok = true;
   if (warp < Z::UnpackWarps) {
     const int quarter = warp & 3, team = warp >> 2, row = quarter * 32 + lane;
@@ -395,6 +394,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
       a.skip(Z::Teams, Z::Slots);
     }
   } else if (warp < kWeightCopies) {
+    float acc[Z::Columns];
     const int quarter = warp & 3, part = (warp - Z::UnpackWarps) >> 2, row = quarter * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16) + Z::DColumn + part * Z::Columns;
     if (lane < Z::Slots) mbar_arrive(&S.ready[lane]);            // nothing to take of the first use
@@ -457,10 +457,10 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
             keep(x[0]);
             keep(x[1]);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) acc[c] = __fmaf_rn(s[i], x[0][c], acc[c]);
+            for (int c = 0; c < 16; c += 2) add_two(acc + c, s[i], x[0] + c);
             if (g + i + 1 < P.groups) {
 #pragma unroll
-              for (int c = 0; c < 16; ++c) acc[c] = __fmaf_rn(s[i + 1], x[1][c], acc[c]);
+              for (int c = 0; c < 16; c += 2) add_two(acc + c, s[i + 1], x[1] + c);
             }
           } else {
             add_unit<Z::Columns>(acc, from + i * NT, s[i]);
@@ -502,6 +502,14 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
           }
         }
       }
+    }
+    if (split > 1) {
+      // With its last sums taken a warp knows that every product and so every copy is done: the ring is
+      // free.  Otherwise copies may be in flight, and NaN stands for the sums.
+      if (!ok) drain_after_failure();
+      float* const parts = reinterpret_cast<float*>(ring);         // [NT][128]
+#pragma unroll
+      for (int c = 0; c < Z::Columns; ++c) parts[(part * Z::Columns + c) * kRows + row] = acc[c];
     }
   } else if (warp == kWeightCopies) {
     RingAt w;
@@ -567,15 +575,8 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   __syncwarp();
 
   if (split > 1) {
-    // every copy has landed and every product is done (or NaN stands for them): the ring is free
-    float* const parts = reinterpret_cast<float*>(ring);           // [NT][128]
     const bool sums = warp >= Z::UnpackWarps && warp < kWeightCopies;
     const int row = (warp & 3) * 32 + lane, part = (warp - Z::UnpackWarps) >> 2;
-    __syncthreads();
-    if (sums) {
-#pragma unroll
-      for (int c = 0; c < Z::Columns; ++c) parts[(part * Z::Columns + c) * kRows + row] = acc[c];
-    }
     cluster_sync();
     if (sums) {
       const int v = plan.col0(item0) + row, r0 = plan.row0(item0, NT);
