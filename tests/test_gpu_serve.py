@@ -545,3 +545,66 @@ def test_a_decode_step(sv):
             if i < k:
                 qr = torch.softmax(q[b, i].cpu().double() / 0.8, 0)
                 assert float(u[b, i]) * qr[v] < pr[v] * (1 + 1e-5)
+
+
+# --------------------------------------------------------- calls beside one another
+
+@pytest.mark.parametrize("n", [1, 5, 17, 33, 65, 130])
+def test_linear_after_a_call_that_leaves_nan(sv, n):
+    """Rows that a call does not have reach nothing, whatever the tile holds for them."""
+    V, H = 3000, 512
+    q, scale, _ = weights_of(V, H, 128, False, 6)
+    packed, sc, x = SP.pack(q).cuda(), scale.cuda(), torch.randn(n, H, generator=gen(n)).to(BF).cuda()
+    want = sv.linear_w4(x, packed, sc)["logits"]
+    assert torch.isfinite(want).all()
+    poison = torch.full((512, H), NAN, dtype=BF, device="cuda")
+    for rows in (512, 64, 32, 16):
+        assert torch.isnan(sv.linear_w4(poison[:rows], packed, sc)["logits"]).all()
+        assert torch.equal(sv.linear_w4(x, packed, sc)["logits"], want)
+
+
+def test_host_threads(sv):
+    """Threads with a stream each, at once: the results of the same calls one after another."""
+    import threading
+    V, H, B, R = 5000, 512, 4, 5
+    work = []
+    for k in range(4):
+        w = torch.randn(V, H, generator=gen(60 + k)).to(BF).cuda()
+        x = torch.randn(B, R, H, generator=gen(70 + k)).to(BF).cuda()
+        _, a = request(B, R, V, 300, 80 + k, biases=8, allowed=0.9)
+        work.append((w, x, {n: v.cuda() for n, v in a.items()}))
+
+    def step(w, x, a):
+        w4 = sv.quantize_w4(w, 64, zero=True)
+        rows = sv.linear_w4(x, w4["packed"], w4["scale"], w4["zero"], group=64)["logits"]
+        return sv.adjust_logits(rows, **a)["logits"]
+    want = [step(*w) for w in work]
+    torch.cuda.synchronize()
+    got, streams = [[] for _ in work], [torch.cuda.Stream() for _ in work]
+
+    def run(k):
+        with torch.cuda.stream(streams[k]):
+            for _ in range(8):
+                got[k].append(step(*work[k]))
+            streams[k].synchronize()
+    threads = [threading.Thread(target=run, args=(k,)) for k in range(len(work))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for k, w in enumerate(want):
+        assert len(got[k]) == 8 and all(torch.equal(g.view(torch.int16), w.view(torch.int16)) for g in got[k])
+
+
+def test_quantize_offsets_past_32_bits(sv):
+    """More than 2^32 weights."""
+    V, H, group = 70_000_001, 64, 32
+    w = torch.randn(V, H, dtype=BF, device="cuda")
+    r = sv.quantize_w4(w, group, zero=True)
+    back = sv.dequantize_w4(r["packed"], r["scale"], r["zero"], group=group)["weight"]
+    at = torch.cat([torch.arange(40), torch.randint(0, V, (2000,), generator=gen(8)), torch.arange(V - 40, V)])
+    q, scale, z = SP.quantize(w[at.cuda()].cpu(), group, True)
+    assert torch.equal(SP.unpack(r["packed"][at.cuda()].cpu()), q)
+    assert torch.equal(r["scale"][at.cuda()].cpu(), scale) and torch.equal(r["zero"][at.cuda()].cpu(), z)
+    assert torch.equal(back[at.cuda()].cpu(), SP.weights(q, scale, z, group).to(BF))
+    assert r["status"].eq(0).all()
