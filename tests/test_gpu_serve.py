@@ -608,3 +608,39 @@ def test_quantize_offsets_past_32_bits(sv):
     assert torch.equal(r["scale"][at.cuda()].cpu(), scale) and torch.equal(r["zero"][at.cuda()].cpu(), z)
     assert torch.equal(back[at.cuda()].cpu(), SP.weights(q, scale, z, group).to(BF))
     assert r["status"].eq(0).all()
+
+
+FIRST_CAPTURED = """
+import torch
+import speculative_decoding_verification_26_gb300 as sv
+g = torch.Generator().manual_seed(3)
+w = torch.randn(3000, 512, generator=g).bfloat16().cuda()
+x = torch.randn(2, 3, 512, generator=g).bfloat16().cuda()
+history = torch.randint(0, 3000, (2, 40), generator=g).int().cuda()
+rep = torch.full((2,), 1.5).cuda()
+def step():
+    w4 = sv.quantize_w4(w, 64, zero=True)
+    rows = sv.linear_w4(x, w4["packed"], w4["scale"], w4["zero"], group=64)["logits"]
+    back = sv.dequantize_w4(w4["packed"], w4["scale"], w4["zero"], group=64)["weight"]
+    return back, sv.adjust_logits(rows, history, repetition=rep)["logits"]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    outs = step()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in outs]
+assert all(torch.equal(a, b) for a, b in zip(got, step()))
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_are_captured(sv):
+    """Kernels are configured on the first call that needs them, in a capture too."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CAPTURED], cwd=root, env={**os.environ, "PYTHONPATH": root},
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
