@@ -95,31 +95,60 @@ struct Eight {
   }
 };
 
-// What the lanes of a group agree on: the largest magnitude, and with zero points the range.
+// What the lanes of a group agree on: the largest magnitude, and with zero points the range (then
+// NaN goes through all of it).
 struct Range {
   uint32_t most;
   float lo, hi;
 };
+__device__ __forceinline__ float least(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float greatest(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t least2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t greatest2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 template <int DT, int LANES, bool ZERO>
 __device__ __forceinline__ Range range_of(const Eight<DT>& w) {
   Range r;
-  r.most = w.most();
   r.lo = r.hi = 0.f;
-  if constexpr (ZERO) {
+  if constexpr (!ZERO) {
+    r.most = w.most();
+  } else if constexpr (DT == SPEC_BF16) {
+    const uint32_t lo = least2(least2(w.w[0], w.w[1]), least2(w.w[2], w.w[3]));
+    const uint32_t hi = greatest2(greatest2(w.w[0], w.w[1]), greatest2(w.w[2], w.w[3]));
+    r.lo = least(least(bf16_lo(lo), bf16_hi(lo)), 0.f);
+    r.hi = greatest(greatest(bf16_lo(hi), bf16_hi(hi)), 0.f);
+  } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      r.lo = fminf(r.lo, w.at(j));
-      r.hi = fmaxf(r.hi, w.at(j));
+      r.lo = least(r.lo, w.at(j));
+      r.hi = greatest(r.hi, w.at(j));
     }
   }
 #pragma unroll
   for (int off = LANES / 2; off >= 1; off >>= 1) {
-    r.most = max(r.most, __shfl_xor_sync(0xffffffffu, r.most, off));
     if constexpr (ZERO) {
-      r.lo = fminf(r.lo, __shfl_xor_sync(0xffffffffu, r.lo, off));
-      r.hi = fmaxf(r.hi, __shfl_xor_sync(0xffffffffu, r.hi, off));
+      r.lo = least(r.lo, __shfl_xor_sync(0xffffffffu, r.lo, off));
+      r.hi = greatest(r.hi, __shfl_xor_sync(0xffffffffu, r.hi, off));
+    } else {
+      r.most = max(r.most, __shfl_xor_sync(0xffffffffu, r.most, off));
     }
   }
+  if constexpr (ZERO) r.most = __float_as_uint(greatest(-r.lo, r.hi)) & 0x7FFFFFFFu;
   return r;
 }
 // A group's scale and zero point, and a lane's word.
@@ -178,15 +207,17 @@ __device__ __forceinline__ bool code_quickly(const Eight<DT>& w, const Range& r,
     if constexpr (DT == SPEC_F32) quick = quick && !near_half(grid, m);
     c.zero = fminf(m - kMagic, 15.f);
   }
-  // the sum of (kMagicBits + n) << 4 p, and of z - kMagicBits: (n + z) << 4 p
-  const float least = kMagic - c.zero, most = kMagic + 15.f - c.zero;
+  // the sum of (kMagicBits + n) << 4 p, and of z - kMagicBits: (n + z) << 4 p.  With zero points n + z can be
+  // 16, both rounded up, but not less than 0: of the least weight it is 0 (n = -z; -lo / s <= 15 (1 + 2^-8)
+  // is rounded to 15 at most), and n does not fall with the weight.
+  const float most = kMagic + 15.f - c.zero;
   uint32_t word = ZERO ? ((uint32_t)(int)c.zero - kMagicBits) * 0x11111111u : (8u - kMagicBits) * 0x11111111u;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     const float grid = on_grid(w.at(j), inv);
     float m = at_magic(grid);
     if constexpr (DT == SPEC_F32) quick = quick && !near_half(grid, m);
-    if constexpr (ZERO) m = fminf(fmaxf(m, least), most);
+    if constexpr (ZERO) m = fminf(m, most);
     word += __float_as_uint(m) << 4 * nibble_of(j);
   }
   c.word = word;
