@@ -332,8 +332,14 @@ int blocks(int V, int rows) { return (int)((V + (kW4Threads / 32) * (long long)r
 template <int DT, int LANES, bool ZERO>
 void quantize(const W4Params& P, int nsm, cudaStream_t s) {
   constexpr int kRows = DT == SPEC_BF16 ? 4 : 2;
-  if (few<kRows>(P.V, nsm)) quantize_kernel<DT, LANES, ZERO, 1, kRows><<<blocks(P.V, 1), kW4Threads, 0, s>>>(P);
-  else quantize_kernel<DT, LANES, ZERO, kRows, 1><<<blocks(P.V, kRows), kW4Threads, 0, s>>>(P);
+  // fp32 with zero points goes by stretches always: 20000 x 8192 weights take 142 us so and 162 by rows
+  if constexpr (DT != SPEC_F32 || !ZERO) {
+    if (!few<kRows>(P.V, nsm)) {
+      quantize_kernel<DT, LANES, ZERO, kRows, 1><<<blocks(P.V, kRows), kW4Threads, 0, s>>>(P);
+      return;
+    }
+  }
+  quantize_kernel<DT, LANES, ZERO, 1, kRows><<<blocks(P.V, 1), kW4Threads, 0, s>>>(P);
 }
 template <int LANES>
 void quantize_of(const W4Params& P, int nsm, cudaStream_t s) {
