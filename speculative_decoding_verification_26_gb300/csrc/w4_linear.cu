@@ -227,10 +227,12 @@ struct W4Maps {
 };
 
 // What a CTA does: its tiles, and of each the stages [first, first + stages) of 256 k.
+template <int NT>
 struct Plan {
+  static constexpr bool One = NT < 128;      // tile of rows (a call with more rows has tiles of 128)
   int items, step, row_tiles, first, stages;
-  __device__ __forceinline__ int row0(int item, int nt) const { return item % row_tiles * nt; }
-  __device__ __forceinline__ int col0(int item) const { return item / row_tiles * kRows; }
+  __device__ __forceinline__ int row0(int item) const { return One ? 0 : item % row_tiles * NT; }
+  __device__ __forceinline__ int col0(int item) const { return (One ? item : item / row_tiles) * kRows; }
 };
 
 template <int NT, int GROUP, bool ZERO>
@@ -246,7 +248,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
   constexpr int kWeightCopies = Z::UnpackWarps + Z::SumWarps, kHiddenCopies = kWeightCopies + 1, kProducts = kWeightCopies + 2;
   const Waits waits{&S.failed, P.wait_limit};
 
-  Plan plan;
+  Plan<NT> plan;
   plan.row_tiles = (P.n + NT - 1) / NT;
   plan.items = plan.row_tiles * ((P.V + kRows - 1) / kRows);
   const int rank = blockIdx.x % split, item0 = blockIdx.x / split;
@@ -477,13 +479,14 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
         for (int c = 0; c < Z::Columns; ++c) acc[c] = NAN;
       }
       if (split == 1) {
-        const int r0 = plan.row0(item, NT) + part * Z::Columns, rows = P.n - r0;
+        const int r0 = plan.row0(item) + part * Z::Columns, rows = P.n - r0;
         const size_t o = (size_t)r0 * P.V + v;
         if (P.dtype == SPEC_BF16 && even) {
           // two lanes exchange columns: each stores two neighbours of a row at once
           __nv_bfloat16* to = reinterpret_cast<__nv_bfloat16*>(P.out) + o + (lane & 1 ? (ptrdiff_t)P.V - 1 : 0);
 #pragma unroll
           for (int c = 0; c < Z::Columns; c += 2, to += 2 * (size_t)P.V) {
+            if (NT == 16 && c >= rows) break;
             const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? acc[c] : acc[c + 1], 1);
             const __nv_bfloat162 two = lane & 1 ? __floats2bfloat162_rn(other, acc[c + 1]) : __floats2bfloat162_rn(acc[c], other);
             if (c + (lane & 1) < rows && v < P.V) *reinterpret_cast<__nv_bfloat162*>(to) = two;
@@ -533,7 +536,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
           mbar_arrive_expect_tx(&S.x_full[x.stage], box_bytes * (Z::XK / 64));
 #pragma unroll
           for (int c = 0; c < Z::XK / 64; ++c)
-            copy_box(x_ring + x.stage * Z::XSlot + c * Z::XBox, &M.hidden, k + 64 * c, plan.row0(item, NT), &S.x_full[x.stage]);
+            copy_box(x_ring + x.stage * Z::XSlot + c * Z::XBox, &M.hidden, k + 64 * c, plan.row0(item), &S.x_full[x.stage]);
         }
         x.next(Z::XS);
       }
@@ -548,9 +551,9 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     a.skip(mine, Z::Slots);
     x.skip(mine / kPer, Z::XS);
     int sub = mine % kPer;
-    uint32_t a_seen = 0;
+    uint32_t a_seen = 0, x_seen = 0;
     for (long long slot = mine, slots = (long long)tiles * plan.stages * Z::Subs; slot < slots; slot += Z::Issuers) {
-      if (!(ok = wait_for(&S.x_full[x.stage], x.phase, waits) && wait_for(&S.ready[a.stage], a.phase, waits, a_seen))) break;
+      if (!(ok = wait_for(&S.x_full[x.stage], x.phase, waits, x_seen) && wait_for(&S.ready[a.stage], a.phase, waits, a_seen))) break;
       tc_fence_after();
       const uint32_t at = tmem + a.stage * Z::ACols, to = tmem + Z::DColumn + a.stage * Z::DCols;
       const uint64_t desc = tc_desc(x_ring + x.stage * Z::XSlot + sub * Z::SlotK / 64 * Z::XBox + sub * Z::SlotK % 64 * 2, true);
@@ -567,6 +570,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
       sub += Z::Issuers;
       x.skip(sub / kPer, Z::XS);
       sub %= kPer;
+      x_seen = over(&S.x_full[x.stage], x.phase);
     }
   }
   __syncwarp();
@@ -579,7 +583,7 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     const int row = (warp & 3) * 32 + lane, part = (warp - Z::UnpackWarps) >> 2;
     cluster_sync();
     if (sums) {
-      const int v = plan.col0(item0) + row, r0 = plan.row0(item0, NT);
+      const int v = plan.col0(item0) + row, r0 = plan.row0(item0);
       for (int c = rank + part * split; c < NT && r0 + c < P.n; c += split * (Z::SumWarps / 4)) {
         float sum = 0.f;
         for (int k = 0; k < split; ++k) {
