@@ -10,8 +10,8 @@
 // most 128 long.
 //
 // A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states (16 to 128, the
-// least that holds them: 36 us for one row and 37 for 16 against 151936 x 2048 weights in groups of
-// 128, 40 for 32, 46 for 64, 69 for 128, 247 for 512).  The k of a tile goes by stages of 256 (16 KB of
+// least that holds them: 35 us for one row and 36 for 16 against 151936 x 2048 weights in groups of
+// 128, 39 for 32, 45 for 64, 69 for 128, 247 for 512).  The k of a tile goes by stages of 256 (16 KB of
 // weights), cut into slots of whole groups: a slot has its own columns of tensor memory for A and
 // for the sums of its groups, and two barriers, "ready" (unpacked, and the sums of its last use
 // taken) and "done" (products finished): one wait and one commit of the issuing warp a slot.
@@ -24,10 +24,11 @@
 // Where there are few tiles and much k, a cluster of CTAs splits the k of a tile, and the parts
 // are joined through distributed shared memory in the order of their ranks.
 //
-// What bounds it: for few rows the hand-overs between the roles.  The weights alone stream through
-// the ring in 28 us (5.8 TB/s), and with hand-overs but without unpacking, products and sums a call
-// takes 33 to 37; unpacking has 2.75 instructions a pair of weights.  For many rows the warps that
-// take the sums (64 columns of each group to a thread).  With barriers of their own for A, hidden
+// What bounds it: for few rows launch and first copies, and unpacking (2.75 instructions a pair of
+// weights) with the hand-overs between the roles; the weights alone stream through the ring in 28 us
+// (5.8 TB/s).  For many rows the way from a slot's products to its sums and on to the next products
+// in its columns of tensor memory, which hold two slots: a slot of 128 k takes 1000 clocks, 512 of
+// them products.  With barriers of their own for A, hidden
 // states and sums at every 128 k one row took 54 us; with products issued by a single lane of a
 // diverged warp 132.  mma.sync with the weights straight in registers took 108 us for up to 8 rows
 // (its m16n8k16 goes out every 20 clocks of a scheduler, and needs the scales of 16 rows a warp).
