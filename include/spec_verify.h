@@ -436,7 +436,7 @@ int spec_linear_w4(const void* hidden, int dtype, int n, const uint8_t* packed, 
  *   x <- x / repetition if x > 0, else x repetition   (v in the history, prompt
  *        included, or among those drafts)
  *   x <- x - (c frequency + presence)                 (c > 0)
- *   x <- x + the biases listed for v, added in their order
+ *   x <- x + the sum of the biases listed for v, held in 64 bits
  *   x <- -inf                                         (the mask's bit of v is 0)
  * in fp32, rounded once.  Logits that nothing of this touches keep their bits, and
  * a NaN or infinity is taken like any other value.
