@@ -141,7 +141,9 @@ int spec_profile_next_call(void* begin_event, void* end_event);
  * setting applies to calls enqueued afterwards by any host thread;
  * cycles <= 0 restores the default of 4e9 cycles (about 2 s at 2 GHz), which
  * no healthy call comes near.  A low value (1) makes most requests of a call
- * time out; it is meant only for tests of that path.  The wait for a CTA's
+ * time out; it is meant only for tests of that path.  Most waits sleep in
+ * hardware, some microseconds at least, and what comes within a sleep is in
+ * time however low the limit.  The wait for a CTA's
  * own copies in flight before it exits always keeps the default.  Returns
  * SPEC_OK. */
 int spec_set_wait_limit(long long cycles);

@@ -109,6 +109,18 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const W
     }
   }
 }
+// The same without sleep.  Hardware sleeps for microseconds whatever shorter time it is asked for, so
+// wait_for never gives up on what comes sooner, however low the limit.
+__device__ __forceinline__ bool poll_for(uint64_t* bar, uint32_t parity, const Waits& waits) {
+  const long long t0 = clock64();
+  while (!__all_sync(0xffffffffu, over(bar, parity))) {
+    if (__any_sync(0xffffffffu, *waits.failed || clock64() - t0 > waits.limit)) {
+      *waits.failed = 1;
+      return false;
+    }
+  }
+  return true;
+}
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(one));
@@ -539,6 +551,8 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
           for (int c = 0; c < Z::XK / 64; ++c)
             copy_box(x_ring + x.stage * Z::XSlot + c * Z::XBox, &M.hidden, k + 64 * c, plan.row0(item), &S.x_full[x.stage]);
         }
+        // a limit shorter than a sleep holds for each of these copies (polled for in every wait: 1 to 4 % of a call)
+        if (waits.limit < kSleepNs && !(ok = poll_for(&S.x_full[x.stage], x.phase, waits))) break;
         x.next(Z::XS);
       }
     }
