@@ -545,18 +545,13 @@ __global__ void __launch_bounds__(256) finish_grads(const __grid_constant__ CePa
   }
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled g_encode = nullptr;              // set once by configure_linear_ce
-
 // bf16 matrix of `height` rows of `width`, `stride` apart, boxes of 64 columns x `box` rows
 bool encode(CUtensorMap* map, const void* p, uint64_t width, uint64_t stride, uint64_t height, uint32_t box) {
   const cuuint64_t dims[2] = {width, height}, strides[1] = {stride * 2};
   const cuuint32_t boxes[2] = {(cuuint32_t)kTcK, box}, ones[2] = {1, 1};
-  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, boxes, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(p), dims, strides, boxes, ones,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <bool BWD>
@@ -568,12 +563,8 @@ void launch_gather(const CeParams& P, cudaStream_t s) {
 }  // namespace
 
 cudaError_t configure_linear_ce() {
-  cudaDriverEntryPointQueryResult found;
-  void* f = nullptr;
-  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+  cudaError_t e = find_encoder();
   if (e != cudaSuccess) return e;
-  if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
-  g_encode = reinterpret_cast<EncodeTiled>(f);
   const int smem = (int)kTcSmem;
   e = cudaFuncSetAttribute(ce_forward, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(ce_softmax<0>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);

@@ -16,9 +16,31 @@
 
 #include <cuda.h>
 
+#include <atomic>
+
 #include "rows.cuh"
 
 namespace sv {
+
+// ---------------------------------------------------------------------------
+// The driver's encoder of tensor maps, looked up on the process's first call that needs it (and again
+// where that failed).  Host threads may look it up and use it at the same time, for several devices.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline std::atomic<EncodeTiled> g_encode_tiled{nullptr};
+inline cudaError_t find_encoder() {
+  if (g_encode_tiled.load(std::memory_order_relaxed)) return cudaSuccess;
+  cudaDriverEntryPointQueryResult found;
+  void* f = nullptr;
+  const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return e;
+  if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
+  g_encode_tiled.store(reinterpret_cast<EncodeTiled>(f), std::memory_order_relaxed);
+  return cudaSuccess;
+}
+// after find_encoder
+inline EncodeTiled encoder() { return g_encode_tiled.load(std::memory_order_relaxed); }
 
 constexpr int kTcTile = 256;                 // tile rows and columns of a pair
 constexpr int kTcHalf = 128;                 // of one CTA

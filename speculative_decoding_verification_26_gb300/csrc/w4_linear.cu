@@ -622,18 +622,12 @@ linear_kernel(const __grid_constant__ W4Params P, const __grid_constant__ W4Maps
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTcColumns) : "memory");
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled g_encode_w4 = nullptr;           // set once by configure_w4
-
 // rows of `width` elements of `size` bytes, boxes of 128 bytes x `box` rows
 bool encode(CUtensorMap* map, CUtensorMapDataType type, int size, const void* p, uint64_t width, uint64_t height, uint32_t box) {
   const cuuint64_t dims[2] = {width, height}, strides[1] = {width * size};
   const cuuint32_t boxes[2] = {(cuuint32_t)(128 / size), box}, ones[2] = {1, 1};
-  return g_encode_w4(map, type, 2, const_cast<void*>(p), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-         CUDA_SUCCESS;
+  return encoder()(map, type, 2, const_cast<void*>(p), dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int NT, int GROUP>
@@ -690,12 +684,8 @@ cudaError_t allow_all() {
 }  // namespace
 
 cudaError_t configure_w4() {
-  cudaDriverEntryPointQueryResult found;
-  void* f = nullptr;
-  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+  cudaError_t e = find_encoder();
   if (e != cudaSuccess) return e;
-  if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorNotSupported;
-  g_encode_w4 = reinterpret_cast<EncodeTiled>(f);
   e = allow_all<16>();
   if (e == cudaSuccess) e = allow_all<32>();
   if (e == cudaSuccess) e = allow_all<64>();
