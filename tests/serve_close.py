@@ -1,6 +1,8 @@
 """Comparisons of the calls around the vocabulary rows of a decode step with their
 plain 64-bit implementations.  A tolerance holds where a finite value is expected;
 infinities have to be equal, NaN to be NaN."""
+import math
+
 import torch
 
 import serve_plain as SP
@@ -38,6 +40,24 @@ def adjusted(x, a, refused=()):
     if len(refused):
         tol[torch.tensor(list(refused))] = 0
     return y, tol
+
+
+def product(x, q, scale, zero, group, dtype):
+    """(logits, tolerances) of spec_linear_w4, by its formula: each group's sum times its scale.  Sums of
+    exact products in fp32: (8 + sqrt H) 2^-23 of the magnitudes of all terms, and half a step of the type."""
+    n, H = x.shape
+    V = q.shape[0]
+    z = 8.0 if zero is None else zero.double().repeat_interleave(group, 1)[:, :H]
+    w = q.double() - z
+    want, mag = torch.zeros(n, V, dtype=torch.double), torch.zeros(n, V, dtype=torch.double)
+    for g, k in enumerate(range(0, H, group)):
+        h, part, s = x[:, k:k + group].double(), w[:, k:k + group], scale[:, g].double()
+        # (a matrix product may leave out or reorder terms with infinities: these are summed one by one)
+        sums = torch.stack([(h * part[v]).sum(1) for v in range(V)], 1) if not torch.isfinite(h).all() else h @ part.t()
+        want += sums * s
+        mag += (h.abs() @ part.abs().t()).nan_to_num(math.inf) * s.abs()
+    want = in_type(want, dtype)
+    return want, (8 + math.sqrt(H)) * 2.0 ** -23 * mag + HALF[dtype] * want.abs()
 
 
 def check_adjusted(call, x, a, refused=(), lay=lambda x: x, lay_out=lambda x: x):

@@ -7,7 +7,7 @@ import torch
 
 import serve_close as SC
 import serve_plain as SP
-from test_gpu_serve import BF, F32, request as make
+from test_gpu_serve import BF, F32, request as make, weights_of
 
 INF, NAN = math.inf, math.nan
 
@@ -60,3 +60,24 @@ def test_removed_logits_that_are_not(dtype, spoil):
     only = {"mask": a["mask"]}                        # the mask alone, too
     with pytest.raises(AssertionError):
         SC.check_adjusted(lambda *p, **k: plain(*p, spoil=spoil, **k), x, only, lay=torch.clone, lay_out=torch.clone)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_products_with_infinities_that_are_wrong(dtype):
+    q, scale, z = weights_of(60, 160, 32, True, 3)
+    x = torch.randn(4, 160).to(BF)
+    x[2, 40], scale[5, 1], scale[6, 4] = INF, INF, -INF
+    want, tol = SC.product(x, q, scale, z, 32, dtype)
+    right = want.to(dtype).double()
+    SC.all_close(right, want, tol)
+    assert torch.isinf(want[2]).any() and torch.isinf(want[0, 5]) and torch.isinf(want[0, 6])
+    for at in ((2, int(torch.isinf(want[2]).nonzero()[0])), (0, 5), (3, 6)):
+        for value in (0.0, -float(right[at]), NAN):
+            wrong = right.clone()
+            wrong[at] = value
+            with pytest.raises(AssertionError):
+                SC.all_close(wrong, want, tol)
+    # a finite product is what the matrix of weights gives
+    w = SP.weights(q, scale, z, 32)
+    fine = torch.isfinite(want)
+    assert torch.allclose(want[fine], (x.double() @ w.t())[fine], rtol=1e-12, atol=1e-12)
