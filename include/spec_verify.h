@@ -397,6 +397,7 @@ int spec_linear_ce_backward(const void* hidden, const void* weight, int dtype, i
  *          for i = 0 .. 7;
  *   scale  [V, ceil(H / group)] bf16;
  *   zero   [V, ceil(H / group)] uint8, 0 to 15, or NULL: every z is 8.
+ *          (Not checked: with a byte above 15 the weights of its group have no meaning.)
  * Sizes: 1 <= V < 2^28, 32 <= H <= 65536, H a multiple of 32; weight and packed
  * 16-byte aligned.
  * spec_w4_quantize: for each group of weight [V, H] (SPEC_F32 or SPEC_BF16), with

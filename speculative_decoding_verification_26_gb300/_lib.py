@@ -691,7 +691,8 @@ def quantize_w4(weight, group=128, *, zero=False, out=None):
 
 def dequantize_w4(packed, scale, zero=None, *, group=128, dtype=None, out=None):
     """The weights [V, H] that quantize_w4's results stand for, in `dtype` (bf16
-    by default, or fp32).  Returns {"weight": [V, H]} (see spec_w4_dequantize)."""
+    by default, or fp32).  Zero points are 0 to 15, not checked.  Returns
+    {"weight": [V, H]} (see spec_w4_dequantize)."""
     h = _hot()
     V, H, per = _w4_sizes(packed, group)
     dev = packed.device
@@ -705,7 +706,8 @@ def dequantize_w4(packed, scale, zero=None, *, group=128, dtype=None, out=None):
 
 def linear_w4(hidden, packed, scale, zero=None, *, group=128, dtype=None, out=None):
     """hidden [..., H] (bf16) times 4-bit weights (quantize_w4), transposed:
-    {"logits": [..., V]} in `dtype` (bf16 by default, or fp32) (see spec_linear_w4)."""
+    {"logits": [..., V]} in `dtype` (bf16 by default, or fp32).  Zero points are 0 to
+    15, not checked (see spec_linear_w4)."""
     h = _hot()
     V, H, per = _w4_sizes(packed, group)
     dev = packed.device
