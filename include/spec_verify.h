@@ -439,7 +439,7 @@ int spec_linear_w4(const void* hidden, int dtype, int n, const uint8_t* packed, 
  *   x <- x / repetition if x > 0, else x repetition   (v in the history, prompt
  *        included, or among those drafts)
  *   x <- x - (c frequency + presence)                 (c > 0)
- *   x <- x + the sum of the biases listed for v, held in 64 bits
+ *   x <- x + the biases listed for v, summed in their order
  *   x <- -inf                                         (the mask's bit of v is 0)
  * in fp32, rounded once.  Logits that nothing of this touches keep their bits, and
  * a NaN or infinity is taken like any other value.
@@ -455,7 +455,8 @@ int spec_linear_w4(const void* hidden, int dtype, int n, const uint8_t* packed, 
  *   repetition, frequency, presence [B] fp32 or NULL (1, 0, 0), finite, repetition
  *              above 0;
  *   bias_index, bias_value [B, biases], or NULL with biases = 0: an index of -1 is
- *              left out; a value is finite or -inf;
+ *              left out; a value is finite or -inf.  A sum of finite values has no
+ *              limit of its own: only x with it may be past the largest fp32;
  *   mask       [B, R, ceil(V / 32)] 32-bit words or NULL: bit v mod 32 of word
  *              v / 32 is 1 for a token that is allowed.  Rows may be left without one;
  *   status     [B] or NULL: 0, or bits SPEC_ST_BAD_TOKEN (a token or index outside

@@ -5,9 +5,11 @@
 // behind the prompt, and those drafts), and v "seen" when it occurs anywhere,
 //   x <- seen ? (x > 0 ? x / rep : x rep) : x;   x <- x - (c freq + pres) where c > 0;
 //   x <- x + sum of the biases listed for v;     x <- -inf where the mask has 0,
-// in fp32, rounded once to the row's type.  The biases of a token are summed in 64 bits: the
-// sum of up to 4096 finite ones is finite there, so that a -inf among them stays -inf, and x plus
-// a single one, rounded to fp32, is the sum in fp32.  Logits that nothing touches keep their bits.
+// in fp32, rounded once to the row's type.  Logits that nothing touches keep their bits.
+//   A sum of biases that leaves +-2^100 is held times 2^-13: there 4096 finite biases stay finite,
+// so that a -inf among them stays -inf, and an fma adds it to the logit with one rounding.  (Sums in
+// 64 bits cost 320 -> 430 us for 64 x 8 x 151936 bf16 logits with 4096 biases, and 67 -> 430 for
+// one request whose 4096 biases are of one token.)
 //
 // A CTA takes a range of the vocabulary for all R rows of a request.  It counts the
 // history's tokens of its range in shared memory (whole numbers: the order of the
@@ -35,20 +37,20 @@ constexpr int kRows = 2;                     // rows taken at once
 constexpr uint32_t kInPrompt = 0x80000000u, kInDraft = 0x40000000u, kTouched = 0x20000000u,
                    kCount = 0x1FFFFFFFu;   // of a count word
 
-// In shared memory: this, counts [range]; with biases a sum for each token that has some (of
-// no more tokens than there are biases, or places in the range) and the places' sums [range];
-// the touched tokens' places in the range, and the rows' masks of the range (a word more each).
+// In shared memory: this, counts [range]; with biases their sums [range] and a bit for each that is
+// held times kNarrow; the touched tokens' places in the range, and the rows' masks of the range (a
+// word more each).
 struct AdjustShared {
   int draft[SPEC_MAX_G + 1];
   int bad, listed;
   int pad[2];
 };
-__host__ __device__ constexpr int bias_sums(int range, int biases) { return (biases < range ? biases + 1 : range) / 2 * 2; }
-__host__ __device__ constexpr size_t adjust_smem_bytes(int range, bool any, int biases, int masked_rows) {
-  return sizeof(AdjustShared) + (any ? (size_t)range * (biases > 0 ? 8 : 6) + bias_sums(range, biases) * sizeof(double) : 0) +
+__host__ __device__ constexpr size_t adjust_smem_bytes(int range, bool any, bool biases, int masked_rows) {
+  return sizeof(AdjustShared) + (any ? (size_t)range * 6 + (biases ? range * 4 + range / 8 : 0) : 0) +
          ((size_t)masked_rows * (range / 8 + 4) + 15) / 16 * 16;
 }
-static_assert(sizeof(AdjustShared) % 16 == 0, "sums and masks are aligned");
+constexpr float kWide = 0x1p100f, kNarrow = 0x1p-13f;
+static_assert(SPEC_MAX_BIASES <= 1 << 12, "a sum of biases");
 
 struct Penalties {
   float rep, freq, pres;
@@ -148,15 +150,15 @@ __global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_
   AdjustShared& S = *reinterpret_cast<AdjustShared*>(adjust_smem);
   const int range = 1 << shift;
   uint32_t* const count = reinterpret_cast<uint32_t*>(adjust_smem + sizeof(AdjustShared));
-  double* const bias = reinterpret_cast<double*>(count + range);
-  uint16_t* const list = reinterpret_cast<uint16_t*>(bias + bias_sums(range, P.biases));
-  uint16_t* const sum_of = list + range;                 // of a token that is kTouched
+  float* const bias = reinterpret_cast<float*>(count + range);
+  uint32_t* const narrowed = count + 2 * range;
+  uint16_t* const list = reinterpret_cast<uint16_t*>(P.biases > 0 ? narrowed + range / 32 : count + range);
   const int b = blockIdx.x / splits, part = blockIdx.x % splits, t = threadIdx.x;
   const int lo = part << shift, hi = min(P.V, lo + range);
   const bool counts = P.L > 0 || P.D > 0, any = counts || P.biases > 0;
 
   const int W = (P.V + 31) / 32, pitch = range / 32 + 1;
-  uint32_t* const masks_here = reinterpret_cast<uint32_t*>(adjust_smem + adjust_smem_bytes(range, any, P.biases, 0));
+  uint32_t* const masks_here = reinterpret_cast<uint32_t*>(adjust_smem + adjust_smem_bytes(range, any, P.biases > 0, 0));
   const size_t first = (size_t)b * P.R * P.V + lo, row_bytes = (size_t)P.V * ES;        // element of row 0
   const unsigned char* const in0 = P.in + first * ES;
   unsigned char* const out0 = P.out + first * ES;
@@ -198,6 +200,8 @@ __global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_
     if (t == 0) S.bad = S.listed = 0;
     // (the counts of a request without history or drafts are read for its biases)
     for (int e = t; e < range; e += kAdjustThreads) count[e] = 0;
+    if (P.biases > 0)
+      for (int e = t; e < range + range / 32; e += kAdjustThreads) count[range + e] = 0;      // 0.f
   }
   __syncthreads();
 
@@ -289,7 +293,6 @@ __global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_
       // biases of one token are added in the order of the list: the last warp takes 32 at a
       // time, the first lane of a token its sum
       const int lane = t & 31;
-      int taken = 0;                         // sums
       for (int e0 = 0; e0 < P.biases; e0 += 32) {
         const int e = e0 + lane;
         int v = -1;
@@ -302,25 +305,34 @@ __global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_
         }
         const bool mine = v >= lo && v < hi;
         if (__any_sync(0xffffffffu, mine)) {
-          const uint32_t same = __match_any_sync(0xffffffffu, mine ? v : -1 - lane), before = (1u << lane) - 1;
-          const bool leads = mine && (same & before) == 0, first = leads && !(count[v - lo] & kTouched);
-          const uint32_t firsts = __ballot_sync(0xffffffffu, first);
-          int at = taken + __popc(firsts & before);
-          taken += __popc(firsts);
-          double sum = 0.;
-          if (leads && !first) {
-            at = sum_of[v - lo];
-            sum = bias[at];
+          const uint32_t same = __match_any_sync(0xffffffffu, mine ? v : -1 - lane);
+          const bool leads = mine && (same & ((1u << lane) - 1)) == 0;
+          const int at = mine ? v - lo : 0;
+          const float start = bias[at];
+          float sum = start + x;
+          if (__any_sync(0xffffffffu, mine && same != 1u << lane)) {
+            sum = start;
+            for (int k = 0; k < 32; ++k) {
+              const float y = __shfl_sync(0xffffffffu, x, k);
+              if (same >> k & 1) sum += y;
+            }
           }
-          // (as many turns as the most frequent of them takes: an addition in 64 bits is slow)
-          for (uint32_t rest = leads ? same : 0; __any_sync(0xffffffffu, rest != 0); rest &= rest - 1) {
-            const float y = __shfl_sync(0xffffffffu, x, rest ? __ffs(rest) - 1 : lane);
-            if (rest) sum += y;
+          const bool held = narrowed[at >> 5] >> (at & 31) & 1, wide = leads && (held || !(fabsf(sum) <= kWide));
+          if (__any_sync(0xffffffffu, wide)) {
+            float narrow = held ? start : start * kNarrow;
+            for (int k = 0; k < 32; ++k) {
+              const float y = __shfl_sync(0xffffffffu, x, k);
+              if (same >> k & 1) narrow = __fmaf_rn(y, kNarrow, narrow);
+            }
+            if (wide) {
+              sum = narrow;
+              atomicOr(&narrowed[at >> 5], 1u << (at & 31));
+            }
           }
-          if (leads) bias[at] = sum;
-          if (first) {
-            sum_of[v - lo] = (uint16_t)at;
-            touch(v - lo, atomicOr(&count[v - lo], kTouched));
+          __syncwarp();
+          if (leads) {
+            bias[at] = sum;
+            touch(at, atomicOr(&count[at], kTouched));
           }
           __syncwarp();
         }
@@ -376,7 +388,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_
     const uint32_t c = count[at];
     Bits* const to = reinterpret_cast<Bits*>(out0 + i * row_bytes) + at;       // the logit, copied: it is in L2
     float x = adjusted(Lg::value(*to), c, lo + at, i, S, p);
-    if (P.biases > 0 && (c & kTouched)) x = __double2float_rn((double)x + bias[sum_of[at]]);
+    if (P.biases > 0 && (c & kTouched)) x = __fmaf_rn(bias[at], narrowed[at >> 5] >> (at & 31) & 1 ? 1.f / kNarrow : 1.f, x);
     else if ((c & (kInPrompt | kCount)) == 0 && !drafted(c, lo + at, i, S)) continue;       // a draft of a later row alone
     *to = Lg::pack(x);
   }
@@ -387,7 +399,7 @@ __global__ void __launch_bounds__(kAdjustThreads, 8) adjust_kernel(const __grid_
 template <int DT, bool ALIGNED>
 static cudaError_t allow() {
   return cudaFuncSetAttribute(adjust_kernel<DT, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)adjust_smem_bytes(kMaxRange, true, SPEC_MAX_BIASES, SPEC_MAX_G + 1));
+                              (int)adjust_smem_bytes(kMaxRange, true, true, SPEC_MAX_G + 1));
 }
 cudaError_t configure_adjust() {
   cudaError_t e = allow<SPEC_BF16, true>();
@@ -404,7 +416,7 @@ cudaError_t launch_adjust(const AdjustParams& P, int nsm, cudaStream_t s) {
   const auto splits_of = [&](int sh) { return (P.V + (1ll << sh) - 1) >> sh; };
   while (shift > 10 && splits_of(shift) * P.B < 4ll * nsm) --shift;
   const int splits = (int)splits_of(shift);
-  const size_t smem = adjust_smem_bytes(1 << shift, P.L > 0 || P.D > 0 || P.biases > 0, P.biases, P.mask ? P.R : 0);
+  const size_t smem = adjust_smem_bytes(1 << shift, P.L > 0 || P.D > 0 || P.biases > 0, P.biases > 0, P.mask ? P.R : 0);
   const unsigned grid = (unsigned)(splits * (long long)P.B);
   const int es = P.dtype == SPEC_BF16 ? 2 : 4;
   const bool aligned = ((size_t)P.V * es) % 16 == 0 && reinterpret_cast<uintptr_t>(P.in) % 16 == 0 && reinterpret_cast<uintptr_t>(P.out) % 16 == 0;

@@ -1,8 +1,10 @@
 """Biases of a token that is listed several times.
 
-The sum of a token's biases is held in 64 bits and added to its logit, rounded once to
-fp32 and once to the type.  The sum of n biases in the order of their list is computed
-here by the same n additions, so without penalties the logits are equal, not close.
+A token's biases are added in the order of their list, each sum rounded to the 24 bits
+of fp32 but not bounded by its largest value, and the last one to the logit, rounded once
+to fp32 and once to the type.  The same roundings are made here, so without penalties
+the logits are equal, not close.  (A sum of two numbers of 24 bits in 64 bits, rounded
+to 24, is the sum rounded to 24: 53 >= 2 24 + 2.)
 """
 import math
 
@@ -17,14 +19,22 @@ INF = math.inf
 BIG = 3e38                                            # two of them are past the largest fp32
 
 
+def rounded(s):
+    """To 24 bits, in 64; the values here are no subnormal numbers."""
+    if not math.isfinite(s):
+        return s
+    m, e = math.frexp(s)
+    return math.ldexp(round(m * (1 << 24)), e - 24)        # halves to even
+
+
 def expected(x, index, value):
-    """Rows with the biases alone: sums in 64 bits, in the order of the list."""
+    """Rows with the biases alone."""
     y = x.clone()
     for b in range(x.shape[0]):
         sums = {}
         for v, a in zip(index[b].tolist(), value[b].tolist()):
             if v >= 0:
-                sums[v] = sums.get(v, 0.0) + a
+                sums[v] = rounded(sums.get(v, 0.0) + a)
         for v, s in sums.items():
             y[b, :, v] = (x[b, :, v].double() + s).float().to(x.dtype)
     return y
