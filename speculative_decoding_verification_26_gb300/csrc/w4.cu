@@ -7,7 +7,9 @@
 // Both kernels read and write each value once: HBM bounds them, and the instructions
 // of a weight come next (4 for a bf16 weight, from its bits to its place in a word).  A
 // warp takes several rows, or several stretches of one, so that their loads are on their way
-// together.  151936 x 2048 bf16 weights, groups of 128: 131 us (6.0 TB/s), issue 69 % busy, and 120
+// together.  Lanes behind the end of a row that is no multiple of 256 weights hold zeros, for which the
+// warp goes the slow way of a scale of 0: 151936 x 1184 bf16 weights in groups of 128 take 89 us (67 by
+// their bytes).  151936 x 2048 bf16 weights, groups of 128: 131 us (6.0 TB/s), issue 69 % busy, and 120
 // us back (6.5 TB/s).
 #include "rows.cuh"
 #include "serve.cuh"
@@ -42,7 +44,8 @@ __device__ __forceinline__ bool near_half(float grid, float magic) {
   return fabsf(__fadd_rn(grid, -__fadd_rn(magic, -(kMagic - 192.f)))) > 0.5f - 1.f / 16384;
 }
 
-// a / d for d = 7 or 15, rounded to nearest: the remainder a - q d is exact, and a quotient by
+// a / d for d = 7 or 15, rounded to nearest, by one correction of a near quotient with its remainder
+// (Markstein 1990, "Computation of elementary functions"): the remainder a - q d is exact, and a quotient by
 // 7 or 15 that is no tie is 1/30 of a unit in the last place from one at least, where the
 // correction is good to 2^-24 of it.  Not for a near the smallest numbers.
 template <int D>

@@ -11,7 +11,7 @@
 //
 // A CTA (one an SM) takes tiles of 128 vocabulary rows x NT rows of hidden states (16 to 128, the
 // least that holds them: 35 us for one row and 36 for 16 against 151936 x 2048 weights in groups of
-// 128, 39 for 32, 45 for 64, 69 for 128, 247 for 512).  The k of a tile goes by stages of 256 (16 KB of
+// 128, 39 for 32, 45 for 64, 69 for 128, 247 to 263 for 512).  The k of a tile goes by stages of 256 (16 KB of
 // weights), cut into slots of whole groups: a slot has its own columns of tensor memory for A and
 // for the sums of its groups, and two barriers, "ready" (unpacked, and the sums of its last use
 // taken) and "done" (products finished): one wait and one commit of the issuing warp a slot.
