@@ -99,7 +99,7 @@ def program(tmp_path_factory):
 def test_the_encoder_is_shared_without_a_race(program, family):
     """Looked up until it is found (once in vain, once more here), not again for another device."""
     r = subprocess.run([program, family], capture_output=True, text=True, timeout=120)
-    if "unexpected memory mapping" in r.stderr:          # the checker wants addresses that are not randomised as far
+    if "unexpected memory mapping" in r.stderr:          # the sanitizer wants addresses less random
         r = subprocess.run(["setarch", "-R", program, family], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr[:3000]
     a, b, lookups, encoded = map(int, r.stdout.split())
